@@ -46,7 +46,11 @@ EXPORTS = ("wq8_plan_create", "wq8_plan_destroy", "wq8_plan_query", "wq8_plan_ma
            "wq8_weights_prepare", "wq8_conv_forward", "wq8_stage1", "wq8_stage2",
            "wq8_stage2_i32", "wq8_stage3", "wq8_stage23", "wq8_direct_query",
            "wq8_direct_weights_prepare", "wq8_direct_quantize_x", "wq8_direct_conv",
-           "wq8_direct_forward", "wq8_conv_forward_noalloc", "wq8_status_string", "wq8_last_error")
+           "wq8_direct_forward", "wq8_conv_forward_noalloc", "wq8_status_string", "wq8_last_error",
+           # group norm and matrix product, wrapped in ops.py
+           "wq8_norm_plan_create", "wq8_norm_plan_destroy", "wq8_norm_plan_query", "wq8_norm_forward",
+           "wq8_norm_backward", "wq8_linear_plan_create", "wq8_linear_plan_destroy",
+           "wq8_linear_plan_query", "wq8_linear_forward", "wq8_linear_backward")
 
 # bytes of the device array wq8_conv_forward_noalloc uses as its workspace
 NOALLOC_MAX_WORKSPACE = 64 << 20
@@ -84,12 +88,21 @@ def load(path: str = LIB_PATH):
     lib.wq8_direct_conv.argtypes = [P, P, P, P, P, P, P]
     lib.wq8_direct_forward.argtypes = [P, P, P, P, P, P, S, P]
     lib.wq8_conv_forward_noalloc.argtypes = [P, P, P, P, P, P]
+    for kind in ("norm", "linear"):
+        getattr(lib, f"wq8_{kind}_plan_create").argtypes = [P, C.POINTER(P)]
+        getattr(lib, f"wq8_{kind}_plan_destroy").argtypes = [P]
+        getattr(lib, f"wq8_{kind}_plan_destroy").restype = None
+        getattr(lib, f"wq8_{kind}_plan_query").argtypes = [P, C.POINTER(S), C.POINTER(S)]
+    lib.wq8_norm_forward.argtypes = [P] * 9 + [S, P]
+    lib.wq8_norm_backward.argtypes = [P] * 13 + [S, P]
+    lib.wq8_linear_forward.argtypes = [P] * 8 + [S, P]
+    lib.wq8_linear_backward.argtypes = [P] * 9 + [S, P]
     lib.wq8_status_string.argtypes = [i]
     lib.wq8_status_string.restype = C.c_char_p
     lib.wq8_last_error.argtypes = []
     lib.wq8_last_error.restype = C.c_char_p
     for name in EXPORTS:
-        if name not in ("wq8_plan_destroy", "wq8_status_string", "wq8_last_error"):
+        if not name.endswith("_destroy") and name not in ("wq8_status_string", "wq8_last_error"):
             getattr(lib, name).restype = C.c_int
     _lib = lib
     return lib

@@ -1,0 +1,88 @@
+// Matrix product with bias, activation and residual: y = act(x w^T + bias) + residual.
+#include "wq8_gemm_device.h"
+
+namespace wq8 {
+
+void gemm_tile_size(int t, int *bm, int *bn) {
+    (void)t;
+    *bm = 128;
+    *bn = 128;
+}
+
+int gemm_kstep(wq8_dtype t) { return t == WQ8_F32 ? 32 : 64; }
+
+namespace {
+
+template <typename YT>
+struct EpiForward {
+    const float *bias;
+    const YT *residual;
+    YT *y, *z;
+    int64_t ys, rs;
+    int N, act, planar, pixels;
+
+    __device__ __forceinline__ void operator()(int m, int n, f32x4 v, int cnt) const {
+        if (bias) {
+            const Vec<float, 4> b = load_vec_n<float, 4>(bias + n, cnt);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += b.v[e];
+        }
+        Vec<YT, 4> r;
+        if (z) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r.v[e] = from_f32<YT>(v[e]);
+            store_vec_n<YT, 4>(z + (int64_t)m * N + n, r, cnt);
+        }
+        with_act(act, [&](auto a) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = act_fwd<decltype(a)::value>(v[e]);
+        });
+        if (residual) {
+            if (planar) {
+                const int img = m / pixels, p = m - img * pixels;
+                const YT *src = residual + ((int64_t)img * N + n) * pixels + p;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < cnt) v[e] += to_f32(src[(int64_t)e * pixels]);
+            } else {
+                const Vec<YT, 4> s = load_vec_n<YT, 4>(residual + (int64_t)m * rs + n, cnt);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += to_f32(s.v[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r.v[e] = from_f32<YT>(v[e]);
+        store_vec_n<YT, 4>(y + (int64_t)m * ys + n, r, cnt);
+    }
+};
+
+template <typename XT, typename YT>
+void forward(const LinearGeo &g, const LinearPtrs &p, hipStream_t st) {
+    GemmArgs a = {};
+    a.A = p.x;
+    a.B = p.w;
+    a.lda = g.xs;
+    a.ldb = g.K;
+    a.M = g.M;
+    a.N = g.N;
+    a.K = g.K;
+    const EpiForward<YT> epi = {p.bias, (const YT *)p.residual, (YT *)p.y, (YT *)p.z, g.ys, g.rs, g.N, g.act, g.r_planar,
+                                g.pixels};
+    run_gemm<XT, true, true>(g.f, a, epi, p.partial, st);
+}
+
+}  // namespace
+
+wq8_status launch_linear_forward(const LinearGeo &g, wq8_dtype xdt, wq8_dtype ydt, const LinearPtrs &p, void *stream) {
+    const hipStream_t st = (hipStream_t)stream;
+    if (xdt == WQ8_F32) {
+        if (ydt == WQ8_F32) forward<float, float>(g, p, st);
+        else forward<float, bf16_t>(g, p, st);
+    } else {
+        if (ydt == WQ8_F32) forward<bf16_t, float>(g, p, st);
+        else forward<bf16_t, bf16_t>(g, p, st);
+    }
+    return check_launch("matrix product");
+}
+
+}  // namespace wq8

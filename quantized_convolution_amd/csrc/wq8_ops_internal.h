@@ -1,0 +1,124 @@
+// Declarations shared by the host plans and the kernels of the group norm and
+// the matrix product.
+#pragma once
+
+#include "../../include/wino_q8_ops.h"
+#include "wq8_internal.h"
+
+namespace wq8 {
+
+// Compute units of an MI355X: launch shapes are chosen when a plan is made,
+// where no device need be present.
+constexpr int kCus = 256;
+
+// ------------------------------------------------------------- group norm
+constexpr int kNormMaxSlab = 1024;  // channels per block
+
+constexpr int kNormE = 4;            // steps unrolled by the short kernels
+
+// Elements per access: 16 bytes of the wider type, 8 at most.
+constexpr int norm_max_vec(size_t xs, size_t ys) { return xs == 2 && ys == 2 ? 8 : 4; }
+
+// Steps whose values a thread of a 1024-thread block can hold: 128 registers,
+// 64 of them for the values of x (forward) or of x and dy (backward).
+constexpr int norm_max_steps(int V, bool backward) {
+    return V == 1 ? kNormE : (V == 2 ? 32 : 16) / (backward ? 2 : 1);
+}
+
+// One pass of the group norm. A block handles a slab of `slabC` channels (K
+// whole groups, or 1/J of one) over `chunk` pixels of one image. With
+// channels-last x a thread holds V adjacent channels of one pixel per step,
+// `tc` threads across the slab and `tp` pixels per step; with NCHW x it holds V
+// adjacent pixels of one channel, `tp` threads across the pixels. A step covers
+// `window` pixels of the slab's channels.
+struct NormShape {
+    int threads, V, K, J, slabC, nslab;
+    int tc, tp, window;
+    int steps, E;             // steps per block, and the unrolled count that holds them
+    int chunk, nchunk;        // pixels per block, blocks along the pixels
+    int fused;                // 1: nchunk == J == 1, statistics and output in one kernel
+};
+
+struct NormGeo {
+    int N, C, P, G, cpg;
+    float eps;
+    int act;
+    int64_t xs, ys;           // elements between pixels (NHWC)
+    int x_nhwc, y_nhwc;
+    NormShape f, b;           // forward, backward
+};
+
+struct NormPtrs {
+    const void *x, *dy;
+    const float *shift, *gamma, *beta;
+    void *y, *dx;
+    float *mean, *rstd;                  // forward: outputs (never NULL here)
+    const float *mean_in, *rstd_in;      // backward
+    float *dgamma, *dbeta, *dshift;      // may be NULL
+    float *part;                         // partial sums of split passes
+    float *sums;                         // backward: [2][N][C] sums over the pixels
+    float *group;                        // split backward: [N][G][2] group means
+};
+
+wq8_status launch_norm_forward(const NormGeo &g, wq8_dtype xdt, wq8_dtype ydt, const NormPtrs &p,
+                               void *stream);
+wq8_status launch_norm_backward(const NormGeo &g, wq8_dtype xdt, wq8_dtype ydt, const NormPtrs &p,
+                                void *stream);
+
+// ---------------------------------------------------------- matrix product
+// C[m][n] = sum_k A(m, k) B(n, k). An operand is stored with k contiguous
+// (`KC`: element (m, k) at m * ld + k) or with its rows' index contiguous
+// (element (m, k) at k * ld + m).
+enum GemmForm { kFormForward = 0, kFormDx = 1, kFormDw = 2 };  // A, B: KC KC; KC MC; MC MC
+
+// Block tile and the split of k over blocks of one product.
+struct GemmShape {
+    int tile;      // index into the built tiles
+    int splits;    // blocks along k; > 1: fp32 partial products, joined by a second kernel
+    int ksteps;    // k steps per split
+};
+
+struct LinearGeo {
+    int M, K, N;              // rows, Cin, Cout
+    int act;
+    int64_t xs, ys, rs;       // elements between rows of x, of y and of an NHWC residual
+    int r_planar, pixels;
+    GemmShape f, dx, dw;
+    int dz_own;               // backward: dz is written to the workspace (else it is dy itself)
+    int dz_chunk, dz_nchunk;  // rows per block of the dz kernel, blocks along the rows
+};
+
+struct LinearPtrs {
+    const void *x, *w, *dy, *zin, *residual;
+    const float *bias;
+    void *y, *z, *dx, *dw;
+    float *dbias;
+    void *dz;                 // workspace: dz in x's type
+    float *colsum;            // workspace: [dz_nchunk][N] column sums
+    float *partial;           // workspace: split products
+};
+
+// Rows and columns of tile `t`, and k per step (128 bytes of the type).
+void gemm_tile_size(int t, int *bm, int *bn);
+int gemm_kstep(wq8_dtype t);
+
+wq8_status launch_linear_forward(const LinearGeo &g, wq8_dtype xdt, wq8_dtype ydt,
+                                 const LinearPtrs &p, void *stream);
+wq8_status launch_linear_backward(const LinearGeo &g, wq8_dtype xdt, wq8_dtype ydt,
+                                  const LinearPtrs &p, void *stream);
+
+}  // namespace wq8
+
+struct wq8_linear_plan {
+    wq8::LinearGeo geo;
+    wq8_dtype xdt, ydt;
+    size_t f_off_partial, f_bytes;
+    size_t b_off_dz, b_off_colsum, b_off_partial, b_bytes;
+};
+
+struct wq8_norm_plan {
+    wq8::NormGeo geo;
+    wq8_dtype xdt, ydt;
+    size_t f_off_part, f_off_stats, f_bytes;           // forward workspace
+    size_t b_off_sums, b_off_group, b_off_part, b_bytes;  // backward workspace
+};

@@ -1,0 +1,466 @@
+// Plans and entry points of the group norm and the matrix product: argument
+// checks, launch shapes and workspace layouts. Nothing is enqueued when a
+// check fails.
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <new>
+
+#include "wq8_ops_internal.h"
+
+using namespace wq8;
+
+namespace {
+
+size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+wq8_status need(const void *p, const char *name) {
+    if (!p) return fail(WQ8_ERR_INVALID_ARG, "%s is NULL", name);
+    if ((uintptr_t)p & 15u) return fail(WQ8_ERR_MISALIGNED, "%s is not 16-byte aligned", name);
+    return WQ8_OK;
+}
+
+wq8_status optional(const void *p, const char *name) { return p ? need(p, name) : WQ8_OK; }
+
+#define WQ8_TRY(expr)                  \
+    do {                               \
+        wq8_status _st = (expr);       \
+        if (_st != WQ8_OK) return _st; \
+    } while (0)
+#define WQ8_NEED(p) WQ8_TRY(need((const void *)(p), #p))
+#define WQ8_OPTIONAL(p) WQ8_TRY(optional((const void *)(p), #p))
+
+wq8_status need_workspace(const void *ws, size_t have, size_t want) {
+    if (want == 0) return WQ8_OK;
+    if (have < want)
+        return fail(WQ8_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", have, want);
+    return need(ws, "workspace");
+}
+
+bool is_dtype(int t) { return t == WQ8_F32 || t == WQ8_BF16; }
+int size_of(wq8_dtype t) { return t == WQ8_F32 ? 4 : 2; }
+bool is_act(int a) { return a >= WQ8_ACT_NONE && a <= WQ8_ACT_GELU_TANH; }
+bool is_layout(int l) { return l == WQ8_NHWC || l == WQ8_NCHW; }
+
+// --------------------------------------------------------- norm's launch shape
+// The fused shape for slabs of K groups, or steps > most if no block of up to
+// 1024 threads holds them.
+NormShape fused_shape(const NormGeo &g, int V, int K, bool backward) {
+    NormShape s;
+    memset(&s, 0, sizeof s);
+    s.V = V;
+    s.K = K;
+    s.J = 1;
+    s.slabC = K * g.cpg;
+    s.nslab = g.G / K;
+    s.chunk = g.P;
+    s.nchunk = 1;
+    s.fused = 1;
+    s.steps = 1 << 30;
+    if (s.slabC > kNormMaxSlab) return s;
+    const int most = norm_max_steps(V, backward);
+    // threads across the channels (NHWC) or the channels times the pixel
+    // vectors (NCHW); along the rest, as many as leave kNormE steps or fewer
+    const int across = g.x_nhwc ? s.slabC / V : s.slabC;
+    const int along = g.x_nhwc ? g.P : ceil_div(g.P, V);
+    if (across > 1024) return s;
+    int lanes = 1024 / across;
+    if (lanes > along) lanes = along;
+    const int steps = ceil_div(along, lanes);
+    s.E = steps <= kNormE ? kNormE : most;
+    if (steps <= kNormE) {  // the fewest threads with that many steps
+        lanes = ceil_div(along, kNormE);
+        if (across * lanes < 256) lanes = 256 / across < along ? (256 / across > lanes ? 256 / across : lanes) : along;
+    }
+    s.steps = ceil_div(along, lanes);
+    s.tc = across;
+    s.tp = lanes;
+    s.window = g.x_nhwc ? lanes : lanes * V;
+    s.threads = (int)round_up((size_t)across * lanes, 64);
+    return s;
+}
+
+// Split shape: blocks of 256 threads, kNormE steps along the pixels.
+NormShape split_shape(const NormGeo &g, int V) {
+    constexpr int T = 256;
+    NormShape s;
+    memset(&s, 0, sizeof s);
+    s.V = V;
+    s.J = 1;
+    s.K = 1;
+    s.threads = T;
+    s.E = kNormE;
+    if (g.x_nhwc) {
+        const int across = g.cpg / V;
+        if (across > T || g.cpg > kNormMaxSlab) {
+            const int most = T < kNormMaxSlab / V ? T : kNormMaxSlab / V;
+            s.J = ceil_div(across, most);
+            s.slabC = ceil_div(across, s.J) * V;
+            s.J = ceil_div(g.cpg, s.slabC);
+        } else {
+            // whole groups: the count that leaves the fewest threads idle, the
+            // longest rows among equals
+            int best = -1;
+            for (int k = 1; k <= g.G && k * across <= T && k * g.cpg <= kNormMaxSlab; ++k) {
+                if (g.G % k != 0) continue;
+                const int busy = k * across * (T / (k * across));
+                if (busy >= best) {
+                    best = busy;
+                    s.K = k;
+                }
+            }
+            s.slabC = s.K * g.cpg;
+        }
+        s.tc = s.slabC / V;
+        s.tp = T / s.tc;
+        if (s.tp > g.P) s.tp = g.P;
+        s.window = s.tp;
+    } else {
+        const int along = ceil_div(g.P, V);
+        if (g.cpg > T) {
+            s.J = ceil_div(g.cpg, T);
+            s.slabC = ceil_div(g.cpg, s.J);
+            s.J = ceil_div(g.cpg, s.slabC);
+        } else {
+            s.slabC = g.cpg;
+        }
+        s.tc = s.slabC;
+        s.tp = T / s.slabC < along ? T / s.slabC : along;
+        s.window = s.tp * V;
+    }
+    s.nslab = g.G / s.K * s.J;
+    const int steps = ceil_div(g.P, s.window);
+    s.steps = steps < kNormE ? steps : kNormE;
+    s.chunk = s.steps * s.window;
+    s.nchunk = ceil_div(g.P, s.chunk);
+    s.fused = 0;
+    return s;
+}
+
+NormShape choose_norm(const NormGeo &g, int xsz, int ysz, bool backward) {
+    int V = norm_max_vec(xsz, ysz);
+    if (g.x_nhwc)
+        while (g.cpg % V != 0) V /= 2;
+    const int most = norm_max_steps(V, backward);
+    NormShape s = fused_shape(g, V, 1, backward);
+    if (s.steps > most) return split_shape(g, V);
+    // wider slabs (longer contiguous rows) while the card stays full
+    for (int k = 2; k <= g.G; ++k) {
+        if (g.G % k != 0 || (int64_t)g.N * (g.G / k) < kCus) continue;
+        if (k * g.cpg * xsz > 256) break;
+        const NormShape t = fused_shape(g, V, k, backward);
+        if (t.steps <= most) s = t;
+    }
+    return s;
+}
+
+wq8_status build_norm(const wq8_norm_desc *d, wq8_norm_plan *p) {
+    if (d->N < 0 || d->C < 1 || d->H < 1 || d->W < 1)
+        return fail(WQ8_ERR_INVALID_ARG, "sizes must be positive (N=%d C=%d H=%d W=%d)", d->N, d->C, d->H, d->W);
+    if (d->groups < 1 || d->C % d->groups != 0)
+        return fail(WQ8_ERR_INVALID_ARG, "C = %d is not a multiple of groups = %d", d->C, d->groups);
+    if (!(d->eps >= 0.0f) || !isfinite(d->eps)) return fail(WQ8_ERR_INVALID_ARG, "eps must be finite and not negative");
+    if (!is_act(d->act)) return fail(WQ8_ERR_INVALID_ARG, "unknown activation %d", (int)d->act);
+    if (!is_dtype(d->x_dtype) || !is_dtype(d->y_dtype)) return fail(WQ8_ERR_INVALID_ARG, "unknown dtype");
+    if (!is_layout(d->x_layout) || !is_layout(d->y_layout)) return fail(WQ8_ERR_INVALID_ARG, "unknown layout");
+    const auto stride_ok = [&](int stride, wq8_layout l) { return stride == 0 || (l == WQ8_NHWC && stride >= d->C); };
+    if (!stride_ok(d->x_stride, d->x_layout) || !stride_ok(d->y_stride, d->y_layout))
+        return fail(WQ8_ERR_INVALID_ARG, "a pixel stride is for NHWC only and at least C = %d (x_stride=%d y_stride=%d)",
+                    d->C, d->x_stride, d->y_stride);
+    const int64_t lim = (int64_t)1 << 31, P = (int64_t)d->H * d->W;
+    // pixels of an image and values of its channels are counted in 32 bits;
+    // images and whole tensors are addressed in 64
+    if (P * d->C >= lim || (int64_t)d->N * d->groups >= lim || (int64_t)d->N * d->C >= lim)
+        return fail(WQ8_ERR_UNSUPPORTED, "an image of 2^31 values or more");
+    NormGeo &g = p->geo;
+    g.N = d->N;
+    g.C = d->C;
+    g.P = (int)P;
+    g.G = d->groups;
+    g.cpg = d->C / d->groups;
+    g.eps = d->eps;
+    g.act = d->act;
+    g.x_nhwc = d->x_layout == WQ8_NHWC;
+    g.y_nhwc = d->y_layout == WQ8_NHWC;
+    g.xs = d->x_stride ? d->x_stride : d->C;
+    g.ys = d->y_stride ? d->y_stride : d->C;
+    p->xdt = d->x_dtype;
+    p->ydt = d->y_dtype;
+    g.f = choose_norm(g, size_of(p->xdt), size_of(p->ydt), false);
+    g.b = choose_norm(g, size_of(p->xdt), size_of(p->ydt), true);
+    if ((int64_t)g.N * g.f.nslab * g.f.nchunk >= lim || (int64_t)g.N * g.b.nslab * g.b.nchunk >= lim)
+        return fail(WQ8_ERR_UNSUPPORTED, "more than 2^31 blocks");
+    const size_t N = g.N, G = g.G, C = g.C;
+    p->f_off_stats = 0;  // mean, rstd where the caller wants none
+    p->f_off_part = round_up(N * G * 8, 256);
+    p->f_bytes = p->f_off_part + (g.f.fused ? 0 : N * G * g.f.nchunk * g.f.J * 8);
+    p->b_off_sums = 0;
+    p->b_off_group = round_up(2 * N * C * 4, 256);
+    p->b_off_part = p->b_off_group + round_up(N * G * 8, 256);
+    p->b_bytes = p->b_off_part + (g.b.fused ? 0 : N * g.b.nchunk * 3 * C * 4);
+    return WQ8_OK;
+}
+
+// ------------------------------------------------------ product's launch shape
+GemmShape choose_gemm(int64_t M, int64_t N, int64_t K, wq8_dtype t) {
+    GemmShape s;
+    s.tile = 0;
+    int bm, bn;
+    gemm_tile_size(s.tile, &bm, &bn);
+    const int64_t tiles = ceil_div64(M, bm) * ceil_div64(N, bn), steps = ceil_div64(K, gemm_kstep(t));
+    // split k while tiles leave compute units idle and a split keeps 8 steps
+    int64_t splits = tiles > 0 ? kCus / tiles : 1;
+    if (splits > steps / 8) splits = steps / 8;
+    if (splits < 1) splits = 1;
+    s.ksteps = (int)ceil_div64(steps, splits);
+    s.splits = s.ksteps > 0 ? (int)ceil_div64(steps, s.ksteps) : 1;
+    return s;
+}
+
+wq8_status build_linear(const wq8_linear_desc *d, wq8_linear_plan *p) {
+    if (d->rows < 0 || d->Cin < 1 || d->Cout < 1)
+        return fail(WQ8_ERR_INVALID_ARG, "sizes must be positive (rows=%lld Cin=%d Cout=%d)", (long long)d->rows, d->Cin,
+                    d->Cout);
+    if (!is_act(d->act)) return fail(WQ8_ERR_INVALID_ARG, "unknown activation %d", (int)d->act);
+    if (!is_dtype(d->x_dtype) || !is_dtype(d->y_dtype)) return fail(WQ8_ERR_INVALID_ARG, "unknown dtype");
+    if (!is_layout(d->r_layout)) return fail(WQ8_ERR_INVALID_ARG, "unknown layout");
+    if (d->r_layout == WQ8_NCHW && (d->pixels < 1 || d->rows % d->pixels != 0))
+        return fail(WQ8_ERR_INVALID_ARG, "rows = %lld is not a multiple of pixels = %d", (long long)d->rows, d->pixels);
+    if ((d->x_stride && d->x_stride < d->Cin) || (d->y_stride && d->y_stride < d->Cout) ||
+        (d->r_stride && (d->r_layout == WQ8_NCHW || d->r_stride < d->Cout)))
+        return fail(WQ8_ERR_INVALID_ARG, "a row stride is shorter than a row, or given for an NCHW residual");
+    const int64_t big = (int64_t)1 << 22;
+    // rows and tiles are counted in 32 bits, and a tile's rows (256 of 4 bytes
+    // a column) are addressed in 32; tensors in 64
+    if (d->rows >= ((int64_t)1 << 31) - 1024 || d->Cin >= big || d->Cout >= big || d->x_stride >= big || d->y_stride >= big ||
+        d->r_stride >= big)
+        return fail(WQ8_ERR_UNSUPPORTED, "2^31 rows, or 2^22 columns, or more");
+    LinearGeo &g = p->geo;
+    g.M = (int)d->rows;
+    g.K = d->Cin;
+    g.N = d->Cout;
+    g.act = d->act;
+    g.xs = d->x_stride ? d->x_stride : d->Cin;
+    g.ys = d->y_stride ? d->y_stride : d->Cout;
+    g.rs = d->r_stride ? d->r_stride : d->Cout;
+    g.r_planar = d->r_layout == WQ8_NCHW;
+    g.pixels = d->pixels;
+    p->xdt = d->x_dtype;
+    p->ydt = d->y_dtype;
+    g.f = choose_gemm(g.M, g.N, g.K, p->xdt);
+    g.dx = choose_gemm(g.M, g.K, g.N, p->xdt);
+    g.dw = choose_gemm(g.N, g.K, g.M, p->xdt);
+    // dy serves as dz where the activation leaves it as it is and the products
+    // can read its type
+    g.dz_own = g.act != WQ8_ACT_NONE || p->xdt != p->ydt;
+    g.dz_chunk = 64;
+    g.dz_nchunk = ceil_div(g.M, g.dz_chunk);
+    const auto tiles = [](const GemmShape &s, int64_t M, int64_t N) {
+        int bm, bn;
+        gemm_tile_size(s.tile, &bm, &bn);
+        return ceil_div64(M, bm) * ceil_div64(N, bn) * s.splits;
+    };
+    const int64_t lim = (int64_t)1 << 31;
+    if (ceil_div64(g.N, 256) * g.dz_nchunk >= lim || tiles(g.f, g.M, g.N) >= lim || tiles(g.dx, g.M, g.K) >= lim || tiles(g.dw, g.N, g.K) >= lim)
+        return fail(WQ8_ERR_UNSUPPORTED, "more than 2^31 blocks");
+    const size_t M = g.M, N = g.N, K = g.K;
+    const auto partial = [](const GemmShape &s, size_t m, size_t n) { return s.splits > 1 ? s.splits * m * n * 4 : 0; };
+    p->f_off_partial = 0;
+    p->f_bytes = partial(g.f, M, N);
+    p->b_off_dz = 0;
+    p->b_off_colsum = g.dz_own ? round_up(M * N * size_of(p->xdt), 256) : 0;
+    p->b_off_partial = p->b_off_colsum + round_up((size_t)g.dz_nchunk * N * 4, 256);
+    const size_t pdx = partial(g.dx, M, K), pdw = partial(g.dw, N, K);
+    p->b_bytes = p->b_off_partial + (pdx > pdw ? pdx : pdw);
+    return WQ8_OK;
+}
+
+// Makes a plan of type P by f(desc, plan).
+template <typename P, typename D>
+wq8_status create(const D *desc, P **out, wq8_status (*f)(const D *, P *)) {
+    clear_error();
+    if (!out) return fail(WQ8_ERR_INVALID_ARG, "null output pointer");
+    *out = nullptr;
+    if (!desc) return fail(WQ8_ERR_INVALID_ARG, "null descriptor");
+    P *p = new (std::nothrow) P;
+    if (!p) return fail(WQ8_ERR_NO_MEMORY, "out of host memory");
+    memset((void *)p, 0, sizeof *p);
+    const wq8_status st = f(desc, p);
+    if (st != WQ8_OK) {
+        delete p;
+        return st;
+    }
+    *out = p;
+    return WQ8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+wq8_status wq8_norm_plan_create(const wq8_norm_desc *desc, wq8_norm_plan **out) {
+    return create(desc, out, build_norm);
+}
+
+void wq8_norm_plan_destroy(wq8_norm_plan *plan) { delete plan; }
+
+wq8_status wq8_norm_plan_query(const wq8_norm_plan *p, size_t *forward_bytes, size_t *backward_bytes) {
+    clear_error();
+    if (!p) return fail(WQ8_ERR_INVALID_ARG, "null plan");
+    if (forward_bytes) *forward_bytes = p->f_bytes;
+    if (backward_bytes) *backward_bytes = p->b_bytes;
+    return WQ8_OK;
+}
+
+wq8_status wq8_norm_forward(const wq8_norm_plan *p, const void *x, const float *shift, const float *gamma,
+                            const float *beta, void *y, float *mean, float *rstd, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    clear_error();
+    if (!p) return fail(WQ8_ERR_INVALID_ARG, "null plan");
+    if (p->geo.N == 0) return WQ8_OK;
+    WQ8_NEED(x);
+    WQ8_OPTIONAL(shift);
+    WQ8_OPTIONAL(gamma);
+    WQ8_OPTIONAL(beta);
+    WQ8_NEED(y);
+    WQ8_OPTIONAL(mean);
+    WQ8_OPTIONAL(rstd);
+    if (x == y) return fail(WQ8_ERR_INVALID_ARG, "x and y must not overlap");
+    WQ8_TRY(need_workspace(workspace, workspace_bytes, p->f_bytes));
+    NormPtrs a;
+    memset(&a, 0, sizeof a);
+    float *stats = (float *)((char *)workspace + p->f_off_stats);
+    a.x = x;
+    a.shift = shift;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.y = y;
+    a.mean = mean ? mean : stats;
+    a.rstd = rstd ? rstd : stats + (size_t)p->geo.N * p->geo.G;
+    a.part = (float *)((char *)workspace + p->f_off_part);
+    return launch_norm_forward(p->geo, p->xdt, p->ydt, a, stream);
+}
+
+wq8_status wq8_norm_backward(const wq8_norm_plan *p, const void *dy, const void *x, const float *shift,
+                             const float *gamma, const float *beta, const float *mean, const float *rstd, void *dx,
+                             float *dgamma, float *dbeta, float *dshift, void *workspace, size_t workspace_bytes,
+                             void *stream) {
+    clear_error();
+    if (!p) return fail(WQ8_ERR_INVALID_ARG, "null plan");
+    if (p->geo.N > 0) {
+        WQ8_NEED(dy);
+        WQ8_NEED(x);
+        WQ8_OPTIONAL(shift);
+        WQ8_OPTIONAL(gamma);
+        WQ8_OPTIONAL(beta);
+        WQ8_NEED(mean);
+        WQ8_NEED(rstd);
+        WQ8_NEED(dx);
+        WQ8_OPTIONAL(dshift);
+        if (dx == x || dx == dy) return fail(WQ8_ERR_INVALID_ARG, "dx must not overlap x or dy");
+    }
+    WQ8_OPTIONAL(dgamma);
+    WQ8_OPTIONAL(dbeta);
+    WQ8_TRY(need_workspace(workspace, workspace_bytes, p->b_bytes));
+    char *ws = (char *)workspace;
+    NormPtrs a;
+    memset(&a, 0, sizeof a);
+    a.dy = dy;
+    a.x = x;
+    a.shift = shift;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.mean_in = mean;
+    a.rstd_in = rstd;
+    a.dx = dx;
+    a.dgamma = dgamma;
+    a.dbeta = dbeta;
+    a.dshift = dshift;
+    a.sums = (float *)(ws + p->b_off_sums);
+    a.group = (float *)(ws + p->b_off_group);
+    a.part = (float *)(ws + p->b_off_part);
+    return launch_norm_backward(p->geo, p->xdt, p->ydt, a, stream);
+}
+
+wq8_status wq8_linear_plan_create(const wq8_linear_desc *desc, wq8_linear_plan **out) {
+    return create(desc, out, build_linear);
+}
+
+void wq8_linear_plan_destroy(wq8_linear_plan *plan) { delete plan; }
+
+wq8_status wq8_linear_plan_query(const wq8_linear_plan *p, size_t *forward_bytes, size_t *backward_bytes) {
+    clear_error();
+    if (!p) return fail(WQ8_ERR_INVALID_ARG, "null plan");
+    if (forward_bytes) *forward_bytes = p->f_bytes;
+    if (backward_bytes) *backward_bytes = p->b_bytes;
+    return WQ8_OK;
+}
+
+wq8_status wq8_linear_forward(const wq8_linear_plan *p, const void *x, const void *w, const float *bias,
+                              const void *residual, void *y, void *z, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+    clear_error();
+    if (!p) return fail(WQ8_ERR_INVALID_ARG, "null plan");
+    if (p->geo.M == 0) return WQ8_OK;
+    WQ8_NEED(x);
+    WQ8_NEED(w);
+    WQ8_OPTIONAL(bias);
+    WQ8_OPTIONAL(residual);
+    WQ8_NEED(y);
+    WQ8_OPTIONAL(z);
+    if (y == x || y == w || z == y || (z && (z == x || z == w || z == residual)) || (p->geo.r_planar && y == residual))
+        return fail(WQ8_ERR_INVALID_ARG, "y and z must not overlap each other or an input");
+    if (y == residual && p->geo.rs != p->geo.ys)
+        return fail(WQ8_ERR_INVALID_ARG, "a residual that is y itself needs y's row stride");
+    WQ8_TRY(need_workspace(workspace, workspace_bytes, p->f_bytes));
+    LinearPtrs a;
+    memset(&a, 0, sizeof a);
+    a.x = x;
+    a.w = w;
+    a.bias = bias;
+    a.residual = residual;
+    a.y = y;
+    a.z = z;
+    a.partial = (float *)((char *)workspace + p->f_off_partial);
+    return launch_linear_forward(p->geo, p->xdt, p->ydt, a, stream);
+}
+
+wq8_status wq8_linear_backward(const wq8_linear_plan *p, const void *dy, const void *x, const void *w, const void *z,
+                               void *dx, void *dw, float *dbias, void *workspace, size_t workspace_bytes,
+                               void *stream) {
+    clear_error();
+    if (!p) return fail(WQ8_ERR_INVALID_ARG, "null plan");
+    if (p->geo.M > 0) {
+        WQ8_NEED(dy);
+        if (dw) WQ8_NEED(x);
+        if (dx) WQ8_NEED(w);
+        if (p->geo.act != WQ8_ACT_NONE) WQ8_NEED(z);
+        WQ8_OPTIONAL(dx);
+        if (dx && (dx == dy || dx == x || dx == w || dx == z || dx == dw))
+            return fail(WQ8_ERR_INVALID_ARG, "dx must not overlap an input or dw");
+        if (dw && (dw == dy || dw == x || dw == w || dw == z))
+            return fail(WQ8_ERR_INVALID_ARG, "dw must not overlap an input");
+    }
+    WQ8_OPTIONAL(dw);
+    WQ8_OPTIONAL(dbias);
+    WQ8_TRY(need_workspace(workspace, workspace_bytes, p->b_bytes));
+    char *ws = (char *)workspace;
+    LinearPtrs a;
+    memset(&a, 0, sizeof a);
+    a.dy = dy;
+    a.x = x;
+    a.w = w;
+    a.zin = z;
+    a.dx = dx;
+    a.dw = dw;
+    a.dbias = dbias;
+    a.dz = p->geo.dz_own ? (void *)(ws + p->b_off_dz) : nullptr;
+    a.colsum = (float *)(ws + p->b_off_colsum);
+    a.partial = (float *)(ws + p->b_off_partial);
+    return launch_linear_backward(p->geo, p->xdt, p->ydt, a, stream);
+}
+
+}  // extern "C"

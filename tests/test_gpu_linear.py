@@ -1,0 +1,238 @@
+"""Matrix product with bias, activation and residual on the GPU against its
+definition in 64 bits: types, odd sizes, slices, residual layouts, gradients."""
+import pytest
+import torch
+
+import ops_reference as R
+import quantized_convolution_amd as q
+
+pytestmark = pytest.mark.gpu
+F32, BF = torch.float32, torch.bfloat16
+
+
+def strided(t, extra):
+    """`t` on the GPU in rows of a wider tensor whose other columns are NaN."""
+    if not extra:
+        return t.cuda()
+    wide = torch.full((t.shape[0], t.shape[1] + extra), float("nan"), dtype=t.dtype, device="cuda")
+    wide[:, :t.shape[1]] = t.cuda()
+    return wide[:, :t.shape[1]]
+
+
+def make(rows, Cin, Cout, xt, yt, seed):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    return dict(x=r(rows, Cin).to(xt), w=(r(Cout, Cin) / Cin ** 0.5).to(xt), bias=0.5 * r(Cout), res=r(rows, Cout).to(yt),
+                dy=r(rows, Cout).to(yt))
+
+
+def forward(rows, Cin, Cout, act="none", xt=F32, yt=F32, bias=True, residual="none", pixels=0, want_z=False, sx=0, sy=0, sr=0,
+            seed=0):
+    print(f"[linear] {rows}x{Cin}x{Cout} {act} {xt}->{yt} residual={residual} strides +{sx} +{sy} +{sr}", flush=True)
+    d = make(rows, Cin, Cout, xt, yt, seed)
+    planar = residual == "planar"
+    plan = q.LinearPlan(rows, Cin, Cout, act=act, x_dtype=xt, y_dtype=yt, r_layout="nchw" if planar else "nhwc", pixels=pixels,
+                        x_stride=Cin + sx if sx else 0, y_stride=Cout + sy if sy else 0, r_stride=Cout + sr if sr else 0)
+    res = None
+    if residual == "rows":
+        res = strided(d["res"], sr)
+    elif planar:
+        res = d["res"].reshape(rows // pixels, pixels, Cout).permute(0, 2, 1).contiguous().cuda()
+    y = strided(torch.zeros(rows, Cout, dtype=yt), sy)
+    z = torch.empty(rows, Cout, dtype=yt, device="cuda") if want_z else None
+    q.wq8_linear_forward(plan, strided(d["x"], sx), d["w"].cuda(), d["bias"].cuda() if bias else None, res, y=y, z=z)
+    torch.cuda.synchronize()
+    ry, rz = R.linear_forward(d["x"], d["w"], d["bias"] if bias else None, d["res"] if residual != "none" else None, act, yt)
+    R.check(y, *ry, "y")
+    if want_z:
+        R.check(z, *rz, "z")
+    if sy:  # what lies beside the slice is untouched
+        assert torch.isnan(y.as_strided((rows, sy), (Cout + sy, 1), Cout)).all()
+
+
+def backward(rows, Cin, Cout, act="none", xt=F32, yt=F32, sx=0, sy=0, seed=0):
+    print(f"[linear backward] {rows}x{Cin}x{Cout} {act} {xt}->{yt} strides +{sx} +{sy}", flush=True)
+    d = make(rows, Cin, Cout, xt, yt, seed)
+    z = (d["x"].double() @ d["w"].double().T + d["bias"].double()).to(yt)
+    plan = q.LinearPlan(rows, Cin, Cout, act=act, x_dtype=xt, y_dtype=yt, x_stride=Cin + sx if sx else 0,
+                        y_stride=Cout + sy if sy else 0)
+    dx = strided(torch.zeros(rows, Cin, dtype=xt), sx)
+    _, dw, db = q.wq8_linear_backward(plan, strided(d["dy"], sy), strided(d["x"], sx), d["w"].cuda(), z=z.cuda(), dx=dx,
+                                      want_dbias=True)
+    torch.cuda.synchronize()
+    want = R.linear_backward(d["dy"], d["x"], d["w"], z, act, xt, xt == BF and (act != "none" or yt != BF))
+    R.check(dx, *want["dx"], "dx")
+    R.check(dw, *want["dw"], "dw")
+    R.check(db, *want["dbias"], "dbias")
+
+
+TYPES = [(F32, F32), (BF, BF), (BF, F32), (F32, BF)]
+# one row, one column, one k, odd ones, tile edges on either side, several tiles
+SIZES = [(1, 1, 1), (1, 64, 64), (3, 5, 7), (8, 320, 200), (16, 33, 130), (17, 129, 31), (65, 64, 127), (128, 72, 128), (129, 200, 257),
+         (300, 515, 129), (64, 1000, 48)]
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("size", SIZES)
+def test_forward_sizes(xt, yt, size):
+    forward(*size, "none", xt, yt)
+    forward(*size, "silu", xt, yt, residual="rows", want_z=True, seed=1)
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("size", SIZES)
+def test_backward_sizes(xt, yt, size):
+    backward(*size, "none", xt, yt)
+    backward(*size, "silu", xt, yt, seed=1)
+
+
+@pytest.mark.parametrize("act", R.ACTS)
+@pytest.mark.parametrize("xt", [F32, BF])
+def test_activations(act, xt):
+    forward(70, 96, 90, act, xt, xt, want_z=True, seed=2)
+    forward(70, 96, 90, act, xt, xt, bias=False, residual="rows", seed=3)
+    backward(70, 96, 90, act, xt, xt, seed=2)
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("images,pixels,Cout", [(1, 1, 5), (3, 49, 64), (2, 256, 72), (5, 7, 33), (200, 1, 130)])
+def test_planar_residual(xt, yt, images, pixels, Cout):
+    forward(images * pixels, 40, Cout, "gelu", xt, yt, residual="planar", pixels=pixels, seed=4)
+
+
+@pytest.mark.parametrize("xt", [F32, BF])
+@pytest.mark.parametrize("extra", [1, 4, 8, 56])
+def test_slices(xt, extra):
+    for size in ((37, 72, 50), (130, 128, 136), (4, 128, 96)):
+        forward(*size, "silu", xt, xt, residual="rows", sx=extra, sy=extra, sr=extra, seed=5)
+        backward(*size, "silu", xt, xt, sx=extra, sy=extra, seed=5)
+        backward(*size, "none", xt, xt, sx=extra, sy=extra, seed=6)
+
+
+# few tiles and a long sum: k is split over blocks and joined
+@pytest.mark.parametrize("xt", [F32, BF])
+@pytest.mark.parametrize("size", [(20, 4100, 24), (100, 2050, 130), (4100, 40, 50), (2500, 130, 100), (33, 64, 5000)])
+def test_long_sums(xt, size):
+    forward(*size, "gelu", xt, xt, residual="rows", want_z=True, seed=7)
+    backward(*size, "gelu_tanh", xt, xt, seed=7)
+
+
+def test_residual_in_place():
+    d = make(70, 64, 40, F32, F32, 3)
+    plan = q.LinearPlan(70, 64, 40)
+    y = d["res"].cuda()
+    q.wq8_linear_forward(plan, d["x"].cuda(), d["w"].cuda(), d["bias"].cuda(), y, y=y)
+    torch.cuda.synchronize()
+    R.check(y, *R.linear_forward(d["x"], d["w"], d["bias"], d["res"], "none", F32)[0], "y")
+
+
+@pytest.mark.parametrize("xt", [F32, BF])
+def test_only_what_is_wanted(xt):
+    d = make(70, 64, 40, xt, xt, 3)
+    plan = q.LinearPlan(70, 64, 40, x_dtype=xt)
+    a = (plan, d["dy"].cuda(), d["x"].cuda(), d["w"].cuda())
+    full = q.wq8_linear_backward(*a, want_dbias=True)
+    for k in range(3):
+        wants = dict(want_dx=k == 0, want_dw=k == 1, want_dbias=k == 2)
+        got = q.wq8_linear_backward(*a, **wants)
+        torch.cuda.synchronize()
+        assert [g is not None for g in got] == [k == i for i in range(3)]
+        assert torch.equal(got[k], full[k])
+
+
+def test_no_rows():
+    plan = q.LinearPlan(0, 16, 8, act="silu")
+    x, dy, w = torch.empty(0, 16, device="cuda"), torch.empty(0, 8, device="cuda"), torch.ones(8, 16, device="cuda")
+    assert q.wq8_linear_forward(plan, x, w).shape == (0, 8)
+    dx, dw, db = q.wq8_linear_backward(plan, dy, x, w, z=dy, dw=torch.ones_like(w), dbias=torch.ones(8, device="cuda"))
+    torch.cuda.synchronize()
+    assert dx.shape == (0, 16) and (dw == 0).all() and (db == 0).all()
+
+
+@pytest.mark.parametrize("xt", [F32, BF])
+@pytest.mark.parametrize("rows", [4, 150])
+def test_not_finite_stays_in_its_row(xt, rows):
+    """What is added to fill a tile must not meet an infinity: 0 * inf is NaN."""
+    for Cin in (72, 77):
+        d = make(rows, Cin, 90, xt, xt, 5)
+        d["x"][2, 5], d["x"][3, Cin - 1] = float("inf"), float("nan")
+        plan = q.LinearPlan(rows, Cin, 90, act="none", x_dtype=xt)
+        y = q.wq8_linear_forward(plan, d["x"].cuda(), d["w"].cuda(), d["bias"].cuda())
+        torch.cuda.synchronize()
+        y = y.cpu().float()
+        fine = torch.ones(rows, dtype=torch.bool)
+        fine[2:4] = False
+        assert torch.isfinite(y[fine]).all()
+        assert (y[2] == torch.sign(d["w"][:, 5].float()) * float("inf")).all() and torch.isnan(y[3]).all()
+
+
+def test_relu_keeps_nan():
+    d = make(4, 8, 4, F32, F32, 1)
+    d["x"][1, 1] = float("nan")
+    y = q.wq8_linear_forward(q.LinearPlan(4, 8, 4, act="relu"), d["x"].cuda(), d["w"].cuda())
+    torch.cuda.synchronize()
+    assert torch.isnan(y[1]).all() and (y[[0, 2, 3]] >= 0).all()
+
+
+def test_gradient_against_differences():
+    """Central differences of the forward along random directions (see the
+    group norm's): z along a direction moves by sums of Cin terms of order
+    h / sqrt(Cin), and the loss sums n values."""
+    rows, Cin, Cout, h = 40, 24, 36, 2.0 ** -6
+    n = rows * Cout
+    d = {k: v.cuda() for k, v in make(rows, Cin, Cout, F32, F32, 9).items()}
+    plan = q.LinearPlan(rows, Cin, Cout, act="gelu")
+    names = ("x", "w", "bias")
+
+    def loss(a):
+        y = q.wq8_linear_forward(plan, a["x"], a["w"], a["bias"], a["res"])
+        return (y.double() * d["dy"].double()).sum().item()
+
+    _, z = q.wq8_linear_forward(plan, d["x"], d["w"], d["bias"], d["res"], want_z=True)
+    grads = dict(zip(names, q.wq8_linear_backward(plan, d["dy"], d["x"], d["w"], z=z, want_dbias=True)))
+    g = torch.Generator().manual_seed(1)
+    for k in names:
+        v = torch.randn(d[k].shape, generator=g).cuda()
+        if k == "w":
+            v /= Cin ** 0.5
+        up, down = dict(d, **{k: d[k] + h * v}), dict(d, **{k: d[k] - h * v})
+        diff = (loss(up) - loss(down)) / (2 * h)
+        want = (grads[k].double() * v.double()).sum().item()
+        tol = 10 * R.U * n ** 0.5 * 3 / h + 4 ** 3 * n * h * h / 6
+        assert abs(diff - want) <= tol, (k, diff, want, tol)
+
+
+@pytest.mark.parametrize("xt", [F32, BF])
+def test_repeats_and_does_not_depend_on_the_workspace(xt):
+    rows, Cin, Cout = 300, 2100, 70
+    d = {k: v.cuda() for k, v in make(rows, Cin, Cout, xt, xt, 9).items()}
+    plan = q.LinearPlan(rows, Cin, Cout, act="silu", x_dtype=xt)
+    got = []
+    for fill in (0, 255, 127):
+        ws = torch.full((plan.workspace_bytes,), fill, dtype=torch.uint8, device="cuda")
+        wb = torch.full((plan.backward_workspace_bytes,), fill, dtype=torch.uint8, device="cuda")
+        y, z = q.wq8_linear_forward(plan, d["x"], d["w"], d["bias"], d["res"], want_z=True, workspace=ws)
+        g = q.wq8_linear_backward(plan, d["dy"], d["x"], d["w"], z=z, want_dbias=True, workspace=wb)
+        got.append([t.clone() for t in (y, z, *g)])
+    torch.cuda.synchronize()
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+def test_offsets_past_32_bits():
+    """x of more than 2^32 bytes and 2^31 elements, y too: the last rows are right, in both directions."""
+    rows, Cin, Cout = 2 ** 20 + 65, 2056, 2064
+    x = torch.zeros((rows, Cin), dtype=BF, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x[-3:] = torch.randn((3, Cin), generator=g, device="cuda", dtype=BF)
+    w = (torch.randn((Cout, Cin), generator=g, device="cuda") / Cin ** 0.5).to(BF)
+    plan = q.LinearPlan(rows, Cin, Cout, x_dtype=BF)
+    y = q.wq8_linear_forward(plan, x, w)
+    R.check(y[-3:], *R.linear_forward(x[-3:].cpu(), w.cpu(), None, None, "none", BF)[0], "y")
+    assert (y[:-3] == 0).all()
+    dy = y  # as good as any
+    dx, dw, _ = q.wq8_linear_backward(plan, dy, x, w)
+    want = R.linear_backward(dy[-3:].cpu(), x[-3:].cpu(), w.cpu(), None, "none", BF, False)
+    R.check(dx[-3:], *want["dx"], "dx")
+    R.check(dw, *want["dw"], "dw")
+    assert (dx[:-3] == 0).all()
