@@ -39,48 +39,104 @@ struct GemmArgs {
     float *partial;    // [splits][M][N] where k is split, else NULL
 };
 
-// LDS position (in elements) of element (r, k) of an operand tile of R rows
-// whose 16-byte unit starts at (r, k).
-template <typename T, bool KC, int R>
-__device__ __forceinline__ int lds_unit(int row, int unit) {
-    constexpr int U = 16 / sizeof(T);
-    if constexpr (KC) {  // row: m, unit: along k
-        return row * (8 * U) + ((unit ^ (row & 7)) * U);
-    } else {             // row: k, unit: along m
-        constexpr int UR = R / U;  // units per row
-        const int sw = sizeof(T) == 2 ? (((row & 3) | ((row >> 1) & 4)) << 1) & (UR - 1) : (((row >> 2) & 3) << 2) & (UR - 1);
-        return row * R + ((unit ^ sw) * U);
+// Where a tile keeps its 16-byte units. `unit` runs along the contiguous
+// dimension of row `row` (k contiguous: row = m or n; otherwise row = k).
+// FIRST: the operand whose rows become the sums' columns (B, see kRowOf).
+template <typename T, bool KC, bool FIRST, int R>
+__device__ __forceinline__ int swizzle(int row, int unit) {
+    constexpr int UR = KC ? 8 : R / (16 / (int)sizeof(T));  // units per row
+    if constexpr (KC) {
+        // 16 lanes read one unit of 16 rows (128 bytes apart): spread them over
+        // the 16 units of 256 bytes, two rows' worth. B's rows are 8a + b.
+        const int s = FIRST ? ((row >> 1) & 1) | ((row >> 2) & 6) : (row >> 1) & 7;
+        return unit ^ s;
+    } else if constexpr (sizeof(T) == 2) {
+        return unit ^ ((((row & 3) | ((row >> 1) & 4)) << 1) & (UR - 1));
+    } else {
+        return unit ^ ((((row >> 2) & 3) << 2) & (UR - 1));
     }
 }
 
-// Stages one k step of an operand: R rows from r0, k from k0, what lies
-// outside rows x kend as zeros.
-template <typename T, bool KC, int R, int THREADS>
-__device__ __forceinline__ void stage(T *lds, const T *src, int64_t ld, int r0, int rows, int k0, int kend) {
-    constexpr int U = 16 / sizeof(T), UNITS = R * 8;
-#pragma unroll
-    for (int i = 0; i < UNITS / THREADS; ++i) {
-        const int q = i * THREADS + threadIdx.x;
-        int row, unit, n;
-        const T *p;
-        if constexpr (KC) {
-            row = q / 8;
-            unit = q % 8;
-            const int k = k0 + unit * U;
-            n = r0 + row < rows ? min(kend - k, U) : 0;
-            p = src + (int64_t)(r0 + row) * ld + k;
-        } else {
-            constexpr int UR = R / U;
-            row = q / UR;
-            unit = q % UR;
-            const int m = r0 + unit * U;
-            n = k0 + row < kend ? min(rows - m, U) : 0;
-            p = src + (int64_t)(k0 + row) * ld + m;
-        }
-        const Vec<T, U> v = load_vec_n<T, U>(p, n);
-        *(Vec<T, U> *)(lds + lds_unit<T, KC, R>(row, unit)) = v;
-    }
+template <typename T, bool KC, bool FIRST, int R>
+__device__ __forceinline__ int lds_unit(int row, int unit) {
+    constexpr int U = 16 / sizeof(T);
+    return row * (KC ? 8 * U : R) + swizzle<T, KC, FIRST, R>(row, unit) * U;
 }
+
+// Stages k steps of an operand of R tile rows. Units that lie in LDS one after
+// another are one thread each, so a wave's 64 units can be one load from
+// memory to LDS; the swizzle is in the address that a thread reads.
+template <typename T, bool KC, bool FIRST, int R, int THREADS>
+struct Stager {
+    static constexpr int U = 16 / sizeof(T), UR = KC ? 8 : R / U, COUNT = R * 8 / THREADS, BK = 128 / sizeof(T);
+    static_assert(R * 8 % THREADS == 0, "whole waves");
+
+    const T *src;
+    int64_t ld;
+    int r0, rows, K;
+    uint32_t off[COUNT];
+
+    __device__ __forceinline__ static void place(int i, int &row, int &unit) {
+        const int q = i * THREADS + threadIdx.x;
+        row = q / UR;
+        unit = swizzle<T, KC, FIRST, R>(row, q % UR);
+    }
+
+    // Byte offsets of the direct loads from the tile's first element of a step.
+    // Rows past the end repeat the last one: their sums are not stored. Needs
+    // 16-byte aligned rows, and whole units along the rows' index.
+    __device__ __forceinline__ void prepare() {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            int row, unit;
+            place(i, row, unit);
+            if constexpr (KC) off[i] = (uint32_t)(min(row, rows - 1 - r0) * (uint32_t)ld + unit * U) * (uint32_t)sizeof(T);
+            else off[i] = (uint32_t)(row * (uint32_t)ld + min(unit * U, rows - U - r0)) * (uint32_t)sizeof(T);
+        }
+    }
+
+    // One whole step from memory to LDS, past the registers.
+    __device__ __forceinline__ void direct(T *lds, int step) const {
+        const T *base = KC ? src + (int64_t)r0 * ld + (int64_t)step * BK : src + (int64_t)step * BK * ld + r0;
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, -1, kBufferFlags);
+        const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) T *)lds + (threadIdx.x >> 6) * 1024;
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            const uint32_t m0 = __builtin_amdgcn_readfirstlane(at + i * THREADS * 16);
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                         :
+                         : "s"(m0), "v"(off[i]), "s"(r)
+                         : "memory", "m0");
+        }
+    }
+
+    // One step through registers, at any alignment, zeros outside the operand.
+    __device__ __forceinline__ void load(Vec<T, U> (&v)[COUNT], int step) const {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            int row, unit, n;
+            const T *p;
+            place(i, row, unit);
+            if constexpr (KC) {
+                const int k = step * BK + unit * U;
+                n = r0 + row < rows ? min(K - k, U) : 0;
+                p = src + (int64_t)(r0 + row) * ld + k;
+            } else {
+                const int k = step * BK + row, m = r0 + unit * U;
+                n = k < K ? min(rows - m, U) : 0;
+                p = src + (int64_t)k * ld + m;
+            }
+            v[i] = load_vec_n<T, U>(p, n);
+        }
+    }
+    __device__ __forceinline__ void store(T *lds, const Vec<T, U> (&v)[COUNT]) const {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) *(Vec<T, U> *)(lds + (i * THREADS + threadIdx.x) * U) = v[i];
+    }
+};
+
+// Waits until this wave's direct loads have landed in LDS.
+__device__ __forceinline__ void wait_direct() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 template <typename T>
 struct Frag;
@@ -93,114 +149,176 @@ struct Frag<float> {
     f32x4 v;
 };
 
-// The fragment of rows r0..r0+15 and the kk-th 64 bytes of k.
-template <typename T, bool KC, int R>
-__device__ __forceinline__ Frag<T> read_frag(const T *lds, int r0, int kk, int lane) {
+// Row of a fragment's lane r = l % 16. A: consecutive rows. B: tile pairs share
+// 32 columns, the even one taking the first 4 of every 8 and the odd one the
+// last, so that a lane's sums of both are 8 adjacent columns.
+template <bool FIRST>
+__device__ __forceinline__ int row_of(int r, int odd) {
+    return FIRST ? (r >> 2) * 8 + (r & 3) + odd * 4 : r;
+}
+
+// The fragment of the tile rows from r0 and the kk-th 64 bytes of k.
+template <typename T, bool KC, bool FIRST, int R>
+__device__ __forceinline__ Frag<T> read_frag(const T *lds, int r0, int odd, int kk, int lane) {
     Frag<T> f;
     if constexpr (KC) {
-        f.v = *(const decltype(f.v) *)(lds + lds_unit<T, true, R>(r0 + (lane & 15), kk * 4 + (lane >> 4)));
+        const int row = r0 + row_of<FIRST>(lane & 15, odd);
+        f.v = *(const decltype(f.v) *)(lds + lds_unit<T, true, FIRST, R>(row, kk * 4 + (lane >> 4)));
     } else if constexpr (sizeof(T) == 2) {
         // one read gives a lane 4 consecutive k of its row: its group of 16
-        // lanes fetches 4 rows of k, 4 lanes and 32 bytes each
+        // lanes fetches 4 rows of k, 4 lanes and 4 runs of 8 bytes each
         typedef __attribute__((address_space(3))) s16x4 lds4;
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
         s16x4 h[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int k = kk * 32 + (lane >> 4) * 8 + j * 4 + ((lane & 15) >> 2), m = r0 + (lane & 3) * 4;
-            const T *p = lds + lds_unit<T, false, R>(k, m / 8) + m % 8;
+            const int k = kk * 32 + (lane >> 4) * 8 + j * 4 + ((lane & 15) >> 2), m = r0 + row_of<FIRST>((lane & 3) * 4, odd);
+            const T *p = lds + lds_unit<T, false, FIRST, R>(k, m / 8) + m % 8;
             h[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p);
         }
-        typedef short s16x8 __attribute__((ext_vector_type(8)));
         const s16x8 b = __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
         f.v = __builtin_bit_cast(bf16x8, b);
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int k = kk * 16 + (lane >> 4) * 4 + j, m = r0 + (lane & 15);
-            f.v[j] = lds[lds_unit<T, false, R>(k, m / 4) + m % 4];
+            const int k = kk * 16 + (lane >> 4) * 4 + j, m = r0 + row_of<FIRST>(lane & 15, odd);
+            f.v[j] = lds[lds_unit<T, false, FIRST, R>(k, m / 4) + m % 4];
         }
     }
     return f;
 }
 
-// acc[i] of lane l: row n = 4 (l / 16) + i of the first operand, row m = l % 16
-// of the second.
-__device__ __forceinline__ void mma(f32x4 &acc, const Frag<bf16_t> &n, const Frag<bf16_t> &m) {
+// acc[i] of lane l: row 4 (l / 16) + i of the first operand (B, the columns n),
+// row l % 16 of the second (A, the rows m). fp32: the e-th of 4 instructions.
+constexpr int mma_parts(size_t size) { return size == 2 ? 1 : 4; }
+__device__ __forceinline__ void mma(f32x4 &acc, const Frag<bf16_t> &n, const Frag<bf16_t> &m, int) {
     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(n.v, m.v, acc, 0, 0, 0);
 }
-__device__ __forceinline__ void mma(f32x4 &acc, const Frag<float> &n, const Frag<float> &m) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(n.v[j], m.v[j], acc, 0, 0, 0);
+__device__ __forceinline__ void mma(f32x4 &acc, const Frag<float> &n, const Frag<float> &m, int e) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(n.v[e], m.v[e], acc, 0, 0, 0);
 }
 
-// EPI: epilogue(m, n, 4 sums of columns n.., how many of them exist).
-template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, typename EPI>
+// EPI: epilogue(m, n, 8 sums of columns n.., how many of them exist).
+// DIRECT: whole k steps go from memory to LDS without registers; a last partial
+// one, and every one of operands that are not aligned for that, goes through
+// registers. Two buffers: while one is multiplied the other is filled.
+template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool DIRECT, typename EPI>
 __global__ __launch_bounds__(WM *WN * 64) void k_gemm(GemmArgs a, EPI epi) {
     constexpr int BK = 128 / sizeof(T), THREADS = WM * WN * 64;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles per wave
-    __shared__ __align__(16) T As[BM * BK], Bs[BN * BK];
+    static_assert(TN % 2 == 0, "column tiles come in pairs");
+    extern __shared__ __align__(128) char smem[];
+    T *const lds = (T *)smem;
+    constexpr int STAGE = (BM + BN) * BK, BS = BM * BK;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int tiles = a.tiles_m * a.tiles_n;
     const int b = xcd_block(blockIdx.x, gridDim.x);
-    const int split = b / tiles, t = b % tiles;
-    const int m0 = (t / a.tiles_n) * BM, n0 = (t % a.tiles_n) * BN;
+    const int split = b / tiles, t = b - split * tiles;
+    // tiles in bands of 8 rows of tiles: blocks that run together share panels
+    const int band = t / (8 * a.tiles_n), in = t - band * 8 * a.tiles_n;
+    const int height = min(8, a.tiles_m - band * 8);
+    const int m0 = (band * 8 + in % height) * BM, n0 = (in / height) * BN;
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
 
-    f32x4 acc[TM][TN] = {};
+    Stager<T, AKC, false, BM, THREADS> sa = {(const T *)a.A, a.lda, m0, a.M, a.K, {}};
+    Stager<T, BKC, true, BN, THREADS> sb = {(const T *)a.B, a.ldb, n0, a.N, a.K, {}};
+    if constexpr (DIRECT) {
+        sa.prepare();
+        sb.prepare();
+    }
     const int ks = split * a.ksteps, ke = min(ks + a.ksteps, (a.K + BK - 1) / BK);
-    for (int s = ks; s < ke; ++s) {
-        stage<T, AKC, BM, THREADS>(As, (const T *)a.A, a.lda, m0, a.M, s * BK, a.K);
-        stage<T, BKC, BN, THREADS>(Bs, (const T *)a.B, a.ldb, n0, a.N, s * BK, a.K);
-        __syncthreads();
+    const int kd = DIRECT ? min(ke, a.K / BK) : ks;  // steps [ks, kd) are whole and direct
+
+    f32x4 acc[TM][TN] = {};
+    const auto multiply = [&](const T *buf) {
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             Frag<T> fa[TM], fb[TN];
 #pragma unroll
-            for (int i = 0; i < TM; ++i) fa[i] = read_frag<T, AKC, BM>(As, wm + i * 16, kk, lane);
+            for (int i = 0; i < TM; ++i) fa[i] = read_frag<T, AKC, false, BM>(buf, wm + i * 16, 0, kk, lane);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb[j] = read_frag<T, BKC, BN>(Bs, wn + j * 16, kk, lane);
+            for (int j = 0; j < TN; ++j)
+                fb[j] = read_frag<T, BKC, true, BN>(buf + BS, wn + (j / 2) * 32, j % 2, kk, lane);
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+            for (int e = 0; e < mma_parts(sizeof(T)); ++e)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) mma(acc[i][j], fb[j], fa[i]);
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) mma(acc[i][j], fb[j], fa[i], e);
         }
-        __syncthreads();
+    };
+
+    int s = ks;
+    if (DIRECT && s < kd) {
+        sa.direct(lds, s);
+        sb.direct(lds + BS, s);
+        for (; s < kd; ++s) {
+            T *const cur = lds + ((s - ks) & 1) * STAGE, *const nxt = lds + ((s - ks + 1) & 1) * STAGE;
+            wait_direct();
+            __syncthreads();
+            if (s + 1 < kd) {
+                sa.direct(nxt, s + 1);
+                sb.direct(nxt + BS, s + 1);
+            }
+            multiply(cur);
+        }
     }
+    if (s < ke) {
+        Vec<T, 16 / sizeof(T)> va[decltype(sa)::COUNT], vb[decltype(sb)::COUNT];
+        sa.load(va, s);
+        sb.load(vb, s);
+        for (; s < ke; ++s) {
+            T *const cur = lds + ((s - ks) & 1) * STAGE;
+            sa.store(cur, va);
+            sb.store(cur + BS, vb);
+            __syncthreads();
+            if (s + 1 < ke) {
+                sa.load(va, s + 1);
+                sb.load(vb, s + 1);
+            }
+            multiply(cur);
+        }
+    }
+
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int m = m0 + wm + i * 16 + (lane & 15);
         if (m >= a.M) continue;
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int n = n0 + wn + j * 16 + (lane >> 4) * 4;
-            if (n >= a.N) continue;
-            if (a.partial) {
-                Vec<float, 4> r;
+        for (int j = 0; j < TN; j += 2) {
+            const int n = n0 + wn + j * 16 + (lane >> 4) * 8, cnt = a.N - n;
+            if (cnt <= 0) continue;
+            Vec<float, 8> r;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) r.v[e] = acc[i][j][e];
-                store_vec_n<float, 4>(a.partial + ((int64_t)split * a.M + m) * a.N + n, r, a.N - n);
-            } else {
-                epi(m, n, acc[i][j], a.N - n);
-            }
+            for (int e = 0; e < 8; ++e) r.v[e] = acc[i][j + e / 4][e % 4];
+            if (a.partial) store_vec_n<float, 8>(a.partial + ((int64_t)split * a.M + m) * a.N + n, r, cnt);
+            else epi(m, n, r, cnt);
         }
     }
 }
 
 // Joins split products, in the order of k, and runs the epilogue: a thread per
-// 4 columns of a row.
+// 8 columns of a row.
 template <typename EPI>
 __global__ __launch_bounds__(256) void k_gemm_join(GemmArgs a, int splits, EPI epi) {
-    const int nq = (a.N + 3) / 4;
+    const int nq = (a.N + 7) / 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= (int64_t)a.M * nq) return;
-    const int m = (int)(i / nq), n = (int)(i % nq) * 4;
-    f32x4 s = {};
+    const int m = (int)(i / nq), n = (int)(i % nq) * 8;
+    Vec<float, 8> s = {};
     for (int k = 0; k < splits; ++k) {
-        const Vec<float, 4> v = load_vec_n<float, 4>(a.partial + ((int64_t)k * a.M + m) * a.N + n, a.N - n);
+        const Vec<float, 8> v = load_vec_n<float, 8>(a.partial + ((int64_t)k * a.M + m) * a.N + n, a.N - n);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] += v.v[e];
+        for (int e = 0; e < 8; ++e) s.v[e] += v.v[e];
     }
     epi(m, n, s, a.N - n);
+}
+
+// Whether an operand's steps can go to LDS directly.
+template <typename T, bool KC>
+bool direct_ok(int64_t ld, int rows) {
+    constexpr int U = 16 / sizeof(T);
+    return ld % U == 0 && (KC || rows % U == 0);
 }
 
 template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, typename EPI>
@@ -209,10 +327,19 @@ void run_tile(const GemmShape &s, GemmArgs a, const EPI &epi, float *partial, hi
     a.tiles_n = (a.N + BN - 1) / BN;
     a.ksteps = s.ksteps;
     a.partial = s.splits > 1 ? partial : nullptr;
-    const unsigned blocks = (unsigned)((int64_t)a.tiles_m * a.tiles_n * s.splits);
-    hipLaunchKernelGGL((k_gemm<T, AKC, BKC, BM, BN, WM, WN, EPI>), dim3(blocks), dim3(WM * WN * 64), 0, st, a, epi);
+    const dim3 grid((unsigned)((int64_t)a.tiles_m * a.tiles_n * s.splits)), blk(WM * WN * 64);
+    const size_t bytes = 2 * (BM + BN) * 128;
+    const auto go = [&](auto kernel) {
+        if (bytes > 65536)
+            (void)hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        hipLaunchKernelGGL(kernel, grid, blk, bytes, st, a, epi);
+    };
+    if (direct_ok<T, AKC>(a.lda, a.M) && direct_ok<T, BKC>(a.ldb, a.N))
+        go(k_gemm<T, AKC, BKC, BM, BN, WM, WN, true, EPI>);
+    else
+        go(k_gemm<T, AKC, BKC, BM, BN, WM, WN, false, EPI>);
     if (s.splits > 1) {
-        const int64_t work = (int64_t)a.M * ((a.N + 3) / 4);
+        const int64_t work = (int64_t)a.M * ((a.N + 7) / 8);
         hipLaunchKernelGGL((k_gemm_join<EPI>), dim3((unsigned)((work + 255) / 256)), dim3(256), 0, st, a, s.splits, epi);
     }
 }
@@ -220,6 +347,7 @@ void run_tile(const GemmShape &s, GemmArgs a, const EPI &epi, float *partial, hi
 template <typename T, bool AKC, bool BKC, typename EPI>
 void run_gemm(const GemmShape &s, const GemmArgs &a, const EPI &epi, float *partial, hipStream_t st) {
     if (a.M == 0 || a.N == 0) return;
+    if (s.tile == 1) return run_tile<T, AKC, BKC, 256, 256, 2, 4>(s, a, epi, partial, st);
     run_tile<T, AKC, BKC, 128, 128, 2, 2>(s, a, epi, partial, st);
 }
 

@@ -73,11 +73,11 @@ struct EpiStore {
     T *out;
     int64_t ld;
 
-    __device__ __forceinline__ void operator()(int m, int n, f32x4 v, int cnt) const {
-        Vec<T, 4> r;
+    __device__ __forceinline__ void operator()(int m, int n, Vec<float, 8> v, int cnt) const {
+        Vec<T, 8> r;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r.v[e] = from_f32<T>(v[e]);
-        store_vec_n<T, 4>(out + (int64_t)m * ld + n, r, cnt);
+        for (int e = 0; e < 8; ++e) r.v[e] = from_f32<T>(v.v[e]);
+        store_vec_n<T, 8>(out + (int64_t)m * ld + n, r, cnt);
     }
 };
 

@@ -4,9 +4,8 @@
 namespace wq8 {
 
 void gemm_tile_size(int t, int *bm, int *bn) {
-    (void)t;
-    *bm = 128;
-    *bn = 128;
+    *bm = t == 1 ? 256 : 128;
+    *bn = t == 1 ? 256 : 128;
 }
 
 int gemm_kstep(wq8_dtype t) { return t == WQ8_F32 ? 32 : 64; }
@@ -21,38 +20,38 @@ struct EpiForward {
     int64_t ys, rs;
     int N, act, planar, pixels;
 
-    __device__ __forceinline__ void operator()(int m, int n, f32x4 v, int cnt) const {
+    __device__ __forceinline__ void operator()(int m, int n, Vec<float, 8> v, int cnt) const {
         if (bias) {
-            const Vec<float, 4> b = load_vec_n<float, 4>(bias + n, cnt);
+            const Vec<float, 8> b = load_vec_n<float, 8>(bias + n, cnt);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += b.v[e];
+            for (int e = 0; e < 8; ++e) v.v[e] += b.v[e];
         }
-        Vec<YT, 4> r;
+        Vec<YT, 8> r;
         if (z) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) r.v[e] = from_f32<YT>(v[e]);
-            store_vec_n<YT, 4>(z + (int64_t)m * N + n, r, cnt);
+            for (int e = 0; e < 8; ++e) r.v[e] = from_f32<YT>(v.v[e]);
+            store_vec_n<YT, 8>(z + (int64_t)m * N + n, r, cnt);
         }
         with_act(act, [&](auto a) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = act_fwd<decltype(a)::value>(v[e]);
+            for (int e = 0; e < 8; ++e) v.v[e] = act_fwd<decltype(a)::value>(v.v[e]);
         });
         if (residual) {
             if (planar) {
                 const int img = m / pixels, p = m - img * pixels;
                 const YT *src = residual + ((int64_t)img * N + n) * pixels + p;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < cnt) v[e] += to_f32(src[(int64_t)e * pixels]);
+                for (int e = 0; e < 8; ++e)
+                    if (e < cnt) v.v[e] += to_f32(src[(int64_t)e * pixels]);
             } else {
-                const Vec<YT, 4> s = load_vec_n<YT, 4>(residual + (int64_t)m * rs + n, cnt);
+                const Vec<YT, 8> s = load_vec_n<YT, 8>(residual + (int64_t)m * rs + n, cnt);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] += to_f32(s.v[e]);
+                for (int e = 0; e < 8; ++e) v.v[e] += to_f32(s.v[e]);
             }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r.v[e] = from_f32<YT>(v[e]);
-        store_vec_n<YT, 4>(y + (int64_t)m * ys + n, r, cnt);
+        for (int e = 0; e < 8; ++e) r.v[e] = from_f32<YT>(v.v[e]);
+        store_vec_n<YT, 8>(y + (int64_t)m * ys + n, r, cnt);
     }
 };
 

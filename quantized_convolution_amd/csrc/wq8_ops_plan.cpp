@@ -207,7 +207,7 @@ wq8_status build_norm(const wq8_norm_desc *d, wq8_norm_plan *p) {
 // ------------------------------------------------------ product's launch shape
 GemmShape choose_gemm(int64_t M, int64_t N, int64_t K, wq8_dtype t) {
     GemmShape s;
-    s.tile = 0;
+    s.tile = ceil_div64(M, 256) * ceil_div64(N, 256) >= kCus && t == WQ8_BF16;
     int bm, bn;
     gemm_tile_size(s.tile, &bm, &bn);
     const int64_t tiles = ceil_div64(M, bm) * ceil_div64(N, bn), steps = ceil_div64(K, gemm_kstep(t));
