@@ -106,7 +106,7 @@ struct Stager {
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                          :
                          : "s"(m0), "v"(off[i]), "s"(r)
-                         : "memory", "m0");
+                         : "memory");
         }
     }
 

@@ -46,24 +46,42 @@ template <typename T, int V>
 __device__ __forceinline__ void store_vec(T *p, const Vec<T, V> &r) {
     __builtin_memcpy(p, &r, sizeof r);
 }
-// The first n of V elements, the rest zero (n <= 0: all zero, nothing read).
+// The first n of V elements, the rest zero (n <= 0: all zero, nothing read). A
+// part of a vector takes one access per set bit of n.
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load_vec_n(const T *p, int n) {
+    Vec<T, V> r = {};
     if (n >= V) return load_vec<T, V>(p);
-    Vec<T, V> r;
+    if constexpr (V > 1) {
+        constexpr int H = V / 2;
+        if (n >= H) {
+            const Vec<T, H> lo = load_vec<T, H>(p), hi = load_vec_n<T, H>(p + H, n - H);
 #pragma unroll
-    for (int i = 0; i < V; ++i) r.v[i] = i < n ? p[i] : T(0);
+            for (int i = 0; i < H; ++i) r.v[i] = lo.v[i], r.v[H + i] = hi.v[i];
+        } else if (n > 0) {
+            const Vec<T, H> lo = load_vec_n<T, H>(p, n);
+#pragma unroll
+            for (int i = 0; i < H; ++i) r.v[i] = lo.v[i];
+        }
+    }
     return r;
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_vec_n(T *p, const Vec<T, V> &r, int n) {
     if (n >= V) {
         store_vec<T, V>(p, r);
-        return;
-    }
+    } else if constexpr (V > 1) {
+        constexpr int H = V / 2;
+        Vec<T, H> lo, hi;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (i < n) p[i] = r.v[i];
+        for (int i = 0; i < H; ++i) lo.v[i] = r.v[i], hi.v[i] = r.v[H + i];
+        if (n >= H) {
+            store_vec<T, H>(p, lo);
+            store_vec_n<T, H>(p + H, hi, n - H);
+        } else if (n > 0) {
+            store_vec_n<T, H>(p, lo, n);
+        }
+    }
 }
 
 // ------------------------------------------------------------- activations

@@ -14,29 +14,31 @@ constexpr int kCus = 256;
 // ------------------------------------------------------------- group norm
 constexpr int kNormMaxSlab = 1024;  // channels per block
 
-constexpr int kNormE = 4;            // steps unrolled by the short kernels
+constexpr int kNormE = 4;            // steps unrolled by the short fused kernels
+// By the split kernels: 8 vectors in flight per thread.
+constexpr int norm_split_steps(bool backward) { return backward ? 4 : 8; }
+
+constexpr int kNormSplitThreads = 256;
 
 // Elements per access: 16 bytes of the wider type, 8 at most.
 constexpr int norm_max_vec(size_t xs, size_t ys) { return xs == 2 && ys == 2 ? 8 : 4; }
 
 // Steps whose values a thread of a 1024-thread block can hold: 128 registers,
 // 64 of them for the values of x (forward) or of x and dy (backward).
-constexpr int norm_max_steps(int V, bool backward) {
-    return V == 1 ? kNormE : (V == 2 ? 32 : 16) / (backward ? 2 : 1);
-}
+constexpr int norm_max_steps(bool backward) { return backward ? 8 : 16; }
 
 // One pass of the group norm. A block handles a slab of `slabC` channels (K
 // whole groups, or 1/J of one) over `chunk` pixels of one image. With
 // channels-last x a thread holds V adjacent channels of one pixel per step,
 // `tc` threads across the slab and `tp` pixels per step; with NCHW x it holds V
-// adjacent pixels of one channel, `tp` threads across the pixels. A step covers
-// `window` pixels of the slab's channels.
+// adjacent pixels of one channel, `tp` threads across the pixels and `tc`
+// across the channels. A step covers `window` pixels of the slab's channels.
 struct NormShape {
     int threads, V, K, J, slabC, nslab;
     int tc, tp, window;
-    int steps, E;             // steps per block, and the unrolled count that holds them
+    int steps;                // steps per block
+    int split;                // 1: statistics and output in two kernels
     int chunk, nchunk;        // pixels per block, blocks along the pixels
-    int fused;                // 1: nchunk == J == 1, statistics and output in one kernel
 };
 
 struct NormGeo {
@@ -55,9 +57,10 @@ struct NormPtrs {
     float *mean, *rstd;                  // forward: outputs (never NULL here)
     const float *mean_in, *rstd_in;      // backward
     float *dgamma, *dbeta, *dshift;      // may be NULL
-    float *part;                         // partial sums of split passes
-    float *sums;                         // backward: [2][N][C] sums over the pixels
-    float *group;                        // split backward: [N][G][2] group means
+    float *part;                         // forward, split: [N][G][nchunk J][2] mean, M2;
+                                         // backward: [N][nchunk][3][C] sums over the pixels
+    float *gpart;                        // backward, split: [N][G][nchunk J][2] group sums
+    float *group;                        // backward, split: [N][G][2] group means
 };
 
 wq8_status launch_norm_forward(const NormGeo &g, wq8_dtype xdt, wq8_dtype ydt, const NormPtrs &p,
@@ -120,5 +123,5 @@ struct wq8_norm_plan {
     wq8::NormGeo geo;
     wq8_dtype xdt, ydt;
     size_t f_off_part, f_off_stats, f_bytes;           // forward workspace
-    size_t b_off_sums, b_off_group, b_off_part, b_bytes;  // backward workspace
+    size_t b_off_part, b_off_group, b_off_gpart, b_bytes;  // backward workspace
 };

@@ -48,7 +48,7 @@ bool is_layout(int l) { return l == WQ8_NHWC || l == WQ8_NCHW; }
 // --------------------------------------------------------- norm's launch shape
 // The fused shape for slabs of K groups, or steps > most if no block of up to
 // 1024 threads holds them.
-NormShape fused_shape(const NormGeo &g, int V, int K, bool backward) {
+NormShape fused_shape(const NormGeo &g, int V, int K) {
     NormShape s;
     memset(&s, 0, sizeof s);
     s.V = V;
@@ -58,22 +58,19 @@ NormShape fused_shape(const NormGeo &g, int V, int K, bool backward) {
     s.nslab = g.G / K;
     s.chunk = g.P;
     s.nchunk = 1;
-    s.fused = 1;
     s.steps = 1 << 30;
     if (s.slabC > kNormMaxSlab) return s;
-    const int most = norm_max_steps(V, backward);
     // threads across the channels (NHWC) or the channels times the pixel
     // vectors (NCHW); along the rest, as many as leave kNormE steps or fewer
-    const int across = g.x_nhwc ? s.slabC / V : s.slabC;
+    const int across = g.x_nhwc ? ceil_div(s.slabC, V) : s.slabC;
     const int along = g.x_nhwc ? g.P : ceil_div(g.P, V);
-    if (across > 1024) return s;
     int lanes = 1024 / across;
     if (lanes > along) lanes = along;
     const int steps = ceil_div(along, lanes);
-    s.E = steps <= kNormE ? kNormE : most;
-    if (steps <= kNormE) {  // the fewest threads with that many steps
+    if (steps <= kNormE) {  // the fewest threads with that many steps, 256 if there is work
+        const int least = 256 / across;
         lanes = ceil_div(along, kNormE);
-        if (across * lanes < 256) lanes = 256 / across < along ? (256 / across > lanes ? 256 / across : lanes) : along;
+        if (lanes < least) lanes = least < along ? least : along;
     }
     s.steps = ceil_div(along, lanes);
     s.tc = across;
@@ -83,30 +80,30 @@ NormShape fused_shape(const NormGeo &g, int V, int K, bool backward) {
     return s;
 }
 
-// Split shape: blocks of 256 threads, kNormE steps along the pixels.
-NormShape split_shape(const NormGeo &g, int V) {
-    constexpr int T = 256;
+// Split shape: blocks of 256 threads, up to `most_steps` steps along the pixels.
+NormShape split_shape(const NormGeo &g, int V, int most_steps) {
+    constexpr int T = kNormSplitThreads;
     NormShape s;
     memset(&s, 0, sizeof s);
     s.V = V;
     s.J = 1;
     s.K = 1;
     s.threads = T;
-    s.E = kNormE;
+    s.split = 1;
     if (g.x_nhwc) {
-        const int across = g.cpg / V;
-        if (across > T || g.cpg > kNormMaxSlab) {
-            const int most = T < kNormMaxSlab / V ? T : kNormMaxSlab / V;
-            s.J = ceil_div(across, most);
-            s.slabC = ceil_div(across, s.J) * V;
+        const int across = ceil_div(g.cpg, V), most = kNormMaxSlab / V < T ? kNormMaxSlab / V : T;
+        if (across > most) {
+            s.slabC = ceil_div(across, ceil_div(across, most)) * V;
             s.J = ceil_div(g.cpg, s.slabC);
         } else {
-            // whole groups: the count that leaves the fewest threads idle, the
+            // whole groups: the count that leaves the fewest lanes idle, the
             // longest rows among equals
-            int best = -1;
-            for (int k = 1; k <= g.G && k * across <= T && k * g.cpg <= kNormMaxSlab; ++k) {
+            double best = -1;
+            for (int k = 1; k <= g.G; ++k) {
+                const int vecs = ceil_div(k * g.cpg, V);
+                if (vecs > most) break;
                 if (g.G % k != 0) continue;
-                const int busy = k * across * (T / (k * across));
+                const double busy = (double)k * g.cpg / V * (T / vecs);
                 if (busy >= best) {
                     best = busy;
                     s.K = k;
@@ -114,47 +111,56 @@ NormShape split_shape(const NormGeo &g, int V) {
             }
             s.slabC = s.K * g.cpg;
         }
-        s.tc = s.slabC / V;
+        s.tc = ceil_div(s.slabC, V);
         s.tp = T / s.tc;
         if (s.tp > g.P) s.tp = g.P;
         s.window = s.tp;
     } else {
         const int along = ceil_div(g.P, V);
+        s.slabC = g.cpg;
         if (g.cpg > T) {
-            s.J = ceil_div(g.cpg, T);
-            s.slabC = ceil_div(g.cpg, s.J);
+            s.slabC = ceil_div(g.cpg, ceil_div(g.cpg, T));
             s.J = ceil_div(g.cpg, s.slabC);
-        } else {
-            s.slabC = g.cpg;
         }
         s.tc = s.slabC;
         s.tp = T / s.slabC < along ? T / s.slabC : along;
         s.window = s.tp * V;
     }
     s.nslab = g.G / s.K * s.J;
-    const int steps = ceil_div(g.P, s.window);
-    s.steps = steps < kNormE ? steps : kNormE;
+    // fewer steps where the blocks would not fill the card
+    int steps = ceil_div(g.P, s.window);
+    if (steps > most_steps) steps = most_steps;
+    while (steps > 2 && (int64_t)g.N * s.nslab * ceil_div(g.P, steps * s.window) < 2 * kCus) --steps;
+    s.steps = steps;
     s.chunk = s.steps * s.window;
     s.nchunk = ceil_div(g.P, s.chunk);
-    s.fused = 0;
     return s;
 }
 
 NormShape choose_norm(const NormGeo &g, int xsz, int ysz, bool backward) {
-    int V = norm_max_vec(xsz, ysz);
-    if (g.x_nhwc)
-        while (g.cpg % V != 0) V /= 2;
-    const int most = norm_max_steps(V, backward);
-    NormShape s = fused_shape(g, V, 1, backward);
-    if (s.steps > most) return split_shape(g, V);
-    // wider slabs (longer contiguous rows) while the card stays full
-    for (int k = 2; k <= g.G; ++k) {
-        if (g.G % k != 0 || (int64_t)g.N * (g.G / k) < kCus) continue;
-        if (k * g.cpg * xsz > 256) break;
-        const NormShape t = fused_shape(g, V, k, backward);
-        if (t.steps <= most) s = t;
+    const int vmax = norm_max_vec(xsz, ysz), most = norm_max_steps(backward);
+    // vectors within one group where the group's channels allow 8 bytes or more;
+    // else vectors that straddle groups, in slabs of whole vectors
+    int V = vmax;
+    while (g.x_nhwc && V > 4 && g.cpg % V != 0) V /= 2;
+    if (g.x_nhwc && g.cpg % V != 0) V = vmax;
+    NormShape s;
+    s.steps = 1 << 30;
+    for (int k = 1; k <= g.G; ++k) {
+        if (g.G % k != 0) continue;
+        if (g.x_nhwc && k * g.cpg % V != 0 && k < g.G) continue;
+        const NormShape t = fused_shape(g, V, k);
+        if (t.steps > most) break;
+        // wider slabs (longer contiguous rows) while the card stays full
+        const bool fills = (int64_t)g.N * t.nslab >= kCus && t.slabC * xsz <= 256;
+        if (s.steps > most || fills) s = t;
     }
-    return s;
+    if (s.steps <= most) {
+        // a block holds a group: one pass, if there are blocks enough or little to do
+        const int64_t blocks = (int64_t)g.N * s.nslab, values = (int64_t)g.P * s.slabC;
+        if (blocks >= kCus / 2 || values <= 16384) return s;
+    }
+    return split_shape(g, vmax, norm_split_steps(backward));
 }
 
 wq8_status build_norm(const wq8_norm_desc *d, wq8_norm_plan *p) {
@@ -194,13 +200,14 @@ wq8_status build_norm(const wq8_norm_desc *d, wq8_norm_plan *p) {
     if ((int64_t)g.N * g.f.nslab * g.f.nchunk >= lim || (int64_t)g.N * g.b.nslab * g.b.nchunk >= lim)
         return fail(WQ8_ERR_UNSUPPORTED, "more than 2^31 blocks");
     const size_t N = g.N, G = g.G, C = g.C;
+    const size_t fparts = g.f.nchunk * g.f.J, bparts = g.b.nchunk * g.b.J;
     p->f_off_stats = 0;  // mean, rstd where the caller wants none
     p->f_off_part = round_up(N * G * 8, 256);
-    p->f_bytes = p->f_off_part + (g.f.fused ? 0 : N * G * g.f.nchunk * g.f.J * 8);
-    p->b_off_sums = 0;
-    p->b_off_group = round_up(2 * N * C * 4, 256);
-    p->b_off_part = p->b_off_group + round_up(N * G * 8, 256);
-    p->b_bytes = p->b_off_part + (g.b.fused ? 0 : N * g.b.nchunk * 3 * C * 4);
+    p->f_bytes = p->f_off_part + (g.f.split ? N * G * fparts * 8 : 0);
+    p->b_off_part = 0;
+    p->b_off_group = round_up(N * g.b.nchunk * 3 * C * 4, 256);
+    p->b_off_gpart = p->b_off_group + round_up(N * G * 8, 256);
+    p->b_bytes = p->b_off_gpart + (g.b.split ? N * G * bparts * 8 : 0);
     return WQ8_OK;
 }
 
@@ -379,9 +386,9 @@ wq8_status wq8_norm_backward(const wq8_norm_plan *p, const void *dy, const void 
     a.dgamma = dgamma;
     a.dbeta = dbeta;
     a.dshift = dshift;
-    a.sums = (float *)(ws + p->b_off_sums);
-    a.group = (float *)(ws + p->b_off_group);
     a.part = (float *)(ws + p->b_off_part);
+    a.group = (float *)(ws + p->b_off_group);
+    a.gpart = (float *)(ws + p->b_off_gpart);
     return launch_norm_backward(p->geo, p->xdt, p->ydt, a, stream);
 }
 
