@@ -10,147 +10,235 @@ namespace {
 // Split, a first kernel leaves each group's weighted sums as well, and a second
 // one joins those of its groups and writes dx. The parameters' gradients and
 // dshift come from `part` in a last, small kernel.
-template <typename XT, typename YT, int V, int KIND, bool CROSS, int E, int MODE>
-__global__ __launch_bounds__(MODE == kFused ? 1024 : kNormSplitThreads) void k_norm_bwd(NormGeo g, NormPtrs a) {
-    constexpr bool CL = KIND != kPlanar;
-    constexpr int NC = CL ? V : 1, NG = group_values<V, KIND>();
-    extern __shared__ __align__(16) char smem[];
-    const NormShape &s = g.b;
-    float *const gm = (float *)smem, *const chan = gm + 2 * s.K, *const red = chan + 2 * s.slabC;
-    const Where w = locate<V, CL>(g, s, xcd_block(blockIdx.x, gridDim.x));
-    const XT *x = (const XT *)a.x;
-    const YT *dy = (const YT *)a.dy;
 
-    Vec<XT, V> fx[E];
-    Vec<YT, V> fd[E];
+// What a thread knows of its channels.
+template <int V, int KIND>
+struct Channels {
+    static constexpr int NC = thread_channels<V, KIND>(), NG = group_values<V, KIND>();
+    float off[NC], ga[NC], be[NC], rstd[NG];  // off = shift - mean
+    int kg[NC];
+
+    __device__ __forceinline__ void load(const NormGeo &g, const NormPtrs &a, const Where &w) {
+        const int64_t group0 = (int64_t)w.n * g.G + w.g0;
+        per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, 0.0f);
+        per_channel<V, KIND>(ga, a.gamma, w.c, 1.0f);
+        per_channel<V, KIND>(be, a.beta, w.c, 0.0f);
+        groups_of<V, KIND>(kg, g, g.b, w);
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (e < s.steps) {
-            const int p = pixel_of<V, CL>(s, w, e), n = count_of<V, CL>(w, p);
-            fx[e] = load_part<XT, V, KIND>(addr<XT, V, CL>(x, g, g.xs, w.n, w.c, p), n);
-            if constexpr (!CROSS)
-                fd[e] = load_part<YT, V, KIND>(addr<YT, V, CL>(dy, g, g.ys, w.n, w.c, p), n);
-        }
-    if constexpr (CROSS) {
+        for (int k = 0; k < NC; ++k) off[k] -= a.mean_in[group0 + kg[k]];
+#pragma unroll
+        for (int k = 0; k < NG; ++k) rstd[k] = a.rstd_in[group0 + kg[k]];
+    }
+};
+
+// dy of E steps from step `first`; with the other layout by way of LDS, zeros
+// for what others own (ends with a barrier).
+template <typename YT, int V, int KIND, bool CROSS, int E>
+__device__ __forceinline__ void load_dy(Vec<YT, V> (&f)[E], const YT *dy, const NormGeo &g, const Where &w, int first, YT *tile) {
+    constexpr bool CL = KIND != kPlanar;
+    const NormShape &s = g.b;
+    if constexpr (!CROSS) {
+        load_steps<YT, V, KIND, E>(f, dy, g, s, g.ys, w, first);
+    } else {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            if (e < s.steps) {
-                YT *tile = (YT *)smem;
-                global_to_tile<YT, CL>(tile, dy, g, s, w, g.ys, w.p0 + e * s.window);
-                __syncthreads();
-                const int n = count_of<V, CL>(w, pixel_of<V, CL>(s, w, e));
+            if (first + e < s.steps) {
+                const int te = e % s.tsteps;
+                if (te == 0) {
+                    if (e > 0) __syncthreads();
+                    global_to_tile<YT, CL>(tile, dy, g, s, w, g.ys, w.p0 + (first + e) * s.window);
+                    __syncthreads();
+                }
+                const Step at = step_of<V, KIND>(s, w, first + e);
+                const int p0 = w.p0 + (first + e - te) * s.window;
 #pragma unroll
-                for (int k = 0; k < V; ++k) fd[e].v[k] = k < n ? tile[tile_at<CL, V>(s, w, k)] : YT(0);
-                __syncthreads();
+                for (int k = 0; k < V; ++k) f[e].v[k] = k >= at.lo ? tile[tile_at<V, KIND>(s, w, p0, at.p, k)] : YT(0);
             }
+        __syncthreads();
     }
+}
+
+// Adds the steps' dz, dz h and h to the thread's sums.
+template <typename XT, typename YT, int V, int KIND, int E>
+__device__ __forceinline__ void add_sums(float *s1, float *s2, float *s3, const Vec<XT, V> (&fx)[E], const Vec<YT, V> (&fd)[E],
+                                         const Channels<V, KIND> &c, const NormGeo &g, const Where &w, int first) {
+    with_act(g.act, [&](auto act) {
+        for_owned<V, KIND, E>(g.b, w, first, [&](int e, int k) {
+            const int kc = c.NC == 1 ? 0 : k;
+            const float h = (to_f32(fx[e].v[k]) + c.off[kc]) * c.rstd[c.NG == 1 ? 0 : k];
+            const float dz = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value>(fmaf(h, c.ga[kc], c.be[kc]));
+            s1[kc] += dz;
+            s2[kc] = fmaf(dz, h, s2[kc]);
+            s3[kc] += h;
+        });
+    });
+}
+
+// Joins the threads' sums: the channels' into `part`, the groups' weighted
+// totals into gm[2 K].
+template <int V, int KIND>
+__device__ __forceinline__ void join_sums(const float (&s1)[thread_channels<V, KIND>()],
+                                          const float (&s2)[thread_channels<V, KIND>()],
+                                          const float (&s3)[thread_channels<V, KIND>()], const NormGeo &g, const NormPtrs &a,
+                                          const Where &w, float *red, float *gm) {
+    constexpr bool CL = KIND != kPlanar;
+    const NormShape &s = g.b;
+    float *const c1 = gm + 2 * s.K, *const c2 = c1 + s.slabC;
+    channel_sum<V, CL>(s1, s, w, red, c1);
+    channel_sum<V, CL>(s2, s, w, red, c2);
+    const auto weight = [&](int c) { return a.gamma ? a.gamma[w.slab0 + c] : 1.0f; };
+    groups_of_channels(g, s, w, [&](int c) { return weight(c) * c1[c]; }, gm, 2);
+    groups_of_channels(g, s, w, [&](int c) { return weight(c) * c2[c]; }, gm + 1, 2);
+    float *out = a.part + ((int64_t)w.n * s.nchunk + w.chunk) * 3 * g.C + w.slab0;
+    const int nc = w.cend - w.slab0;
+    for (int c = threadIdx.x; c < nc; c += blockDim.x) {
+        out[c] = c1[c];
+        out[g.C + c] = c2[c];
+    }
+    __syncthreads();
+    if (a.dshift) {
+        channel_sum<V, CL>(s3, s, w, red, c1);
+        for (int c = threadIdx.x; c < nc; c += blockDim.x) out[2 * (int64_t)g.C + c] = c1[c];
+    }
+}
+
+// dx of the steps, gm: the groups' means of gamma dz and of gamma dz h.
+template <typename XT, typename YT, int V, int KIND, bool CROSS, int E>
+__device__ __forceinline__ void write_dx(const Vec<XT, V> (&fx)[E], const Vec<YT, V> (&fd)[E], const Channels<V, KIND> &c,
+                                         const float (&m1)[Channels<V, KIND>::NG], const float (&m2)[Channels<V, KIND>::NG],
+                                         const NormGeo &g, const Where &w, XT *dx, int first) {
+    constexpr bool CL = KIND != kPlanar;
+    const NormShape &s = g.b;
+    with_act(g.act, [&](auto act) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (first + e < s.steps) {
+                const Step at = step_of<V, KIND>(s, w, first + e);
+                Vec<XT, V> r;
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const int kc = CL ? k : 0, kk = c.NG == 1 ? 0 : k;
+                    const float h = (to_f32(fx[e].v[k]) + c.off[kc]) * c.rstd[kk];
+                    const float dz = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value>(fmaf(h, c.ga[kc], c.be[kc]));
+                    r.v[k] = from_f32<XT>(c.rstd[kk] * (fmaf(dz, c.ga[kc], -m1[kk]) - h * m2[kk]));
+                }
+                XT *const to = addr<XT, V, KIND>(dx, g, g.xs, w, at.p);
+                if (CROSS && at.lo > 0) {  // dy of what others own is not here
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        if (k >= at.lo) to[k] = r.v[k];
+                } else if (at.lo < V) {
+                    store_vec<XT, V>(to, r);
+                }
+            }
+    });
+}
+
+template <int V, int KIND>
+__device__ __forceinline__ void take_group_means(const Channels<V, KIND> &c, const float *gm, float *m1, float *m2) {
+#pragma unroll
+    for (int k = 0; k < c.NG; ++k) {
+        m1[k] = gm[2 * c.kg[k]];
+        m2[k] = gm[2 * c.kg[k] + 1];
+    }
+}
+
+template <typename XT, typename YT, int V, int KIND, bool CROSS, int E>
+__global__ __launch_bounds__(1024) void k_norm_bwd_fused(NormGeo g, NormPtrs a) {
+    constexpr bool CL = KIND != kPlanar;
+    constexpr int NC = thread_channels<V, KIND>(), NG = group_values<V, KIND>();
+    extern __shared__ __align__(16) char smem[];
+    const NormShape &s = g.b;
+    float *const red = (float *)smem, *const gm = red + norm_sum_floats(s, CL);
+    const Where w = locate<V, KIND>(g, s);
+    Vec<XT, V> fx[E];
+    Vec<YT, V> fd[E];
+    load_steps<XT, V, KIND, E>(fx, (const XT *)a.x, g, s, g.xs, w, 0);
+    load_dy<YT, V, KIND, CROSS, E>(fd, (const YT *)a.dy, g, w, 0, (YT *)smem);
+    Channels<V, KIND> c;
+    c.load(g, a, w);
+    float s1[NC] = {}, s2[NC] = {}, s3[NC] = {};
+    add_sums<XT, YT, V, KIND, E>(s1, s2, s3, fx, fd, c, g, w, 0);
+    if constexpr (!keeps_derived(V, E, KIND)) {
+        forget(fx);
+        forget(fd);
+    }
+    join_sums<V, KIND>(s1, s2, s3, g, a, w, red, gm);
     const int64_t group0 = (int64_t)w.n * g.G + w.g0;
-    float off[NC], ga[NC], be[NC], rstd[NG];
-    per_channel<V, CL>(off, a.shift, (int64_t)w.n * g.C + w.c, w.nc, 0.0f);
-    per_channel<V, CL>(ga, a.gamma, w.c, w.nc, 1.0f);
-    per_channel<V, CL>(be, a.beta, w.c, w.nc, 0.0f);
-#pragma unroll
-    for (int k = 0; k < NC; ++k) off[k] -= a.mean_in[group0 + group_of<V, KIND>(g, s, w, k)];
-#pragma unroll
-    for (int k = 0; k < NG; ++k) rstd[k] = a.rstd_in[group0 + group_of<V, KIND>(g, s, w, k)];
+    for (int k = threadIdx.x; k < 2 * s.K; k += blockDim.x)
+        a.group[2 * group0 + k] = gm[k] = gm[k] / (float)((double)g.P * g.cpg);
+    __syncthreads();
+    float m1[NG], m2[NG];
+    take_group_means<V, KIND>(c, gm, m1, m2);
+    write_dx<XT, YT, V, KIND, CROSS, E>(fx, fd, c, m1, m2, g, w, (XT *)a.dx, 0);
+}
 
-    if constexpr (MODE != kApply) {
-        float s1[NC] = {}, s2[NC] = {}, s3[NC] = {};
-        with_act(g.act, [&](auto act) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (e < s.steps) {
-                    const int n = count_of<V, CL>(w, pixel_of<V, CL>(s, w, e));
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const int kc = CL ? k : 0;
-                        const float h = (to_f32(fx[e].v[k]) + off[kc]) * rstd[NG == 1 ? 0 : k];
-                        const float dz = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value>(fmaf(h, ga[kc], be[kc]));
-                        if (k < n) {
-                            s1[kc] += dz;
-                            s2[kc] = fmaf(dz, h, s2[kc]);
-                            s3[kc] += h;
-                        }
-                    }
-                }
-        });
-        if constexpr (MODE == kFused) {
-            forget(fx);
-            forget(fd);
+template <typename XT, typename YT, int V, int KIND, bool CROSS, int E>
+__global__ __launch_bounds__(kNormSplitThreads) void k_norm_bwd_sums(NormGeo g, NormPtrs a) {
+    constexpr bool CL = KIND != kPlanar;
+    constexpr int NC = thread_channels<V, KIND>();
+    extern __shared__ __align__(16) char smem[];
+    const NormShape &s = g.b;
+    float *const red = (float *)smem, *const gm = red + norm_sum_floats(s, CL);
+    const Where w = locate<V, KIND>(g, s);
+    Channels<V, KIND> c;
+    c.load(g, a, w);
+    float s1[NC] = {}, s2[NC] = {}, s3[NC] = {};
+    for (int first = 0; first < s.steps; first += E) {
+        Vec<XT, V> fx[E];
+        Vec<YT, V> fd[E];
+        load_steps<XT, V, KIND, E>(fx, (const XT *)a.x, g, s, g.xs, w, first);
+        load_dy<YT, V, KIND, CROSS, E>(fd, (const YT *)a.dy, g, w, first, (YT *)smem);
+        add_sums<XT, YT, V, KIND, E>(s1, s2, s3, fx, fd, c, g, w, first);
+    }
+    join_sums<V, KIND>(s1, s2, s3, g, a, w, red, gm);
+    const int64_t group0 = (int64_t)w.n * g.G + w.g0;
+    for (int k = threadIdx.x; k < 2 * s.K; k += blockDim.x) {
+        const int64_t at = (group0 + k / 2) * (s.nchunk * s.J) + w.chunk * s.J + w.part;
+        a.gpart[2 * at + k % 2] = gm[k];
+    }
+}
+
+template <typename XT, typename YT, int V, int KIND, bool CROSS, int E>
+__global__ __launch_bounds__(kNormSplitThreads) void k_norm_bwd_apply(NormGeo g, NormPtrs a) {
+    constexpr int NG = group_values<V, KIND>();
+    extern __shared__ __align__(16) char smem[];
+    const NormShape &s = g.b;
+    float *const gm = (float *)smem;
+    const Where w = locate<V, KIND>(g, s);
+    Channels<V, KIND> c;
+    c.load(g, a, w);
+    const int64_t group0 = (int64_t)w.n * g.G + w.g0;
+    const int lane = threadIdx.x & 63, np = s.nchunk * s.J;
+    for (int k = threadIdx.x >> 6; k < s.K; k += kNormSplitThreads / 64) {
+        const float *part = a.gpart + 2 * (group0 + k) * np;
+        float t1 = 0.0f, t2 = 0.0f;
+        for (int i = lane; i < np; i += 64) {
+            t1 += part[2 * i];
+            t2 += part[2 * i + 1];
         }
-        float *const c1 = chan, *const c2 = chan + s.slabC;
-        channel_sum<V, CL>(s1, s, w, red, c1);
-        channel_sum<V, CL>(s2, s, w, red, c2);
-        const auto weight = [&](int c) { return a.gamma ? a.gamma[w.slab0 + c] : 1.0f; };
-        groups_of_channels(g, s, w, [&](int c) { return weight(c) * c1[c]; }, gm, 2);
-        groups_of_channels(g, s, w, [&](int c) { return weight(c) * c2[c]; }, gm + 1, 2);
-        float *out = a.part + ((int64_t)w.n * s.nchunk + w.chunk) * 3 * g.C + w.slab0;
-        const int nc = w.cend - w.slab0;
-        for (int c = threadIdx.x; c < nc; c += blockDim.x) {
-            out[c] = c1[c];
-            out[g.C + c] = c2[c];
-        }
-        __syncthreads();
-        if (a.dshift) {
-            channel_sum<V, CL>(s3, s, w, red, c1);
-            for (int c = threadIdx.x; c < nc; c += blockDim.x) out[2 * (int64_t)g.C + c] = c1[c];
-        }
-        for (int k = threadIdx.x; k < 2 * s.K; k += blockDim.x) {
-            if constexpr (MODE == kReduce) {
-                const int64_t at = (group0 + k / 2) * (s.nchunk * s.J) + w.chunk * s.J + w.part;
-                a.gpart[2 * at + k % 2] = gm[k];
-            } else {
-                a.group[2 * group0 + k] = gm[k] = gm[k] / (float)((double)g.P * g.cpg);
-            }
-        }
-    } else {
-        const int lane = threadIdx.x & 63, np = s.nchunk * s.J;
-        for (int k = threadIdx.x >> 6; k < s.K; k += blockDim.x >> 6) {
-            const float *part = a.gpart + 2 * (group0 + k) * np;
-            float t1 = 0.0f, t2 = 0.0f;
-            for (int i = lane; i < np; i += 64) {
-                t1 += part[2 * i];
-                t2 += part[2 * i + 1];
-            }
-            const float m = (float)((double)g.P * g.cpg);
-            t1 = wave_sum(t1) / m;
-            t2 = wave_sum(t2) / m;
-            if (lane == 0) {
-                gm[2 * k] = t1;
-                gm[2 * k + 1] = t2;
-                if (w.chunk == 0 && w.part == 0) {
-                    a.group[2 * (group0 + k)] = t1;
-                    a.group[2 * (group0 + k) + 1] = t2;
-                }
+        const float m = (float)((double)g.P * g.cpg);
+        t1 = wave_sum(t1) / m;
+        t2 = wave_sum(t2) / m;
+        if (lane == 0) {
+            gm[2 * k] = t1;
+            gm[2 * k + 1] = t2;
+            if (w.chunk == 0 && w.part == 0) {
+                a.group[2 * (group0 + k)] = t1;
+                a.group[2 * (group0 + k) + 1] = t2;
             }
         }
     }
-
-    if constexpr (MODE != kReduce) {
-        __syncthreads();
-        float m1[NG], m2[NG];
-#pragma unroll
-        for (int k = 0; k < NG; ++k) {
-            m1[k] = gm[2 * group_of<V, KIND>(g, s, w, k)];
-            m2[k] = gm[2 * group_of<V, KIND>(g, s, w, k) + 1];
-        }
-        XT *dx = (XT *)a.dx;
-        with_act(g.act, [&](auto act) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (e < s.steps) {
-                    const int p = pixel_of<V, CL>(s, w, e), n = count_of<V, CL>(w, p);
-                    Vec<XT, V> r;
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const int kc = CL ? k : 0, kg = NG == 1 ? 0 : k;
-                        const float h = (to_f32(fx[e].v[k]) + off[kc]) * rstd[kg];
-                        const float dz = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value>(fmaf(h, ga[kc], be[kc]));
-                        r.v[k] = from_f32<XT>(rstd[kg] * (fmaf(dz, ga[kc], -m1[kg]) - h * m2[kg]));
-                    }
-                    store_part<XT, V, KIND>((XT *)addr<XT, V, CL>(dx, g, g.xs, w.n, w.c, p), r, n);
-                }
-        });
+    __syncthreads();
+    float m1[NG], m2[NG];
+    take_group_means<V, KIND>(c, gm, m1, m2);
+    if constexpr (CROSS) __syncthreads();  // the tile takes the means' place
+    for (int first = 0; first < s.steps; first += E) {
+        Vec<XT, V> fx[E];
+        Vec<YT, V> fd[E];
+        load_steps<XT, V, KIND, E>(fx, (const XT *)a.x, g, s, g.xs, w, first);
+        load_dy<YT, V, KIND, CROSS, E>(fd, (const YT *)a.dy, g, w, first, (YT *)smem);
+        write_dx<XT, YT, V, KIND, CROSS, E>(fx, fd, c, m1, m2, g, w, (XT *)a.dx, first);
     }
 }
 
@@ -203,15 +291,14 @@ struct RunBackward {
     void operator()() const {
         const NormShape &s = g.b;
         const dim3 grid((unsigned)((int64_t)g.N * s.nslab * s.nchunk)), blk(s.threads);
-        const size_t red = (size_t)(2 * s.K + 2 * s.slabC + sum_floats(s, KIND)) * 4;
+        const size_t red = (size_t)(2 * s.K + 2 * s.slabC + norm_sum_floats(s, KIND != kPlanar)) * 4;
         const size_t tile = CROSS ? tile_lds<YT>(s, KIND != kPlanar) : 0;
-        const size_t both = red > tile ? red : tile, own = (size_t)2 * s.K * 4;
+        const size_t most = red > tile ? red : tile, means = (size_t)2 * s.K * 4;
         if constexpr (!SPLIT) {
-            hipLaunchKernelGGL((k_norm_bwd<XT, YT, V, KIND, CROSS, E, kFused>), grid, blk, both, st, g, p);
+            hipLaunchKernelGGL((k_norm_bwd_fused<XT, YT, V, KIND, CROSS, E>), grid, blk, most, st, g, p);
         } else {
-            hipLaunchKernelGGL((k_norm_bwd<XT, YT, V, KIND, CROSS, E, kReduce>), grid, blk, both, st, g, p);
-            hipLaunchKernelGGL((k_norm_bwd<XT, YT, V, KIND, CROSS, E, kApply>), grid, blk, own > tile ? own : tile, st,
-                               g, p);
+            hipLaunchKernelGGL((k_norm_bwd_sums<XT, YT, V, KIND, CROSS, E>), grid, blk, most, st, g, p);
+            hipLaunchKernelGGL((k_norm_bwd_apply<XT, YT, V, KIND, CROSS, E>), grid, blk, means > tile ? means : tile, st, g, p);
         }
     }
 };

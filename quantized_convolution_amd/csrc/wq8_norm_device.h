@@ -16,6 +16,23 @@ namespace {
 enum { kFused = 0, kReduce = 1, kApply = 2 };
 
 // ---------------------------------------------------------- block geometry
+// KIND: how a thread's values fall into channels and groups.
+//   kPlanar    NCHW: V pixels of one channel
+//   kUniform   NHWC: V channels of one group (V divides the group's channels)
+//   kStraddle  NHWC: V channels, of any groups
+// A vector that would pass the end of its row starts earlier instead, so that
+// every load is a whole vector inside the tensor: its first `lo` values belong
+// to another thread. They are left out of the sums; stored, they are the
+// values that the other thread stores. lo = V: the thread owns nothing there,
+// and what it loads is any valid vector.
+enum { kPlanar = 0, kUniform = 1, kStraddle = 2 };
+
+// Channels of a thread, and values it keeps apart in a sum per group.
+template <int V, int KIND>
+constexpr int thread_channels() { return KIND == kPlanar ? 1 : V; }
+template <int V, int KIND>
+constexpr int group_values() { return KIND == kStraddle ? V : 1; }
+
 struct Where {
     int n, chunk, part;          // part: index along J
     int slab0, cend;             // channels of this block: [slab0, cend)
@@ -23,13 +40,13 @@ struct Where {
     int p0, pend;                // pixels of this block
     int tp, tc;                  // this thread's place in a window
     int c;                       // its first (NHWC) or only (NCHW) channel
-    int nc;                      // its channels that exist (0: it owns nothing)
+    int lo;                      // its channels that others own
 };
 
-template <int V, bool CL>
-__device__ __forceinline__ Where locate(const NormGeo &g, const NormShape &s, int b) {
+template <int V, int KIND>
+__device__ __forceinline__ Where locate(const NormGeo &g, const NormShape &s) {
     Where w;
-    const int tid = threadIdx.x;
+    const int b = xcd_block(blockIdx.x, gridDim.x), tid = threadIdx.x;
     w.chunk = b % s.nchunk;
     const int r = b / s.nchunk, slab = r % s.nslab;
     w.n = r / s.nslab;
@@ -46,65 +63,76 @@ __device__ __forceinline__ Where locate(const NormGeo &g, const NormShape &s, in
     }
     w.p0 = w.chunk * s.chunk;
     w.pend = min(w.p0 + s.chunk, g.P);
-    if constexpr (CL) {
+    if constexpr (KIND != kPlanar) {
         w.tc = tid % s.tc;
         w.tp = tid / s.tc;
-        w.c = w.slab0 + w.tc * V;
-        w.nc = w.tp < s.tp ? min(max(w.cend - w.c, 0), V) : 0;
+        const int c = w.slab0 + w.tc * V;
+        w.c = min(c, w.cend - V);
+        w.lo = w.tp < s.tp ? min(c - w.c, V) : V;
     } else {
         w.tp = tid % s.tp;
         w.tc = tid / s.tp;
-        w.c = w.slab0 + w.tc;
-        w.nc = w.c < w.cend;
+        const int c = w.slab0 + w.tc;
+        w.c = min(c, w.cend - 1);
+        w.lo = c == w.c ? 0 : V;
     }
     return w;
 }
 
-// Pixel of step e, and how many of the thread's V elements exist.
-template <int V, bool CL>
-__device__ __forceinline__ int pixel_of(const NormShape &s, const Where &w, int e) {
-    return w.p0 + e * s.window + w.tp * (CL ? 1 : V);
-}
-template <int V, bool CL>
-__device__ __forceinline__ int count_of(const Where &w, int p) {
-    if (CL) return p < w.pend ? w.nc : 0;
-    return w.nc ? min(max(w.pend - p, 0), V) : 0;
-}
-
-// KIND: how a thread's values fall into groups.
-//   kPlanar    NCHW: V pixels of one channel
-//   kUniform   NHWC: V channels of one group (V divides the group's channels)
-//   kStraddle  NHWC: V channels, of any groups; the last thread's may be fewer
-enum { kPlanar = 0, kUniform = 1, kStraddle = 2 };
-
-// Values a thread keeps apart in a sum per group.
+// First pixel of the thread's vector in step e, and its values that others own.
+struct Step {
+    int p, lo;
+};
 template <int V, int KIND>
-constexpr int group_values() { return KIND == kStraddle ? V : 1; }
+__device__ __forceinline__ Step step_of(const NormShape &s, const Where &w, int e) {
+    if constexpr (KIND != kPlanar) {
+        const int p = w.p0 + e * s.window + w.tp;
+        return {min(p, w.pend - 1), p < w.pend ? w.lo : V};
+    } else {
+        const int p = w.p0 + e * s.window + w.tp * V, q = min(p, w.pend - V);
+        return {q, w.lo ? V : min(p - q, V)};
+    }
+}
 
-// A thread's vector, of which n elements exist: all or none where vectors lie
-// within groups.
 template <typename T, int V, int KIND>
-__device__ __forceinline__ Vec<T, V> load_part(const T *p, int n) {
-    if constexpr (KIND == kUniform) {
-        Vec<T, V> r = {};
-        if (n > 0) r = load_vec<T, V>(p);
-        return r;
-    } else {
-        return load_vec_n<T, V>(p, n);
-    }
+__device__ __forceinline__ T *addr(T *x, const NormGeo &g, int64_t stride, const Where &w, int p) {
+    return KIND != kPlanar ? x + ((int64_t)w.n * g.P + p) * stride + w.c : x + ((int64_t)w.n * g.C + w.c) * g.P + p;
 }
-template <typename T, int V, int KIND>
-__device__ __forceinline__ void store_part(T *p, const Vec<T, V> &r, int n) {
-    if constexpr (KIND == kUniform) {
-        if (n > 0) store_vec<T, V>(p, r);
-    } else {
-        store_vec_n<T, V>(p, r, n);
-    }
+
+// The thread's vectors of E steps from step `first`.
+template <typename T, int V, int KIND, int E>
+__device__ __forceinline__ void load_steps(Vec<T, V> (&f)[E], const T *x, const NormGeo &g, const NormShape &s, int64_t stride,
+                                           const Where &w, int first) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (first + e < s.steps)
+            f[e] = load_vec<T, V>(addr<const T, V, KIND>(x, g, stride, w, step_of<V, KIND>(s, w, first + e).p));
 }
+
+// f(e, k) for the values that the thread owns in E steps from step `first`.
+template <int V, int KIND, int E, typename F>
+__device__ __forceinline__ void for_owned(const NormShape &s, const Where &w, int first, F f) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (first + e < s.steps) {
+            const int lo = step_of<V, KIND>(s, w, first + e).lo;
+            if (lo == 0) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) f(e, k);
+            } else if (KIND != kUniform && lo < V) {
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (k >= lo) f(e, k);
+            }
+        }
+}
+
+// Whether there are registers to keep what one pass over the values derived
+// from them for the next one.
+constexpr bool keeps_derived(int V, int E, int kind) { return V * E <= (kind == kStraddle ? 16 : 32); }
 
 // Makes the compiler forget what it derived from the values: it would keep
-// every conversion and sum of one pass over them for the next, several
-// registers a value, and spill.
+// every conversion and sum, several registers a value, and spill.
 template <typename T, int V, int E>
 __device__ __forceinline__ void forget(Vec<T, V> (&f)[E]) {
     constexpr int W = V * sizeof(T) / 4;
@@ -118,69 +146,72 @@ __device__ __forceinline__ void forget(Vec<T, V> (&f)[E]) {
     }
 }
 
-template <typename T, int V, bool CL>
-__device__ __forceinline__ const T *addr(const T *x, const NormGeo &g, int64_t stride, int n, int c,
-                                         int p) {
-    return CL ? x + ((int64_t)n * g.P + p) * stride + c : x + ((int64_t)n * g.C + c) * g.P + p;
-}
-
 // ------------------------------------------------- windows in the other layout
 // Threads follow x's layout; tensor `t` has the other one. The tile in LDS
-// holds it as t does, [channel][pixel] or [pixel][channel], rows padded by
-// two elements to spread the banks.
+// holds `tsteps` windows of it as t does, [channel][pixel] or [pixel][channel],
+// rows padded by two elements to spread the banks.
 template <bool CL>
 __device__ __forceinline__ int tile_row(const NormShape &s) {
-    return (CL ? s.window : s.slabC) + 2;
+    return (CL ? s.tsteps * s.window : s.slabC) + 2;
+}
+
+// Rows and their length of the tile whose first pixel is p.
+template <bool CL>
+__device__ __forceinline__ void tile_extent(const NormShape &s, const Where &w, int p, int &outer, int &inner) {
+    const int wp = min(s.tsteps * s.window, w.pend - p), wc = w.cend - w.slab0;
+    inner = CL ? wp : wc;
+    outer = CL ? wc : wp;
 }
 
 template <typename T, bool CL>
-__device__ __forceinline__ void tile_to_global(const T *tile, T *t, const NormGeo &g,
-                                               const NormShape &s, const Where &w, int64_t stride,
-                                               int p) {
+__device__ __forceinline__ T *tile_addr(T *t, const NormGeo &g, const Where &w, int64_t stride, int p, int row, int at) {
+    return CL ? t + ((int64_t)w.n * g.C + w.slab0 + row) * g.P + p + at
+              : t + ((int64_t)w.n * g.P + p + row) * stride + w.slab0 + at;
+}
+
+template <typename T, bool CL>
+__device__ __forceinline__ void tile_to_global(const T *tile, T *t, const NormGeo &g, const NormShape &s, const Where &w,
+                                               int64_t stride, int p) {
     constexpr int VO = 16 / sizeof(T);
-    const int wp = min(s.window, w.pend - p), wc = w.cend - w.slab0, row = tile_row<CL>(s);
-    const int inner = CL ? wp : wc, outer = CL ? wc : wp;
-    const int nv = (inner + VO - 1) / VO;
+    int outer, inner;
+    tile_extent<CL>(s, w, p, outer, inner);
+    const int nv = (inner + VO - 1) / VO, row = tile_row<CL>(s);
     for (int i = threadIdx.x; i < outer * nv; i += blockDim.x) {
         const int o = i / nv, v = (i - o * nv) * VO;
         Vec<T, VO> r;
 #pragma unroll
         for (int k = 0; k < VO; ++k) r.v[k] = v + k < inner ? tile[o * row + v + k] : T(0);
-        T *dst = CL ? t + ((int64_t)w.n * g.C + w.slab0 + o) * g.P + p + v
-                    : t + ((int64_t)w.n * g.P + p + o) * stride + w.slab0 + v;
-        store_vec_n<T, VO>(dst, r, inner - v);
+        store_vec_n<T, VO>(tile_addr<T, CL>(t, g, w, stride, p, o, v), r, inner - v);
     }
 }
 
 template <typename T, bool CL>
-__device__ __forceinline__ void global_to_tile(T *tile, const T *t, const NormGeo &g,
-                                               const NormShape &s, const Where &w, int64_t stride,
-                                               int p) {
+__device__ __forceinline__ void global_to_tile(T *tile, const T *t, const NormGeo &g, const NormShape &s, const Where &w,
+                                               int64_t stride, int p) {
     constexpr int VO = 16 / sizeof(T);
-    const int wp = min(s.window, w.pend - p), wc = w.cend - w.slab0, row = tile_row<CL>(s);
-    const int inner = CL ? wp : wc, outer = CL ? wc : wp;
-    const int nv = (inner + VO - 1) / VO;
+    int outer, inner;
+    tile_extent<CL>(s, w, p, outer, inner);
+    const int nv = (inner + VO - 1) / VO, row = tile_row<CL>(s);
     for (int i = threadIdx.x; i < outer * nv; i += blockDim.x) {
         const int o = i / nv, v = (i - o * nv) * VO;
-        const T *src = CL ? t + ((int64_t)w.n * g.C + w.slab0 + o) * g.P + p + v
-                          : t + ((int64_t)w.n * g.P + p + o) * stride + w.slab0 + v;
-        const Vec<T, VO> r = load_vec_n<T, VO>(src, inner - v);
+        const Vec<T, VO> r = load_vec_n<T, VO>(tile_addr<const T, CL>(t, g, w, stride, p, o, v), inner - v);
 #pragma unroll
         for (int k = 0; k < VO; ++k)
             if (v + k < inner) tile[o * row + v + k] = r.v[k];
     }
 }
 
-// The tile's place of element k of this thread.
-template <bool CL, int V>
-__device__ __forceinline__ int tile_at(const NormShape &s, const Where &w, int k) {
-    return CL ? (w.tc * V + k) * tile_row<CL>(s) + w.tp
-              : (w.tp * V + k) * tile_row<CL>(s) + w.tc;
+// The tile's place of value k of a vector that starts at pixel p; the tile
+// starts at pixel p0.
+template <int V, int KIND>
+__device__ __forceinline__ int tile_at(const NormShape &s, const Where &w, int p0, int p, int k) {
+    return KIND != kPlanar ? (w.c - w.slab0 + k) * tile_row<true>(s) + p - p0
+                           : (p - p0 + k) * tile_row<false>(s) + w.c - w.slab0;
 }
 
 // ------------------------------------------------------------- reductions
 // Sum of each channel over the block's pixels: thread values v[V] (NHWC: V
-// channels; NCHW: v[0] of one channel, zero where the thread owns none) ->
+// channels; NCHW: v[0] of one channel; zero where the thread owns none) ->
 // out[slabC] in LDS. `lds` holds threads * V floats (NHWC) and then
 // max(threads, slabC).
 template <int V, bool CL>
@@ -190,16 +221,24 @@ __device__ __forceinline__ void channel_sum(const float (&v)[CL ? V : 1], const 
     float *const lds2 = lds + (CL ? T * V : 0);
     int Q;
     if constexpr (CL) {
-        const int row = s.tc * V;
-        if (w.tp < s.tp)
+        const int nc = w.cend - w.slab0, nv = (nc + V - 1) / V, row = s.tc * V, last = (nv - 1) * V, shift = nv * V - nc;
+        if (w.tp < s.tp) {
+            if constexpr (V == 1) {
+                lds[w.tp * row + w.tc] = v[0];
+            } else {
 #pragma unroll
-            for (int k = 0; k < V; ++k) lds[w.tp * row + w.tc * V + k] = k < w.nc ? v[k] : 0.0f;
+                for (int k = 0; k < V; k += 4)
+                    *(float4 *)(lds + w.tp * row + w.tc * V + k) = float4{v[k], v[k + 1], v[k + 2], v[k + 3]};
+            }
+        }
         __syncthreads();
         Q = max(1, min(T / s.slabC, s.tp));
         for (int i = tid; i < s.slabC * Q; i += T) {
             const int q = i / s.slabC, c = i - q * s.slabC;
+            if (c >= nc) continue;
             float t = 0.0f;
-            for (int r = q; r < s.tp; r += Q) t += lds[r * row + c];
+            // the last column's vector starts `shift` channels early
+            for (int r = q; r < s.tp; r += Q) t += lds[r * row + c + (c >= last ? shift : 0)];
             lds2[c * Q + q] = t;
         }
     } else {
@@ -238,8 +277,8 @@ __device__ __forceinline__ void groups_of_channels(const NormGeo &g, const NormS
     }
 }
 
-// Sum over the block of each of its K groups -> tot[K] in LDS. Ends with a
-// barrier; `lds` as for channel_sum, then slabC floats.
+// Sum over the block of each of its K groups -> tot[K] in LDS, from values that
+// are zero where a thread owns none. Ends with a barrier; `lds` as for channel_sum.
 template <int V, int KIND>
 __device__ __forceinline__ void group_sum(const float (&v)[group_values<V, KIND>()], const NormGeo &g,
                                           const NormShape &s, const Where &w, float *lds, float *tot) {
@@ -248,7 +287,7 @@ __device__ __forceinline__ void group_sum(const float (&v)[group_values<V, KIND>
         float u = 0.0f;
 #pragma unroll
         for (int k = 0; k < group_values<V, KIND>(); ++k)
-            if (k < w.nc) u += v[k];
+            u += v[k];
         u = wave_sum(u);
         if (lane == 0) lds[wave] = u;
         __syncthreads();
@@ -257,11 +296,31 @@ __device__ __forceinline__ void group_sum(const float (&v)[group_values<V, KIND>
             if (lane == 0) tot[0] = u;
         }
     } else if constexpr (KIND == kStraddle) {
-        float *chan = lds + blockDim.x * V + max((int)blockDim.x, s.slabC);
-        channel_sum<V, true>(v, s, w, lds, chan);
-        groups_of_channels(g, s, w, [&](int c) { return chan[c]; }, tot, 1);
+        // each thread's values by group, the j-th of its groups in its slot j
+        const auto start = [&](int col) { return min(col * V, s.slabC - V); };
+        const int S = min((V - 1) / g.cpg + 2, V), c0 = start(w.tc), first = c0 / g.cpg;
+        for (int j = 0; j < S; ++j) {
+            const int a = (first + j) * g.cpg - c0;  // values [a, a + cpg) are of the group
+            float u = 0.0f;
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                if (k >= a && k < a + g.cpg) u += v[k];
+            lds[tid * S + j] = u;
+        }
+        __syncthreads();
+        for (int k = wave; k < s.K; k += nw) {
+            // columns that own values of group k
+            const int a = k * g.cpg / V, n = ((k + 1) * g.cpg - 1) / V - a + 1;
+            float t = 0.0f;
+            for (int i = lane; i < n * s.tp; i += 64) {
+                const int r = i / n, col = a + i - r * n;
+                t += lds[(r * s.tc + col) * S + k - start(col) / g.cpg];
+            }
+            t = wave_sum(t);
+            if (lane == 0) tot[k] = t;
+        }
     } else {
-        lds[tid] = w.nc ? v[0] : 0.0f;
+        lds[tid] = v[0];
         __syncthreads();
         constexpr bool CL = KIND == kUniform;
         const int per = CL ? g.cpg / V : g.cpg * s.tp;  // a row of one group's threads
@@ -279,31 +338,33 @@ __device__ __forceinline__ void group_sum(const float (&v)[group_values<V, KIND>
     __syncthreads();
 }
 
-// Group, counted from the block's first, of the thread's k-th value.
+// Groups, counted from the block's first, of the thread's channels.
 template <int V, int KIND>
-__device__ __forceinline__ int group_of(const NormGeo &g, const NormShape &s, const Where &w, int k) {
-    if (s.J > 1) return 0;
-    const int c = w.c - w.slab0 + (KIND == kStraddle ? k : 0);
-    return min(c / g.cpg, s.K - 1);
+__device__ __forceinline__ void groups_of(int *kg, const NormGeo &g, const NormShape &s, const Where &w) {
+    const int c = w.c - w.slab0;
+    int k = s.J > 1 ? 0 : c / g.cpg, left = s.J > 1 ? V + 1 : g.cpg - (c - k * g.cpg);
+#pragma unroll
+    for (int i = 0; i < thread_channels<V, KIND>(); ++i) {
+        kg[i] = k;
+        if (KIND == kStraddle && --left == 0) {
+            ++k;
+            left = g.cpg;
+        }
+    }
 }
 
-// Values of a per-channel array for this thread's channels (1 for NCHW).
-template <int V, bool CL>
-__device__ __forceinline__ void per_channel(float (&r)[CL ? V : 1], const float *a, int64_t at, int nc,
-                                            float none) {
+// Values of a per-channel array for this thread's channels.
+template <int V, int KIND>
+__device__ __forceinline__ void per_channel(float *r, const float *a, int64_t at, float none) {
 #pragma unroll
-    for (int k = 0; k < (CL ? V : 1); ++k) r[k] = a && k < nc ? a[at + k] : none;
+    for (int k = 0; k < thread_channels<V, KIND>(); ++k) r[k] = a ? a[at + k] : none;
 }
 
 // -------------------------------------------------------------- launching
-// Floats of LDS that group_sum or channel_sum takes, without their results.
-inline int sum_floats(const NormShape &s, int kind) {
-    return (kind == kPlanar ? 0 : s.threads * s.V) + (s.threads > s.slabC ? s.threads : s.slabC);
-}
-
 template <typename T>
 size_t tile_lds(const NormShape &s, bool cl) {
-    return (size_t)(cl ? s.tc * s.V : s.window) * ((cl ? s.window : s.slabC) + 2) * sizeof(T);
+    const int window = s.tsteps * s.window;
+    return (size_t)(cl ? s.slabC : window) * ((cl ? window : s.slabC) + 2) * sizeof(T);
 }
 
 // Calls run<XT, YT, V, KIND, CROSS, SPLIT, E>() for the plan's types, layouts
@@ -326,7 +387,8 @@ template <bool BWD, typename XT, typename YT, typename R>
 void pick_vector(const NormGeo &g, const R &run) {
     const NormShape &s = BWD ? g.b : g.f;
     constexpr int VM = norm_max_vec(sizeof(XT), sizeof(YT));
-    if (!g.x_nhwc) return pick_steps<BWD, XT, YT, VM, kPlanar>(g, run);
+    if (!g.x_nhwc) return s.V == 1 ? pick_steps<BWD, XT, YT, 1, kPlanar>(g, run) : pick_steps<BWD, XT, YT, VM, kPlanar>(g, run);
+    if (s.V == 1) return pick_steps<BWD, XT, YT, 1, kUniform>(g, run);
     if (g.cpg % s.V != 0) return pick_steps<BWD, XT, YT, VM, kStraddle>(g, run);
     if constexpr (VM == 8)
         if (s.V == 8) return pick_steps<BWD, XT, YT, 8, kUniform>(g, run);

@@ -51,124 +51,211 @@ __device__ __forceinline__ void join_stats(const NormGeo &g, const NormPtrs &a, 
     rstd = 1.0f / sqrtf(wave_sum(t) / m + g.eps);
 }
 
-template <typename XT, typename YT, int V, int KIND, bool CROSS, int E, int MODE>
-__global__ __launch_bounds__(MODE == kFused ? 1024 : kNormSplitThreads) void k_norm_fwd(NormGeo g, NormPtrs a) {
+// What remains of the fused and of the output kernel: z = (v - mean) rstd gamma
+// + beta as one fma, the activation, and the vectors' way out. first: the step
+// that f[0] holds.
+template <typename XT, typename YT, int V, int KIND, bool CROSS, int E>
+__device__ __forceinline__ void write_out(const Vec<XT, V> (&f)[E], const float *off, const float *sc, const float *be,
+                                          const NormGeo &g, const Where &w, YT *y, int first, YT *tile) {
     constexpr bool CL = KIND != kPlanar;
-    constexpr int NC = CL ? V : 1, NG = group_values<V, KIND>();
-    extern __shared__ __align__(16) char smem[];
     const NormShape &s = g.f;
-    float *const gstat = (float *)smem, *const red = gstat + 2 * s.K;  // means, then M2 or rstd
-    const Where w = locate<V, CL>(g, s, xcd_block(blockIdx.x, gridDim.x));
-    const XT *x = (const XT *)a.x;
-    YT *y = (YT *)a.y;
-
-    Vec<XT, V> f[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        if (e < s.steps) {
-            const int p = pixel_of<V, CL>(s, w, e);
-            f[e] = load_part<XT, V, KIND>(addr<XT, V, CL>(x, g, g.xs, w.n, w.c, p), count_of<V, CL>(w, p));
-        }
-    }
-    float off[NC];  // shift, later shift - mean
-    per_channel<V, CL>(off, a.shift, (int64_t)w.n * g.C + w.c, w.nc, 0.0f);
-    const int64_t group0 = (int64_t)w.n * g.G + w.g0;
-
-    if constexpr (MODE != kApply) {
-        // values of a group in the block
-        const int chans = s.J == 1 ? g.cpg : w.cend - w.slab0;
-        const float cnt = (float)(w.pend - w.p0) * (float)chans;
-        float t[NG] = {};
+    with_act(g.act, [&](auto act) {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            if (e < s.steps) {
-                const int n = count_of<V, CL>(w, pixel_of<V, CL>(s, w, e));
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (k < n) t[NG == 1 ? 0 : k] += to_f32(f[e].v[k]) + off[CL ? k : 0];
-            }
-        group_sum<V, KIND>(t, g, s, w, red, gstat);
-        forget(f);
-        float mean[NG];
-#pragma unroll
-        for (int k = 0; k < NG; ++k) mean[k] = gstat[group_of<V, KIND>(g, s, w, k)] / cnt;
-#pragma unroll
-        for (int k = 0; k < NG; ++k) t[k] = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (e < s.steps) {
-                const int n = count_of<V, CL>(w, pixel_of<V, CL>(s, w, e));
+            if (first + e < s.steps) {
+                const Step at = step_of<V, KIND>(s, w, first + e);
+                Vec<YT, V> r;
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
-                    const float d = to_f32(f[e].v[k]) + off[CL ? k : 0] - mean[NG == 1 ? 0 : k];
-                    if (k < n) t[NG == 1 ? 0 : k] = fmaf(d, d, t[NG == 1 ? 0 : k]);
+                    const int kc = CL ? k : 0;
+                    r.v[k] = from_f32<YT>(act_fwd<decltype(act)::value>(fmaf(to_f32(f[e].v[k]) + off[kc], sc[kc], be[kc])));
+                }
+                if constexpr (!CROSS) {
+                    if (at.lo < V) store_vec<YT, V>(addr<YT, V, KIND>(y, g, g.ys, w, at.p), r);
+                } else {
+                    const int te = e % s.tsteps, p0 = w.p0 + (first + e - te) * s.window;
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        if (k >= at.lo) tile[tile_at<V, KIND>(s, w, p0, at.p, k)] = r.v[k];
+                    if (te == s.tsteps - 1 || e == E - 1 || first + e == s.steps - 1) {
+                        __syncthreads();
+                        tile_to_global<YT, CL>(tile, y, g, s, w, g.ys, p0);
+                        __syncthreads();
+                    }
                 }
             }
-        group_sum<V, KIND>(t, g, s, w, red, gstat + s.K);
-        if constexpr (MODE == kFused) forget(f);
-        for (int k = threadIdx.x; k < s.K; k += blockDim.x) {
-            const float mu = gstat[k] / cnt, m2 = gstat[s.K + k];
-            if constexpr (MODE == kReduce) {
-                const int64_t at = (group0 + k) * (s.nchunk * s.J) + w.chunk * s.J + w.part;
-                a.part[2 * at] = mu;
-                a.part[2 * at + 1] = m2;
-            } else {
-                a.mean[group0 + k] = gstat[k] = mu;
-                a.rstd[group0 + k] = gstat[s.K + k] = 1.0f / sqrtf(m2 / cnt + g.eps);
+    });
+}
+
+// off = shift - mean, sc = rstd gamma, be = beta of the thread's channels;
+// gstat: the block's groups' means, then their rstd.
+template <int V, int KIND>
+__device__ __forceinline__ void scales(float *off, float *sc, float *be, const NormGeo &g, const NormPtrs &a, const Where &w,
+                                       const float *gstat) {
+    constexpr int NC = thread_channels<V, KIND>();
+    const NormShape &s = g.f;
+    per_channel<V, KIND>(sc, a.gamma, w.c, 1.0f);
+    per_channel<V, KIND>(be, a.beta, w.c, 0.0f);
+    int kg[NC];
+    groups_of<V, KIND>(kg, g, s, w);
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+        off[k] -= gstat[kg[k]];
+        sc[k] *= gstat[s.K + kg[k]];
+    }
+}
+
+// One pass: a block holds its groups' values in registers.
+template <typename XT, typename YT, int V, int KIND, bool CROSS, int E>
+__global__ __launch_bounds__(1024) void k_norm_fused(NormGeo g, NormPtrs a) {
+    constexpr int NC = thread_channels<V, KIND>(), NG = group_values<V, KIND>();
+    extern __shared__ __align__(16) char smem[];
+    const NormShape &s = g.f;
+    float *const red = (float *)smem, *const gstat = red + norm_sum_floats(s, KIND != kPlanar);  // means, then M2, then rstd
+    const Where w = locate<V, KIND>(g, s);
+
+    Vec<XT, V> f[E];
+    load_steps<XT, V, KIND, E>(f, (const XT *)a.x, g, s, g.xs, w, 0);
+    float off[NC];
+    per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, 0.0f);
+    const float cnt = (float)((double)g.P * g.cpg);
+    float t[NG] = {};
+    for_owned<V, KIND, E>(s, w, 0, [&](int e, int k) { t[NG == 1 ? 0 : k] += to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k]; });
+    group_sum<V, KIND>(t, g, s, w, red, gstat);
+    if constexpr (!keeps_derived(V, E, KIND)) forget(f);
+    int kg[NC];
+    groups_of<V, KIND>(kg, g, s, w);
+    float mean[NG];
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+        mean[k] = gstat[kg[k]] / cnt;
+        t[k] = 0.0f;
+    }
+    for_owned<V, KIND, E>(s, w, 0, [&](int e, int k) {
+        const float d = to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k] - mean[NG == 1 ? 0 : k];
+        t[NG == 1 ? 0 : k] = fmaf(d, d, t[NG == 1 ? 0 : k]);
+    });
+    group_sum<V, KIND>(t, g, s, w, red, gstat + s.K);
+    if constexpr (!keeps_derived(V, E, KIND)) forget(f);
+    const int64_t group0 = (int64_t)w.n * g.G + w.g0;
+    for (int k = threadIdx.x; k < s.K; k += blockDim.x) {
+        a.mean[group0 + k] = gstat[k] = gstat[k] / cnt;
+        a.rstd[group0 + k] = gstat[s.K + k] = 1.0f / sqrtf(gstat[s.K + k] / cnt + g.eps);
+    }
+    __syncthreads();
+    float sc[NC], be[NC];
+    scales<V, KIND>(off, sc, be, g, a, w, gstat);
+    if constexpr (CROSS) __syncthreads();  // the tile takes the statistics' place
+    write_out<XT, YT, V, KIND, CROSS, E>(f, off, sc, be, g, w, (YT *)a.y, 0, (YT *)smem);
+}
+
+// Split, first kernel: mean and M2 of each of the block's groups over its
+// pixels. A thread sums d and d^2 of d = v - pivot, the pivot the mean of its
+// own first B values. M2 = sum d^2 - (sum d)^2 / n then loses little however
+// large the mean is: with the thread's true mean off the pivot by D, the first
+// B values alone make M2 >= B D^2, so what is subtracted, n D^2, is at most
+// n / B times the result. Threads are joined about the block's mean.
+template <typename XT, int V, int KIND, int E>
+__global__ __launch_bounds__(kNormSplitThreads) void k_norm_stats(NormGeo g, NormPtrs a) {
+    constexpr int NC = thread_channels<V, KIND>(), NG = group_values<V, KIND>();
+    extern __shared__ __align__(16) char smem[];
+    const NormShape &s = g.f;
+    float *const red = (float *)smem, *const gstat = red + norm_sum_floats(s, KIND != kPlanar);
+    const Where w = locate<V, KIND>(g, s);
+    float off[NC];
+    per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, 0.0f);
+
+    // values per sum; by channel where a thread's channels are kept apart
+    float have = 0.0f;
+    float pivot[NG], s1[NG] = {}, s2[NG] = {};
+    for (int first = 0; first < s.steps; first += E) {
+        Vec<XT, V> f[E];
+        load_steps<XT, V, KIND, E>(f, (const XT *)a.x, g, s, g.xs, w, first);
+        float more = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (first + e < s.steps) {
+                const int lo = step_of<V, KIND>(s, w, first + e).lo;
+                more += KIND == kStraddle ? (lo < V ? 1.0f : 0.0f) : (float)(V - lo);
             }
+        if (first == 0) {
+            float t[NG] = {};
+            for_owned<V, KIND, E>(s, w, 0, [&](int e, int k) { t[NG == 1 ? 0 : k] += to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k]; });
+            const float inv = 1.0f / fmaxf(more, 1.0f);
+#pragma unroll
+            for (int k = 0; k < NG; ++k) pivot[k] = t[k] * inv;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) off[k] -= pivot[NG == 1 ? 0 : k];
         }
-    } else {
-        for (int k = threadIdx.x >> 6; k < s.K; k += blockDim.x >> 6) {
-            float mu, r;
-            join_stats(g, a, group0 + k, mu, r);
-            if ((threadIdx.x & 63) == 0) {
-                gstat[k] = mu;
-                gstat[s.K + k] = r;
-                if (w.chunk == 0 && w.part == 0) {
-                    a.mean[group0 + k] = mu;
-                    a.rstd[group0 + k] = r;
-                }
+        have += more;
+        for_owned<V, KIND, E>(s, w, first, [&](int e, int k) {
+            const int kk = NG == 1 ? 0 : k;
+            const float d = to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k];
+            s1[kk] += d;
+            s2[kk] = fmaf(d, d, s2[kk]);
+        });
+    }
+    const int chans = s.J == 1 ? g.cpg : w.cend - w.slab0;
+    const float cnt = (float)(w.pend - w.p0) * (float)chans, inv = 1.0f / fmaxf(have, 1.0f);
+    // nothing of what others own, in any value
+    float t[NG], mean[NG], n[NG];
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+        n[k] = KIND == kStraddle && k < w.lo ? 0.0f : have;
+        mean[k] = fmaf(s1[k], inv, pivot[k]);
+        t[k] = n[k] > 0.0f ? mean[k] * n[k] : 0.0f;
+    }
+    group_sum<V, KIND>(t, g, s, w, red, gstat);
+    int kg[NC];
+    groups_of<V, KIND>(kg, g, s, w);
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+        const float d = mean[k] - gstat[kg[k]] / cnt;
+        const float m2 = fmaf(-s1[k], s1[k] * inv, s2[k]);
+        t[k] = n[k] > 0.0f ? fmaf(d * d, n[k], m2) : 0.0f;
+    }
+    group_sum<V, KIND>(t, g, s, w, red, gstat + s.K);
+    const int64_t group0 = (int64_t)w.n * g.G + w.g0;
+    for (int k = threadIdx.x; k < s.K; k += blockDim.x) {
+        const int64_t at = (group0 + k) * (s.nchunk * s.J) + w.chunk * s.J + w.part;
+        a.part[2 * at] = gstat[k] / cnt;
+        a.part[2 * at + 1] = gstat[s.K + k];
+    }
+}
+
+// Split, second kernel: joins its groups' parts and writes y.
+template <typename XT, typename YT, int V, int KIND, bool CROSS, int E>
+__global__ __launch_bounds__(kNormSplitThreads) void k_norm_apply(NormGeo g, NormPtrs a) {
+    constexpr int NC = thread_channels<V, KIND>();
+    extern __shared__ __align__(16) char smem[];
+    const NormShape &s = g.f;
+    float *const gstat = (float *)smem;
+    const Where w = locate<V, KIND>(g, s);
+    const int64_t group0 = (int64_t)w.n * g.G + w.g0;
+    Vec<XT, V> f[E];
+    load_steps<XT, V, KIND, E>(f, (const XT *)a.x, g, s, g.xs, w, 0);
+    float off[NC], sc[NC], be[NC];
+    per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, 0.0f);
+    for (int k = threadIdx.x >> 6; k < s.K; k += kNormSplitThreads / 64) {
+        float mu, r;
+        join_stats(g, a, group0 + k, mu, r);
+        if ((threadIdx.x & 63) == 0) {
+            gstat[k] = mu;
+            gstat[s.K + k] = r;
+            if (w.chunk == 0 && w.part == 0) {
+                a.mean[group0 + k] = mu;
+                a.rstd[group0 + k] = r;
             }
         }
     }
-
-    if constexpr (MODE != kReduce) {
-        __syncthreads();
-        float sc[NC], be[NC];
-        per_channel<V, CL>(sc, a.gamma, w.c, w.nc, 1.0f);
-        per_channel<V, CL>(be, a.beta, w.c, w.nc, 0.0f);
-#pragma unroll
-        for (int k = 0; k < NC; ++k) {
-            const int gk = group_of<V, KIND>(g, s, w, k);
-            off[k] -= gstat[gk];
-            sc[k] *= gstat[s.K + gk];
-        }
-        if constexpr (CROSS) __syncthreads();  // the tile takes the statistics' place
-        with_act(g.act, [&](auto act) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (e < s.steps) {
-                    const int p = pixel_of<V, CL>(s, w, e), n = count_of<V, CL>(w, p);
-                    Vec<YT, V> r;
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const int kc = CL ? k : 0;
-                        const float z = fmaf(to_f32(f[e].v[k]) + off[kc], sc[kc], be[kc]);
-                        r.v[k] = from_f32<YT>(act_fwd<decltype(act)::value>(z));
-                    }
-                    if constexpr (!CROSS) {
-                        store_part<YT, V, KIND>((YT *)addr<YT, V, CL>(y, g, g.ys, w.n, w.c, p), r, n);
-                    } else {
-                        YT *tile = (YT *)smem;
-                        if (w.nc)
-#pragma unroll
-                            for (int k = 0; k < V; ++k) tile[tile_at<CL, V>(s, w, k)] = r.v[k];
-                        __syncthreads();
-                        tile_to_global<YT, CL>(tile, y, g, s, w, g.ys, w.p0 + e * s.window);
-                        __syncthreads();
-                    }
-                }
-        });
+    __syncthreads();
+    scales<V, KIND>(off, sc, be, g, a, w, gstat);
+    if constexpr (CROSS) __syncthreads();
+    for (int first = 0;;) {
+        write_out<XT, YT, V, KIND, CROSS, E>(f, off, sc, be, g, w, (YT *)a.y, first, (YT *)smem);
+        first += E;
+        if (first >= s.steps) break;
+        load_steps<XT, V, KIND, E>(f, (const XT *)a.x, g, s, g.xs, w, first);
     }
 }
 
@@ -181,15 +268,13 @@ struct RunForward {
     void operator()() const {
         const NormShape &s = g.f;
         const dim3 grid((unsigned)((int64_t)g.N * s.nslab * s.nchunk)), blk(s.threads);
-        const size_t red = (size_t)(2 * s.K + sum_floats(s, KIND) + (KIND == kStraddle ? s.slabC : 0)) * 4;
+        const size_t red = (size_t)(2 * s.K + norm_sum_floats(s, KIND != kPlanar)) * 4, stats = (size_t)2 * s.K * 4;
         const size_t tile = CROSS ? tile_lds<YT>(s, KIND != kPlanar) : 0;
-        const size_t both = red > tile ? red : tile, own = (size_t)2 * s.K * 4;
         if constexpr (!SPLIT) {
-            hipLaunchKernelGGL((k_norm_fwd<XT, YT, V, KIND, CROSS, E, kFused>), grid, blk, both, st, g, p);
+            hipLaunchKernelGGL((k_norm_fused<XT, YT, V, KIND, CROSS, E>), grid, blk, red > tile ? red : tile, st, g, p);
         } else {
-            hipLaunchKernelGGL((k_norm_fwd<XT, XT, V, KIND, false, E, kReduce>), grid, blk, red, st, g, p);
-            hipLaunchKernelGGL((k_norm_fwd<XT, YT, V, KIND, CROSS, E, kApply>), grid, blk, own > tile ? own : tile, st,
-                               g, p);
+            hipLaunchKernelGGL((k_norm_stats<XT, V, KIND, E>), grid, blk, red, st, g, p);
+            hipLaunchKernelGGL((k_norm_apply<XT, YT, V, KIND, CROSS, E>), grid, blk, stats > tile ? stats : tile, st, g, p);
         }
     }
 };

@@ -7,6 +7,7 @@
 
 #include <type_traits>
 
+#include "wq8_device.h"
 #include "wq8_ops_internal.h"
 
 namespace wq8 {
@@ -161,10 +162,22 @@ __device__ __forceinline__ void with_act(int act, F f) {
     }
 }
 
+// v of the lane that the DPP control names.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over the 64 lanes, in all of them.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int s = 32; s; s >>= 1) v += __shfl_xor(v, s);
-    return v;
+    v += dpp<kDppXor1>(v);
+    v += dpp<kDppXor2>(v);
+    v += dpp<kDppXor7>(v);  // the other half of 8: quads already agree
+    v += dpp<kDppXor8>(v);
+    const auto r16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r16[0]) + __uint_as_float(r16[1]);
+    const auto r32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r32[0]) + __uint_as_float(r32[1]);
 }
 
 }  // namespace wq8

@@ -39,7 +39,14 @@ struct NormShape {
     int steps;                // steps per block
     int split;                // 1: statistics and output in two kernels
     int chunk, nchunk;        // pixels per block, blocks along the pixels
+    int tsteps;               // steps whose windows change layout together in LDS
 };
+
+// Floats of LDS that the kernels' sums take, without their results: a row of
+// the vectors' values per thread (NHWC), and a value per thread or channel.
+constexpr int norm_sum_floats(const NormShape &s, bool nhwc) {
+    return (nhwc ? s.threads * s.V : 0) + (s.threads > s.slabC ? s.threads : s.slabC);
+}
 
 struct NormGeo {
     int N, C, P, G, cpg;

@@ -80,8 +80,8 @@ NormShape fused_shape(const NormGeo &g, int V, int K) {
     return s;
 }
 
-// Split shape: blocks of 256 threads, up to `most_steps` steps along the pixels.
-NormShape split_shape(const NormGeo &g, int V, int most_steps) {
+// Split shape: blocks of 256 threads that take `batch` steps at a time.
+NormShape split_shape(const NormGeo &g, int V, int batch, int xsz) {
     constexpr int T = kNormSplitThreads;
     NormShape s;
     memset(&s, 0, sizeof s);
@@ -91,23 +91,24 @@ NormShape split_shape(const NormGeo &g, int V, int most_steps) {
     s.threads = T;
     s.split = 1;
     if (g.x_nhwc) {
-        const int across = ceil_div(g.cpg, V), most = kNormMaxSlab / V < T ? kNormMaxSlab / V : T;
+        const int across = ceil_div(g.cpg, V), most = kNormMaxSlab / V < T ? kNormMaxSlab / V : T;  // columns
         if (across > most) {
             s.slabC = ceil_div(across, ceil_div(across, most)) * V;
             s.J = ceil_div(g.cpg, s.slabC);
         } else {
-            // whole groups: the count that leaves the fewest lanes idle, the
-            // longest rows among equals
+            // whole groups: the first count of at least 256 bytes a row that keeps
+            // 7 of 8 lanes busy, else the most bytes, else the most lanes (more
+            // groups to a block are more parts for it to join)
             double best = -1;
             for (int k = 1; k <= g.G; ++k) {
                 const int vecs = ceil_div(k * g.cpg, V);
                 if (vecs > most) break;
-                if (g.G % k != 0) continue;
-                const double busy = (double)k * g.cpg / V * (T / vecs);
-                if (busy >= best) {
-                    best = busy;
-                    s.K = k;
-                }
+                if (g.G % k != 0 || k * g.cpg < V) continue;
+                const double busy = (double)k * g.cpg / V * (T / vecs) / T;
+                if (busy < best && busy < 0.875) continue;
+                best = busy;
+                s.K = k;
+                if (busy >= 0.875 && k * g.cpg * xsz >= 256) break;
             }
             s.slabC = s.K * g.cpg;
         }
@@ -127,28 +128,54 @@ NormShape split_shape(const NormGeo &g, int V, int most_steps) {
         s.window = s.tp * V;
     }
     s.nslab = g.G / s.K * s.J;
-    // fewer steps where the blocks would not fill the card
-    int steps = ceil_div(g.P, s.window);
-    if (steps > most_steps) steps = most_steps;
-    while (steps > 2 && (int64_t)g.N * s.nslab * ceil_div(g.P, steps * s.window) < 2 * kCus) --steps;
+    // blocks of a batch of steps, fewer where they would not fill the card, several
+    // batches where that still leaves 8 blocks a compute unit, the most that run at once
+    const int64_t rows = (int64_t)g.N * s.nslab;
+    const auto blocks = [&](int64_t steps) { return rows * ceil_div64(g.P, steps * s.window); };
+    int steps = batch;
+    while (steps > 2 && blocks(steps) < 2 * kCus) --steps;
+    while (steps >= batch && steps < ceil_div(g.P, s.window) && blocks(steps + batch) >= 8 * kCus) steps += batch;
+    if (steps > ceil_div(g.P, s.window)) steps = ceil_div(g.P, s.window);
     s.steps = steps;
     s.chunk = s.steps * s.window;
     s.nchunk = ceil_div(g.P, s.chunk);
     return s;
 }
 
+// Steps whose windows fit 48 KiB of LDS (rows padded by two elements), one at
+// least: 1024 threads' vectors do.
+void set_tile_steps(const NormGeo &g, NormShape &s, int ysz, int batch) {
+    const auto bytes = [&](int64_t n) {
+        return (g.x_nhwc ? s.slabC * (n * s.window + 2) : n * s.window * (s.slabC + 2)) * ysz;
+    };
+    s.tsteps = 1;
+    while (s.tsteps < batch && s.tsteps < s.steps && bytes(s.tsteps + 1) <= 49152) ++s.tsteps;
+}
+
+// Whether some slab of whole groups, or of a group's part, holds a vector of V
+// channels and no more than a block may have.
+bool slab_holds(const NormGeo &g, int V) {
+    for (int k = 1; k <= g.G; ++k)
+        if (g.G % k == 0 && k * g.cpg >= V) return k == 1 || k * g.cpg <= kNormMaxSlab;
+    return false;
+}
+
 NormShape choose_norm(const NormGeo &g, int xsz, int ysz, bool backward) {
     const int vmax = norm_max_vec(xsz, ysz), most = norm_max_steps(backward);
-    // vectors within one group where the group's channels allow 8 bytes or more;
-    // else vectors that straddle groups, in slabs of whole vectors
+    // single values where no row holds a vector
+    const bool single = g.x_nhwc ? !slab_holds(g, vmax) : g.P < vmax;
+    // vectors within one group where the group's channels allow 8 bytes or more,
+    // else vectors that straddle groups
     int V = vmax;
     while (g.x_nhwc && V > 4 && g.cpg % V != 0) V /= 2;
     if (g.x_nhwc && g.cpg % V != 0) V = vmax;
+    if (single) V = 1;
     NormShape s;
     s.steps = 1 << 30;
     for (int k = 1; k <= g.G; ++k) {
-        if (g.G % k != 0) continue;
-        if (g.x_nhwc && k * g.cpg % V != 0 && k < g.G) continue;
+        // whole vectors across the slab, nearly
+        const int vecs = ceil_div(k * g.cpg, V) * V;
+        if (g.G % k != 0 || (g.x_nhwc && k < g.G && k * g.cpg * 8 < vecs * 7) || (g.x_nhwc && k * g.cpg < V)) continue;
         const NormShape t = fused_shape(g, V, k);
         if (t.steps > most) break;
         // wider slabs (longer contiguous rows) while the card stays full
@@ -158,9 +185,14 @@ NormShape choose_norm(const NormGeo &g, int xsz, int ysz, bool backward) {
     if (s.steps <= most) {
         // a block holds a group: one pass, if there are blocks enough or little to do
         const int64_t blocks = (int64_t)g.N * s.nslab, values = (int64_t)g.P * s.slabC;
-        if (blocks >= kCus / 2 || values <= 16384) return s;
+        if (blocks >= kCus / 2 || values <= 16384) {
+            set_tile_steps(g, s, ysz, s.steps);
+            return s;
+        }
     }
-    return split_shape(g, vmax, norm_split_steps(backward));
+    s = split_shape(g, single ? 1 : vmax, norm_split_steps(backward), xsz);
+    set_tile_steps(g, s, ysz, norm_split_steps(backward));
+    return s;
 }
 
 wq8_status build_norm(const wq8_norm_desc *d, wq8_norm_plan *p) {
