@@ -42,7 +42,7 @@ __device__ __forceinline__ void load_dy(Vec<YT, V> (&f)[E], const YT *dy, const 
     } else {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            if (first + e < s.steps) {
+            if (first + e < s.steps) {  // uniform: the tile's barriers
                 const int te = e % s.tsteps;
                 if (te == 0) {
                     if (e > 0) __syncthreads();
@@ -63,10 +63,11 @@ template <typename XT, typename YT, int V, int KIND, int E>
 __device__ __forceinline__ void add_sums(float *s1, float *s2, float *s3, const Vec<XT, V> (&fx)[E], const Vec<YT, V> (&fd)[E],
                                          const Channels<V, KIND> &c, const NormGeo &g, const Where &w, int first) {
     with_act(g.act, [&](auto act) {
-        for_owned<V, KIND, E>(g.b, w, first, [&](int e, int k) {
+        for_values<V, KIND, E>(g.b, w, first, [&](int e, int k, auto ok) {
             const int kc = c.NC == 1 ? 0 : k;
-            const float h = (to_f32(fx[e].v[k]) + c.off[kc]) * c.rstd[c.NG == 1 ? 0 : k];
-            const float dz = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value>(fmaf(h, c.ga[kc], c.be[kc]));
+            const float hv = (to_f32(fx[e].v[k]) + c.off[kc]) * c.rstd[c.NG == 1 ? 0 : k], h = ok ? hv : 0.0f;
+            const float dv = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value>(fmaf(h, c.ga[kc], c.be[kc]));
+            const float dz = ok ? dv : 0.0f;
             s1[kc] += dz;
             s2[kc] = fmaf(dz, h, s2[kc]);
             s3[kc] += h;
@@ -77,13 +78,15 @@ __device__ __forceinline__ void add_sums(float *s1, float *s2, float *s3, const 
 // Joins the threads' sums: the channels' into `part`, the groups' weighted
 // totals into gm[2 K].
 template <int V, int KIND>
-__device__ __forceinline__ void join_sums(const float (&s1)[thread_channels<V, KIND>()],
-                                          const float (&s2)[thread_channels<V, KIND>()],
-                                          const float (&s3)[thread_channels<V, KIND>()], const NormGeo &g, const NormPtrs &a,
-                                          const Where &w, float *red, float *gm) {
+__device__ __forceinline__ void join_sums(const NormGeo &g, const NormPtrs &a, const Where &w,
+                                          float (&s1)[Channels<V, KIND>::NC], float (&s2)[Channels<V, KIND>::NC],
+                                          float (&s3)[Channels<V, KIND>::NC], float *red, float *gm) {
     constexpr bool CL = KIND != kPlanar;
     const NormShape &s = g.b;
     float *const c1 = gm + 2 * s.K, *const c2 = c1 + s.slabC;
+    drop_unowned<V, KIND>(w, s1);
+    drop_unowned<V, KIND>(w, s2);
+    drop_unowned<V, KIND>(w, s3);
     channel_sum<V, CL>(s1, s, w, red, c1);
     channel_sum<V, CL>(s2, s, w, red, c2);
     const auto weight = [&](int c) { return a.gamma ? a.gamma[w.slab0 + c] : 1.0f; };
@@ -163,7 +166,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_fused(NormGeo g, NormPtrs a) 
         forget(fx);
         forget(fd);
     }
-    join_sums<V, KIND>(s1, s2, s3, g, a, w, red, gm);
+    join_sums<V, KIND>(g, a, w, s1, s2, s3, red, gm);
     const int64_t group0 = (int64_t)w.n * g.G + w.g0;
     for (int k = threadIdx.x; k < 2 * s.K; k += blockDim.x)
         a.group[2 * group0 + k] = gm[k] = gm[k] / (float)((double)g.P * g.cpg);
@@ -191,7 +194,7 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_bwd_sums(NormGeo g, 
         load_dy<YT, V, KIND, CROSS, E>(fd, (const YT *)a.dy, g, w, first, (YT *)smem);
         add_sums<XT, YT, V, KIND, E>(s1, s2, s3, fx, fd, c, g, w, first);
     }
-    join_sums<V, KIND>(s1, s2, s3, g, a, w, red, gm);
+    join_sums<V, KIND>(g, a, w, s1, s2, s3, red, gm);
     const int64_t group0 = (int64_t)w.n * g.G + w.g0;
     for (int k = threadIdx.x; k < 2 * s.K; k += blockDim.x) {
         const int64_t at = (group0 + k / 2) * (s.nchunk * s.J) + w.chunk * s.J + w.part;

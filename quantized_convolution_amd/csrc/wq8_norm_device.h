@@ -99,32 +99,44 @@ __device__ __forceinline__ T *addr(T *x, const NormGeo &g, int64_t stride, const
     return KIND != kPlanar ? x + ((int64_t)w.n * g.P + p) * stride + w.c : x + ((int64_t)w.n * g.C + w.c) * g.P + p;
 }
 
-// The thread's vectors of E steps from step `first`.
+// The thread's vectors of E steps from step `first`. Steps past the block's last
+// one load its last vector again: a load under a condition would be waited for
+// before the next one is sent.
 template <typename T, int V, int KIND, int E>
 __device__ __forceinline__ void load_steps(Vec<T, V> (&f)[E], const T *x, const NormGeo &g, const NormShape &s, int64_t stride,
                                            const Where &w, int first) {
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        if (first + e < s.steps)
-            f[e] = load_vec<T, V>(addr<const T, V, KIND>(x, g, stride, w, step_of<V, KIND>(s, w, first + e).p));
+        f[e] = load_vec<T, V>(addr<const T, V, KIND>(x, g, stride, w, step_of<V, KIND>(s, w, first + e).p));
 }
 
-// f(e, k) for the values that the thread owns in E steps from step `first`.
+// f(e, k, ok) for the values of E steps from step `first`; ok: the value exists
+// and no other thread's vector has it. Where the steps end before the block's
+// pixels do, ok is the constant true, also for threads and channels that own
+// nothing: drop_unowned() clears what they have summed.
 template <int V, int KIND, int E, typename F>
-__device__ __forceinline__ void for_owned(const NormShape &s, const Where &w, int first, F f) {
+__device__ __forceinline__ void for_values(const NormShape &s, const Where &w, int first, F f) {
+    if (w.p0 + (first + E) * s.window <= w.pend) {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (first + e < s.steps) {
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int k = 0; k < V; ++k) f(e, k, std::true_type{});
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
             const int lo = step_of<V, KIND>(s, w, first + e).lo;
-            if (lo == 0) {
 #pragma unroll
-                for (int k = 0; k < V; ++k) f(e, k);
-            } else if (KIND != kUniform && lo < V) {
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (k >= lo) f(e, k);
-            }
+            for (int k = 0; k < V; ++k) f(e, k, k >= lo);
         }
+    }
+}
+
+// Sums of what the thread does not own: nothing.
+template <int V, int KIND, int N>
+__device__ __forceinline__ void drop_unowned(const Where &w, float (&sum)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (N == 1 ? w.lo == V || (KIND == kPlanar && w.lo) : k < w.lo) sum[k] = 0.0f;
 }
 
 // Whether there are registers to keep what one pass over the values derived
@@ -356,8 +368,13 @@ __device__ __forceinline__ void groups_of(int *kg, const NormGeo &g, const NormS
 // Values of a per-channel array for this thread's channels.
 template <int V, int KIND>
 __device__ __forceinline__ void per_channel(float *r, const float *a, int64_t at, float none) {
+    constexpr int NC = thread_channels<V, KIND>();
+    Vec<float, NC> v;
 #pragma unroll
-    for (int k = 0; k < thread_channels<V, KIND>(); ++k) r[k] = a ? a[at + k] : none;
+    for (int k = 0; k < NC; ++k) v.v[k] = none;
+    if (a) v = load_vec<float, NC>(a + at);
+#pragma unroll
+    for (int k = 0; k < NC; ++k) r[k] = v.v[k];
 }
 
 // -------------------------------------------------------------- launching
@@ -380,7 +397,8 @@ void pick_steps(const NormGeo &g, const R &run) {
     };
     if (s.split) go(std::true_type{}, std::integral_constant<int, norm_split_steps(BWD)>{});
     else if (s.steps <= kNormE) go(std::false_type{}, std::integral_constant<int, kNormE>{});
-    else go(std::false_type{}, std::integral_constant<int, norm_max_steps(BWD)>{});
+    else if (s.steps <= 2 * kNormE) go(std::false_type{}, std::integral_constant<int, 2 * kNormE>{});
+    else if constexpr (norm_max_steps(BWD) > 2 * kNormE) go(std::false_type{}, std::integral_constant<int, norm_max_steps(BWD)>{});
 }
 
 template <bool BWD, typename XT, typename YT, typename R>

@@ -120,7 +120,11 @@ __global__ __launch_bounds__(1024) void k_norm_fused(NormGeo g, NormPtrs a) {
     per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, 0.0f);
     const float cnt = (float)((double)g.P * g.cpg);
     float t[NG] = {};
-    for_owned<V, KIND, E>(s, w, 0, [&](int e, int k) { t[NG == 1 ? 0 : k] += to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k]; });
+    for_values<V, KIND, E>(s, w, 0, [&](int e, int k, auto ok) {
+        const float v = to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k];
+        t[NG == 1 ? 0 : k] += ok ? v : 0.0f;
+    });
+    drop_unowned<V, KIND>(w, t);
     group_sum<V, KIND>(t, g, s, w, red, gstat);
     if constexpr (!keeps_derived(V, E, KIND)) forget(f);
     int kg[NC];
@@ -131,10 +135,11 @@ __global__ __launch_bounds__(1024) void k_norm_fused(NormGeo g, NormPtrs a) {
         mean[k] = gstat[kg[k]] / cnt;
         t[k] = 0.0f;
     }
-    for_owned<V, KIND, E>(s, w, 0, [&](int e, int k) {
-        const float d = to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k] - mean[NG == 1 ? 0 : k];
+    for_values<V, KIND, E>(s, w, 0, [&](int e, int k, auto ok) {
+        const float v = to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k] - mean[NG == 1 ? 0 : k], d = ok ? v : 0.0f;
         t[NG == 1 ? 0 : k] = fmaf(d, d, t[NG == 1 ? 0 : k]);
     });
+    drop_unowned<V, KIND>(w, t);
     group_sum<V, KIND>(t, g, s, w, red, gstat + s.K);
     if constexpr (!keeps_derived(V, E, KIND)) forget(f);
     const int64_t group0 = (int64_t)w.n * g.G + w.g0;
@@ -173,14 +178,16 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_stats(NormGeo g, Nor
         load_steps<XT, V, KIND, E>(f, (const XT *)a.x, g, s, g.xs, w, first);
         float more = 0.0f;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (first + e < s.steps) {
-                const int lo = step_of<V, KIND>(s, w, first + e).lo;
-                more += KIND == kStraddle ? (lo < V ? 1.0f : 0.0f) : (float)(V - lo);
-            }
+        for (int e = 0; e < E; ++e) {
+            const int lo = step_of<V, KIND>(s, w, first + e).lo;
+            more += KIND == kStraddle ? (lo < V ? 1.0f : 0.0f) : (float)(V - lo);
+        }
         if (first == 0) {
             float t[NG] = {};
-            for_owned<V, KIND, E>(s, w, 0, [&](int e, int k) { t[NG == 1 ? 0 : k] += to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k]; });
+            for_values<V, KIND, E>(s, w, 0, [&](int e, int k, auto ok) {
+                const float v = to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k];
+                t[NG == 1 ? 0 : k] += ok ? v : 0.0f;
+            });
             const float inv = 1.0f / fmaxf(more, 1.0f);
 #pragma unroll
             for (int k = 0; k < NG; ++k) pivot[k] = t[k] * inv;
@@ -188,9 +195,9 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_stats(NormGeo g, Nor
             for (int k = 0; k < NC; ++k) off[k] -= pivot[NG == 1 ? 0 : k];
         }
         have += more;
-        for_owned<V, KIND, E>(s, w, first, [&](int e, int k) {
+        for_values<V, KIND, E>(s, w, first, [&](int e, int k, auto ok) {
             const int kk = NG == 1 ? 0 : k;
-            const float d = to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k];
+            const float v = to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k], d = ok ? v : 0.0f;
             s1[kk] += d;
             s2[kk] = fmaf(d, d, s2[kk]);
         });

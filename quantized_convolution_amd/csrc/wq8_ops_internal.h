@@ -14,7 +14,7 @@ constexpr int kCus = 256;
 // ------------------------------------------------------------- group norm
 constexpr int kNormMaxSlab = 1024;  // channels per block
 
-constexpr int kNormE = 4;            // steps unrolled by the short fused kernels
+constexpr int kNormE = 4;            // steps unrolled by the short fused kernels, twice that by the middle ones
 // By the split kernels: 8 vectors in flight per thread.
 constexpr int norm_split_steps(bool backward) { return backward ? 4 : 8; }
 
