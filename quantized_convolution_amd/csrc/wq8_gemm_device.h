@@ -198,7 +198,8 @@ __device__ __forceinline__ void mma(f32x4 &acc, const Frag<float> &n, const Frag
     acc = __builtin_amdgcn_mfma_f32_16x16x4f32(n.v[e], m.v[e], acc, 0, 0, 0);
 }
 
-// EPI: epilogue(m, n, 8 sums of columns n.., how many of them exist).
+// EPI: run(each) calls each(f) once, and each calls f(m, n, 8 sums of columns
+// n.., how many of them exist) for all of a thread's sums.
 // DIRECT: whole k steps go from memory to LDS without registers; a last partial
 // one, and every one of operands that are not aligned for that, goes through
 // registers. Two buffers: while one is multiplied the other is filled.
@@ -280,21 +281,28 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(GemmArgs a, EPI epi) {
         }
     }
 
+    const auto each = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int m = m0 + wm + i * 16 + (lane & 15);
-        if (m >= a.M) continue;
+        for (int i = 0; i < TM; ++i) {
+            const int m = m0 + wm + i * 16 + (lane & 15);
+            if (m >= a.M) continue;
 #pragma unroll
-        for (int j = 0; j < TN; j += 2) {
-            const int n = n0 + wn + j * 16 + (lane >> 4) * 8, cnt = a.N - n;
-            if (cnt <= 0) continue;
-            Vec<float, 8> r;
+            for (int j = 0; j < TN; j += 2) {
+                const int n = n0 + wn + j * 16 + (lane >> 4) * 8, cnt = a.N - n;
+                if (cnt <= 0) continue;
+                Vec<float, 8> r;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r.v[e] = acc[i][j + e / 4][e % 4];
-            if (a.partial) store_vec_n<float, 8>(a.partial + ((int64_t)split * a.M + m) * a.N + n, r, cnt);
-            else epi(m, n, r, cnt);
+                for (int e = 0; e < 8; ++e) r.v[e] = acc[i][j + e / 4][e % 4];
+                f(m, n, r, cnt);
+            }
         }
-    }
+    };
+    if (a.partial)
+        each([&](int m, int n, const Vec<float, 8> &r, int cnt) {
+            store_vec_n<float, 8>(a.partial + ((int64_t)split * a.M + m) * a.N + n, r, cnt);
+        });
+    else
+        epi.run(each);
 }
 
 // Joins split products, in the order of k, and runs the epilogue: a thread per
@@ -311,14 +319,7 @@ __global__ __launch_bounds__(256) void k_gemm_join(GemmArgs a, int splits, EPI e
 #pragma unroll
         for (int e = 0; e < 8; ++e) s.v[e] += v.v[e];
     }
-    epi(m, n, s, a.N - n);
-}
-
-// Whether an operand's steps can go to LDS directly.
-template <typename T, bool KC>
-bool direct_ok(int64_t ld, int rows) {
-    constexpr int U = 16 / sizeof(T);
-    return ld % U == 0 && (KC || rows % U == 0);
+    epi.run([&](auto f) { f(m, n, s, a.N - n); });
 }
 
 template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, typename EPI>
@@ -334,21 +335,29 @@ void run_tile(const GemmShape &s, GemmArgs a, const EPI &epi, float *partial, hi
             (void)hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         hipLaunchKernelGGL(kernel, grid, blk, bytes, st, a, epi);
     };
-    if (direct_ok<T, AKC>(a.lda, a.M) && direct_ok<T, BKC>(a.ldb, a.N))
+    if (s.direct) {
         go(k_gemm<T, AKC, BKC, BM, BN, WM, WN, true, EPI>);
-    else
-        go(k_gemm<T, AKC, BKC, BM, BN, WM, WN, false, EPI>);
+    } else {
+        // no registers for a step of the largest tile: the plan does not choose it
+        if constexpr (BM * BN < 256 * 256) go(k_gemm<T, AKC, BKC, BM, BN, WM, WN, false, EPI>);
+    }
     if (s.splits > 1) {
         const int64_t work = (int64_t)a.M * ((a.N + 7) / 8);
         hipLaunchKernelGGL((k_gemm_join<EPI>), dim3((unsigned)((work + 255) / 256)), dim3(256), 0, st, a, s.splits, epi);
     }
 }
 
+// The tiles of kGemmTiles, in its order.
 template <typename T, bool AKC, bool BKC, typename EPI>
 void run_gemm(const GemmShape &s, const GemmArgs &a, const EPI &epi, float *partial, hipStream_t st) {
     if (a.M == 0 || a.N == 0) return;
-    if (s.tile == 1) return run_tile<T, AKC, BKC, 256, 256, 2, 4>(s, a, epi, partial, st);
-    run_tile<T, AKC, BKC, 128, 128, 2, 2>(s, a, epi, partial, st);
+    switch (s.tile) {
+        case 0: return run_tile<T, AKC, BKC, 256, 256, 2, 4>(s, a, epi, partial, st);
+        case 1: return run_tile<T, AKC, BKC, 128, 128, 2, 2>(s, a, epi, partial, st);
+        case 2: return run_tile<T, AKC, BKC, 128, 64, 2, 2>(s, a, epi, partial, st);
+        case 3: return run_tile<T, AKC, BKC, 64, 64, 2, 2>(s, a, epi, partial, st);
+        default: return run_tile<T, AKC, BKC, 16, 128, 1, 2>(s, a, epi, partial, st);
+    }
 }
 
 }  // namespace

@@ -73,17 +73,20 @@ struct EpiStore {
     T *out;
     int64_t ld;
 
-    __device__ __forceinline__ void operator()(int m, int n, Vec<float, 8> v, int cnt) const {
-        Vec<T, 8> r;
+    template <typename EACH>
+    __device__ __forceinline__ void run(EACH each) const {
+        each([&](int m, int n, const Vec<float, 8> &v, int cnt) {
+            Vec<T, 8> r;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r.v[e] = from_f32<T>(v.v[e]);
-        store_vec_n<T, 8>(out + (int64_t)m * ld + n, r, cnt);
+            for (int e = 0; e < 8; ++e) r.v[e] = from_f32<T>(v.v[e]);
+            store_vec_n<T, 8>(out + (int64_t)m * ld + n, r, cnt);
+        });
     }
 };
 
 template <typename XT, typename YT>
 void backward(const LinearGeo &g, const LinearPtrs &p, hipStream_t st) {
-    constexpr int V = norm_max_vec(sizeof(XT), sizeof(YT));
+    constexpr int V = 16 / (sizeof(XT) > sizeof(YT) ? sizeof(XT) : sizeof(YT));
     if (g.M > 0 && (g.dz_own || p.dbias)) {
         const int ncol = (g.N + 64 * V - 1) / (64 * V);
         const dim3 grid((unsigned)((int64_t)ncol * g.dz_nchunk));

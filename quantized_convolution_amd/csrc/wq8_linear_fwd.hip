@@ -3,13 +3,6 @@
 
 namespace wq8 {
 
-void gemm_tile_size(int t, int *bm, int *bn) {
-    *bm = t == 1 ? 256 : 128;
-    *bn = t == 1 ? 256 : 128;
-}
-
-int gemm_kstep(wq8_dtype t) { return t == WQ8_F32 ? 32 : 64; }
-
 namespace {
 
 template <typename YT>
@@ -20,7 +13,15 @@ struct EpiForward {
     int64_t ys, rs;
     int N, act, planar, pixels;
 
-    __device__ __forceinline__ void operator()(int m, int n, Vec<float, 8> v, int cnt) const {
+    template <typename EACH>
+    __device__ __forceinline__ void run(EACH each) const {
+        with_act(act, [&](auto a) {
+            each([&](int m, int n, Vec<float, 8> v, int cnt) { one<decltype(a)::value>(m, n, v, cnt); });
+        });
+    }
+
+    template <int ACT>
+    __device__ __forceinline__ void one(int m, int n, Vec<float, 8> v, int cnt) const {
         if (bias) {
             const Vec<float, 8> b = load_vec_n<float, 8>(bias + n, cnt);
 #pragma unroll
@@ -32,10 +33,8 @@ struct EpiForward {
             for (int e = 0; e < 8; ++e) r.v[e] = from_f32<YT>(v.v[e]);
             store_vec_n<YT, 8>(z + (int64_t)m * N + n, r, cnt);
         }
-        with_act(act, [&](auto a) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v.v[e] = act_fwd<decltype(a)::value>(v.v[e]);
-        });
+        for (int e = 0; e < 8; ++e) v.v[e] = act_fwd<ACT>(v.v[e]);
         if (residual) {
             if (planar) {
                 const int img = m / pixels, p = m - img * pixels;

@@ -1,5 +1,7 @@
-// Backward of the group norm with an activation (see wq8_norm_fwd.hip for the
+// Backward of the group norm with an activation (see wq8_norm_fwd.h for the
 // mathematics, the split and the layouts).
+#pragma once
+
 #include "wq8_norm_device.h"
 
 namespace wq8 {
@@ -59,11 +61,11 @@ __device__ __forceinline__ void load_dy(Vec<YT, V> (&f)[E], const YT *dy, const 
 }
 
 // Adds the steps' dz, dz h and h to the thread's sums.
-template <typename XT, typename YT, int V, int KIND, int E>
+template <typename XT, typename YT, int V, int KIND, int E, bool BATCH>
 __device__ __forceinline__ void add_sums(float *s1, float *s2, float *s3, const Vec<XT, V> (&fx)[E], const Vec<YT, V> (&fd)[E],
                                          const Channels<V, KIND> &c, const NormGeo &g, const Where &w, int first) {
     with_act(g.act, [&](auto act) {
-        for_values<V, KIND, E>(g.b, w, first, [&](int e, int k, auto ok) {
+        for_values<V, KIND, E, BATCH>(g.b, w, first, [&](int e, int k, auto ok) {
             const int kc = c.NC == 1 ? 0 : k;
             const float hv = (to_f32(fx[e].v[k]) + c.off[kc]) * c.rstd[c.NG == 1 ? 0 : k], h = ok ? hv : 0.0f;
             const float dv = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value>(fmaf(h, c.ga[kc], c.be[kc]));
@@ -161,7 +163,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_fused(NormGeo g, NormPtrs a) 
     Channels<V, KIND> c;
     c.load(g, a, w);
     float s1[NC] = {}, s2[NC] = {}, s3[NC] = {};
-    add_sums<XT, YT, V, KIND, E>(s1, s2, s3, fx, fd, c, g, w, 0);
+    add_sums<XT, YT, V, KIND, E, false>(s1, s2, s3, fx, fd, c, g, w, 0);
     if constexpr (!keeps_derived(V, E, KIND)) {
         forget(fx);
         forget(fd);
@@ -192,7 +194,7 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_bwd_sums(NormGeo g, 
         Vec<YT, V> fd[E];
         load_steps<XT, V, KIND, E>(fx, (const XT *)a.x, g, s, g.xs, w, first);
         load_dy<YT, V, KIND, CROSS, E>(fd, (const YT *)a.dy, g, w, first, (YT *)smem);
-        add_sums<XT, YT, V, KIND, E>(s1, s2, s3, fx, fd, c, g, w, first);
+        add_sums<XT, YT, V, KIND, E, true>(s1, s2, s3, fx, fd, c, g, w, first);
     }
     join_sums<V, KIND>(g, a, w, s1, s2, s3, red, gm);
     const int64_t group0 = (int64_t)w.n * g.G + w.g0;
@@ -306,12 +308,10 @@ struct RunBackward {
     }
 };
 
-}  // namespace
-
-wq8_status launch_norm_backward(const NormGeo &g, wq8_dtype xdt, wq8_dtype ydt, const NormPtrs &p,
-                                void *stream) {
+template <typename XT>
+wq8_status norm_backward(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, void *stream) {
     const hipStream_t st = (hipStream_t)stream;
-    if (g.N > 0) pick_kernel<true>(g, xdt, ydt, RunBackward{g, p, st});
+    if (g.N > 0) pick_kernel<true, XT>(g, ydt, RunBackward{g, p, st});
     if (p.dgamma || p.dbeta || (p.dshift && g.N > 0)) {
         const int ncol = (g.C + 15) / 16, rows = p.dshift ? g.N + 1 : 1;
         hipLaunchKernelGGL(k_norm_params, dim3((unsigned)((int64_t)ncol * rows)), dim3(256), 0, st, g, p, ncol, !p.dshift);
@@ -319,4 +319,5 @@ wq8_status launch_norm_backward(const NormGeo &g, wq8_dtype xdt, wq8_dtype ydt, 
     return check_launch("group norm backward");
 }
 
+}  // namespace
 }  // namespace wq8

@@ -110,13 +110,14 @@ __device__ __forceinline__ void load_steps(Vec<T, V> (&f)[E], const T *x, const 
         f[e] = load_vec<T, V>(addr<const T, V, KIND>(x, g, stride, w, step_of<V, KIND>(s, w, first + e).p));
 }
 
-// f(e, k, ok) for the values of E steps from step `first`; ok: the value exists
-// and no other thread's vector has it. Where the steps end before the block's
-// pixels do, ok is the constant true, also for threads and channels that own
-// nothing: drop_unowned() clears what they have summed.
-template <int V, int KIND, int E, typename F>
+// f(e, k, ok) for the values of E steps from step `first`; ok: the value is one
+// of the block's, and in NCHW no other thread's vector has it. What a thread or
+// a channel that owns nothing has summed, drop_unowned() clears. BATCH: where
+// the steps end before the block's pixels do, ok is the constant true (two
+// copies of the code, too many registers where the values are held for more).
+template <int V, int KIND, int E, bool BATCH, typename F>
 __device__ __forceinline__ void for_values(const NormShape &s, const Where &w, int first, F f) {
-    if (w.p0 + (first + E) * s.window <= w.pend) {
+    if (BATCH && w.p0 + (first + E) * s.window <= w.pend) {
 #pragma unroll
         for (int e = 0; e < E; ++e)
 #pragma unroll
@@ -124,9 +125,11 @@ __device__ __forceinline__ void for_values(const NormShape &s, const Where &w, i
     } else {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int lo = step_of<V, KIND>(s, w, first + e).lo;
+            const int p = w.p0 + (first + e) * s.window + w.tp * (KIND == kPlanar ? V : 1);
+            const bool in = p < w.pend;
+            const int lo = KIND == kPlanar ? step_of<V, KIND>(s, w, first + e).lo : 0;
 #pragma unroll
-            for (int k = 0; k < V; ++k) f(e, k, k >= lo);
+            for (int k = 0; k < V; ++k) f(e, k, KIND == kPlanar ? k >= lo : in);
         }
     }
 }
@@ -395,16 +398,15 @@ void pick_steps(const NormGeo &g, const R &run) {
         if (g.x_nhwc != g.y_nhwc) run.template operator()<XT, YT, V, KIND, true, S, E>();
         else run.template operator()<XT, YT, V, KIND, false, S, E>();
     };
-    if (s.split) go(std::true_type{}, std::integral_constant<int, norm_split_steps(BWD)>{});
+    if (s.split) go(std::true_type{}, std::integral_constant<int, kNormE>{});
     else if (s.steps <= kNormE) go(std::false_type{}, std::integral_constant<int, kNormE>{});
-    else if (s.steps <= 2 * kNormE) go(std::false_type{}, std::integral_constant<int, 2 * kNormE>{});
-    else if constexpr (norm_max_steps(BWD) > 2 * kNormE) go(std::false_type{}, std::integral_constant<int, norm_max_steps(BWD)>{});
+    else go(std::false_type{}, std::integral_constant<int, norm_max_steps(BWD, KIND == kStraddle)>{});
 }
 
 template <bool BWD, typename XT, typename YT, typename R>
 void pick_vector(const NormGeo &g, const R &run) {
     const NormShape &s = BWD ? g.b : g.f;
-    constexpr int VM = norm_max_vec(sizeof(XT), sizeof(YT));
+    constexpr int VM = norm_max_vec(sizeof(XT), sizeof(YT), BWD);
     if (!g.x_nhwc) return s.V == 1 ? pick_steps<BWD, XT, YT, 1, kPlanar>(g, run) : pick_steps<BWD, XT, YT, VM, kPlanar>(g, run);
     if (s.V == 1) return pick_steps<BWD, XT, YT, 1, kUniform>(g, run);
     if (g.cpg % s.V != 0) return pick_steps<BWD, XT, YT, VM, kStraddle>(g, run);
@@ -413,15 +415,10 @@ void pick_vector(const NormGeo &g, const R &run) {
     pick_steps<BWD, XT, YT, 4, kUniform>(g, run);
 }
 
-template <bool BWD, typename R>
-void pick_kernel(const NormGeo &g, wq8_dtype xdt, wq8_dtype ydt, const R &run) {
-    if (xdt == WQ8_F32) {
-        if (ydt == WQ8_F32) pick_vector<BWD, float, float>(g, run);
-        else pick_vector<BWD, float, bf16_t>(g, run);
-    } else {
-        if (ydt == WQ8_F32) pick_vector<BWD, bf16_t, float>(g, run);
-        else pick_vector<BWD, bf16_t, bf16_t>(g, run);
-    }
+template <bool BWD, typename XT, typename R>
+void pick_kernel(const NormGeo &g, wq8_dtype ydt, const R &run) {
+    if (ydt == WQ8_F32) pick_vector<BWD, XT, float>(g, run);
+    else pick_vector<BWD, XT, bf16_t>(g, run);
 }
 
 }  // namespace

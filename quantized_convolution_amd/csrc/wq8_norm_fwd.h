@@ -20,6 +20,8 @@
 // Layouts: threads follow the layout of x. When y (or dy) has the other
 // layout each step's window of pixels x channels passes through LDS, so both
 // sides access global memory along their contiguous dimension.
+#pragma once
+
 #include "wq8_norm_device.h"
 
 namespace wq8 {
@@ -120,7 +122,7 @@ __global__ __launch_bounds__(1024) void k_norm_fused(NormGeo g, NormPtrs a) {
     per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, 0.0f);
     const float cnt = (float)((double)g.P * g.cpg);
     float t[NG] = {};
-    for_values<V, KIND, E>(s, w, 0, [&](int e, int k, auto ok) {
+    for_values<V, KIND, E, false>(s, w, 0, [&](int e, int k, auto ok) {
         const float v = to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k];
         t[NG == 1 ? 0 : k] += ok ? v : 0.0f;
     });
@@ -135,7 +137,7 @@ __global__ __launch_bounds__(1024) void k_norm_fused(NormGeo g, NormPtrs a) {
         mean[k] = gstat[kg[k]] / cnt;
         t[k] = 0.0f;
     }
-    for_values<V, KIND, E>(s, w, 0, [&](int e, int k, auto ok) {
+    for_values<V, KIND, E, false>(s, w, 0, [&](int e, int k, auto ok) {
         const float v = to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k] - mean[NG == 1 ? 0 : k], d = ok ? v : 0.0f;
         t[NG == 1 ? 0 : k] = fmaf(d, d, t[NG == 1 ? 0 : k]);
     });
@@ -184,7 +186,7 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_stats(NormGeo g, Nor
         }
         if (first == 0) {
             float t[NG] = {};
-            for_values<V, KIND, E>(s, w, 0, [&](int e, int k, auto ok) {
+            for_values<V, KIND, E, true>(s, w, 0, [&](int e, int k, auto ok) {
                 const float v = to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k];
                 t[NG == 1 ? 0 : k] += ok ? v : 0.0f;
             });
@@ -195,7 +197,7 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_stats(NormGeo g, Nor
             for (int k = 0; k < NC; ++k) off[k] -= pivot[NG == 1 ? 0 : k];
         }
         have += more;
-        for_values<V, KIND, E>(s, w, first, [&](int e, int k, auto ok) {
+        for_values<V, KIND, E, true>(s, w, first, [&](int e, int k, auto ok) {
             const int kk = NG == 1 ? 0 : k;
             const float v = to_f32(f[e].v[k]) + off[NC == 1 ? 0 : k], d = ok ? v : 0.0f;
             s1[kk] += d;
@@ -286,12 +288,11 @@ struct RunForward {
     }
 };
 
-}  // namespace
-
-wq8_status launch_norm_forward(const NormGeo &g, wq8_dtype xdt, wq8_dtype ydt, const NormPtrs &p,
-                               void *stream) {
-    pick_kernel<false>(g, xdt, ydt, RunForward{g, p, (hipStream_t)stream});
+template <typename XT>
+wq8_status norm_forward(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, void *stream) {
+    pick_kernel<false, XT>(g, ydt, RunForward{g, p, (hipStream_t)stream});
     return check_launch("group norm");
 }
 
+}  // namespace
 }  // namespace wq8

@@ -14,18 +14,17 @@ constexpr int kCus = 256;
 // ------------------------------------------------------------- group norm
 constexpr int kNormMaxSlab = 1024;  // channels per block
 
-constexpr int kNormE = 4;            // steps unrolled by the short fused kernels, twice that by the middle ones
-// By the split kernels: 8 vectors in flight per thread.
-constexpr int norm_split_steps(bool backward) { return backward ? 4 : 8; }
-
+constexpr int kNormE = 4;            // steps unrolled by the split and the short fused kernels
 constexpr int kNormSplitThreads = 256;
 
-// Elements per access: 16 bytes of the wider type, 8 at most.
-constexpr int norm_max_vec(size_t xs, size_t ys) { return xs == 2 && ys == 2 ? 8 : 4; }
+// Elements per access: 16 bytes of the wider type, 8 at most; 4 in the
+// backward, which keeps sums and scales of each channel.
+constexpr int norm_max_vec(size_t xs, size_t ys, bool backward) { return xs == 2 && ys == 2 && !backward ? 8 : 4; }
 
 // Steps whose values a thread of a 1024-thread block can hold: 128 registers,
-// 64 of them for the values of x (forward) or of x and dy (backward).
-constexpr int norm_max_steps(bool backward) { return backward ? 8 : 16; }
+// 64 of them for the values of x (forward) or of x and dy (backward), fewer
+// where it keeps a group per channel as well.
+constexpr int norm_max_steps(bool backward, bool straddle) { return !backward ? 16 : straddle ? 4 : 8; }
 
 // One pass of the group norm. A block handles a slab of `slabC` channels (K
 // whole groups, or 1/J of one) over `chunk` pixels of one image. With
@@ -70,20 +69,21 @@ struct NormPtrs {
     float *group;                        // backward, split: [N][G][2] group means
 };
 
-wq8_status launch_norm_forward(const NormGeo &g, wq8_dtype xdt, wq8_dtype ydt, const NormPtrs &p,
-                               void *stream);
-wq8_status launch_norm_backward(const NormGeo &g, wq8_dtype xdt, wq8_dtype ydt, const NormPtrs &p,
-                                void *stream);
+// By the type of x (one source file each).
+wq8_status launch_norm_forward_f32(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, void *stream);
+wq8_status launch_norm_forward_bf16(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, void *stream);
+wq8_status launch_norm_backward_f32(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, void *stream);
+wq8_status launch_norm_backward_bf16(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, void *stream);
 
 // ---------------------------------------------------------- matrix product
 // C[m][n] = sum_k A(m, k) B(n, k). An operand is stored with k contiguous
-// (`KC`: element (m, k) at m * ld + k) or with its rows' index contiguous
+// (element (m, k) at m * ld + k) or with its rows' index contiguous
 // (element (m, k) at k * ld + m).
-enum GemmForm { kFormForward = 0, kFormDx = 1, kFormDw = 2 };  // A, B: KC KC; KC MC; MC MC
 
 // Block tile and the split of k over blocks of one product.
 struct GemmShape {
-    int tile;      // index into the built tiles
+    int tile;      // index into kGemmTiles
+    int direct;    // whole k steps go from memory to LDS past the registers
     int splits;    // blocks along k; > 1: fp32 partial products, joined by a second kernel
     int ksteps;    // k steps per split
 };
@@ -108,9 +108,17 @@ struct LinearPtrs {
     float *partial;           // workspace: split products
 };
 
-// Rows and columns of tile `t`, and k per step (128 bytes of the type).
-void gemm_tile_size(int t, int *bm, int *bn);
-int gemm_kstep(wq8_dtype t);
+// The built tiles: rows, columns, blocks that a compute unit holds, and the
+// share of the largest tile's rate that a full card reaches in bf16 and in fp32
+// (8192^3: 1337, 1150, 917 and 648 TFLOP/s in bf16; 8192 x 4096 x 4096: 146 to
+// 140 in fp32). The last one is for a few rows.
+struct GemmTile {
+    int bm, bn, blocks;
+    double bf16, f32;
+};
+constexpr GemmTile kGemmTiles[] = {
+    {256, 256, 1, 1.0, 1.0}, {128, 128, 2, 0.86, 0.98}, {128, 64, 3, 0.69, 0.98}, {64, 64, 5, 0.49, 0.96}, {16, 128, 4, 0.3, 0.5}};
+constexpr int kGemmTileCount = 5;
 
 wq8_status launch_linear_forward(const LinearGeo &g, wq8_dtype xdt, wq8_dtype ydt,
                                  const LinearPtrs &p, void *stream);

@@ -48,7 +48,7 @@ bool is_layout(int l) { return l == WQ8_NHWC || l == WQ8_NCHW; }
 // --------------------------------------------------------- norm's launch shape
 // The fused shape for slabs of K groups, or steps > most if no block of up to
 // 1024 threads holds them.
-NormShape fused_shape(const NormGeo &g, int V, int K) {
+NormShape fused_shape(const NormGeo &g, int V, int K, int most) {
     NormShape s;
     memset(&s, 0, sizeof s);
     s.V = V;
@@ -61,17 +61,13 @@ NormShape fused_shape(const NormGeo &g, int V, int K) {
     s.steps = 1 << 30;
     if (s.slabC > kNormMaxSlab) return s;
     // threads across the channels (NHWC) or the channels times the pixel
-    // vectors (NCHW); along the rest, as many as leave kNormE steps or fewer
+    // vectors (NCHW); along the rest, as many as take all of the unrolled steps
+    // (a block whose steps end with its pixels checks no bounds)
     const int across = g.x_nhwc ? ceil_div(s.slabC, V) : s.slabC;
     const int along = g.x_nhwc ? g.P : ceil_div(g.P, V);
-    int lanes = 1024 / across;
-    if (lanes > along) lanes = along;
-    const int steps = ceil_div(along, lanes);
-    if (steps <= kNormE) {  // the fewest threads with that many steps, 256 if there is work
-        const int least = 256 / across;
-        lanes = ceil_div(along, kNormE);
-        if (lanes < least) lanes = least < along ? least : along;
-    }
+    int lanes = ceil_div(along, kNormE);
+    if (across * lanes > 1024) lanes = ceil_div(along, most);
+    if (across * lanes > 1024) return s;
     s.steps = ceil_div(along, lanes);
     s.tc = across;
     s.tp = lanes;
@@ -128,14 +124,13 @@ NormShape split_shape(const NormGeo &g, int V, int batch, int xsz) {
         s.window = s.tp * V;
     }
     s.nslab = g.G / s.K * s.J;
-    // blocks of a batch of steps, fewer where they would not fill the card, several
-    // batches where that still leaves 8 blocks a compute unit, the most that run at once
+    // one batch of steps to a block, or as many as still leave 8 blocks a
+    // compute unit, the most that run at once
     const int64_t rows = (int64_t)g.N * s.nslab;
-    const auto blocks = [&](int64_t steps) { return rows * ceil_div64(g.P, steps * s.window); };
+    const int all = ceil_div(g.P, s.window);
     int steps = batch;
-    while (steps > 2 && blocks(steps) < 2 * kCus) --steps;
-    while (steps >= batch && steps < ceil_div(g.P, s.window) && blocks(steps + batch) >= 8 * kCus) steps += batch;
-    if (steps > ceil_div(g.P, s.window)) steps = ceil_div(g.P, s.window);
+    while (steps < all && rows * ceil_div(all, steps + batch) >= 8 * kCus) steps += batch;
+    if (steps > all) steps = all;
     s.steps = steps;
     s.chunk = s.steps * s.window;
     s.nchunk = ceil_div(g.P, s.chunk);
@@ -161,7 +156,7 @@ bool slab_holds(const NormGeo &g, int V) {
 }
 
 NormShape choose_norm(const NormGeo &g, int xsz, int ysz, bool backward) {
-    const int vmax = norm_max_vec(xsz, ysz), most = norm_max_steps(backward);
+    const int vmax = norm_max_vec(xsz, ysz, backward);
     // single values where no row holds a vector
     const bool single = g.x_nhwc ? !slab_holds(g, vmax) : g.P < vmax;
     // vectors within one group where the group's channels allow 8 bytes or more,
@@ -170,13 +165,14 @@ NormShape choose_norm(const NormGeo &g, int xsz, int ysz, bool backward) {
     while (g.x_nhwc && V > 4 && g.cpg % V != 0) V /= 2;
     if (g.x_nhwc && g.cpg % V != 0) V = vmax;
     if (single) V = 1;
+    const int most = norm_max_steps(backward, g.x_nhwc && g.cpg % V != 0);
     NormShape s;
     s.steps = 1 << 30;
     for (int k = 1; k <= g.G; ++k) {
         // whole vectors across the slab, nearly
         const int vecs = ceil_div(k * g.cpg, V) * V;
         if (g.G % k != 0 || (g.x_nhwc && k < g.G && k * g.cpg * 8 < vecs * 7) || (g.x_nhwc && k * g.cpg < V)) continue;
-        const NormShape t = fused_shape(g, V, k);
+        const NormShape t = fused_shape(g, V, k, most);
         if (t.steps > most) break;
         // wider slabs (longer contiguous rows) while the card stays full
         const bool fills = (int64_t)g.N * t.nslab >= kCus && t.slabC * xsz <= 256;
@@ -190,8 +186,8 @@ NormShape choose_norm(const NormGeo &g, int xsz, int ysz, bool backward) {
             return s;
         }
     }
-    s = split_shape(g, single ? 1 : vmax, norm_split_steps(backward), xsz);
-    set_tile_steps(g, s, ysz, norm_split_steps(backward));
+    s = split_shape(g, single ? 1 : vmax, kNormE, xsz);
+    set_tile_steps(g, s, ysz, kNormE);
     return s;
 }
 
@@ -244,19 +240,51 @@ wq8_status build_norm(const wq8_norm_desc *d, wq8_norm_plan *p) {
 }
 
 // ------------------------------------------------------ product's launch shape
-GemmShape choose_gemm(int64_t M, int64_t N, int64_t K, wq8_dtype t) {
-    GemmShape s;
-    s.tile = ceil_div64(M, 256) * ceil_div64(N, 256) >= kCus && t == WQ8_BF16;
-    int bm, bn;
-    gemm_tile_size(s.tile, &bm, &bn);
-    const int64_t tiles = ceil_div64(M, bm) * ceil_div64(N, bn), steps = ceil_div64(K, gemm_kstep(t));
-    // split k while tiles leave compute units idle and a split keeps 8 steps
-    int64_t splits = tiles > 0 ? kCus / tiles : 1;
-    if (splits > steps / 8) splits = steps / 8;
-    if (splits < 1) splits = 1;
-    s.ksteps = (int)ceil_div64(steps, splits);
-    s.splits = s.ksteps > 0 ? (int)ceil_div64(steps, s.ksteps) : 1;
-    return s;
+// Tile and split by the least modelled time, in microseconds. A compute unit
+// works through n blocks of `steps` k steps at the tile's rate, a third more
+// slowly where it has but one block to itself; each round of blocks that it
+// holds at once adds its start and end (much of it for the largest tile, whose
+// compute unit has nothing else to do then); a split writes and reads fp32 sums
+// and launches once more. Measured against it over 40 shapes and tiles (bf16
+// 8192 x 640 x 640: 11.8, 11.2, 12.7 modelled and 13.2, 12.5, 13.4 measured for
+// 128 x 128, 128 x 64, 64 x 64; fp32 2048 x 2560 x 1280 in 64 x 64: 120 and 124,
+// split in two 112 and 113).
+GemmShape choose_gemm(int64_t M, int64_t N, int64_t K, wq8_dtype t, bool direct) {
+    const int64_t kstep = t == WQ8_F32 ? 32 : 64, steps = ceil_div64(K, kstep);
+    GemmShape best;
+    memset(&best, 0, sizeof best);
+    best.splits = 1;
+    double least = 1e30;
+    for (int i = direct ? 0 : 1; i < kGemmTileCount; ++i) {
+        const GemmTile &g = kGemmTiles[i];
+        const int64_t tiles = ceil_div64(M, g.bm) * ceil_div64(N, g.bn);
+        const double rate = t == WQ8_F32 ? 0.56 * g.f32 : 5.2 * g.bf16;  // Mflop per us and compute unit
+        const double step = 2e-6 * g.bm * g.bn * kstep / rate;
+        for (int64_t want = 1; want <= 16 && (want == 1 || want * 2 <= steps); ++want) {
+            const int64_t per = steps ? ceil_div64(steps, want) : 0, splits = steps ? ceil_div64(steps, per) : 1;
+            if (splits != want) continue;
+            const int64_t n = ceil_div64(tiles * splits, kCus);
+            double us = (double)n * per * step * (n == 1 && g.blocks > 1 ? 1.3 : 1.0);
+            us += (double)ceil_div64(n, g.blocks) * (i == 0 ? 16.0 : 2.5);
+            if (splits > 1) us += 3.0 + (double)M * N * 8e-6 * splits / 5.0;
+            if (us < least) {
+                least = us;
+                best.tile = i;
+                best.splits = (int)splits;
+                best.ksteps = (int)per;
+            }
+        }
+    }
+    best.direct = direct;
+    return best;
+}
+
+// Whether an operand's k steps can go to LDS directly: rows that start on 16
+// bytes, and whole 16-byte units along the rows' index where that is the
+// contiguous one (k itself may end anywhere).
+bool direct_ok(wq8_dtype t, int64_t ld, bool k_contiguous, int64_t rows) {
+    const int64_t unit = t == WQ8_F32 ? 4 : 8;
+    return ld % unit == 0 && (k_contiguous || rows % unit == 0);
 }
 
 wq8_status build_linear(const wq8_linear_desc *d, wq8_linear_plan *p) {
@@ -289,18 +317,18 @@ wq8_status build_linear(const wq8_linear_desc *d, wq8_linear_plan *p) {
     g.pixels = d->pixels;
     p->xdt = d->x_dtype;
     p->ydt = d->y_dtype;
-    g.f = choose_gemm(g.M, g.N, g.K, p->xdt);
-    g.dx = choose_gemm(g.M, g.K, g.N, p->xdt);
-    g.dw = choose_gemm(g.N, g.K, g.M, p->xdt);
     // dy serves as dz where the activation leaves it as it is and the products
     // can read its type
     g.dz_own = g.act != WQ8_ACT_NONE || p->xdt != p->ydt;
     g.dz_chunk = 64;
     g.dz_nchunk = ceil_div(g.M, g.dz_chunk);
+    const int64_t ldz = g.dz_own ? g.N : g.ys;
+    const wq8_dtype t = p->xdt;
+    g.f = choose_gemm(g.M, g.N, g.K, t, direct_ok(t, g.xs, true, g.M) && direct_ok(t, g.K, true, g.N));
+    g.dx = choose_gemm(g.M, g.K, g.N, t, direct_ok(t, ldz, true, g.M) && direct_ok(t, g.K, false, g.K));
+    g.dw = choose_gemm(g.N, g.K, g.M, t, direct_ok(t, ldz, false, g.N) && direct_ok(t, g.xs, false, g.K));
     const auto tiles = [](const GemmShape &s, int64_t M, int64_t N) {
-        int bm, bn;
-        gemm_tile_size(s.tile, &bm, &bn);
-        return ceil_div64(M, bm) * ceil_div64(N, bn) * s.splits;
+        return ceil_div64(M, kGemmTiles[s.tile].bm) * ceil_div64(N, kGemmTiles[s.tile].bn) * s.splits;
     };
     const int64_t lim = (int64_t)1 << 31;
     if (ceil_div64(g.N, 256) * g.dz_nchunk >= lim || tiles(g.f, g.M, g.N) >= lim || tiles(g.dx, g.M, g.K) >= lim || tiles(g.dw, g.N, g.K) >= lim)
@@ -380,7 +408,7 @@ wq8_status wq8_norm_forward(const wq8_norm_plan *p, const void *x, const float *
     a.mean = mean ? mean : stats;
     a.rstd = rstd ? rstd : stats + (size_t)p->geo.N * p->geo.G;
     a.part = (float *)((char *)workspace + p->f_off_part);
-    return launch_norm_forward(p->geo, p->xdt, p->ydt, a, stream);
+    return (p->xdt == WQ8_F32 ? launch_norm_forward_f32 : launch_norm_forward_bf16)(p->geo, p->ydt, a, stream);
 }
 
 wq8_status wq8_norm_backward(const wq8_norm_plan *p, const void *dy, const void *x, const float *shift,
@@ -421,7 +449,7 @@ wq8_status wq8_norm_backward(const wq8_norm_plan *p, const void *dy, const void 
     a.part = (float *)(ws + p->b_off_part);
     a.group = (float *)(ws + p->b_off_group);
     a.gpart = (float *)(ws + p->b_off_gpart);
-    return launch_norm_backward(p->geo, p->xdt, p->ydt, a, stream);
+    return (p->xdt == WQ8_F32 ? launch_norm_backward_f32 : launch_norm_backward_bf16)(p->geo, p->ydt, a, stream);
 }
 
 wq8_status wq8_linear_plan_create(const wq8_linear_desc *desc, wq8_linear_plan **out) {
