@@ -305,14 +305,15 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(GemmArgs a, EPI epi) {
         epi.run(each);
 }
 
-// Joins split products, in the order of k, and runs the epilogue: a thread per
-// 8 columns of a row.
+// Joins split products, in the order of k, and runs the epilogue. A thread takes
+// 8 columns of a row and a wave 32 columns of 16 rows, as in the product: whole
+// 128-byte runs of the sums, and 16 adjacent pixels of an NCHW residual.
 template <typename EPI>
 __global__ __launch_bounds__(256) void k_gemm_join(GemmArgs a, int splits, EPI epi) {
-    const int nq = (a.N + 7) / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)a.M * nq) return;
-    const int m = (int)(i / nq), n = (int)(i % nq) * 8;
+    const int lane = threadIdx.x & 63, ncol = (a.N + 127) / 128;
+    const int row = blockIdx.x / ncol, col = blockIdx.x - row * ncol;
+    const int m = row * 16 + (lane & 15), n = col * 128 + (threadIdx.x >> 6) * 32 + (lane >> 4) * 8;
+    if (m >= a.M || n >= a.N) return;
     Vec<float, 8> s = {};
     for (int k = 0; k < splits; ++k) {
         const Vec<float, 8> v = load_vec_n<float, 8>(a.partial + ((int64_t)k * a.M + m) * a.N + n, a.N - n);
@@ -342,8 +343,8 @@ void run_tile(const GemmShape &s, GemmArgs a, const EPI &epi, float *partial, hi
         if constexpr (BM * BN < 256 * 256) go(k_gemm<T, AKC, BKC, BM, BN, WM, WN, false, EPI>);
     }
     if (s.splits > 1) {
-        const int64_t work = (int64_t)a.M * ((a.N + 7) / 8);
-        hipLaunchKernelGGL((k_gemm_join<EPI>), dim3((unsigned)((work + 255) / 256)), dim3(256), 0, st, a, s.splits, epi);
+        const int64_t blocks = (int64_t)((a.M + 15) / 16) * ((a.N + 127) / 128);
+        hipLaunchKernelGGL((k_gemm_join<EPI>), dim3((unsigned)blocks), dim3(256), 0, st, a, s.splits, epi);
     }
 }
 

@@ -9,47 +9,56 @@
 namespace wq8 {
 namespace {
 
-// dz of 64 x V columns (a wave per row) over `chunk` rows, and their sums.
+// dz of 64 x V columns (a wave per row, kDzRows rows in flight) over `chunk` rows,
+// and their sums. A vector that would pass the last column starts earlier: its
+// first `lo` values are another thread's, stored twice and summed once.
+constexpr int kDzRows = 4;
 template <typename XT, typename YT, int V>
 __global__ __launch_bounds__(256) void k_dz(LinearGeo g, LinearPtrs a, int ncol, int want_sum) {
     __shared__ float red[3][64 * V];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int chunk = blockIdx.x / ncol;
-    const int n = ((blockIdx.x - chunk * ncol) * 64 + lane) * V, cnt = g.N - n;
+    const int c = ((blockIdx.x - chunk * ncol) * 64 + lane) * V, n = min(c, g.N - V), lo = min(c - n, V);
     const int r0 = chunk * g.dz_chunk, r1 = min(r0 + g.dz_chunk, g.M);
     const YT *dy = (const YT *)a.dy, *z = (const YT *)a.zin;
     XT *dz = (XT *)a.dz;
     float sum[V] = {};
-    if (cnt > 0)
-        with_act(g.act, [&](auto act) {
-            constexpr int A = decltype(act)::value;
-            for (int r = r0 + wave; r < r1; r += 4) {
-                const Vec<YT, V> d = load_vec_n<YT, V>(dy + (int64_t)r * g.ys + n, cnt);
-                Vec<YT, V> zz;
-                if constexpr (A != WQ8_ACT_NONE) zz = load_vec_n<YT, V>(z + (int64_t)r * g.N + n, cnt);
-                Vec<XT, V> o;
+    with_act(g.act, [&](auto act) {
+        constexpr int A = decltype(act)::value;
+        for (int r = r0 + wave; r < r1; r += 4 * kDzRows) {
+            Vec<YT, V> d[kDzRows], zz[kDzRows];
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    float v = to_f32(d.v[k]);
-                    if constexpr (A != WQ8_ACT_NONE) v *= act_slope<A>(to_f32(zz.v[k]));
-                    sum[k] += v;
-                    o.v[k] = from_f32<XT>(v);
-                }
-                if (dz) store_vec_n<XT, V>(dz + (int64_t)r * g.N + n, o, cnt);
+            for (int i = 0; i < kDzRows; ++i) {
+                const int64_t row = min(r + 4 * i, r1 - 1);
+                d[i] = load_vec<YT, V>(dy + row * g.ys + n);
+                if constexpr (A != WQ8_ACT_NONE) zz[i] = load_vec<YT, V>(z + row * g.N + n);
             }
-        });
+#pragma unroll
+            for (int i = 0; i < kDzRows; ++i)
+                if (r + 4 * i < r1) {
+                    Vec<XT, V> o;
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        float v = to_f32(d[i].v[k]);
+                        if constexpr (A != WQ8_ACT_NONE) v *= act_slope<A>(to_f32(zz[i].v[k]));
+                        sum[k] += v;
+                        o.v[k] = from_f32<XT>(v);
+                    }
+                    if (dz && lo < V) store_vec<XT, V>(dz + (int64_t)(r + 4 * i) * g.N + n, o);
+                }
+        }
+    });
     if (!want_sum) return;
     if (wave > 0)
 #pragma unroll
         for (int k = 0; k < V; ++k) red[wave - 1][lane * V + k] = sum[k];
     __syncthreads();
-    if (wave == 0 && cnt > 0) {
-        Vec<float, V> o;
+    if (wave == 0)
 #pragma unroll
         for (int k = 0; k < V; ++k)
-            o.v[k] = (sum[k] + red[0][lane * V + k]) + (red[1][lane * V + k] + red[2][lane * V + k]);
-        store_vec_n<float, V>(a.colsum + (int64_t)chunk * g.N + n, o, cnt);
-    }
+            if (k >= lo)
+                a.colsum[(int64_t)chunk * g.N + n + k] =
+                    (sum[k] + red[0][lane * V + k]) + (red[1][lane * V + k] + red[2][lane * V + k]);
 }
 
 // dbias: the chunks' column sums, 16 columns x 16 lanes along the chunks.
@@ -88,9 +97,13 @@ template <typename XT, typename YT>
 void backward(const LinearGeo &g, const LinearPtrs &p, hipStream_t st) {
     constexpr int V = 16 / (sizeof(XT) > sizeof(YT) ? sizeof(XT) : sizeof(YT));
     if (g.M > 0 && (g.dz_own || p.dbias)) {
-        const int ncol = (g.N + 64 * V - 1) / (64 * V);
-        const dim3 grid((unsigned)((int64_t)ncol * g.dz_nchunk));
-        hipLaunchKernelGGL((k_dz<XT, YT, V>), grid, dim3(256), 0, st, g, p, ncol, p.dbias != nullptr);
+        const auto go = [&](auto kernel, int v) {
+            const int ncol = (g.N + 64 * v - 1) / (64 * v);
+            hipLaunchKernelGGL(kernel, dim3((unsigned)((int64_t)ncol * g.dz_nchunk)), dim3(256), 0, st, g, p, ncol,
+                               p.dbias != nullptr);
+        };
+        if (g.N >= V) go(k_dz<XT, YT, V>, V);
+        else go(k_dz<XT, YT, 1>, 1);
     }
     if (p.dbias) hipLaunchKernelGGL(k_dbias, dim3((g.N + 15) / 16), dim3(256), 0, st, g, p);
     const void *dz = g.dz_own ? p.dz : p.dy;

@@ -246,7 +246,7 @@ wq8_status build_norm(const wq8_norm_desc *d, wq8_norm_plan *p) {
 // holds at once adds its start and end (much of it for the largest tile, whose
 // compute unit has nothing else to do then); a split writes and reads fp32 sums
 // and launches once more. Measured against it over 40 shapes and tiles (bf16
-// 8192 x 640 x 640: 11.8, 11.2, 12.7 modelled and 13.2, 12.5, 13.4 measured for
+// 8192 x 640 x 640: 13.3, 11.2, 12.7 modelled and 13.2, 12.5, 13.4 measured for
 // 128 x 128, 128 x 64, 64 x 64; fp32 2048 x 2560 x 1280 in 64 x 64: 120 and 124,
 // split in two 112 and 113).
 GemmShape choose_gemm(int64_t M, int64_t N, int64_t K, wq8_dtype t, bool direct) {
@@ -265,7 +265,7 @@ GemmShape choose_gemm(int64_t M, int64_t N, int64_t K, wq8_dtype t, bool direct)
             if (splits != want) continue;
             const int64_t n = ceil_div64(tiles * splits, kCus);
             double us = (double)n * per * step * (n == 1 && g.blocks > 1 ? 1.3 : 1.0);
-            us += (double)ceil_div64(n, g.blocks) * (i == 0 ? 16.0 : 2.5);
+            us += (double)ceil_div64(n, g.blocks) * (i == 0 ? 10.0 : i == 1 ? 4.0 : 2.5);
             if (splits > 1) us += 3.0 + (double)M * N * 8e-6 * splits / 5.0;
             if (us < least) {
                 least = us;
@@ -320,7 +320,9 @@ wq8_status build_linear(const wq8_linear_desc *d, wq8_linear_plan *p) {
     // dy serves as dz where the activation leaves it as it is and the products
     // can read its type
     g.dz_own = g.act != WQ8_ACT_NONE || p->xdt != p->ydt;
+    // rows per block: 4 waves of 4 rows in flight, more where blocks abound
     g.dz_chunk = 64;
+    while (g.dz_chunk > 16 && ceil_div64(g.M, g.dz_chunk) * ceil_div64(g.N, 512) < 4 * kCus) g.dz_chunk /= 2;
     g.dz_nchunk = ceil_div(g.M, g.dz_chunk);
     const int64_t ldz = g.dz_own ? g.N : g.ys;
     const wq8_dtype t = p->xdt;
@@ -331,7 +333,7 @@ wq8_status build_linear(const wq8_linear_desc *d, wq8_linear_plan *p) {
         return ceil_div64(M, kGemmTiles[s.tile].bm) * ceil_div64(N, kGemmTiles[s.tile].bn) * s.splits;
     };
     const int64_t lim = (int64_t)1 << 31;
-    if (ceil_div64(g.N, 256) * g.dz_nchunk >= lim || tiles(g.f, g.M, g.N) >= lim || tiles(g.dx, g.M, g.K) >= lim || tiles(g.dw, g.N, g.K) >= lim)
+    if (ceil_div64(g.N, 64) * g.dz_nchunk >= lim || tiles(g.f, g.M, g.N) >= lim || tiles(g.dx, g.M, g.K) >= lim || tiles(g.dw, g.N, g.K) >= lim)
         return fail(WQ8_ERR_UNSUPPORTED, "more than 2^31 blocks");
     const size_t M = g.M, N = g.N, K = g.K;
     const auto partial = [](const GemmShape &s, size_t m, size_t n) { return s.splits > 1 ? s.splits * m * n * 4 : 0; };

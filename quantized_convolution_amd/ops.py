@@ -158,19 +158,21 @@ def _empty(shape, stride, dtype, device):
     return torch.empty(shape[:-1] + (stride,), dtype=dtype, device=device)[..., :shape[-1]]
 
 
+# The stream handle of a device without a Stream object around it, where torch
+# offers that: a microsecond less in front of kernels that take five.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 class _Args:
     """Checks the buffers of one call: torch tensors of the dtype, shape and
     strides that the plan gives, all on one GPU. The kernels size their
-    accesses from the plan, so anything else would be out of bounds.
-
-    Buffers are named when one is refused and not before: these checks stand
-    in the way of calls that take the GPU a few microseconds."""
+    accesses from the plan, so anything else would be out of bounds."""
 
     __slots__ = ("device", "where")
 
     def __init__(self):
-        self.device = None
-        self.where = None
+        self.device = None  # index; -1: not a GPU
+        self.where = None   # the first buffer and its name
 
     def need(self, t, name, dtype, shape, strides=None):
         """The tensor's address."""
@@ -185,11 +187,12 @@ class _Args:
                 raise ValueError(f"{name} must be contiguous")
         elif any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
             raise ValueError(f"{name} must have strides {tuple(strides)}, got {tuple(t.stride())}")
+        d = t.get_device()
         if self.device is None:
-            self.device = t.device
-            self.where = name
-        elif t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, {self.where} on {self.device}")
+            self.device = d
+            self.where = (t, name)
+        elif d != self.device:
+            raise ValueError(f"{name} is on {t.device}, {self.where[1]} on {self.where[0].device}")
         return t.data_ptr()
 
     def optional(self, t, name, dtype, shape, strides=None):
@@ -200,7 +203,7 @@ class _Args:
         if nbytes == 0:
             return None, 0
         if t is None:
-            t = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            t = torch.empty(nbytes, dtype=torch.uint8, device=self.where[0].device)
         if not isinstance(t, torch.Tensor):
             raise ValueError("workspace must be a torch tensor")
         have = t.numel() * t.element_size()
@@ -208,24 +211,27 @@ class _Args:
             raise ValueError(f"workspace holds {have} bytes, needs {nbytes}")
         if not t.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        if t.device != self.device:
-            raise ValueError(f"workspace is on {t.device}, {self.where} on {self.device}")
+        if t.get_device() != self.device:
+            raise ValueError(f"workspace is on {t.device}, {self.where[1]} on {self.where[0].device}")
         return t.data_ptr(), have
 
     def call(self, fn, args, stream):
         """The C call with the buffers' device current, on `stream` or that
         device's current stream."""
         d = self.device
-        if d.type != "cuda":
-            raise ValueError(f"{self.where} must be on a GPU, got {d}")
-        if stream is None:
-            stream = torch.cuda.current_stream(d)
-        if torch.cuda.current_device() == d.index:
-            st = fn(*args, stream.cuda_stream)
+        if not self.where[0].is_cuda:
+            raise ValueError(f"{self.where[1]} must be on a GPU, got {self.where[0].device}")
+        if stream is not None:
+            handle = stream.cuda_stream
+        else:
+            handle = _raw_stream(d) if _raw_stream else torch.cuda.current_stream(d).cuda_stream
+        if torch.cuda.current_device() == d:
+            st = fn(*args, handle)
         else:
             with torch.cuda.device(d):
-                st = fn(*args, stream.cuda_stream)
-        _check(st)
+                st = fn(*args, handle)
+        if st:
+            _check(st)
 
 
 def wq8_norm_forward(plan: NormPlan, x, gamma=None, beta=None, shift=None, y=None, mean=None, rstd=None,
