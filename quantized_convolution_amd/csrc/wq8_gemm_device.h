@@ -110,23 +110,50 @@ struct Stager {
         }
     }
 
-    // One step through registers, at any alignment, zeros outside the operand.
+    // A step through registers, at any alignment, in loads without conditions (a
+    // load under one is waited for before the next is sent). Rows past the end
+    // hold anything: their sums are not stored.
+    //
+    // Whether a step needs no care: all of its k exist, and where the rows' index
+    // is the contiguous one a unit that passes the rows' end reads on into the
+    // next k's row, so that must exist as well.
+    __device__ __forceinline__ bool whole(int step) const {
+        return KC ? (step + 1) * BK <= K : (step + 1) * BK < K && rows >= U;
+    }
     __device__ __forceinline__ void load(Vec<T, U> (&v)[COUNT], int step) const {
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
-            int row, unit, n;
-            const T *p;
+            int row, unit;
             place(i, row, unit);
-            if constexpr (KC) {
-                const int k = step * BK + unit * U;
-                n = r0 + row < rows ? min(K - k, U) : 0;
-                p = src + (int64_t)(r0 + row) * ld + k;
+            if constexpr (KC) v[i] = load_vec<T, U>(src + (int64_t)min(r0 + row, rows - 1) * ld + step * BK + unit * U);
+            else v[i] = load_vec<T, U>(src + (int64_t)(step * BK + row) * ld + min(r0 + unit * U, rows - 1));
+        }
+    }
+    // The last step: zeros for k past the end. A unit that passes the end of
+    // its row is read from U before that end and moved down.
+    __device__ __forceinline__ void load_last(Vec<T, U> (&v)[COUNT], int step) const {
+        const int end = KC ? K : rows;  // of the contiguous index
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            int row, unit;
+            place(i, row, unit);
+            const int at = (KC ? step * BK : r0) + unit * U, line = KC ? r0 + row : step * BK + row;
+            const int lines = KC ? rows : K;
+            const T *p = src + (int64_t)min(line, lines - 1) * ld;
+            const int n = KC || line < lines ? end - at : 0;  // values that count
+            if (end >= U) {
+                const int from = min(at, end - U), shift = at - from;
+                const Vec<T, U> r = load_vec<T, U>(p + from);
+#pragma unroll
+                for (int e = 0; e < U; ++e) {
+                    T x = T(0);
+#pragma unroll
+                    for (int q = e; q < U; ++q) x = q - e == shift ? r.v[q] : x;
+                    v[i].v[e] = e < n ? x : T(0);
+                }
             } else {
-                const int k = step * BK + row, m = r0 + unit * U;
-                n = k < K ? min(rows - m, U) : 0;
-                p = src + (int64_t)k * ld + m;
+                v[i] = load_vec_n<T, U>(p + at, n);
             }
-            v[i] = load_vec_n<T, U>(p, n);
         }
     }
     __device__ __forceinline__ void store(T *lds, const Vec<T, U> (&v)[COUNT]) const {
@@ -266,17 +293,22 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(GemmArgs a, EPI epi) {
     }
     if (s < ke) {
         Vec<T, 16 / sizeof(T)> va[decltype(sa)::COUNT], vb[decltype(sb)::COUNT];
-        sa.load(va, s);
-        sb.load(vb, s);
+        const auto fetch = [&](int step) {
+            if (!DIRECT && sa.whole(step) && sb.whole(step)) {
+                sa.load(va, step);
+                sb.load(vb, step);
+            } else {
+                sa.load_last(va, step);
+                sb.load_last(vb, step);
+            }
+        };
+        fetch(s);
         for (; s < ke; ++s) {
             T *const cur = lds + ((s - ks) & 1) * STAGE;
             sa.store(cur, va);
             sb.store(cur + BS, vb);
             __syncthreads();
-            if (s + 1 < ke) {
-                sa.load(va, s + 1);
-                sb.load(vb, s + 1);
-            }
+            if (s + 1 < ke) fetch(s + 1);
             multiply(cur);
         }
     }

@@ -22,9 +22,9 @@ struct Channels {
 
     __device__ __forceinline__ void load(const NormGeo &g, const NormPtrs &a, const Where &w) {
         const int64_t group0 = (int64_t)w.n * g.G + w.g0;
-        per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, 0.0f);
-        per_channel<V, KIND>(ga, a.gamma, w.c, 1.0f);
-        per_channel<V, KIND>(be, a.beta, w.c, 0.0f);
+        per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, kZeros);
+        per_channel<V, KIND>(ga, a.gamma, w.c, kOnes);
+        per_channel<V, KIND>(be, a.beta, w.c, kZeros);
         groups_of<V, KIND>(kg, g, g.b, w);
 #pragma unroll
         for (int k = 0; k < NC; ++k) off[k] -= a.mean_in[group0 + kg[k]];
@@ -186,15 +186,19 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_bwd_sums(NormGeo g, 
     const NormShape &s = g.b;
     float *const red = (float *)smem, *const gm = red + norm_sum_floats(s, CL);
     const Where w = locate<V, KIND>(g, s);
+    Vec<XT, V> fx[E];
+    Vec<YT, V> fd[E];
+    load_steps<XT, V, KIND, E>(fx, (const XT *)a.x, g, s, g.xs, w, 0);
+    load_dy<YT, V, KIND, CROSS, E>(fd, (const YT *)a.dy, g, w, 0, (YT *)smem);
     Channels<V, KIND> c;
     c.load(g, a, w);
     float s1[NC] = {}, s2[NC] = {}, s3[NC] = {};
-    for (int first = 0; first < s.steps; first += E) {
-        Vec<XT, V> fx[E];
-        Vec<YT, V> fd[E];
+    for (int first = 0;;) {
+        add_sums<XT, YT, V, KIND, E, true>(s1, s2, s3, fx, fd, c, g, w, first);
+        first += E;
+        if (first >= s.steps) break;
         load_steps<XT, V, KIND, E>(fx, (const XT *)a.x, g, s, g.xs, w, first);
         load_dy<YT, V, KIND, CROSS, E>(fd, (const YT *)a.dy, g, w, first, (YT *)smem);
-        add_sums<XT, YT, V, KIND, E, true>(s1, s2, s3, fx, fd, c, g, w, first);
     }
     join_sums<V, KIND>(g, a, w, s1, s2, s3, red, gm);
     const int64_t group0 = (int64_t)w.n * g.G + w.g0;
@@ -209,41 +213,57 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_bwd_apply(NormGeo g,
     constexpr int NG = group_values<V, KIND>();
     extern __shared__ __align__(16) char smem[];
     const NormShape &s = g.b;
-    float *const gm = (float *)smem;
+    float *const tot = (float *)smem;
     const Where w = locate<V, KIND>(g, s);
+    Vec<XT, V> fx[E];
+    load_steps<XT, V, KIND, E>(fx, (const XT *)a.x, g, s, g.xs, w, 0);
     Channels<V, KIND> c;
     c.load(g, a, w);
+    // the groups' means, a wave joining 4 groups at once, 128 parts at a time
+    constexpr int GB = 4, PB = 2;
     const int64_t group0 = (int64_t)w.n * g.G + w.g0;
     const int lane = threadIdx.x & 63, np = s.nchunk * s.J;
-    for (int k = threadIdx.x >> 6; k < s.K; k += kNormSplitThreads / 64) {
-        const float *part = a.gpart + 2 * (group0 + k) * np;
-        float t1 = 0.0f, t2 = 0.0f;
-        for (int i = lane; i < np; i += 64) {
-            t1 += part[2 * i];
-            t2 += part[2 * i + 1];
+    const float m = (float)((double)g.P * g.cpg);
+    for (int k0 = (threadIdx.x >> 6) * GB; k0 < s.K; k0 += kNormSplitThreads / 64 * GB) {
+        float t1[GB] = {}, t2[GB] = {};
+        for (int i0 = 0; i0 < np; i0 += 64 * PB) {
+            Vec<float, 2> v[GB][PB];
+#pragma unroll
+            for (int k = 0; k < GB; ++k)
+#pragma unroll
+                for (int i = 0; i < PB; ++i)
+                    v[k][i] = load_vec<float, 2>(a.gpart + 2 * ((group0 + min(k0 + k, s.K - 1)) * np + min(i0 + i * 64 + lane, np - 1)));
+#pragma unroll
+            for (int k = 0; k < GB; ++k)
+#pragma unroll
+                for (int i = 0; i < PB; ++i) {
+                    const bool in = i0 + i * 64 + lane < np;
+                    t1[k] += in ? v[k][i].v[0] : 0.0f;
+                    t2[k] += in ? v[k][i].v[1] : 0.0f;
+                }
         }
-        const float m = (float)((double)g.P * g.cpg);
-        t1 = wave_sum(t1) / m;
-        t2 = wave_sum(t2) / m;
-        if (lane == 0) {
-            gm[2 * k] = t1;
-            gm[2 * k + 1] = t2;
-            if (w.chunk == 0 && w.part == 0) {
-                a.group[2 * (group0 + k)] = t1;
-                a.group[2 * (group0 + k) + 1] = t2;
+#pragma unroll
+        for (int k = 0; k < GB; ++k) {
+            const float m1 = wave_sum(t1[k]) / m, m2 = wave_sum(t2[k]) / m;
+            if (lane == 0 && k0 + k < s.K) {
+                tot[2 * (k0 + k)] = m1;
+                tot[2 * (k0 + k) + 1] = m2;
             }
         }
     }
     __syncthreads();
+    if (w.chunk == 0 && w.part == 0)
+        for (int k = threadIdx.x; k < 2 * s.K; k += kNormSplitThreads) a.group[2 * group0 + k] = tot[k];
     float m1[NG], m2[NG];
-    take_group_means<V, KIND>(c, gm, m1, m2);
+    take_group_means<V, KIND>(c, tot, m1, m2);
     if constexpr (CROSS) __syncthreads();  // the tile takes the means' place
-    for (int first = 0; first < s.steps; first += E) {
-        Vec<XT, V> fx[E];
+    for (int first = 0;;) {
         Vec<YT, V> fd[E];
-        load_steps<XT, V, KIND, E>(fx, (const XT *)a.x, g, s, g.xs, w, first);
         load_dy<YT, V, KIND, CROSS, E>(fd, (const YT *)a.dy, g, w, first, (YT *)smem);
         write_dx<XT, YT, V, KIND, CROSS, E>(fx, fd, c, m1, m2, g, w, (XT *)a.dx, first);
+        first += E;
+        if (first >= s.steps) break;
+        load_steps<XT, V, KIND, E>(fx, (const XT *)a.x, g, s, g.xs, w, first);
     }
 }
 

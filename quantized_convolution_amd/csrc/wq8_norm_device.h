@@ -368,14 +368,16 @@ __device__ __forceinline__ void groups_of(int *kg, const NormGeo &g, const NormS
     }
 }
 
-// Values of a per-channel array for this thread's channels.
+// Values of a per-channel array for this thread's channels; ones or zeros for
+// an array that is not given, from memory as well, so that no load waits for
+// another one's condition.
+static __device__ const float kOnes[8] = {1, 1, 1, 1, 1, 1, 1, 1};
+static __device__ const float kZeros[8] = {};
+
 template <int V, int KIND>
-__device__ __forceinline__ void per_channel(float *r, const float *a, int64_t at, float none) {
+__device__ __forceinline__ void per_channel(float *r, const float *a, int64_t at, const float *none) {
     constexpr int NC = thread_channels<V, KIND>();
-    Vec<float, NC> v;
-#pragma unroll
-    for (int k = 0; k < NC; ++k) v.v[k] = none;
-    if (a) v = load_vec<float, NC>(a + at);
+    const Vec<float, NC> v = load_vec<float, NC>(a ? a + at : none);
 #pragma unroll
     for (int k = 0; k < NC; ++k) r[k] = v.v[k];
 }

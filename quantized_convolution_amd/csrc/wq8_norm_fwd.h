@@ -28,29 +28,67 @@ namespace wq8 {
 namespace {
 
 // ---------------------------------------------------------------- forward
-// Mean and 1/sqrt(variance + eps) of group ng from its blocks' partial
-// statistics (one wave): the parts' means weighted by their counts, then
-// M2 = sum M2_i + n_i (mean_i - mean)^2.
-__device__ __forceinline__ void join_stats(const NormGeo &g, const NormPtrs &a, int64_t ng, float &mean, float &rstd) {
+// Mean and 1/sqrt(variance + eps) of the block's groups from all blocks' partial
+// statistics, to gstat[K] and gstat[K..2K): the parts' means weighted by their
+// counts, then M2 = sum M2_i + n_i (mean_i - mean)^2. A wave joins 4 groups at
+// once, 128 parts of each at a time, with all their loads in flight.
+__device__ __forceinline__ void join_stats(const NormGeo &g, const NormPtrs &a, int64_t group0, float *gstat) {
+    constexpr int GB = 4, PB = 2;
     const NormShape &s = g.f;
     const int lane = threadIdx.x & 63, np = s.nchunk * s.J;
-    const float *part = a.part + 2 * ng * np;
+    const float m = (float)((double)g.P * g.cpg);
     const auto count = [&](int i) {
+        if (i >= np) return 0.0f;
         const int ch = i / s.J, j = i - ch * s.J;
         const int px = min(s.chunk, g.P - ch * s.chunk);
         const int c = s.J == 1 ? g.cpg : min(s.slabC, g.cpg - j * s.slabC);
         return (float)px * (float)c;
     };
-    float t = 0.0f;
-    for (int i = lane; i < np; i += 64) t = fmaf(count(i), part[2 * i], t);
-    const float m = (float)((double)g.P * g.cpg);
-    mean = wave_sum(t) / m;
-    t = 0.0f;
-    for (int i = lane; i < np; i += 64) {
-        const float d = part[2 * i] - mean;
-        t += fmaf(count(i) * d, d, part[2 * i + 1]);
+    for (int k0 = (threadIdx.x >> 6) * GB; k0 < s.K; k0 += kNormSplitThreads / 64 * GB) {
+        Vec<float, 2> v[GB][PB];
+        const auto fetch = [&](int i0) {
+#pragma unroll
+            for (int k = 0; k < GB; ++k)
+#pragma unroll
+                for (int i = 0; i < PB; ++i)
+                    v[k][i] = load_vec<float, 2>(a.part + 2 * ((group0 + min(k0 + k, s.K - 1)) * np + min(i0 + i * 64 + lane, np - 1)));
+        };
+        float t[GB] = {}, mean[GB];
+        for (int i0 = 0; i0 < np; i0 += 64 * PB) {
+            fetch(i0);
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                const float n = count(i0 + i * 64 + lane);
+#pragma unroll
+                for (int k = 0; k < GB; ++k) t[k] += n > 0.0f ? n * v[k][i].v[0] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < GB; ++k) {
+            mean[k] = wave_sum(t[k]) / m;
+            t[k] = 0.0f;
+        }
+        for (int i0 = 0; i0 < np; i0 += 64 * PB) {
+            if (np > 64 * PB) fetch(i0);
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                const float n = count(i0 + i * 64 + lane);
+#pragma unroll
+                for (int k = 0; k < GB; ++k) {
+                    const float d = v[k][i].v[0] - mean[k];
+                    t[k] += n > 0.0f ? fmaf(n * d, d, v[k][i].v[1]) : 0.0f;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < GB; ++k) {
+            const float r = 1.0f / sqrtf(wave_sum(t[k]) / m + g.eps);
+            if (lane == 0 && k0 + k < s.K) {
+                gstat[k0 + k] = mean[k];
+                gstat[s.K + k0 + k] = r;
+            }
+        }
     }
-    rstd = 1.0f / sqrtf(wave_sum(t) / m + g.eps);
 }
 
 // What remains of the fused and of the output kernel: z = (v - mean) rstd gamma
@@ -96,8 +134,8 @@ __device__ __forceinline__ void scales(float *off, float *sc, float *be, const N
                                        const float *gstat) {
     constexpr int NC = thread_channels<V, KIND>();
     const NormShape &s = g.f;
-    per_channel<V, KIND>(sc, a.gamma, w.c, 1.0f);
-    per_channel<V, KIND>(be, a.beta, w.c, 0.0f);
+    per_channel<V, KIND>(sc, a.gamma, w.c, kOnes);
+    per_channel<V, KIND>(be, a.beta, w.c, kZeros);
     int kg[NC];
     groups_of<V, KIND>(kg, g, s, w);
 #pragma unroll
@@ -119,7 +157,7 @@ __global__ __launch_bounds__(1024) void k_norm_fused(NormGeo g, NormPtrs a) {
     Vec<XT, V> f[E];
     load_steps<XT, V, KIND, E>(f, (const XT *)a.x, g, s, g.xs, w, 0);
     float off[NC];
-    per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, 0.0f);
+    per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, kZeros);
     const float cnt = (float)((double)g.P * g.cpg);
     float t[NG] = {};
     for_values<V, KIND, E, false>(s, w, 0, [&](int e, int k, auto ok) {
@@ -170,7 +208,7 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_stats(NormGeo g, Nor
     float *const red = (float *)smem, *const gstat = red + norm_sum_floats(s, KIND != kPlanar);
     const Where w = locate<V, KIND>(g, s);
     float off[NC];
-    per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, 0.0f);
+    per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, kZeros);
 
     // values per sum; by channel where a thread's channels are kept apart
     float have = 0.0f;
@@ -244,20 +282,14 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_apply(NormGeo g, Nor
     Vec<XT, V> f[E];
     load_steps<XT, V, KIND, E>(f, (const XT *)a.x, g, s, g.xs, w, 0);
     float off[NC], sc[NC], be[NC];
-    per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, 0.0f);
-    for (int k = threadIdx.x >> 6; k < s.K; k += kNormSplitThreads / 64) {
-        float mu, r;
-        join_stats(g, a, group0 + k, mu, r);
-        if ((threadIdx.x & 63) == 0) {
-            gstat[k] = mu;
-            gstat[s.K + k] = r;
-            if (w.chunk == 0 && w.part == 0) {
-                a.mean[group0 + k] = mu;
-                a.rstd[group0 + k] = r;
-            }
-        }
-    }
+    per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, kZeros);
+    join_stats(g, a, group0, gstat);
     __syncthreads();
+    if (w.chunk == 0 && w.part == 0)
+        for (int k = threadIdx.x; k < s.K; k += kNormSplitThreads) {
+            a.mean[group0 + k] = gstat[k];
+            a.rstd[group0 + k] = gstat[s.K + k];
+        }
     scales<V, KIND>(off, sc, be, g, a, w, gstat);
     if constexpr (CROSS) __syncthreads();
     for (int first = 0;;) {
