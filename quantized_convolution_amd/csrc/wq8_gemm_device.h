@@ -36,6 +36,7 @@ struct GemmArgs {
     int M, N, K;
     int tiles_m, tiles_n;
     int ksteps;        // per split
+    int splits;
     float *partial;    // [splits][M][N] where k is split, else NULL
 };
 
@@ -230,8 +231,9 @@ __device__ __forceinline__ void mma(f32x4 &acc, const Frag<float> &n, const Frag
 // DIRECT: whole k steps go from memory to LDS without registers; a last partial
 // one, and every one of operands that are not aligned for that, goes through
 // registers. Two buffers: while one is multiplied the other is filled.
+// The b-th of a product's nb blocks.
 template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool DIRECT, typename EPI>
-__global__ __launch_bounds__(WM *WN * 64) void k_gemm(GemmArgs a, EPI epi) {
+__device__ __forceinline__ void gemm_block(const GemmArgs &a, const EPI &epi, int b, int nb) {
     constexpr int BK = 128 / sizeof(T), THREADS = WM * WN * 64;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles per wave
     static_assert(TN % 2 == 0, "column tiles come in pairs");
@@ -240,7 +242,7 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(GemmArgs a, EPI epi) {
     constexpr int STAGE = (BM + BN) * BK, BS = BM * BK;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int tiles = a.tiles_m * a.tiles_n;
-    const int b = xcd_block(blockIdx.x, gridDim.x);
+    b = xcd_block(b, nb);
     const int split = b / tiles, t = b - split * tiles;
     // tiles in bands of 8 rows of tiles: blocks that run together share panels
     const int band = t / (8 * a.tiles_n), in = t - band * 8 * a.tiles_n;
@@ -337,60 +339,76 @@ __global__ __launch_bounds__(WM *WN * 64) void k_gemm(GemmArgs a, EPI epi) {
         epi.run(each);
 }
 
+template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool DIRECT, typename EPI>
+__global__ __launch_bounds__(WM *WN * 64) void k_gemm(GemmArgs a, EPI epi) {
+    gemm_block<T, AKC, BKC, BM, BN, WM, WN, DIRECT>(a, epi, blockIdx.x, gridDim.x);
+}
+
 // Joins split products, in the order of k, and runs the epilogue. A thread takes
 // 8 columns of a row and a wave 32 columns of 16 rows, as in the product: whole
 // 128-byte runs of the sums, and 16 adjacent pixels of an NCHW residual.
 template <typename EPI>
-__global__ __launch_bounds__(256) void k_gemm_join(GemmArgs a, int splits, EPI epi) {
+__device__ __forceinline__ void join_block(const GemmArgs &a, const EPI &epi, int b) {
     const int lane = threadIdx.x & 63, ncol = (a.N + 127) / 128;
-    const int row = blockIdx.x / ncol, col = blockIdx.x - row * ncol;
+    const int row = b / ncol, col = b - row * ncol;
     const int m = row * 16 + (lane & 15), n = col * 128 + (threadIdx.x >> 6) * 32 + (lane >> 4) * 8;
     if (m >= a.M || n >= a.N) return;
     Vec<float, 8> s = {};
-    for (int k = 0; k < splits; ++k) {
+    for (int k = 0; k < a.splits; ++k) {
         const Vec<float, 8> v = load_vec_n<float, 8>(a.partial + ((int64_t)k * a.M + m) * a.N + n, a.N - n);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s.v[e] += v.v[e];
     }
     epi.run([&](auto f) { f(m, n, s, a.N - n); });
 }
+inline int64_t join_blocks(const GemmArgs &a) {
+    return a.splits > 1 ? (int64_t)((a.M + 15) / 16) * ((a.N + 127) / 128) : 0;
+}
 
-template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, typename EPI>
-void run_tile(const GemmShape &s, GemmArgs a, const EPI &epi, float *partial, hipStream_t st) {
+template <typename EPI>
+__global__ __launch_bounds__(256) void k_gemm_join(GemmArgs a, EPI epi) {
+    join_block(a, epi, blockIdx.x);
+}
+
+// A product's tiles of BM x BN and its split; returns its blocks.
+template <int BM, int BN>
+int64_t set_tiles(GemmArgs &a, const GemmShape &s, float *partial) {
     a.tiles_m = (a.M + BM - 1) / BM;
     a.tiles_n = (a.N + BN - 1) / BN;
     a.ksteps = s.ksteps;
+    a.splits = s.splits;
     a.partial = s.splits > 1 ? partial : nullptr;
-    const dim3 grid((unsigned)((int64_t)a.tiles_m * a.tiles_n * s.splits)), blk(WM * WN * 64);
-    const size_t bytes = 2 * (BM + BN) * 128;
-    const auto go = [&](auto kernel) {
-        if (bytes > 65536)
-            (void)hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-        hipLaunchKernelGGL(kernel, grid, blk, bytes, st, a, epi);
-    };
-    if (s.direct) {
-        go(k_gemm<T, AKC, BKC, BM, BN, WM, WN, true, EPI>);
-    } else {
-        // no registers for a step of the largest tile: the plan does not choose it
-        if constexpr (BM * BN < 256 * 256) go(k_gemm<T, AKC, BKC, BM, BN, WM, WN, false, EPI>);
-    }
-    if (s.splits > 1) {
-        const int64_t blocks = (int64_t)((a.M + 15) / 16) * ((a.N + 127) / 128);
-        hipLaunchKernelGGL((k_gemm_join<EPI>), dim3((unsigned)blocks), dim3(256), 0, st, a, s.splits, epi);
-    }
+    return (int64_t)a.tiles_m * a.tiles_n * s.splits;
 }
 
-// The tiles of kGemmTiles, in its order.
-template <typename T, bool AKC, bool BKC, typename EPI>
-void run_gemm(const GemmShape &s, const GemmArgs &a, const EPI &epi, float *partial, hipStream_t st) {
-    if (a.M == 0 || a.N == 0) return;
-    switch (s.tile) {
-        case 0: return run_tile<T, AKC, BKC, 256, 256, 2, 4>(s, a, epi, partial, st);
-        case 1: return run_tile<T, AKC, BKC, 128, 128, 2, 2>(s, a, epi, partial, st);
-        case 2: return run_tile<T, AKC, BKC, 128, 64, 2, 2>(s, a, epi, partial, st);
-        case 3: return run_tile<T, AKC, BKC, 64, 64, 2, 2>(s, a, epi, partial, st);
-        default: return run_tile<T, AKC, BKC, 16, 128, 1, 2>(s, a, epi, partial, st);
-    }
+// Bytes of LDS of a tile, allowed for `kernel` where they pass the default.
+template <int BM, int BN, typename K>
+size_t tile_lds(K kernel) {
+    constexpr size_t bytes = 2 * (BM + BN) * 128;
+    if (bytes > 65536)
+        (void)hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    return bytes;
+}
+
+// Calls run<BM, BN, WM, WN, DIRECT>() for tile s.tile, in the order of
+// kGemmTiles. Not DIRECT, the largest tile has no registers for a step: the
+// plan does not choose it then.
+template <typename R>
+void pick_tile(const GemmShape &s, const R &run) {
+    const auto go = [&](auto direct) {
+        constexpr bool D = decltype(direct)::value;
+        switch (s.tile) {
+            case 0:
+                if constexpr (D) run.template operator()<256, 256, 2, 4, D>();
+                return;
+            case 1: return run.template operator()<128, 128, 2, 2, D>();
+            case 2: return run.template operator()<128, 64, 2, 2, D>();
+            case 3: return run.template operator()<64, 64, 2, 2, D>();
+            default: return run.template operator()<16, 128, 1, 2, D>();
+        }
+    };
+    if (s.direct) go(std::true_type{});
+    else go(std::false_type{});
 }
 
 }  // namespace

@@ -1,9 +1,12 @@
 // Backward of the matrix product with bias, activation and residual.
 //   dz = dy act'(z);  dx = dz w;  dw = dz^T x;  dbias = sum over the rows of dz
 // One kernel forms dz (once, in x's type) with the column sums of the unrounded
-// values; dx and dw are tiled products that read dz, w and x as they lie: the
+// values. A second one runs both products and the column sums' join side by
+// side: they only share inputs, and the blocks of one fill the compute units
+// that the other leaves idle. The products read dz, w and x as they lie: the
 // operand whose row index is contiguous goes through the transposing LDS
-// reads, so nothing is transposed in memory.
+// reads, so nothing is transposed in memory. A last kernel joins the sums of
+// products that are split along k.
 #include "wq8_gemm_device.h"
 
 namespace wq8 {
@@ -61,18 +64,20 @@ __global__ __launch_bounds__(256) void k_dz(LinearGeo g, LinearPtrs a, int ncol,
                     (sum[k] + red[0][lane * V + k]) + (red[1][lane * V + k] + red[2][lane * V + k]);
 }
 
-// dbias: the chunks' column sums, 16 columns x 16 lanes along the chunks.
-__global__ __launch_bounds__(256) void k_dbias(LinearGeo g, LinearPtrs a) {
-    __shared__ float red[16][17];
-    const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4, c = blockIdx.x * 16 + tc;
+// dbias: the chunks' column sums, 16 columns a block, its other threads along
+// the chunks.
+__device__ __forceinline__ void dbias_block(const LinearGeo &g, const LinearPtrs &a, int b) {
+    extern __shared__ __align__(128) char smem[];
+    float *red = (float *)smem;
+    const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4, rows = blockDim.x >> 4, c = b * 16 + tc;
     float t = 0.0f;
     if (c < g.N)
-        for (int r = tr; r < g.dz_nchunk; r += 16) t += a.colsum[(int64_t)r * g.N + c];
-    red[tr][tc] = t;
+        for (int r = tr; r < g.dz_nchunk; r += rows) t += a.colsum[(int64_t)r * g.N + c];
+    red[tr * 17 + tc] = t;
     __syncthreads();
     if (tr == 0 && c < g.N) {
         float s = 0.0f;
-        for (int i = 0; i < 16; ++i) s += red[i][tc];
+        for (int i = 0; i < rows; ++i) s += red[i * 17 + tc];
         a.dbias[c] = s;
     }
 }
@@ -93,10 +98,73 @@ struct EpiStore {
     }
 };
 
+// Blocks [0, nw): dw; [nw, nw + nx): dx; the rest: dbias.
+template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
+__global__ __launch_bounds__(WM *WN * 64) void k_linear_bwd(GemmArgs dw, EpiStore<T> ew, int nw, GemmArgs dx, EpiStore<T> ex,
+                                                            int nx, LinearGeo g, LinearPtrs p) {
+    const int b = blockIdx.x;
+    if (b < nw) gemm_block<T, false, false, BM, BN, WM, WN, DIRECT>(dw, ew, b, nw);
+    else if (b < nw + nx) gemm_block<T, true, false, BM, BN, WM, WN, DIRECT>(dx, ex, b - nw, nx);
+    else dbias_block(g, p, b - nw - nx);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_linear_bwd_join(GemmArgs dw, EpiStore<T> ew, int nw, GemmArgs dx, EpiStore<T> ex) {
+    const int b = blockIdx.x;
+    if (b < nw) join_block(dw, ew, b);
+    else join_block(dx, ex, b - nw);
+}
+
+template <typename T>
+struct RunBackward {
+    const LinearGeo &g;
+    const LinearPtrs &p;
+    hipStream_t st;
+
+    template <int BM, int BN, int WM, int WN, bool DIRECT>
+    void operator()() const {
+        const void *dz = g.dz_own ? p.dz : p.dy;
+        const int64_t ldz = g.dz_own ? g.N : g.ys;
+        GemmArgs dw = {}, dx = {};
+        int64_t nw = 0, nx = 0, jw = 0, jx = 0;
+        if (p.dw) {
+            dw.A = dz;
+            dw.lda = ldz;
+            dw.B = p.x;
+            dw.ldb = g.xs;
+            dw.M = g.N;
+            dw.N = g.K;
+            dw.K = g.M;
+            nw = set_tiles<BM, BN>(dw, g.dw, p.partial_dw);
+            jw = join_blocks(dw);
+        }
+        if (p.dx && g.M > 0) {
+            dx.A = dz;
+            dx.lda = ldz;
+            dx.B = p.w;
+            dx.ldb = g.K;
+            dx.M = g.M;
+            dx.N = g.K;
+            dx.K = g.N;
+            nx = set_tiles<BM, BN>(dx, g.dx, p.partial_dx);
+            jx = join_blocks(dx);
+        }
+        const EpiStore<T> ew = {(T *)p.dw, g.K}, ex = {(T *)p.dx, g.xs};
+        const int64_t blocks = nw + nx + (p.dbias ? (g.N + 15) / 16 : 0);
+        if (blocks > 0) {
+            const auto kernel = k_linear_bwd<T, BM, BN, WM, WN, DIRECT>;
+            hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(WM * WN * 64), (tile_lds<BM, BN>(kernel)), st, dw, ew,
+                               (int)nw, dx, ex, (int)nx, g, p);
+        }
+        if (jw + jx > 0)
+            hipLaunchKernelGGL((k_linear_bwd_join<T>), dim3((unsigned)(jw + jx)), dim3(256), 0, st, dw, ew, (int)jw, dx, ex);
+    }
+};
+
 template <typename XT, typename YT>
 void backward(const LinearGeo &g, const LinearPtrs &p, hipStream_t st) {
     constexpr int V = 16 / (sizeof(XT) > sizeof(YT) ? sizeof(XT) : sizeof(YT));
-    if (g.M > 0 && (g.dz_own || p.dbias)) {
+    if (g.M > 0 && (p.dbias || (g.dz_own && (p.dx || p.dw)))) {
         const auto go = [&](auto kernel, int v) {
             const int ncol = (g.N + 64 * v - 1) / (64 * v);
             hipLaunchKernelGGL(kernel, dim3((unsigned)((int64_t)ncol * g.dz_nchunk)), dim3(256), 0, st, g, p, ncol,
@@ -105,30 +173,7 @@ void backward(const LinearGeo &g, const LinearPtrs &p, hipStream_t st) {
         if (g.N >= V) go(k_dz<XT, YT, V>, V);
         else go(k_dz<XT, YT, 1>, 1);
     }
-    if (p.dbias) hipLaunchKernelGGL(k_dbias, dim3((g.N + 15) / 16), dim3(256), 0, st, g, p);
-    const void *dz = g.dz_own ? p.dz : p.dy;
-    const int64_t ldz = g.dz_own ? g.N : g.ys;
-    GemmArgs a = {};
-    if (p.dx) {
-        a.A = dz;
-        a.lda = ldz;
-        a.B = p.w;
-        a.ldb = g.K;
-        a.M = g.M;
-        a.N = g.K;
-        a.K = g.N;
-        run_gemm<XT, true, false>(g.dx, a, EpiStore<XT>{(XT *)p.dx, g.xs}, p.partial, st);
-    }
-    if (p.dw) {
-        a.A = dz;
-        a.lda = ldz;
-        a.B = p.x;
-        a.ldb = g.xs;
-        a.M = g.N;
-        a.N = g.K;
-        a.K = g.M;
-        run_gemm<XT, false, false>(g.dw, a, EpiStore<XT>{(XT *)p.dw, g.K}, p.partial, st);
-    }
+    pick_tile(g.dw, RunBackward<XT>{g, p, st});
 }
 
 }  // namespace

@@ -55,18 +55,34 @@ struct EpiForward {
 };
 
 template <typename XT, typename YT>
+struct RunForward {
+    const LinearGeo &g;
+    const LinearPtrs &p;
+    hipStream_t st;
+
+    template <int BM, int BN, int WM, int WN, bool DIRECT>
+    void operator()() const {
+        using EPI = EpiForward<YT>;
+        const EPI epi = {p.bias, (const YT *)p.residual, (YT *)p.y, (YT *)p.z, g.ys, g.rs, g.N, g.act, g.r_planar, g.pixels};
+        GemmArgs a = {};
+        a.A = p.x;
+        a.B = p.w;
+        a.lda = g.xs;
+        a.ldb = g.K;
+        a.M = g.M;
+        a.N = g.N;
+        a.K = g.K;
+        const int64_t blocks = set_tiles<BM, BN>(a, g.f, p.partial);
+        const auto kernel = k_gemm<XT, true, true, BM, BN, WM, WN, DIRECT, EPI>;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(WM * WN * 64), (tile_lds<BM, BN>(kernel)), st, a, epi);
+        if (a.splits > 1)
+            hipLaunchKernelGGL((k_gemm_join<EPI>), dim3((unsigned)join_blocks(a)), dim3(256), 0, st, a, epi);
+    }
+};
+
+template <typename XT, typename YT>
 void forward(const LinearGeo &g, const LinearPtrs &p, hipStream_t st) {
-    GemmArgs a = {};
-    a.A = p.x;
-    a.B = p.w;
-    a.lda = g.xs;
-    a.ldb = g.K;
-    a.M = g.M;
-    a.N = g.N;
-    a.K = g.K;
-    const EpiForward<YT> epi = {p.bias, (const YT *)p.residual, (YT *)p.y, (YT *)p.z, g.ys, g.rs, g.N, g.act, g.r_planar,
-                                g.pixels};
-    run_gemm<XT, true, true>(g.f, a, epi, p.partial, st);
+    pick_tile(g.f, RunForward<XT, YT>{g, p, st});
 }
 
 }  // namespace

@@ -93,7 +93,7 @@ struct LinearGeo {
     int act;
     int64_t xs, ys, rs;       // elements between rows of x, of y and of an NHWC residual
     int r_planar, pixels;
-    GemmShape f, dx, dw;
+    GemmShape f, dx, dw;      // dx and dw share a tile: they run in one kernel
     int dz_own;               // backward: dz is written to the workspace (else it is dy itself)
     int dz_chunk, dz_nchunk;  // rows per block of the dz kernel, blocks along the rows
 };
@@ -105,7 +105,7 @@ struct LinearPtrs {
     float *dbias;
     void *dz;                 // workspace: dz in x's type
     float *colsum;            // workspace: [dz_nchunk][N] column sums
-    float *partial;           // workspace: split products
+    float *partial, *partial_dx, *partial_dw;  // workspace: split products
 };
 
 // The built tiles: rows, columns, blocks that a compute unit holds, and the
@@ -131,7 +131,7 @@ struct wq8_linear_plan {
     wq8::LinearGeo geo;
     wq8_dtype xdt, ydt;
     size_t f_off_partial, f_bytes;
-    size_t b_off_dz, b_off_colsum, b_off_partial, b_bytes;
+    size_t b_off_dz, b_off_colsum, b_off_partial, b_off_partial_dw, b_bytes;
 };
 
 struct wq8_norm_plan {

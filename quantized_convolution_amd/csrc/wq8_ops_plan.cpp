@@ -240,43 +240,65 @@ wq8_status build_norm(const wq8_norm_desc *d, wq8_norm_plan *p) {
 }
 
 // ------------------------------------------------------ product's launch shape
-// Tile and split by the least modelled time, in microseconds. A compute unit
-// works through n blocks of `steps` k steps at the tile's rate, a third more
-// slowly where it has but one block to itself; each round of blocks that it
-// holds at once adds its start and end (much of it for the largest tile, whose
-// compute unit has nothing else to do then); a split writes and reads fp32 sums
-// and launches once more. Measured against it over 40 shapes and tiles (bf16
-// 8192 x 640 x 640: 13.3, 11.2, 12.7 modelled and 13.2, 12.5, 13.4 measured for
-// 128 x 128, 128 x 64, 64 x 64; fp32 2048 x 2560 x 1280 in 64 x 64: 120 and 124,
-// split in two 112 and 113).
-GemmShape choose_gemm(int64_t M, int64_t N, int64_t K, wq8_dtype t, bool direct) {
-    const int64_t kstep = t == WQ8_F32 ? 32 : 64, steps = ceil_div64(K, kstep);
-    GemmShape best;
-    memset(&best, 0, sizeof best);
-    best.splits = 1;
+// Tiles and splits by the least modelled time, in microseconds, of one product
+// or of two that run side by side in one kernel. A compute unit works through
+// its share of the blocks at the tile's rate, a third more slowly where it has
+// but one block to itself; each round of blocks that it holds at once adds its
+// start and end (much of it for the largest tile, whose compute unit has
+// nothing else to do then); a split writes and reads fp32 sums and launches
+// once more. Measured against it over 40 shapes and tiles (bf16 8192 x 640 x
+// 640: 13.3, 11.2, 12.7 modelled and 13.2, 12.5, 13.4 measured for 128 x 128,
+// 128 x 64, 64 x 64; fp32 2048 x 2560 x 1280 in 64 x 64: 120 and 124, split in
+// two 112 and 113).
+struct Product {
+    int64_t M, N, K;
+};
+
+void choose_gemm(const Product *q, int count, wq8_dtype t, bool direct, GemmShape *const *out) {
+    constexpr int kMost = 16;  // splits
+    const int64_t kstep = t == WQ8_F32 ? 32 : 64;
     double least = 1e30;
+    for (int i = 0; i < count; ++i) memset(out[i], 0, sizeof *out[i]);
     for (int i = direct ? 0 : 1; i < kGemmTileCount; ++i) {
         const GemmTile &g = kGemmTiles[i];
-        const int64_t tiles = ceil_div64(M, g.bm) * ceil_div64(N, g.bn);
         const double rate = t == WQ8_F32 ? 0.56 * g.f32 : 5.2 * g.bf16;  // Mflop per us and compute unit
         const double step = 2e-6 * g.bm * g.bn * kstep / rate;
-        for (int64_t want = 1; want <= 16 && (want == 1 || want * 2 <= steps); ++want) {
-            const int64_t per = steps ? ceil_div64(steps, want) : 0, splits = steps ? ceil_div64(steps, per) : 1;
-            if (splits != want) continue;
-            const int64_t n = ceil_div64(tiles * splits, kCus);
-            double us = (double)n * per * step * (n == 1 && g.blocks > 1 ? 1.3 : 1.0);
+        for (int combo = 0; combo < (count == 1 ? kMost : kMost * kMost); ++combo) {
+            const int64_t want[2] = {combo % kMost + 1, combo / kMost + 1};
+            int64_t blocks = 0, work = 0, longest = 0, per[2] = {0, 0}, sp[2] = {1, 1};
+            double join = 0.0;
+            bool fits = true;
+            for (int j = 0; j < count; ++j) {
+                const int64_t steps = ceil_div64(q[j].K, kstep);
+                if (want[j] > 1 && want[j] * 2 > steps) fits = false;
+                per[j] = steps ? ceil_div64(steps, want[j]) : 0;
+                sp[j] = steps ? ceil_div64(steps, per[j]) : 1;
+                if (sp[j] != want[j]) fits = false;
+                const int64_t n = ceil_div64(q[j].M, g.bm) * ceil_div64(q[j].N, g.bn) * sp[j];
+                blocks += n;
+                work += n * per[j];
+                if (per[j] > longest) longest = per[j];
+                if (sp[j] > 1) join += (double)q[j].M * q[j].N * 8e-6 * sp[j] / 5.0;
+            }
+            if (!fits) continue;
+            const int64_t n = ceil_div64(blocks, kCus);
+            // equal blocks come in whole rounds; of two products' the rest evens out
+            double us = count == 1 ? (double)n * longest * step : (double)ceil_div64(work, kCus) * step + 0.5 * longest * step;
+            if (us < longest * step) us = longest * step;
+            if (n == 1 && g.blocks > 1) us *= 1.3;
             us += (double)ceil_div64(n, g.blocks) * (i == 0 ? 10.0 : i == 1 ? 4.0 : 2.5);
-            if (splits > 1) us += 3.0 + (double)M * N * 8e-6 * splits / 5.0;
+            if (join > 0.0) us += 3.0 + join;
             if (us < least) {
                 least = us;
-                best.tile = i;
-                best.splits = (int)splits;
-                best.ksteps = (int)per;
+                for (int j = 0; j < count; ++j) {
+                    out[j]->tile = i;
+                    out[j]->direct = direct;
+                    out[j]->splits = (int)sp[j];
+                    out[j]->ksteps = (int)per[j];
+                }
             }
         }
     }
-    best.direct = direct;
-    return best;
 }
 
 // Whether an operand's k steps can go to LDS directly: rows that start on 16
@@ -326,14 +348,19 @@ wq8_status build_linear(const wq8_linear_desc *d, wq8_linear_plan *p) {
     g.dz_nchunk = ceil_div(g.M, g.dz_chunk);
     const int64_t ldz = g.dz_own ? g.N : g.ys;
     const wq8_dtype t = p->xdt;
-    g.f = choose_gemm(g.M, g.N, g.K, t, direct_ok(t, g.xs, true, g.M) && direct_ok(t, g.K, true, g.N));
-    g.dx = choose_gemm(g.M, g.K, g.N, t, direct_ok(t, ldz, true, g.M) && direct_ok(t, g.K, false, g.K));
-    g.dw = choose_gemm(g.N, g.K, g.M, t, direct_ok(t, ldz, false, g.N) && direct_ok(t, g.xs, false, g.K));
+    const Product f = {g.M, g.N, g.K}, bwd[2] = {{g.N, g.K, g.M}, {g.M, g.K, g.N}};
+    GemmShape *const fs[1] = {&g.f}, *const bs[2] = {&g.dw, &g.dx};
+    choose_gemm(&f, 1, t, direct_ok(t, g.xs, true, g.M) && direct_ok(t, g.K, true, g.N), fs);
+    choose_gemm(bwd, 2, t,
+                direct_ok(t, ldz, true, g.M) && direct_ok(t, g.K, false, g.K) && direct_ok(t, ldz, false, g.N) &&
+                    direct_ok(t, g.xs, false, g.K),
+                bs);
     const auto tiles = [](const GemmShape &s, int64_t M, int64_t N) {
         return ceil_div64(M, kGemmTiles[s.tile].bm) * ceil_div64(N, kGemmTiles[s.tile].bn) * s.splits;
     };
     const int64_t lim = (int64_t)1 << 31;
-    if (ceil_div64(g.N, 64) * g.dz_nchunk >= lim || tiles(g.f, g.M, g.N) >= lim || tiles(g.dx, g.M, g.K) >= lim || tiles(g.dw, g.N, g.K) >= lim)
+    if (ceil_div64(g.N, 64) * g.dz_nchunk >= lim || tiles(g.f, g.M, g.N) >= lim ||
+        tiles(g.dx, g.M, g.K) + tiles(g.dw, g.N, g.K) + g.N >= lim)
         return fail(WQ8_ERR_UNSUPPORTED, "more than 2^31 blocks");
     const size_t M = g.M, N = g.N, K = g.K;
     const auto partial = [](const GemmShape &s, size_t m, size_t n) { return s.splits > 1 ? s.splits * m * n * 4 : 0; };
@@ -342,8 +369,8 @@ wq8_status build_linear(const wq8_linear_desc *d, wq8_linear_plan *p) {
     p->b_off_dz = 0;
     p->b_off_colsum = g.dz_own ? round_up(M * N * size_of(p->xdt), 256) : 0;
     p->b_off_partial = p->b_off_colsum + round_up((size_t)g.dz_nchunk * N * 4, 256);
-    const size_t pdx = partial(g.dx, M, K), pdw = partial(g.dw, N, K);
-    p->b_bytes = p->b_off_partial + (pdx > pdw ? pdx : pdw);
+    p->b_off_partial_dw = p->b_off_partial + round_up(partial(g.dx, M, K), 256);
+    p->b_bytes = p->b_off_partial_dw + partial(g.dw, N, K);
     return WQ8_OK;
 }
 
@@ -528,7 +555,8 @@ wq8_status wq8_linear_backward(const wq8_linear_plan *p, const void *dy, const v
     a.dbias = dbias;
     a.dz = p->geo.dz_own ? (void *)(ws + p->b_off_dz) : nullptr;
     a.colsum = (float *)(ws + p->b_off_colsum);
-    a.partial = (float *)(ws + p->b_off_partial);
+    a.partial_dx = (float *)(ws + p->b_off_partial);
+    a.partial_dw = (float *)(ws + p->b_off_partial_dw);
     return launch_linear_backward(p->geo, p->xdt, p->ydt, a, stream);
 }
 
