@@ -184,36 +184,69 @@ __device__ __forceinline__ T *tile_addr(T *t, const NormGeo &g, const Where &w, 
               : t + ((int64_t)w.n * g.P + p + row) * stride + w.slab0 + at;
 }
 
+// The tile's vectors are shared out over the block, 4 to a thread at a time with
+// their loads in flight. A vector that would pass the end of its row starts
+// earlier and carries some values twice.
+constexpr int kTileBatch = 4;
+
+template <typename T, bool CL, typename F>
+__device__ __forceinline__ void for_tile(const NormShape &s, const Where &w, int p, F f) {
+    constexpr int VO = 16 / sizeof(T);
+    int outer, inner;
+    tile_extent<CL>(s, w, p, outer, inner);
+    const int nv = (inner + VO - 1) / VO, total = outer * nv;
+    for (int i0 = threadIdx.x; i0 < total; i0 += kTileBatch * blockDim.x) {
+        int row[kTileBatch], at[kTileBatch];
+#pragma unroll
+        for (int j = 0; j < kTileBatch; ++j) {
+            const int i = min(i0 + j * (int)blockDim.x, total - 1);
+            row[j] = i / nv;
+            at[j] = min((i - row[j] * nv) * VO, max(inner - VO, 0));
+        }
+        f(row, at, inner);
+    }
+}
+
 template <typename T, bool CL>
 __device__ __forceinline__ void tile_to_global(const T *tile, T *t, const NormGeo &g, const NormShape &s, const Where &w,
                                                int64_t stride, int p) {
     constexpr int VO = 16 / sizeof(T);
-    int outer, inner;
-    tile_extent<CL>(s, w, p, outer, inner);
-    const int nv = (inner + VO - 1) / VO, row = tile_row<CL>(s);
-    for (int i = threadIdx.x; i < outer * nv; i += blockDim.x) {
-        const int o = i / nv, v = (i - o * nv) * VO;
-        Vec<T, VO> r;
+    const int trow = tile_row<CL>(s);
+    for_tile<T, CL>(s, w, p, [&](const int *row, const int *at, int inner) {
 #pragma unroll
-        for (int k = 0; k < VO; ++k) r.v[k] = v + k < inner ? tile[o * row + v + k] : T(0);
-        store_vec_n<T, VO>(tile_addr<T, CL>(t, g, w, stride, p, o, v), r, inner - v);
-    }
+        for (int j = 0; j < kTileBatch; ++j) {
+            Vec<T, VO> r;
+#pragma unroll
+            for (int k = 0; k < VO; ++k) r.v[k] = tile[row[j] * trow + at[j] + (inner < VO ? min(k, inner - 1) : k)];
+            T *const to = tile_addr<T, CL>(t, g, w, stride, p, row[j], at[j]);
+            if (inner >= VO) store_vec<T, VO>(to, r);
+            else store_vec_n<T, VO>(to, r, inner);
+        }
+    });
 }
 
 template <typename T, bool CL>
 __device__ __forceinline__ void global_to_tile(T *tile, const T *t, const NormGeo &g, const NormShape &s, const Where &w,
                                                int64_t stride, int p) {
     constexpr int VO = 16 / sizeof(T);
-    int outer, inner;
-    tile_extent<CL>(s, w, p, outer, inner);
-    const int nv = (inner + VO - 1) / VO, row = tile_row<CL>(s);
-    for (int i = threadIdx.x; i < outer * nv; i += blockDim.x) {
-        const int o = i / nv, v = (i - o * nv) * VO;
-        const Vec<T, VO> r = load_vec_n<T, VO>(tile_addr<const T, CL>(t, g, w, stride, p, o, v), inner - v);
+    const int trow = tile_row<CL>(s);
+    for_tile<T, CL>(s, w, p, [&](const int *row, const int *at, int inner) {
+        Vec<T, VO> r[kTileBatch];
+        if (inner >= VO) {
 #pragma unroll
-        for (int k = 0; k < VO; ++k)
-            if (v + k < inner) tile[o * row + v + k] = r.v[k];
-    }
+            for (int j = 0; j < kTileBatch; ++j)
+                r[j] = load_vec<T, VO>(tile_addr<const T, CL>(t, g, w, stride, p, row[j], at[j]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < kTileBatch; ++j)
+                r[j] = load_vec_n<T, VO>(tile_addr<const T, CL>(t, g, w, stride, p, row[j], at[j]), inner);
+        }
+#pragma unroll
+        for (int j = 0; j < kTileBatch; ++j)
+#pragma unroll
+            for (int k = 0; k < VO; ++k)
+                if (k < inner) tile[row[j] * trow + at[j] + k] = r[j].v[k];
+    });
 }
 
 // The tile's place of value k of a vector that starts at pixel p; the tile
