@@ -1,0 +1,126 @@
+"""The operators together: a residual block around the quantized convolutions
+and a feed forward with its gradients, on other streams and under graph capture."""
+import pytest
+import torch
+
+import ops_reference as R
+import quantized_convolution_amd as q
+from quantized_convolution_amd.unet_block import FeedForward, ResBlock
+
+pytestmark = pytest.mark.gpu
+F32, BF = torch.float32, torch.bfloat16
+N, CI, CO, H, W, CT, E = 2, 64, 96, 13, 10, 20, 48
+
+
+def res_weights(dtype, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    w = dict(conv1=0.05 * r(CO, CI, 3, 3), conv2=0.05 * r(CO, CO, 3, 3), norm1=(1 + 0.1 * r(CI), 0.1 * r(CI)),
+             norm2=(1 + 0.1 * r(CO), 0.1 * r(CO)), temb1=(0.2 * r(E, CT)).to(dtype), temb2=(0.2 * r(CO, E)).to(dtype),
+             shortcut=(0.1 * r(CO, CI)).to(dtype), temb1_b=0.1 * r(E), temb2_b=0.1 * r(CO), shortcut_b=0.1 * r(CO))
+    x, t = r(N, H, W, CI).to(dtype), r(N, CT).to(dtype)
+    move = lambda v: tuple(i.cuda() for i in v) if isinstance(v, tuple) else v.cuda()  # noqa: E731
+    return {k: move(v) for k, v in w.items()}, x.cuda(), t.cuda()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_res_block(dtype):
+    """Each operator of the block against its definition on the input that it was given."""
+    w, x, t = res_weights(dtype)
+    b = ResBlock(w, N, CI, CO, H, W, dtype=dtype)
+    out = b(x, t)
+    torch.cuda.synchronize()
+    c = lambda v: v.cpu()  # noqa: E731
+    R.check(b.e1, *R.linear_forward(c(t), c(w["temb1"]), c(w["temb1_b"]), None, "silu", dtype)[0], "temb1")
+    R.check(b.shift, *R.linear_forward(c(b.e1), c(w["temb2"]), c(w["temb2_b"]), None, "none", F32)[0], "shift")
+    n1 = R.Norm(c(x), 32, 1e-5, "silu", None, *map(c, w["norm1"]))
+    R.check(R.nhwc(b.a1, "nchw"), n1.y, n1.forward_errors(dtype)[2], "norm1")
+    assert torch.equal(b.h1, q.wq8_conv_forward(b.conv1, b.a1, *b.q1))
+    n2 = R.Norm(R.nhwc(c(b.h1), "nchw"), 32, 1e-5, "silu", c(b.shift), *map(c, w["norm2"]))
+    R.check(R.nhwc(b.a2, "nchw"), n2.y, n2.forward_errors(dtype)[2], "norm2")
+    assert torch.equal(b.h2, q.wq8_conv_forward(b.conv2, b.a2, *b.q2))
+    res = R.nhwc(c(b.h2), "nchw").reshape(-1, CO)
+    y, bound = R.linear_forward(c(x).reshape(-1, CI), c(w["shortcut"]), c(w["shortcut_b"]), res, "none", dtype)[0]
+    R.check(out.reshape(-1, CO), y, bound, "out")
+
+
+def ff_weights(dtype, C=64, D=160, seed=1):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    w = dict(norm=(1 + 0.1 * r(C), 0.1 * r(C)), w1=(r(D, C) / C ** 0.5).to(dtype), w2=(r(C, D) / D ** 0.5).to(dtype),
+             b1=0.1 * r(D), b2=0.1 * r(C))
+    return w, r(N, H, W, C).to(dtype), r(N, H, W, C).to(dtype)
+
+
+@pytest.mark.parametrize("dtype,tol", [(F32, 2e-5), (BF, 3e-2)])
+def test_feed_forward_gradients(dtype, tol):
+    """Against automatic differentiation in 64 bits. tol, relative in the 2-norm:
+    fp32 rounding through three operators, and in bf16 5 roundings of 2^-8 of
+    what passes between them."""
+    w, x, dy = ff_weights(dtype)
+    move = lambda v: tuple(i.cuda() for i in v) if isinstance(v, tuple) else v.cuda()  # noqa: E731
+    ff = FeedForward({k: move(v) for k, v in w.items()}, N, x.shape[3], H, W, dtype=dtype)
+    out = ff(x.cuda())
+    grads = ff.backward(dy.cuda())
+    torch.cuda.synchronize()
+    p = {k: v.double().requires_grad_() for k, v in dict(x=x, gamma=w["norm"][0], beta=w["norm"][1], w1=w["w1"], b1=w["b1"],
+                                                       w2=w["w2"], b2=w["b2"]).items()}
+    v = p["x"].reshape(N, H * W, 32, -1)
+    d = v - v.mean(dim=(1, 3), keepdim=True)
+    a = (d / torch.sqrt((d * d).mean(dim=(1, 3), keepdim=True) + 1e-5)).reshape(x.shape) * p["gamma"] + p["beta"]
+    y = p["x"] + torch.nn.functional.gelu(a @ p["w1"].T + p["b1"]) @ p["w2"].T + p["b2"]
+    want = dict(zip(p, torch.autograd.grad(y, list(p.values()), dy.double())))
+    off = lambda g, r: ((g.cpu().double() - r).norm() / r.norm()).item()  # noqa: E731
+    assert off(out, y.detach()) < tol
+    for k, r in want.items():
+        assert off(grads[k], r) < tol, k
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_other_stream(dtype):
+    """Work given to a stream runs there, in order, whatever the current one is."""
+    w, x, dy = ff_weights(dtype)
+    C, rows = x.shape[3], N * H * W
+    norm, lin = q.NormPlan(N, C, H, W, x_dtype=dtype), q.LinearPlan(rows, C, C, act="silu", x_dtype=dtype)
+    x, wt = x.cuda(), w["w1"][:C].contiguous().cuda()
+    a, y = norm.empty_output(), lin.empty_output()
+    want = q.wq8_linear_forward(lin, q.wq8_norm_forward(norm, x).view(rows, C), wt)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    q.wq8_norm_forward(norm, x, y=a, stream=s)
+    q.wq8_linear_forward(lin, a.view(rows, C), wt, y=y, stream=s)
+    s.synchronize()
+    assert torch.equal(y, want)
+    with torch.cuda.stream(s):
+        b = q.wq8_linear_forward(lin, q.wq8_norm_forward(norm, x).view(rows, C), wt)
+    s.synchronize()
+    assert torch.equal(b, want)
+
+
+def test_graph_capture():
+    """Forward and backward in one graph, replayed with new inputs between eager passes."""
+    w, x, dy = ff_weights(BF)
+    move = lambda v: tuple(i.cuda() for i in v) if isinstance(v, tuple) else v.cuda()  # noqa: E731
+    w = {k: move(v) for k, v in w.items()}
+    ff, eager = (FeedForward(w, N, x.shape[3], H, W) for _ in range(2))
+    xs, ds = x.cuda(), dy.cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ff(xs)
+        ff.backward(ds)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ff(xs)
+        grads = ff.backward(ds)
+    g = torch.Generator().manual_seed(3)
+    for _ in range(4):
+        xs.copy_(torch.randn(xs.shape, generator=g))
+        ds.copy_(torch.randn(ds.shape, generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, wg = eager(xs), eager.backward(ds)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert all(torch.equal(grads[k], wg[k]) for k in wg)
