@@ -15,8 +15,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libwino_q8_conv.so")
 SOURCES = ["wq8_kernels.hip", "wq8_hgemm.hip", "wq8_direct.hip", "wq8_noalloc.hip", "wq8_plan.cpp", "wq8_api.cpp",
-           "wq8_norm_fwd_f32.hip", "wq8_norm_fwd_bf16.hip", "wq8_norm_bwd_f32.hip", "wq8_norm_bwd_bf16.hip",
-           "wq8_linear_fwd.hip", "wq8_linear_bwd.hip", "wq8_ops_plan.cpp"]
+           "wq8_norm_fwd_f32_f32.hip", "wq8_norm_fwd_f32_bf16.hip", "wq8_norm_fwd_bf16_f32.hip",
+           "wq8_norm_fwd_bf16_bf16.hip", "wq8_norm_bwd_f32.hip", "wq8_norm_bwd_bf16.hip", "wq8_linear_fwd_f32.hip",
+           "wq8_linear_fwd_bf16.hip", "wq8_linear_bwd.hip", "wq8_ops_plan.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -1,4 +1,6 @@
 // Matrix product with bias, activation and residual: y = act(x w^T + bias) + residual.
+#pragma once
+
 #include "wq8_gemm_device.h"
 
 namespace wq8 {
@@ -80,23 +82,13 @@ struct RunForward {
     }
 };
 
-template <typename XT, typename YT>
-void forward(const LinearGeo &g, const LinearPtrs &p, hipStream_t st) {
-    pick_tile(g.f, RunForward<XT, YT>{g, p, st});
-}
-
-}  // namespace
-
-wq8_status launch_linear_forward(const LinearGeo &g, wq8_dtype xdt, wq8_dtype ydt, const LinearPtrs &p, void *stream) {
+template <typename XT>
+wq8_status linear_forward(const LinearGeo &g, wq8_dtype ydt, const LinearPtrs &p, void *stream) {
     const hipStream_t st = (hipStream_t)stream;
-    if (xdt == WQ8_F32) {
-        if (ydt == WQ8_F32) forward<float, float>(g, p, st);
-        else forward<float, bf16_t>(g, p, st);
-    } else {
-        if (ydt == WQ8_F32) forward<bf16_t, float>(g, p, st);
-        else forward<bf16_t, bf16_t>(g, p, st);
-    }
+    if (ydt == WQ8_F32) pick_tile(g.f, RunForward<XT, float>{g, p, st});
+    else pick_tile(g.f, RunForward<XT, bf16_t>{g, p, st});
     return check_launch("matrix product");
 }
 
+}  // namespace
 }  // namespace wq8

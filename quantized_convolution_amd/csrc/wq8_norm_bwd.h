@@ -331,7 +331,10 @@ struct RunBackward {
 template <typename XT>
 wq8_status norm_backward(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, void *stream) {
     const hipStream_t st = (hipStream_t)stream;
-    if (g.N > 0) pick_kernel<true, XT>(g, ydt, RunBackward{g, p, st});
+    if (g.N > 0) {
+        if (ydt == WQ8_F32) pick_vector<true, XT, float>(g, RunBackward{g, p, st});
+        else pick_vector<true, XT, bf16_t>(g, RunBackward{g, p, st});
+    }
     if (p.dgamma || p.dbeta || (p.dshift && g.N > 0)) {
         const int ncol = (g.C + 15) / 16, rows = p.dshift ? g.N + 1 : 1;
         hipLaunchKernelGGL(k_norm_params, dim3((unsigned)((int64_t)ncol * rows)), dim3(256), 0, st, g, p, ncol, !p.dshift);

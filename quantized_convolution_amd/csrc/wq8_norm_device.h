@@ -450,11 +450,5 @@ void pick_vector(const NormGeo &g, const R &run) {
     pick_steps<BWD, XT, YT, 4, kUniform>(g, run);
 }
 
-template <bool BWD, typename XT, typename R>
-void pick_kernel(const NormGeo &g, wq8_dtype ydt, const R &run) {
-    if (ydt == WQ8_F32) pick_vector<BWD, XT, float>(g, run);
-    else pick_vector<BWD, XT, bf16_t>(g, run);
-}
-
 }  // namespace
 }  // namespace wq8

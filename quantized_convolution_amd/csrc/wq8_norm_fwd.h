@@ -320,9 +320,9 @@ struct RunForward {
     }
 };
 
-template <typename XT>
-wq8_status norm_forward(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, void *stream) {
-    pick_kernel<false, XT>(g, ydt, RunForward{g, p, (hipStream_t)stream});
+template <typename XT, typename YT>
+wq8_status norm_forward(const NormGeo &g, const NormPtrs &p, void *stream) {
+    pick_vector<false, XT, YT>(g, RunForward{g, p, (hipStream_t)stream});
     return check_launch("group norm");
 }
 

@@ -69,9 +69,11 @@ struct NormPtrs {
     float *group;                        // backward, split: [N][G][2] group means
 };
 
-// By the type of x (one source file each).
-wq8_status launch_norm_forward_f32(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, void *stream);
-wq8_status launch_norm_forward_bf16(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, void *stream);
+// By types: the kernels of each are compiled in a file of their own.
+wq8_status launch_norm_forward_f32_f32(const NormGeo &g, const NormPtrs &p, void *stream);
+wq8_status launch_norm_forward_f32_bf16(const NormGeo &g, const NormPtrs &p, void *stream);
+wq8_status launch_norm_forward_bf16_f32(const NormGeo &g, const NormPtrs &p, void *stream);
+wq8_status launch_norm_forward_bf16_bf16(const NormGeo &g, const NormPtrs &p, void *stream);
 wq8_status launch_norm_backward_f32(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, void *stream);
 wq8_status launch_norm_backward_bf16(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, void *stream);
 
@@ -120,8 +122,8 @@ constexpr GemmTile kGemmTiles[] = {
     {256, 256, 1, 1.0, 1.0}, {128, 128, 2, 0.86, 0.98}, {128, 64, 3, 0.69, 0.98}, {64, 64, 5, 0.49, 0.96}, {16, 128, 4, 0.3, 0.5}};
 constexpr int kGemmTileCount = 5;
 
-wq8_status launch_linear_forward(const LinearGeo &g, wq8_dtype xdt, wq8_dtype ydt,
-                                 const LinearPtrs &p, void *stream);
+wq8_status launch_linear_forward_f32(const LinearGeo &g, wq8_dtype ydt, const LinearPtrs &p, void *stream);
+wq8_status launch_linear_forward_bf16(const LinearGeo &g, wq8_dtype ydt, const LinearPtrs &p, void *stream);
 wq8_status launch_linear_backward(const LinearGeo &g, wq8_dtype xdt, wq8_dtype ydt,
                                   const LinearPtrs &p, void *stream);
 

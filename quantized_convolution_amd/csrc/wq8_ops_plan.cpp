@@ -437,7 +437,9 @@ wq8_status wq8_norm_forward(const wq8_norm_plan *p, const void *x, const float *
     a.mean = mean ? mean : stats;
     a.rstd = rstd ? rstd : stats + (size_t)p->geo.N * p->geo.G;
     a.part = (float *)((char *)workspace + p->f_off_part);
-    return (p->xdt == WQ8_F32 ? launch_norm_forward_f32 : launch_norm_forward_bf16)(p->geo, p->ydt, a, stream);
+    if (p->xdt == WQ8_F32)
+        return (p->ydt == WQ8_F32 ? launch_norm_forward_f32_f32 : launch_norm_forward_f32_bf16)(p->geo, a, stream);
+    return (p->ydt == WQ8_F32 ? launch_norm_forward_bf16_f32 : launch_norm_forward_bf16_bf16)(p->geo, a, stream);
 }
 
 wq8_status wq8_norm_backward(const wq8_norm_plan *p, const void *dy, const void *x, const float *shift,
@@ -521,7 +523,7 @@ wq8_status wq8_linear_forward(const wq8_linear_plan *p, const void *x, const voi
     a.y = y;
     a.z = z;
     a.partial = (float *)((char *)workspace + p->f_off_partial);
-    return launch_linear_forward(p->geo, p->xdt, p->ydt, a, stream);
+    return (p->xdt == WQ8_F32 ? launch_linear_forward_f32 : launch_linear_forward_bf16)(p->geo, p->ydt, a, stream);
 }
 
 wq8_status wq8_linear_backward(const wq8_linear_plan *p, const void *dy, const void *x, const void *w, const void *z,
