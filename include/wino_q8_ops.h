@@ -44,9 +44,11 @@ typedef enum { WQ8_NHWC = 0, WQ8_NCHW = 1 } wq8_layout;
  *   dz = dy act'(z);  dbeta = sum_{n,p} dz;  dgamma = sum_{n,p} dz h
  *   t = gamma dz;  dx = rstd (t - mean_g t - h mean_g(t h))
  *   dshift[n][c] = sum_p dx
- * All of it in fp32 (the deviations' squares are summed about the mean, not
- * as a difference of two sums); x and y are rounded to their type once. Sums
- * are taken in a fixed order: results repeat bit for bit. */
+ * All of it in fp32. Squared deviations are summed about the mean, or about
+ * the mean of some of a thread's own values with the difference taken off:
+ * a mean far from zero costs no more than its own rounding. x and y are
+ * rounded to their type once. Sums are taken in a fixed order: results repeat
+ * bit for bit. */
 typedef struct wq8_norm_plan wq8_norm_plan; /* opaque */
 
 typedef struct {

@@ -7,6 +7,14 @@
 // operand whose row index is contiguous goes through the transposing LDS
 // reads, so nothing is transposed in memory. A last kernel joins the sums of
 // products that are split along k.
+//
+// dz is rounded to bf16 for bf16 products (their operand type; dbias sums the
+// unrounded values), which adds as much error to dx and dw as their own final
+// rounding. Measured: 8192 x 640 x 2560 bf16 with gelu 115 us, of it dz 26 us
+// (126 MB, 4.8 TB/s, bound by memory), the products 84 us (640 TFLOP/s) and the
+// join 7 us; 1001 x 333 x 515 fp32, rows at odd addresses, 23 us in kernels of
+// 4, 17 and 4 us, bound by launches and load latency. One kernel for both
+// products instead of two, a join each and one for dbias: 127 and 36 us before.
 #include "wq8_gemm_device.h"
 
 namespace wq8 {
