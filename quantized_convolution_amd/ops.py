@@ -50,11 +50,15 @@ class _Plan:
         f, b = C.c_size_t(), C.c_size_t()
         _check(getattr(lib, f"wq8_{self._kind}_plan_query")(h, C.byref(f), C.byref(b)))
         self.workspace_bytes, self.backward_workspace_bytes = f.value, b.value
+        self._forward = getattr(lib, f"wq8_{self._kind}_forward")
+        self._backward = getattr(lib, f"wq8_{self._kind}_backward")
+        self._destroy = getattr(lib, f"wq8_{self._kind}_plan_destroy")
 
     def __del__(self):
-        if getattr(self, "_h", None) is not None:
-            getattr(load(), f"wq8_{self._kind}_plan_destroy")(self._h)
-            self._h = None
+        # the module's own names may be gone when the interpreter ends
+        if getattr(self, "_destroy", None) is not None:
+            self._destroy(self._h)
+            self._destroy = None
 
     @property
     def handle(self):
@@ -176,24 +180,25 @@ class _Args:
 
     def need(self, t, name, dtype, shape, strides=None):
         """The tensor's address."""
-        if not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name} is required" if t is None else f"{name} must be a torch tensor")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if strides is None:
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-        elif any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
-            raise ValueError(f"{name} must have strides {tuple(strides)}, got {tuple(t.stride())}")
-        d = t.get_device()
-        if self.device is None:
-            self.device = d
-            self.where = (t, name)
-        elif d != self.device:
-            raise ValueError(f"{name} is on {t.device}, {self.where[1]} on {self.where[0].device}")
-        return t.data_ptr()
+        try:
+            if t.dtype != dtype:
+                raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+            if strides is None:
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+            elif any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
+                raise ValueError(f"{name} must have strides {tuple(strides)}, got {tuple(t.stride())}")
+            d = t.get_device()
+            if d != self.device:
+                if self.device is not None:
+                    raise ValueError(f"{name} is on {t.device}, {self.where[1]} on {self.where[0].device}")
+                self.device = d
+                self.where = (t, name)
+            return t.data_ptr()
+        except AttributeError:
+            raise ValueError(f"{name} is required" if t is None else f"{name} must be a torch tensor") from None
 
     def optional(self, t, name, dtype, shape, strides=None):
         return None if t is None else self.need(t, name, dtype, shape, strides)
@@ -253,7 +258,7 @@ def wq8_norm_forward(plan: NormPlan, x, gamma=None, beta=None, shift=None, y=Non
     pm = a.optional(mean, "mean", f32, (plan.N, plan.groups))
     pr = a.optional(rstd, "rstd", f32, (plan.N, plan.groups))
     pw, nw = a.workspace(workspace, plan.workspace_bytes)
-    a.call(load().wq8_norm_forward, (plan.handle, px, ps, pg, pb, py, pm, pr, pw, nw), stream)
+    a.call(plan._forward, (plan._h, px, ps, pg, pb, py, pm, pr, pw, nw), stream)
     return (y, mean, rstd) if want_stats else y
 
 
@@ -283,7 +288,7 @@ def wq8_norm_backward(plan: NormPlan, dy, x, mean, rstd, gamma=None, beta=None, 
     pdb = a.optional(dbeta, "dbeta", f32, (C_,))
     pds = a.optional(dshift, "dshift", f32, (plan.N, C_))
     pw, nw = a.workspace(workspace, plan.backward_workspace_bytes)
-    a.call(load().wq8_norm_backward, (plan.handle, pdy, px, ps, pg, pb, pm, pr, pdx, pdg, pdb, pds, pw, nw), stream)
+    a.call(plan._backward, (plan._h, pdy, px, ps, pg, pb, pm, pr, pdx, pdg, pdb, pds, pw, nw), stream)
     return dx, dgamma, dbeta, dshift
 
 
@@ -302,7 +307,7 @@ def wq8_linear_forward(plan: LinearPlan, x, w, bias=None, residual=None, y=None,
     py = a.need(y, "y", plan.y_dtype, plan.y_shape, plan.y_strides)
     pz = a.optional(z, "z", plan.y_dtype, plan.y_shape)
     ws, nw = a.workspace(workspace, plan.workspace_bytes)
-    a.call(load().wq8_linear_forward, (plan.handle, px, pw, pb, pr, py, pz, ws, nw), stream)
+    a.call(plan._forward, (plan._h, px, pw, pb, pr, py, pz, ws, nw), stream)
     return (y, z) if want_z else y
 
 
@@ -324,5 +329,5 @@ def wq8_linear_backward(plan: LinearPlan, dy, x, w, z=None, dx=None, dw=None, db
     pdw = a.optional(dw, "dw", plan.x_dtype, plan.w_shape)
     pdb = a.optional(dbias, "dbias", torch.float32, (plan.Cout,))
     ws, nw = a.workspace(workspace, plan.backward_workspace_bytes)
-    a.call(load().wq8_linear_backward, (plan.handle, pdy, px, pw, pz, pdx, pdw, pdb, ws, nw), stream)
+    a.call(plan._backward, (plan._h, pdy, px, pw, pz, pdx, pdw, pdb, ws, nw), stream)
     return dx, dw, dbias
