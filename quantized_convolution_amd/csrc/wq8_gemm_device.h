@@ -230,11 +230,20 @@ __device__ __forceinline__ void mma(f32x4 &acc, const Frag<float> &n, const Frag
     acc = __builtin_amdgcn_mfma_f32_16x16x4f32(n.v[e], m.v[e], acc, 0, 0, 0);
 }
 
-// EPI: run(each) calls each(f) once, and each calls f(m, n, 8 sums of columns
-// n.., how many of them exist) for all of a thread's sums.
+// EPI, an epilogue: column(n) and item(m, n) read, for any m and n, what belongs
+// to 8 columns and to 8 columns of a row; with(f) calls f once with the
+// activation; store<ACT>(m, n, 8 sums, how many exist, column, item) ends it.
 // DIRECT: whole k steps go from memory to LDS without registers; a last partial
 // one, and every one of operands that are not aligned for that, goes through
 // registers. Two buffers: while one is multiplied the other is filled.
+// The 8 adjacent columns that a lane has in a pair of tiles.
+__device__ __forceinline__ Vec<float, 8> sums(const f32x4 &even, const f32x4 &odd) {
+    Vec<float, 8> r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r.v[e] = even[e], r.v[4 + e] = odd[e];
+    return r;
+}
+
 // The b-th of a product's nb blocks.
 template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool DIRECT, typename EPI>
 __device__ __forceinline__ void gemm_block(const GemmArgs &a, const EPI &epi, int b, int nb) {
@@ -319,28 +328,45 @@ __device__ __forceinline__ void gemm_block(const GemmArgs &a, const EPI &epi, in
         }
     }
 
-    const auto each = [&](auto f) {
+    if (a.partial) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int m = m0 + wm + i * 16 + (lane & 15);
-            if (m >= a.M) continue;
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; j += 2) {
-                const int n = n0 + wn + j * 16 + (lane >> 4) * 8, cnt = a.N - n;
-                if (cnt <= 0) continue;
-                Vec<float, 8> r;
+                const int m = m0 + wm + i * 16 + (lane & 15), n = n0 + wn + j * 16 + (lane >> 4) * 8;
+                if (m < a.M && n < a.N)
+                    store_vec_n<float, 8>(a.partial + ((int64_t)split * a.M + m) * a.N + n, sums(acc[i][j], acc[i][j + 1]),
+                                          a.N - n);
+            }
+        return;
+    }
+    // what the epilogue reads is on its way a row of tiles ahead
+    const int mr = m0 + wm + (lane & 15), nc = n0 + wn + (lane >> 4) * 8;
+    typename EPI::Column col[TN / 2];
+    typename EPI::Item next[TN / 2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) r.v[e] = acc[i][j + e / 4][e % 4];
-                f(m, n, r, cnt);
+    for (int j = 0; j < TN / 2; ++j) {
+        col[j] = epi.column(nc + j * 32);
+        next[j] = epi.item(mr, nc + j * 32);
+    }
+    epi.with([&](auto act) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            typename EPI::Item item[TN / 2];
+#pragma unroll
+            for (int j = 0; j < TN / 2; ++j) {
+                item[j] = next[j];
+                if (i + 1 < TM) next[j] = epi.item(mr + (i + 1) * 16, nc + j * 32);
+            }
+#pragma unroll
+            for (int j = 0; j < TN / 2; ++j) {
+                const int m = mr + i * 16, n = nc + j * 32;
+                if (m < a.M && n < a.N)
+                    epi.template store<decltype(act)::value>(m, n, sums(acc[i][2 * j], acc[i][2 * j + 1]), a.N - n, col[j],
+                                                             item[j]);
             }
         }
-    };
-    if (a.partial)
-        each([&](int m, int n, const Vec<float, 8> &r, int cnt) {
-            store_vec_n<float, 8>(a.partial + ((int64_t)split * a.M + m) * a.N + n, r, cnt);
-        });
-    else
-        epi.run(each);
+    });
 }
 
 template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool DIRECT, typename EPI>
@@ -364,7 +390,9 @@ __device__ __forceinline__ void join_block(const GemmArgs &a, const EPI &epi, in
 #pragma unroll
         for (int e = 0; e < 8; ++e) s.v[e] += v.v[e];
     }
-    epi.run([&](auto f) { f(m, n, s, a.N - n); });
+    const auto column = epi.column(n);
+    const auto item = epi.item(m, n);
+    epi.with([&](auto act) { epi.template store<decltype(act)::value>(m, n, s, a.N - n, column, item); });
 }
 inline int64_t join_blocks(const GemmArgs &a) {
     return a.splits > 1 ? (int64_t)((a.M + 15) / 16) * ((a.N + 127) / 128) : 0;

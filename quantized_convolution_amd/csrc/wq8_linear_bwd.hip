@@ -95,14 +95,21 @@ struct EpiStore {
     T *out;
     int64_t ld;
 
-    template <typename EACH>
-    __device__ __forceinline__ void run(EACH each) const {
-        each([&](int m, int n, const Vec<float, 8> &v, int cnt) {
-            Vec<T, 8> r;
+    struct Column {};
+    struct Item {};
+    __device__ __forceinline__ Column column(int) const { return {}; }
+    __device__ __forceinline__ Item item(int, int) const { return {}; }
+    template <typename F>
+    __device__ __forceinline__ void with(F f) const {
+        f(std::integral_constant<int, WQ8_ACT_NONE>{});
+    }
+
+    template <int ACT>
+    __device__ __forceinline__ void store(int m, int n, const Vec<float, 8> &v, int cnt, Column, Item) const {
+        Vec<T, 8> r;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r.v[e] = from_f32<T>(v.v[e]);
-            store_vec_n<T, 8>(out + (int64_t)m * ld + n, r, cnt);
-        });
+        for (int e = 0; e < 8; ++e) r.v[e] = from_f32<T>(v.v[e]);
+        store_vec_n<T, 8>(out + (int64_t)m * ld + n, r, cnt);
     }
 };
 

@@ -16,28 +16,58 @@
 namespace wq8 {
 namespace {
 
+static __device__ const float kNothing[8] = {};
+
 template <typename YT>
 struct EpiForward {
     const float *bias;
     const YT *residual;
     YT *y, *z;
     int64_t ys, rs;
-    int N, act, planar, pixels;
+    int M, N, act, planar, pixels;
 
-    template <typename EACH>
-    __device__ __forceinline__ void run(EACH each) const {
-        with_act(act, [&](auto a) {
-            each([&](int m, int n, Vec<float, 8> v, int cnt) { one<decltype(a)::value>(m, n, v, cnt); });
-        });
+    struct Column {
+        Vec<float, 8> bias;
+    };
+    struct Item {
+        Vec<YT, 8> residual;
+    };
+
+    // Rows and columns past the end read the last ones' values, and what is not
+    // given reads zeros, so that loads stand under no condition but one for all.
+    __device__ __forceinline__ Column column(int n) const {
+        Column c;
+        if (N % 8 == 0) c.bias = load_vec<float, 8>(bias ? bias + min(n, N - 8) : kNothing);
+        else c.bias = load_vec_n<float, 8>(bias + n, bias ? N - n : 0);
+        return c;
+    }
+
+    __device__ __forceinline__ Item item(int m, int n) const {
+        Item r;
+        const int row = min(m, M - 1);
+        if (planar && residual) {
+            const int img = row / pixels, p = row - img * pixels;
+            const YT *src = residual + (int64_t)img * N * pixels + p;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r.residual.v[e] = src[(int64_t)min(n + e, N - 1) * pixels];
+        } else if (N % 8 == 0) {
+            r.residual = load_vec<YT, 8>(residual ? residual + row * rs + min(n, N - 8) : (const YT *)kNothing);
+        } else {
+            r.residual = load_vec_n<YT, 8>(residual + row * rs + n, residual ? N - n : 0);
+        }
+        return r;
+    }
+
+    template <typename F>
+    __device__ __forceinline__ void with(F f) const {
+        with_act(act, f);
     }
 
     template <int ACT>
-    __device__ __forceinline__ void one(int m, int n, Vec<float, 8> v, int cnt) const {
-        if (bias) {
-            const Vec<float, 8> b = load_vec_n<float, 8>(bias + n, cnt);
+    __device__ __forceinline__ void store(int m, int n, Vec<float, 8> v, int cnt, const Column &col, const Item &item) const {
+        if (bias)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v.v[e] += b.v[e];
-        }
+            for (int e = 0; e < 8; ++e) v.v[e] += col.bias.v[e];
         Vec<YT, 8> r;
         if (z) {
 #pragma unroll
@@ -46,19 +76,9 @@ struct EpiForward {
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) v.v[e] = act_fwd<ACT>(v.v[e]);
-        if (residual) {
-            if (planar) {
-                const int img = m / pixels, p = m - img * pixels;
-                const YT *src = residual + ((int64_t)img * N + n) * pixels + p;
+        if (residual)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e < cnt) v.v[e] += to_f32(src[(int64_t)e * pixels]);
-            } else {
-                const Vec<YT, 8> s = load_vec_n<YT, 8>(residual + (int64_t)m * rs + n, cnt);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v.v[e] += to_f32(s.v[e]);
-            }
-        }
+            for (int e = 0; e < 8; ++e) v.v[e] += to_f32(item.residual.v[e]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) r.v[e] = from_f32<YT>(v.v[e]);
         store_vec_n<YT, 8>(y + (int64_t)m * ys + n, r, cnt);
@@ -74,7 +94,8 @@ struct RunForward {
     template <int BM, int BN, int WM, int WN, bool DIRECT>
     void operator()() const {
         using EPI = EpiForward<YT>;
-        const EPI epi = {p.bias, (const YT *)p.residual, (YT *)p.y, (YT *)p.z, g.ys, g.rs, g.N, g.act, g.r_planar, g.pixels};
+        const EPI epi = {p.bias, (const YT *)p.residual, (YT *)p.y, (YT *)p.z, g.ys, g.rs, g.M, g.N, g.act, g.r_planar,
+                         g.pixels};
         GemmArgs a = {};
         a.A = p.x;
         a.B = p.w;
