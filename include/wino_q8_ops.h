@@ -95,7 +95,9 @@ wq8_status wq8_norm_backward(const wq8_norm_plan *plan, const void *dy, const vo
  * Backward, from dy and the forward's z (needed unless act is NONE):
  *   dz = dy act'(z);  dx = dz w;  dw = dz^T x;  dbias = sum_r dz
  * and the residual's gradient is dy itself. dz enters the two products in
- * x's type (with bf16 it is rounded once); dbias sums it unrounded. Sums are
+ * x's type: with bf16 it is rounded once, and where there are few values to
+ * average that rounding over, its rest is multiplied as well (an infinity in
+ * w or x may then give a NaN in its place). dbias sums it unrounded. Sums are
  * taken in a fixed order: results repeat bit for bit. */
 typedef struct wq8_linear_plan wq8_linear_plan; /* opaque */
 

@@ -41,6 +41,8 @@ struct GemmArgs {
     int tiles_m, tiles_n;
     int ksteps;        // per split
     int splits;
+    int more;          // 1: A is the sum of two matrices, `plane` elements apart;
+    int64_t plane;     // each k step is taken once for each
     float *partial;    // [splits][M][N] where k is split, else NULL
 };
 
@@ -71,7 +73,8 @@ __device__ __forceinline__ int lds_unit(int row, int unit) {
 // Stages k steps of an operand of R tile rows. Units that lie in LDS one after
 // another are one thread each, so a wave's 64 units can be one load from
 // memory to LDS; the swizzle is in the address that a thread reads.
-template <typename T, bool KC, bool FIRST, int R, int THREADS>
+// TWO: the operand, or the other one, may be the sum of two matrices.
+template <typename T, bool KC, bool FIRST, int R, int THREADS, bool TWO>
 struct Stager {
     static constexpr int U = 16 / sizeof(T), UR = KC ? 8 : R / U, COUNT = R * 8 / THREADS, BK = 128 / sizeof(T);
     static_assert(R * 8 % THREADS == 0, "whole waves");
@@ -79,7 +82,18 @@ struct Stager {
     const T *src;
     int64_t ld;
     int r0, rows, K;
+    int more;
+    int64_t plane;
     uint32_t off[COUNT];
+
+    // Steps count the matrices within k steps, so that what both meet in the
+    // other operand is still in the cache the second time.
+    __device__ __forceinline__ const T *matrix(int &step) const {
+        if constexpr (!TWO) return src;
+        const T *m = src + (step & more) * plane;
+        step >>= more;
+        return m;
+    }
 
     __device__ __forceinline__ static void place(int i, int &row, int &unit) {
         const int q = i * THREADS + threadIdx.x;
@@ -102,7 +116,8 @@ struct Stager {
 
     // One whole step from memory to LDS, past the registers.
     __device__ __forceinline__ void direct(T *lds, int step) const {
-        const T *base = KC ? src + (int64_t)r0 * ld + (int64_t)step * BK : src + (int64_t)step * BK * ld + r0;
+        const T *const mat = matrix(step);
+        const T *base = KC ? mat + (int64_t)r0 * ld + (int64_t)step * BK : mat + (int64_t)step * BK * ld + r0;
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, -1, kBufferFlags);
         const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) T *)lds + (threadIdx.x >> 6) * 1024;
 #pragma unroll
@@ -123,28 +138,31 @@ struct Stager {
     // is the contiguous one a unit that passes the rows' end reads on into the
     // next k's row, so that must exist as well.
     __device__ __forceinline__ bool whole(int step) const {
+        if constexpr (TWO) step >>= more;
         return KC ? (step + 1) * BK <= K : (step + 1) * BK < K && rows >= U;
     }
     __device__ __forceinline__ void load(Vec<T, U> (&v)[COUNT], int step) const {
+        const T *const mat = matrix(step);
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
             int row, unit;
             place(i, row, unit);
-            if constexpr (KC) v[i] = load_vec<T, U>(src + (int64_t)min(r0 + row, rows - 1) * ld + step * BK + unit * U);
-            else v[i] = load_vec<T, U>(src + (int64_t)(step * BK + row) * ld + min(r0 + unit * U, rows - 1));
+            if constexpr (KC) v[i] = load_vec<T, U>(mat + (int64_t)min(r0 + row, rows - 1) * ld + step * BK + unit * U);
+            else v[i] = load_vec<T, U>(mat + (int64_t)(step * BK + row) * ld + min(r0 + unit * U, rows - 1));
         }
     }
     // The last step: zeros for k past the end. A unit that passes the end of
     // its row is read from U before that end and moved down.
     __device__ __forceinline__ void load_last(Vec<T, U> (&v)[COUNT], int step) const {
         const int end = KC ? K : rows;  // of the contiguous index
+        const T *const mat = matrix(step);
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
             int row, unit;
             place(i, row, unit);
             const int at = (KC ? step * BK : r0) + unit * U, line = KC ? r0 + row : step * BK + row;
             const int lines = KC ? rows : K;
-            const T *p = src + (int64_t)min(line, lines - 1) * ld;
+            const T *p = mat + (int64_t)min(line, lines - 1) * ld;
             const int n = KC || line < lines ? end - at : 0;  // values that count
             if (end >= U) {
                 const int from = min(at, end - U), shift = at - from;
@@ -245,7 +263,7 @@ __device__ __forceinline__ Vec<float, 8> sums(const f32x4 &even, const f32x4 &od
 }
 
 // The b-th of a product's nb blocks.
-template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool DIRECT, typename EPI>
+template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool DIRECT, bool TWO, typename EPI>
 __device__ __forceinline__ void gemm_block(const GemmArgs &a, const EPI &epi, int b, int nb) {
     constexpr int BK = 128 / sizeof(T), THREADS = WM * WN * 64;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles per wave
@@ -263,14 +281,15 @@ __device__ __forceinline__ void gemm_block(const GemmArgs &a, const EPI &epi, in
     const int m0 = (band * 8 + in % height) * BM, n0 = (in / height) * BN;
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
 
-    Stager<T, AKC, false, BM, THREADS> sa = {(const T *)a.A, a.lda, m0, a.M, a.K, {}};
-    Stager<T, BKC, true, BN, THREADS> sb = {(const T *)a.B, a.ldb, n0, a.N, a.K, {}};
+    Stager<T, AKC, false, BM, THREADS, TWO> sa = {(const T *)a.A, a.lda, m0, a.M, a.K, a.more, a.plane, {}};
+    Stager<T, BKC, true, BN, THREADS, TWO> sb = {(const T *)a.B, a.ldb, n0, a.N, a.K, a.more, 0, {}};
     if constexpr (DIRECT) {
         sa.prepare();
         sb.prepare();
     }
-    const int ks = split * a.ksteps, ke = min(ks + a.ksteps, (a.K + BK - 1) / BK);
-    const int kd = DIRECT ? min(ke, a.K / BK) : ks;  // steps [ks, kd) are whole and direct
+    const int k0 = split * a.ksteps, k1 = min(k0 + a.ksteps, (a.K + BK - 1) / BK);
+    const int more = TWO ? a.more : 0, ks = k0 << more, ke = k1 << more;
+    const int kd = DIRECT ? min(k1, a.K / BK) << more : ks;  // steps [ks, kd) are whole and direct
 
     f32x4 acc[TM][TN] = {};
     const auto multiply = [&](const T *buf) {
@@ -371,7 +390,7 @@ __device__ __forceinline__ void gemm_block(const GemmArgs &a, const EPI &epi, in
 
 template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool DIRECT, typename EPI>
 __global__ __launch_bounds__(WM *WN * 64) void k_gemm(GemmArgs a, EPI epi) {
-    gemm_block<T, AKC, BKC, BM, BN, WM, WN, DIRECT>(a, epi, blockIdx.x, gridDim.x);
+    gemm_block<T, AKC, BKC, BM, BN, WM, WN, DIRECT, false>(a, epi, blockIdx.x, gridDim.x);
 }
 
 // Joins split products, in the order of k, and runs the epilogue. A thread takes

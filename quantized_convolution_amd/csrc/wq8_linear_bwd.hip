@@ -8,9 +8,12 @@
 // reads, so nothing is transposed in memory. A last kernel joins the sums of
 // products that are split along k.
 //
-// dz is rounded to bf16 for bf16 products (their operand type; dbias sums the
-// unrounded values), which adds as much error to dx and dw as their own final
-// rounding. Measured: 8192 x 640 x 2560 bf16 with gelu 115 us, of it dz 26 us
+// For bf16 products dz is rounded to their type (dbias sums the unrounded
+// values). Over many values that adds as much error to dx and dw as their own
+// final rounding: sqrt 2 times the error of one rounding. Over few it can be
+// more, so small problems keep the rest that rounding leaves as a second
+// matrix and multiply both, which costs little next to launch and latency.
+// Measured: 8192 x 640 x 2560 bf16 with gelu 115 us, of it dz 26 us
 // (126 MB, 4.8 TB/s, bound by memory), the products 84 us (640 TFLOP/s) and the
 // join 7 us; 1001 x 333 x 515 fp32, rows at odd addresses, 23 us in kernels of
 // 4, 17 and 4 us, bound by launches and load latency. One kernel for both
@@ -47,15 +50,21 @@ __global__ __launch_bounds__(256) void k_dz(LinearGeo g, LinearPtrs a, int ncol,
 #pragma unroll
             for (int i = 0; i < kDzRows; ++i)
                 if (r + 4 * i < r1) {
-                    Vec<XT, V> o;
+                    Vec<XT, V> o, rest;
 #pragma unroll
                     for (int k = 0; k < V; ++k) {
                         float v = to_f32(d[i].v[k]);
                         if constexpr (A != WQ8_ACT_NONE) v *= act_slope<A>(to_f32(zz[i].v[k]));
                         sum[k] += v;
                         o.v[k] = from_f32<XT>(v);
+                        const float top = to_f32(o.v[k]);
+                        rest.v[k] = from_f32<XT>(fabsf(top) < INFINITY ? v - top : 0.0f);
                     }
-                    if (dz && lo < V) store_vec<XT, V>(dz + (int64_t)(r + 4 * i) * g.N + n, o);
+                    if (dz && lo < V) {
+                        XT *const to = dz + (int64_t)(r + 4 * i) * g.N + n;
+                        store_vec<XT, V>(to, o);
+                        if (g.dz_planes == 2) store_vec<XT, V>(to + (int64_t)g.M * g.N, rest);
+                    }
                 }
         }
     });
@@ -117,9 +126,10 @@ struct EpiStore {
 template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(WM *WN * 64) void k_linear_bwd(GemmArgs dw, EpiStore<T> ew, int nw, GemmArgs dx, EpiStore<T> ex,
                                                             int nx, LinearGeo g, LinearPtrs p) {
+    constexpr bool TWO = sizeof(T) == 2;
     const int b = blockIdx.x;
-    if (b < nw) gemm_block<T, false, false, BM, BN, WM, WN, DIRECT>(dw, ew, b, nw);
-    else if (b < nw + nx) gemm_block<T, true, false, BM, BN, WM, WN, DIRECT>(dx, ex, b - nw, nx);
+    if (b < nw) gemm_block<T, false, false, BM, BN, WM, WN, DIRECT, TWO>(dw, ew, b, nw);
+    else if (b < nw + nx) gemm_block<T, true, false, BM, BN, WM, WN, DIRECT, TWO>(dx, ex, b - nw, nx);
     else dbias_block(g, p, b - nw - nx);
 }
 
@@ -144,6 +154,8 @@ struct RunBackward {
         int64_t nw = 0, nx = 0, jw = 0, jx = 0;
         if (p.dw) {
             dw.A = dz;
+            dw.more = g.dz_planes - 1;
+            dw.plane = (int64_t)g.M * g.N;
             dw.lda = ldz;
             dw.B = p.x;
             dw.ldb = g.xs;
@@ -155,6 +167,8 @@ struct RunBackward {
         }
         if (p.dx && g.M > 0) {
             dx.A = dz;
+            dx.more = g.dz_planes - 1;
+            dx.plane = (int64_t)g.M * g.N;
             dx.lda = ldz;
             dx.B = p.w;
             dx.ldb = g.K;

@@ -236,3 +236,28 @@ def test_offsets_past_32_bits():
     R.check(dx[-3:], *want["dx"], "dx")
     R.check(dw, *want["dw"], "dw")
     assert (dx[:-3] == 0).all()
+
+
+@pytest.mark.parametrize("act,yt", [("silu", BF), ("gelu", F32), ("none", F32)])
+@pytest.mark.parametrize("size", [(1, 40, 24), (9, 65, 130), (40, 16, 100), (300, 70, 33), (5, 700, 129), (1100, 24, 31)])
+def test_few_values_keep_what_rounding_leaves(act, yt, size):
+    """With few values dz goes into the bf16 products as two matrices: to 16 bits,
+    so that the final rounding is all that is left beside fp32 arithmetic."""
+    rows, Cin, Cout = size
+    d = make(rows, Cin, Cout, BF, yt, 12)
+    z = (d["x"].double() @ d["w"].double().T + d["bias"].double()).to(yt)
+    plan = q.LinearPlan(rows, Cin, Cout, act=act, x_dtype=BF, y_dtype=yt)
+    got = q.wq8_linear_backward(plan, d["dy"].cuda(), d["x"].cuda(), d["w"].cuda(), z=z.cuda(), want_dbias=True)
+    torch.cuda.synchronize()
+    want = R.linear_backward(d["dy"], d["x"], d["w"], z, act, BF, False)
+    dz = d["dy"].double().abs() * (R.slope(z.double(), act).abs() + 1e-6) if act != "none" else d["dy"].double().abs()
+    rest = 2.0 ** -16 * dz  # rounding of the second matrix
+    R.check(got[0], want["dx"][0], want["dx"][1] + 1.01 * (rest @ d["w"].double().abs()), "dx")
+    R.check(got[1], want["dw"][0], want["dw"][1] + 1.01 * (rest.T @ d["x"].double().abs()), "dw")
+    R.check(got[2], *want["dbias"], "dbias")
+
+
+@pytest.mark.parametrize("size", [(600, 300, 400), (520, 264, 328)])
+@pytest.mark.parametrize("act,yt", [("silu", BF), ("none", F32)])
+def test_many_values(size, act, yt):
+    backward(*size, act, BF, yt, seed=13)
