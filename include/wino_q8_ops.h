@@ -94,11 +94,15 @@ wq8_status wq8_norm_backward(const wq8_norm_plan *plan, const void *dy, const vo
  * matrix cores.
  * Backward, from dy and the forward's z (needed unless act is NONE):
  *   dz = dy act'(z);  dx = dz w;  dw = dz^T x;  dbias = sum_r dz
- * and the residual's gradient is dy itself. dz enters the two products in
- * x's type: with bf16 it is rounded once, and where there are few values to
- * average that rounding over, its rest is multiplied as well (an infinity in
- * w or x may then give a NaN in its place). dbias sums it unrounded. Sums are
- * taken in a fixed order: results repeat bit for bit. */
+ * and the residual's gradient is dy itself. dz is an fp32 value; with fp32
+ * inputs, or where it is a bf16 dy itself, it enters the two products as it
+ * is. With bf16 inputs it does so to 16 bits, as the sum of two bf16 values of
+ * its sign: dx and dw are then as exact as their own rounding to bf16 leaves
+ * them, for twice the matrix work and 4 bytes of workspace a value. A caller
+ * who wants it rounded to bf16 once instead (dx and dw off by 2.4e-3 of their
+ * norm where 1.7e-3 is their own rounding) asks for it by round_dz. dbias sums
+ * fp32 values either way. Sums are taken in a fixed order: results repeat bit
+ * for bit. */
 typedef struct wq8_linear_plan wq8_linear_plan; /* opaque */
 
 typedef struct {
@@ -114,6 +118,8 @@ typedef struct {
     int pixels;              /* pixels per image of an NCHW residual; rows % pixels == 0 */
     int x_stride, y_stride, r_stride; /* elements between rows of x and dx, of y and dy,
                                          and of an NHWC residual; 0 = contiguous */
+    int round_dz;            /* backward with bf16 inputs: 0 dz to 16 bits, 1 rounded to
+                                bf16; nothing else is changed by it */
 } wq8_linear_desc;
 
 wq8_status wq8_linear_plan_create(const wq8_linear_desc *desc, wq8_linear_plan **out);

@@ -1,6 +1,6 @@
 // Backward of the matrix product with bias, activation and residual.
 //   dz = dy act'(z);  dx = dz w;  dw = dz^T x;  dbias = sum over the rows of dz
-// One kernel forms dz (once, in x's type) with the column sums of the unrounded
+// One kernel forms dz (once, for the products) with the column sums of its fp32
 // values. A second one runs both products and the column sums' join side by
 // side: they only share inputs, and the blocks of one fill the compute units
 // that the other leaves idle. The products read dz, w and x as they lie: the
@@ -8,14 +8,14 @@
 // reads, so nothing is transposed in memory. A last kernel joins the sums of
 // products that are split along k.
 //
-// For bf16 products dz is rounded to their type (dbias sums the unrounded
-// values). Over many values that adds as much error to dx and dw as their own
-// final rounding: sqrt 2 times the error of one rounding. Over few it can be
-// more, so small problems keep the rest that rounding leaves as a second
-// matrix and multiply both, which costs little next to launch and latency.
-// Measured: 8192 x 640 x 2560 bf16 with gelu 116 us, of it dz 26 us
-// (126 MB, 4.8 TB/s, bound by memory), the products 84 us (640 TFLOP/s) and the
-// join 7 us; 1001 x 333 x 515 fp32, rows at odd addresses, 23 us in kernels of
+// For bf16 products dz is held as two matrices of their type that are
+// multiplied one after the other, k step by k step (dbias sums fp32 values).
+// Rounded to bf16 once, as a caller may ask for, it adds as much error to dx
+// and dw as their own final rounding, sqrt 2 times the error of one rounding,
+// over few values and over many.
+// Measured: 8192 x 640 x 2560 bf16 with gelu 189 us, and 117 us with dz rounded
+// once: dz then takes 26 us (126 MB, 4.8 TB/s, bound by memory), the products
+// 84 us (640 TFLOP/s) and the join 7 us; 1001 x 333 x 515 fp32, rows at odd addresses, 23 us in kernels of
 // 4, 17 and 4 us, bound by launches and load latency. One kernel for both
 // products instead of two, a join each and one for dbias: 127 and 36 us before.
 #include "wq8_gemm_device.h"
@@ -27,6 +27,19 @@ namespace {
 // and their sums. A vector that would pass the last column starts earlier: its
 // first `lo` values are another thread's, stored twice and summed once.
 constexpr int kDzRows = 4;
+
+// v as the sum of two bf16 values: its first 8 bits, cut off, and what that
+// leaves, rounded: within 2^-16 of v. Both have v's sign, and unless v is zero
+// the second is no smaller than the smallest normal number (1.2e-38, nothing
+// beside any product): an infinity that they are multiplied by gives the same
+// infinity twice, where a zero or another sign would make it a NaN.
+__device__ __forceinline__ void split_dz(float v, bf16_t &top, bf16_t &rest) {
+    const uint32_t u = __float_as_uint(v);
+    top = v == v ? (bf16_t)(u >> 16) : from_f32<bf16_t>(v);
+    rest = from_f32<bf16_t>(v - to_f32(top));  // NaN if v is infinite
+    if (!(fabsf(to_f32(rest)) >= 0x1p-126f)) rest = (bf16_t)((u >> 16 & 0x8000u) | (v != 0.0f ? 0x0080u : 0u));
+}
+
 template <typename XT, typename YT, int V>
 __global__ __launch_bounds__(256) void k_dz(LinearGeo g, LinearPtrs a, int ncol, int want_sum) {
     __shared__ float red[3][64 * V];
@@ -56,14 +69,13 @@ __global__ __launch_bounds__(256) void k_dz(LinearGeo g, LinearPtrs a, int ncol,
                         float v = to_f32(d[i].v[k]);
                         if constexpr (A != WQ8_ACT_NONE) v *= act_slope<A>(to_f32(zz[i].v[k]));
                         sum[k] += v;
-                        o.v[k] = from_f32<XT>(v);
-                        const float top = to_f32(o.v[k]);
-                        rest.v[k] = from_f32<XT>(fabsf(top) < INFINITY ? v - top : 0.0f);
+                        if constexpr (sizeof(XT) == 2) split_dz(v, o.v[k], rest.v[k]);
+                        if (sizeof(XT) == 4 || g.dz_planes == 1) o.v[k] = from_f32<XT>(v);
                     }
                     if (dz && lo < V) {
                         XT *const to = dz + (int64_t)(r + 4 * i) * g.N + n;
                         store_vec<XT, V>(to, o);
-                        if (g.dz_planes == 2) store_vec<XT, V>(to + (int64_t)g.M * g.N, rest);
+                        if (sizeof(XT) == 2 && g.dz_planes == 2) store_vec<XT, V>(to + (int64_t)g.M * g.N, rest);
                     }
                 }
         }

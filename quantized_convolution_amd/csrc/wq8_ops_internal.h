@@ -97,7 +97,7 @@ struct LinearGeo {
     int r_planar, pixels;
     GemmShape f, dx, dw;      // dx and dw share a tile: they run in one kernel
     int dz_own;               // backward: dz is written to the workspace (else it is dy itself)
-    int dz_planes;            // 2: dz and what its rounding to bf16 left, as two matrices
+    int dz_planes;            // 2: dz as the sum of two bf16 matrices
     int dz_chunk, dz_nchunk;  // rows per block of the dz kernel, blocks along the rows
 };
 

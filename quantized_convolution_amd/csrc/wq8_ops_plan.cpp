@@ -246,15 +246,15 @@ wq8_status build_norm(const wq8_norm_desc *d, wq8_norm_plan *p) {
 // but one block to itself; each round of blocks that it holds at once adds its
 // start and end (much of it for the largest tile, whose compute unit has
 // nothing else to do then); a split writes and reads fp32 sums and launches
-// once more. Measured against it over 40 shapes and tiles (bf16 8192 x 640 x
-// 640: 13.3, 11.2, 12.7 modelled and 13.2, 12.5, 13.4 measured for 128 x 128,
-// 128 x 64, 64 x 64; fp32 2048 x 2560 x 1280 in 64 x 64: 120 and 124, split in
-// two 112 and 113).
+// once more; with dz in two planes each k step is taken twice. Measured against
+// it over 40 shapes and tiles (bf16 8192 x 640 x 640: 13.3, 11.2, 12.7 modelled
+// and 13.2, 12.5, 13.4 measured for 128 x 128, 128 x 64, 64 x 64; fp32 2048 x
+// 2560 x 1280 in 64 x 64: 120 and 124, split in two 112 and 113).
 struct Product {
     int64_t M, N, K;
 };
 
-void choose_gemm(const Product *q, int count, wq8_dtype t, bool direct, GemmShape *const *out) {
+void choose_gemm(const Product *q, int count, wq8_dtype t, int planes, bool direct, GemmShape *const *out) {
     constexpr int kMost = 16;  // splits
     const int64_t kstep = t == WQ8_F32 ? 32 : 64;
     double least = 1e30;
@@ -262,7 +262,7 @@ void choose_gemm(const Product *q, int count, wq8_dtype t, bool direct, GemmShap
     for (int i = direct ? 0 : 1; i < kGemmTileCount; ++i) {
         const GemmTile &g = kGemmTiles[i];
         const double rate = t == WQ8_F32 ? 0.56 * g.f32 : 5.2 * g.bf16;  // Mflop per us and compute unit
-        const double step = 2e-6 * g.bm * g.bn * kstep / rate;
+        const double step = 2e-6 * g.bm * g.bn * kstep * planes / rate;
         for (int combo = 0; combo < (count == 1 ? kMost : kMost * kMost); ++combo) {
             const int64_t want[2] = {combo % kMost + 1, combo / kMost + 1};
             int64_t blocks = 0, work = 0, longest = 0, per[2] = {0, 0}, sp[2] = {1, 1};
@@ -316,6 +316,7 @@ wq8_status build_linear(const wq8_linear_desc *d, wq8_linear_plan *p) {
     if (!is_act(d->act)) return fail(WQ8_ERR_INVALID_ARG, "unknown activation %d", (int)d->act);
     if (!is_dtype(d->x_dtype) || !is_dtype(d->y_dtype)) return fail(WQ8_ERR_INVALID_ARG, "unknown dtype");
     if (!is_layout(d->r_layout)) return fail(WQ8_ERR_INVALID_ARG, "unknown layout");
+    if (d->round_dz != 0 && d->round_dz != 1) return fail(WQ8_ERR_INVALID_ARG, "round_dz is 0 or 1, not %d", d->round_dz);
     if (d->r_layout == WQ8_NCHW && (d->pixels < 1 || d->rows % d->pixels != 0))
         return fail(WQ8_ERR_INVALID_ARG, "rows = %lld is not a multiple of pixels = %d", (long long)d->rows, d->pixels);
     if ((d->x_stride && d->x_stride < d->Cin) || (d->y_stride && d->y_stride < d->Cout) ||
@@ -342,10 +343,7 @@ wq8_status build_linear(const wq8_linear_desc *d, wq8_linear_plan *p) {
     // dy serves as dz where the activation leaves it as it is and the products
     // can read its type
     g.dz_own = g.act != WQ8_ACT_NONE || p->xdt != p->ydt;
-    // few values to average the rounding of dz over: 2.5e-3 of error in dx was
-    // seen in place of 1.7e-3 with some thousand values, 2.3e-3 with many
-    const int64_t few = 1 << 16, vals[3] = {(int64_t)g.M * g.N, (int64_t)g.M * g.K, (int64_t)g.N * g.K};
-    g.dz_planes = p->xdt == WQ8_BF16 && g.dz_own && (vals[0] < few || vals[1] < few || vals[2] < few) ? 2 : 1;
+    g.dz_planes = p->xdt == WQ8_BF16 && g.dz_own && !d->round_dz ? 2 : 1;
     // rows per block: 4 waves of 4 rows in flight, more where blocks abound
     g.dz_chunk = 64;
     while (g.dz_chunk > 16 && ceil_div64(g.M, g.dz_chunk) * ceil_div64(g.N, 512) < 4 * kCus) g.dz_chunk /= 2;
@@ -354,8 +352,8 @@ wq8_status build_linear(const wq8_linear_desc *d, wq8_linear_plan *p) {
     const wq8_dtype t = p->xdt;
     const Product f = {g.M, g.N, g.K}, bwd[2] = {{g.N, g.K, g.M}, {g.M, g.K, g.N}};  // k of one plane
     GemmShape *const fs[1] = {&g.f}, *const bs[2] = {&g.dw, &g.dx};
-    choose_gemm(&f, 1, t, direct_ok(t, g.xs, true, g.M) && direct_ok(t, g.K, true, g.N), fs);
-    choose_gemm(bwd, 2, t,
+    choose_gemm(&f, 1, t, 1, direct_ok(t, g.xs, true, g.M) && direct_ok(t, g.K, true, g.N), fs);
+    choose_gemm(bwd, 2, t, g.dz_planes,
                 direct_ok(t, ldz, true, g.M) && direct_ok(t, g.K, false, g.K) && direct_ok(t, ldz, false, g.N) &&
                     direct_ok(t, g.xs, false, g.K),
                 bs);

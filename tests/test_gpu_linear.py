@@ -261,3 +261,68 @@ def test_few_values_keep_what_rounding_leaves(act, yt, size):
 @pytest.mark.parametrize("act,yt", [("silu", BF), ("none", F32)])
 def test_many_values(size, act, yt):
     backward(*size, act, BF, yt, seed=13)
+
+
+def dz_bounds(d, z, act, want):
+    """`want` of linear_backward without a rounding of dz, and what two bf16
+    matrices leave of dz: each value cut after 8 bits and the rest rounded to 8
+    more, 2^-16 of it at most."""
+    dz = d["dy"].double().abs() * (R.slope(z.double(), act).abs() + 1e-6)
+    rest = 1.01 * 2.0 ** -16 * dz
+    return {"dx": (want["dx"][0], want["dx"][1] + rest @ d["w"].double().abs()),
+            "dw": (want["dw"][0], want["dw"][1] + rest.T @ d["x"].double().abs()), "dbias": want["dbias"]}
+
+
+@pytest.mark.parametrize("act,yt", [("silu", BF), ("gelu", F32), ("none", F32)])
+@pytest.mark.parametrize("size", [(600, 300, 400), (520, 264, 328), (1100, 2100, 136), (2000, 72, 1024)])
+def test_many_values_keep_what_rounding_leaves(act, yt, size):
+    """As with few values: the precision of dx and dw does not depend on the size."""
+    rows, Cin, Cout = size
+    d = make(rows, Cin, Cout, BF, yt, 14)
+    z = (d["x"].double() @ d["w"].double().T + d["bias"].double()).to(yt)
+    plan = q.LinearPlan(rows, Cin, Cout, act=act, x_dtype=BF, y_dtype=yt)
+    got = q.wq8_linear_backward(plan, d["dy"].cuda(), d["x"].cuda(), d["w"].cuda(), z=z.cuda(), want_dbias=True)
+    torch.cuda.synchronize()
+    want = dz_bounds(d, z, act, R.linear_backward(d["dy"], d["x"], d["w"], z, act, BF, False))
+    for t, k in zip(got, want):
+        R.check(t, *want[k], k)
+
+
+@pytest.mark.parametrize("size", [(20, 40, 24), (600, 300, 400)])
+def test_backward_infinities(size):
+    """An infinity in w or x meets every value of dz that is not zero with that
+    value's sign, however dz is held: no NaN in place of an infinity. Where dz is
+    zero the product is a NaN."""
+    rows, Cin, Cout = size
+    d = make(rows, Cin, Cout, BF, F32, 15)
+    d["dy"][::3] = d["dy"][::3].to(BF).float()  # nothing is left by rounding
+    d["dy"][1, 4], d["dy"][5, 4] = 0.0, -0.0
+    d["w"][4, 7], d["x"][2, 9] = float("inf"), float("-inf")
+    plan = q.LinearPlan(rows, Cin, Cout, x_dtype=BF, y_dtype=F32)
+    dx, dw, _ = q.wq8_linear_backward(plan, d["dy"].cuda(), d["x"].cuda(), d["w"].cuda())
+    torch.cuda.synchronize()
+    dx, dw = dx.cpu().float(), dw.cpu().float()
+    zero = d["dy"][:, 4] == 0
+    assert torch.isnan(dx[zero, 7]).all()
+    assert torch.equal(dx[~zero, 7], torch.sign(d["dy"][~zero, 4]) * float("inf"))
+    assert torch.isfinite(dx[:, :7]).all() and torch.isfinite(dx[:, 8:]).all()
+    assert torch.equal(dw[:, 9], torch.sign(d["dy"][2]) * float("-inf"))
+    assert torch.isfinite(dw[:, :9]).all() and torch.isfinite(dw[:, 10:]).all()
+
+
+@pytest.mark.parametrize("act,yt", [("silu", BF), ("none", F32)])
+@pytest.mark.parametrize("size", [(40, 65, 130), (600, 300, 400)])
+def test_rounded_dz(act, yt, size):
+    """A caller may have dz rounded to bf16 in the products; everything else stays as it is."""
+    rows, Cin, Cout = size
+    d = make(rows, Cin, Cout, BF, yt, 16)
+    z = (d["x"].double() @ d["w"].double().T + d["bias"].double()).to(yt)
+    plans = [q.LinearPlan(rows, Cin, Cout, act=act, x_dtype=BF, y_dtype=yt, round_dz=r) for r in (False, True)]
+    a = [d[k].cuda() for k in ("dy", "x", "w")]
+    exact, got = (q.wq8_linear_backward(p, *a, z=z.cuda(), want_dbias=True) for p in plans)
+    torch.cuda.synchronize()
+    want = R.linear_backward(d["dy"], d["x"], d["w"], z, act, BF, True)
+    for t, k in zip(got, want):
+        R.check(t, *want[k], k)
+    assert torch.equal(got[2], exact[2]) and not torch.equal(got[0], exact[0])
+    assert plans[1].backward_workspace_bytes < plans[0].backward_workspace_bytes

@@ -159,3 +159,17 @@ def test_mixed_devices_are_refused():
     n = O.NormPlan(2, 16, 4, 5, groups=4)
     with pytest.raises(ValueError, match="gamma is on cpu, x on cuda"):
         O.wq8_norm_forward(n, torch.zeros(n.x_shape, device="cuda"), torch.zeros(16))
+
+
+@pytest.mark.parametrize("rows,Cin,Cout", [(16, 32, 24), (16384, 100, 3), (16384, 6, 10240), (4000, 640, 2560)])
+def test_dz_has_one_form_at_every_size(rows, Cin, Cout):
+    """The workspace holds dz of bf16 inputs to 16 bits (4 bytes a value), or rounded where the caller says so (2)."""
+    exact, rounded = (O.LinearPlan(rows, Cin, Cout, act="silu", x_dtype=BF, round_dz=r) for r in (False, True))
+    values = rows * Cout
+    assert exact.backward_workspace_bytes >= 4 * values
+    assert 2 * values <= rounded.backward_workspace_bytes
+    # dy of x's type without an activation is dz itself
+    for r in (False, True):
+        assert O.LinearPlan(rows, Cin, Cout, x_dtype=BF, round_dz=r).workspace_bytes == rounded.workspace_bytes
+    d = O.wq8_linear_desc(rows, Cin, Cout, 2, 1, 1, 0, 0, 0, 0, 0, 2)
+    assert create("linear", d) == -1
