@@ -5,6 +5,10 @@ and residual, forward and backward (argument marshalling only).
 Every function has the name of the C entry point it calls. Buffers are checked
 against the plan before anything reaches the library, ValueError otherwise;
 the library's own refusals raise Wq8Error.
+
+A call runs on `stream`, or on the current one; outputs and workspaces that it
+makes are allocated as that stream's. Buffers that a caller gives are ordered
+and kept by the caller, as with any work on another stream than their own.
 """
 from __future__ import annotations
 
@@ -175,11 +179,13 @@ class _Args:
     strides that the plan gives, all on one GPU. The kernels size their
     accesses from the plan, so anything else would be out of bounds."""
 
-    __slots__ = ("device", "where")
+    __slots__ = ("stream", "device", "where", "ws")
 
-    def __init__(self):
+    def __init__(self, stream=None):
+        self.stream = stream
         self.device = None  # index; -1: not a GPU
         self.where = None   # the first buffer and its name
+        self.ws = None      # the workspace, kept until the call is enqueued
 
     def need(self, t, name, dtype, shape, strides=None):
         """The tensor's address."""
@@ -206,12 +212,20 @@ class _Args:
     def optional(self, t, name, dtype, shape, strides=None):
         return None if t is None else self.need(t, name, dtype, shape, strides)
 
+    def make(self, fn, *args, **kw):
+        """fn(*args, **kw); what it allocates belongs to the call's stream: torch
+        hands a freed block out again in the order of the stream it belongs to."""
+        if self.stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(self.stream):
+            return fn(*args, **kw)
+
     def workspace(self, t, nbytes):
         """(address, bytes) of a workspace, made here if the caller has none."""
         if nbytes == 0:
             return None, 0
         if t is None:
-            t = torch.empty(nbytes, dtype=torch.uint8, device=self.where[0].device)
+            t = self.ws = self.make(torch.empty, nbytes, dtype=torch.uint8, device=self.where[0].device)
         if not isinstance(t, torch.Tensor):
             raise ValueError("workspace must be a torch tensor")
         have = t.numel() * t.element_size()
@@ -223,13 +237,15 @@ class _Args:
             raise ValueError(f"workspace is on {t.device}, {self.where[1]} on {self.where[0].device}")
         return t.data_ptr(), have
 
-    def call(self, fn, args, stream):
-        """The C call with the buffers' device current, on `stream` or that
-        device's current stream."""
-        d = self.device
+    def call(self, fn, args):
+        """The C call with the buffers' device current, on the call's stream or
+        that device's current one."""
+        d, stream = self.device, self.stream
         if not self.where[0].is_cuda:
             raise ValueError(f"{self.where[1]} must be on a GPU, got {self.where[0].device}")
         if stream is not None:
+            if stream.device.index != d:
+                raise ValueError(f"{self.where[1]} is on {self.where[0].device}, the stream on {stream.device}")
             handle = stream.cuda_stream
         else:
             handle = _raw_stream(d) if _raw_stream else torch.cuda.current_stream(d).cuda_stream
@@ -246,22 +262,22 @@ def wq8_norm_forward(plan: NormPlan, x, gamma=None, beta=None, shift=None, y=Non
                      want_stats=False, workspace=None, stream=None):
     """y, or (y, mean, rstd) with want_stats."""
     f32, C_ = torch.float32, plan.C
-    a = _Args()
+    a = _Args(stream)
     px = a.need(x, "x", plan.x_dtype, plan.x_shape, plan.x_strides)
     ps = a.optional(shift, "shift", f32, (plan.N, C_))
     pg = a.optional(gamma, "gamma", f32, (C_,))
     pb = a.optional(beta, "beta", f32, (C_,))
     if y is None:
-        y = plan.empty_output(x.device)
+        y = a.make(plan.empty_output, x.device)
     py = a.need(y, "y", plan.y_dtype, plan.y_shape, plan.y_strides)
     if want_stats and mean is None:
-        mean = torch.empty((plan.N, plan.groups), dtype=f32, device=x.device)
+        mean = a.make(torch.empty, (plan.N, plan.groups), dtype=f32, device=x.device)
     if want_stats and rstd is None:
-        rstd = torch.empty((plan.N, plan.groups), dtype=f32, device=x.device)
+        rstd = a.make(torch.empty, (plan.N, plan.groups), dtype=f32, device=x.device)
     pm = a.optional(mean, "mean", f32, (plan.N, plan.groups))
     pr = a.optional(rstd, "rstd", f32, (plan.N, plan.groups))
     pw, nw = a.workspace(workspace, plan.workspace_bytes)
-    a.call(plan._forward, (plan._h, px, ps, pg, pb, py, pm, pr, pw, nw), stream)
+    a.call(plan._forward, (plan._h, px, ps, pg, pb, py, pm, pr, pw, nw))
     return (y, mean, rstd) if want_stats else y
 
 
@@ -270,7 +286,7 @@ def wq8_norm_backward(plan: NormPlan, dy, x, mean, rstd, gamma=None, beta=None, 
     """(dx, dgamma, dbeta, dshift). Gradients of the parameters that the
     forward was given are made; dgamma and dbeta may be asked for without."""
     f32, C_ = torch.float32, plan.C
-    a = _Args()
+    a = _Args(stream)
     pdy = a.need(dy, "dy", plan.y_dtype, plan.y_shape, plan.y_strides)
     px = a.need(x, "x", plan.x_dtype, plan.x_shape, plan.x_strides)
     pm = a.need(mean, "mean", f32, (plan.N, plan.groups))
@@ -279,58 +295,58 @@ def wq8_norm_backward(plan: NormPlan, dy, x, mean, rstd, gamma=None, beta=None, 
     pb = a.optional(beta, "beta", f32, (C_,))
     ps = a.optional(shift, "shift", f32, (plan.N, C_))
     if dx is None:
-        dx = plan.empty_input(x.device)
+        dx = a.make(plan.empty_input, x.device)
     if dgamma is None and gamma is not None:
-        dgamma = torch.empty(C_, dtype=f32, device=x.device)
+        dgamma = a.make(torch.empty, C_, dtype=f32, device=x.device)
     if dbeta is None and beta is not None:
-        dbeta = torch.empty(C_, dtype=f32, device=x.device)
+        dbeta = a.make(torch.empty, C_, dtype=f32, device=x.device)
     if dshift is None and shift is not None:
-        dshift = torch.empty((plan.N, C_), dtype=f32, device=x.device)
+        dshift = a.make(torch.empty, (plan.N, C_), dtype=f32, device=x.device)
     pdx = a.need(dx, "dx", plan.x_dtype, plan.x_shape, plan.x_strides)
     pdg = a.optional(dgamma, "dgamma", f32, (C_,))
     pdb = a.optional(dbeta, "dbeta", f32, (C_,))
     pds = a.optional(dshift, "dshift", f32, (plan.N, C_))
     pw, nw = a.workspace(workspace, plan.backward_workspace_bytes)
-    a.call(plan._backward, (plan._h, pdy, px, ps, pg, pb, pm, pr, pdx, pdg, pdb, pds, pw, nw), stream)
+    a.call(plan._backward, (plan._h, pdy, px, ps, pg, pb, pm, pr, pdx, pdg, pdb, pds, pw, nw))
     return dx, dgamma, dbeta, dshift
 
 
 def wq8_linear_forward(plan: LinearPlan, x, w, bias=None, residual=None, y=None, z=None, want_z=False,
                        workspace=None, stream=None):
     """y, or (y, z) with want_z."""
-    a = _Args()
+    a = _Args(stream)
     px = a.need(x, "x", plan.x_dtype, plan.x_shape, plan.x_strides)
     pw = a.need(w, "w", plan.x_dtype, plan.w_shape)
     pb = a.optional(bias, "bias", torch.float32, (plan.Cout,))
     pr = a.optional(residual, "residual", plan.y_dtype, plan.r_shape, plan.r_strides)
     if y is None:
-        y = plan.empty_output(x.device)
+        y = a.make(plan.empty_output, x.device)
     if want_z and z is None:
-        z = plan.empty_z(x.device)
+        z = a.make(plan.empty_z, x.device)
     py = a.need(y, "y", plan.y_dtype, plan.y_shape, plan.y_strides)
     pz = a.optional(z, "z", plan.y_dtype, plan.y_shape)
     ws, nw = a.workspace(workspace, plan.workspace_bytes)
-    a.call(plan._forward, (plan._h, px, pw, pb, pr, py, pz, ws, nw), stream)
+    a.call(plan._forward, (plan._h, px, pw, pb, pr, py, pz, ws, nw))
     return (y, z) if want_z else y
 
 
 def wq8_linear_backward(plan: LinearPlan, dy, x, w, z=None, dx=None, dw=None, dbias=None, want_dx=True, want_dw=True,
                         want_dbias=False, workspace=None, stream=None):
     """(dx, dw, dbias); what is neither given nor wanted is None."""
-    a = _Args()
+    a = _Args(stream)
     pdy = a.need(dy, "dy", plan.y_dtype, plan.y_shape, plan.y_strides)
     px = a.need(x, "x", plan.x_dtype, plan.x_shape, plan.x_strides)
     pw = a.need(w, "w", plan.x_dtype, plan.w_shape)
     pz = a.need(z, "z", plan.y_dtype, plan.y_shape) if plan.act != "none" else None
     if dx is None and want_dx:
-        dx = plan.empty_input(x.device)
+        dx = a.make(plan.empty_input, x.device)
     if dw is None and want_dw:
-        dw = torch.empty(plan.w_shape, dtype=plan.x_dtype, device=x.device)
+        dw = a.make(torch.empty, plan.w_shape, dtype=plan.x_dtype, device=x.device)
     if dbias is None and want_dbias:
-        dbias = torch.empty(plan.Cout, dtype=torch.float32, device=x.device)
+        dbias = a.make(torch.empty, plan.Cout, dtype=torch.float32, device=x.device)
     pdx = a.optional(dx, "dx", plan.x_dtype, plan.x_shape, plan.x_strides)
     pdw = a.optional(dw, "dw", plan.x_dtype, plan.w_shape)
     pdb = a.optional(dbias, "dbias", torch.float32, (plan.Cout,))
     ws, nw = a.workspace(workspace, plan.backward_workspace_bytes)
-    a.call(plan._backward, (plan._h, pdy, px, pw, pz, pdx, pdw, pdb, ws, nw), stream)
+    a.call(plan._backward, (plan._h, pdy, px, pw, pz, pdx, pdw, pdb, ws, nw))
     return dx, dw, dbias

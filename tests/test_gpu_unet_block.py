@@ -124,3 +124,61 @@ def test_graph_capture():
         torch.cuda.synchronize()
         assert torch.equal(out, want)
         assert all(torch.equal(grads[k], wg[k]) for k in wg)
+
+
+def split_calls():
+    """Calls whose kernels hand values on through a workspace that the call makes; inputs differ by seed."""
+    norm, lin = q.NormPlan(1, 256, 60, 60, 2, act="silu"), q.LinearPlan(64, 4096, 64, act="silu")
+    assert min(norm.workspace_bytes, norm.backward_workspace_bytes, lin.workspace_bytes, lin.backward_workspace_bytes) > 0
+
+    def run(seed, stream=None):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+        x, dy, gamma, t, w, dz = r(*norm.x_shape), r(*norm.x_shape), r(256), r(64, 4096), r(64, 4096), r(64, 64)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        for _ in range(20):
+            y, mean, rstd = q.wq8_norm_forward(norm, x, gamma, gamma, want_stats=True, stream=stream)
+            grads = q.wq8_norm_backward(norm, dy, x, mean, rstd, gamma, gamma, stream=stream)
+            out, z = q.wq8_linear_forward(lin, t, w, want_z=True, stream=stream)
+            more = q.wq8_linear_backward(lin, dz, t, w, z=z, want_dbias=True, stream=stream)
+        return [y, mean, rstd, *grads[:3], out, z, *more], (x, dy, gamma, t, w, dz)
+
+    return run
+
+
+def test_threads_without_workspaces():
+    """Calls of several threads on one stream, each with the workspace it makes."""
+    import threading
+
+    run = split_calls()
+    want = [run(s)[0] for s in range(4)]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(s):
+        got[s] = run(s)[0]
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_other_stream_while_this_one_allocates():
+    """What a call on another stream makes is not handed to this one while its kernels run."""
+    run = split_calls()
+    want = run(5)[0]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got, inputs = run(5, s)
+    for n in (1 << 12, 1 << 16, 1 << 20, 1 << 22):  # what was freed here, filled again at once
+        for _ in range(8):
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(inputs) == 6

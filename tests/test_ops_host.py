@@ -173,3 +173,71 @@ def test_dz_has_one_form_at_every_size(rows, Cin, Cout):
         assert O.LinearPlan(rows, Cin, Cout, x_dtype=BF, round_dz=r).workspace_bytes == rounded.workspace_bytes
     d = O.wq8_linear_desc(rows, Cin, Cout, 2, 1, 1, 0, 0, 0, 0, 0, 2)
     assert create("linear", d) == -1
+
+
+class _Allocations:
+    """What ops.py allocates in one call: (bytes, made under the call's stream, weak reference)."""
+
+    def __init__(self, monkeypatch):
+        import contextlib
+        import weakref
+
+        self.made, self.inside, self.alive_at_call = [], [], None
+        real = torch.empty
+
+        def empty(*args, **kw):
+            t = real(*args, **{**kw, "device": "cpu"})
+            self.made.append((t.numel() * t.element_size(), bool(self.inside), weakref.ref(t)))
+            return t
+
+        @contextlib.contextmanager
+        def stream(s):
+            if s is not None:
+                self.inside.append(s)
+            yield
+            if s is not None:
+                self.inside.pop()
+
+        def call(args, fn, pointers, stream=None):
+            self.alive_at_call = [ref() is not None for _, _, ref in self.made]
+
+        monkeypatch.setattr(torch, "empty", empty)
+        monkeypatch.setattr(torch.cuda, "stream", stream)
+        monkeypatch.setattr(O._Args, "call", call)
+
+
+def op_calls():
+    n = O.NormPlan(1, 256, 60, 60, 2, act="silu")
+    p = O.LinearPlan(64, 4096, 64, act="silu")
+    g, s = torch.zeros(256), torch.zeros(1, 2)
+    x, y, z, w = torch.zeros(n.x_shape), torch.zeros(64, 64), torch.zeros(64, 64), torch.zeros(64, 4096)
+    t = torch.zeros(64, 4096)
+    return [
+        (n.workspace_bytes, 4, lambda **kw: O.wq8_norm_forward(n, x, g, g, want_stats=True, **kw)),
+        (n.backward_workspace_bytes, 5, lambda **kw: O.wq8_norm_backward(n, x, x, s, s, g, g, shift=torch.zeros(1, 256), **kw)),
+        (p.workspace_bytes, 3, lambda **kw: O.wq8_linear_forward(p, t, w, want_z=True, **kw)),
+        (p.backward_workspace_bytes, 4, lambda **kw: O.wq8_linear_backward(p, y, t, w, z=z, want_dbias=True, **kw)),
+    ]
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_workspace_lives_through_the_call(monkeypatch, which):
+    """A workspace made for the caller must not be back with the allocator before
+    the kernels are enqueued: another thread could be given the same memory."""
+    nbytes, count, run = op_calls()[which]
+    a = _Allocations(monkeypatch)
+    run()
+    assert [n for n, _, _ in a.made].count(nbytes) >= 1 and len(a.made) == count
+    assert a.alive_at_call == [True] * count
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_what_a_call_makes_belongs_to_its_stream(monkeypatch, which):
+    """Workspaces and outputs made for a call on another stream come from that
+    stream's memory: what the current one has freed may still be in use there,
+    and what it allocates next must not be this call's workspace."""
+    _, count, run = op_calls()[which]
+    a = _Allocations(monkeypatch)
+    run(stream="another stream")
+    assert [inside for _, inside, _ in a.made] == [True] * count
+    assert not a.inside
