@@ -8,6 +8,8 @@ import fails loudly; there is no fallback.
 from __future__ import annotations
 
 import ctypes as C
+import functools
+import inspect
 import math
 import os
 
@@ -163,6 +165,23 @@ class _Bufs:
             _check(fn(*args, C.c_void_p(st.cuda_stream)))
 
 
+def _on_stream(fn):
+    """Runs fn with its `stream` as the current one, so that what fn allocates
+    is that stream's: torch hands a freed block out again in the order of the
+    stream that it belongs to."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def run(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+
+    return run
+
+
 class Plan:
     """Owns a wq8_plan handle and the geometry needed to size buffers."""
 
@@ -295,6 +314,7 @@ def wq8_plan_bt_codes(plan: Plan):
     return Bq, sq
 
 
+@_on_stream
 def wq8_weights_prepare(plan: Plan, w, Uq=None, sU=None, stream=None):
     b = _Bufs()
     b(w, "w", torch.float32, (plan.Cout, plan.Cin, 3, 3))
@@ -320,6 +340,7 @@ def _check_codes(plan, b, Vq, sV):
     b(sV, "sV", torch.float32, plan.sv_shape)
 
 
+@_on_stream
 def wq8_conv_forward(plan: Plan, x, Uq, sU, y=None, workspace=None, stream=None):
     b = _Bufs()
     _check_x(plan, b, x)
@@ -352,6 +373,7 @@ def wq8_conv_forward_noalloc(plan: Plan, x, Uq, sU, y, stream=None):
     return y
 
 
+@_on_stream
 def wq8_stage1(plan: Plan, x, Vq=None, sV=None, stream=None):
     b = _Bufs()
     _check_x(plan, b, x)
@@ -363,6 +385,7 @@ def wq8_stage1(plan: Plan, x, Vq=None, sV=None, stream=None):
     return Vq, sV
 
 
+@_on_stream
 def wq8_stage2(plan: Plan, Vq, sV, Uq, sU, M=None, stream=None):
     b = _Bufs()
     _check_codes(plan, b, Vq, sV)
@@ -375,6 +398,7 @@ def wq8_stage2(plan: Plan, Vq, sV, Uq, sU, M=None, stream=None):
     return M
 
 
+@_on_stream
 def wq8_stage2_i32(plan: Plan, Vq, Uq, P=None, stream=None):
     b = _Bufs()
     b(Vq, "Vq", torch.int8, plan.vq_shape)
@@ -387,6 +411,7 @@ def wq8_stage2_i32(plan: Plan, Vq, Uq, P=None, stream=None):
     return P
 
 
+@_on_stream
 def wq8_stage3(plan: Plan, M, y=None, Yq=None, sY=None, want_codes=False, stream=None):
     b = _Bufs()
     b(M, "M", torch.float32, plan.m_shape)
@@ -406,6 +431,7 @@ def wq8_stage3(plan: Plan, M, y=None, Yq=None, sY=None, want_codes=False, stream
     return (y, Yq, sY) if want_codes else y
 
 
+@_on_stream
 def wq8_stage23(plan: Plan, Vq, sV, Uq, sU, y=None, stream=None):
     b = _Bufs()
     _check_codes(plan, b, Vq, sV)
@@ -429,6 +455,7 @@ def _direct_shapes(plan):
             (plan.N, plan.H, plan.W, plan.Cin), (plan.N, plan.H, plan.W, plan.ng))
 
 
+@_on_stream
 def wq8_direct_weights_prepare(plan: Plan, w, Wq=None, sW=None, stream=None):
     wqs, sws, _, _ = _direct_shapes(plan)
     b = _Bufs()
@@ -442,6 +469,7 @@ def wq8_direct_weights_prepare(plan: Plan, w, Wq=None, sW=None, stream=None):
     return Wq, sW
 
 
+@_on_stream
 def wq8_direct_quantize_x(plan: Plan, x, Xq=None, sX=None, stream=None):
     _, _, xqs, sxs = _direct_shapes(plan)
     b = _Bufs()
@@ -455,6 +483,7 @@ def wq8_direct_quantize_x(plan: Plan, x, Xq=None, sX=None, stream=None):
     return Xq, sX
 
 
+@_on_stream
 def wq8_direct_conv(plan: Plan, Xq, sX, Wq, sW, y=None, stream=None):
     wqs, sws, xqs, sxs = _direct_shapes(plan)
     b = _Bufs()
@@ -470,6 +499,7 @@ def wq8_direct_conv(plan: Plan, Xq, sX, Wq, sW, y=None, stream=None):
     return y
 
 
+@_on_stream
 def wq8_direct_forward(plan: Plan, x, Wq, sW, y=None, workspace=None, stream=None):
     wqs, sws, _, _ = _direct_shapes(plan)
     b = _Bufs()
