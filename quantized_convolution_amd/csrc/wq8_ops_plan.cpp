@@ -132,9 +132,20 @@ NormShape split_shape(const NormGeo &g, int V, int batch, int xsz) {
     while (steps < all && rows * ceil_div(all, steps + batch) >= 8 * kCus) steps += batch;
     if (steps > all) steps = all;
     s.steps = steps;
-    s.chunk = s.steps * s.window;
+    const int64_t chunk = (int64_t)s.steps * s.window;
+    s.chunk = chunk < g.P ? (int)chunk : g.P;
     s.nchunk = ceil_div(g.P, s.chunk);
     return s;
+}
+
+// Whether every position that the kernels form fits 32 bits: a block's last
+// batch of steps and its spare threads reach past the image's pixels, and its
+// slab past the channels, before they are clamped.
+bool positions_fit(const NormGeo &g, const NormShape &s) {
+    constexpr int64_t lim = (int64_t)1 << 31, batch = norm_max_steps(false, false);
+    const int64_t last = (int64_t)(s.nchunk - 1) * s.chunk, most = s.steps + batch;
+    return last + s.chunk < lim && last + most * s.window + 1024 * norm_max_vec(2, 2, false) < lim &&
+           (int64_t)g.G / s.K * s.J * s.slabC + 2 * kNormMaxSlab < lim;
 }
 
 // Steps whose windows fit 48 KiB of LDS (rows padded by two elements), one at
@@ -170,8 +181,8 @@ NormShape choose_norm(const NormGeo &g, int xsz, int ysz, bool backward) {
     s.steps = 1 << 30;
     for (int k = 1; k <= g.G; ++k) {
         // whole vectors across the slab, nearly
-        const int vecs = ceil_div(k * g.cpg, V) * V;
-        if (g.G % k != 0 || (g.x_nhwc && k < g.G && k * g.cpg * 8 < vecs * 7) || (g.x_nhwc && k * g.cpg < V)) continue;
+        const int64_t chans = (int64_t)k * g.cpg, vecs = ceil_div64(chans, V) * V;
+        if (g.G % k != 0 || (g.x_nhwc && k < g.G && chans * 8 < vecs * 7) || (g.x_nhwc && chans < V)) continue;
         const NormShape t = fused_shape(g, V, k, most);
         if (t.steps > most) break;
         // wider slabs (longer contiguous rows) while the card stays full
@@ -225,6 +236,8 @@ wq8_status build_norm(const wq8_norm_desc *d, wq8_norm_plan *p) {
     p->ydt = d->y_dtype;
     g.f = choose_norm(g, size_of(p->xdt), size_of(p->ydt), false);
     g.b = choose_norm(g, size_of(p->xdt), size_of(p->ydt), true);
+    if (!positions_fit(g, g.f) || !positions_fit(g, g.b))
+        return fail(WQ8_ERR_UNSUPPORTED, "an image whose last block would pass 2^31 pixels or channels");
     if ((int64_t)g.N * g.f.nslab * g.f.nchunk >= lim || (int64_t)g.N * g.b.nslab * g.b.nchunk >= lim)
         return fail(WQ8_ERR_UNSUPPORTED, "more than 2^31 blocks");
     const size_t N = g.N, G = g.G, C = g.C;

@@ -241,3 +241,17 @@ def test_what_a_call_makes_belongs_to_its_stream(monkeypatch, which):
     run(stream="another stream")
     assert [inside for _, inside, _ in a.made] == [True] * count
     assert not a.inside
+
+
+@pytest.mark.parametrize("x_layout,y_layout", [(0, 0), (0, 1), (1, 0), (1, 1)])
+@pytest.mark.parametrize("N,C,H,W,groups,status", [
+    (1, 1, 46340, 46341, 1, -2),        # the last block's end would be pixel 2^31
+    (1, 1, 1, (1 << 31) - 1, 1, -2), (1, 1, 46340, 46280, 1, 0),
+    (1, (1 << 31) - 1, 1, 1, 1, -2), (1, (1 << 31) - 64, 1, 1, 1, -2), (1, 1 << 30, 1, 1, 4, 0),
+])
+def test_positions_fit_32_bits(N, C, H, W, groups, status, x_layout, y_layout):
+    """Pixels and channels are counted in 32 bits, those that a block's last
+    steps would reach past the image's end among them."""
+    for t in (0, 1):
+        d = O.wq8_norm_desc(N, C, H, W, groups, 1e-5, 2, t, t, x_layout, y_layout, 0, 0)
+        assert create("norm", d) == status
