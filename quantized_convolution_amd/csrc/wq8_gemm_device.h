@@ -390,7 +390,9 @@ __device__ __forceinline__ void gemm_block(const GemmArgs &a, const EPI &epi, in
 
 template <typename T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, bool DIRECT, typename EPI>
 __global__ __launch_bounds__(WM *WN * 64) void k_gemm(GemmArgs a, EPI epi) {
-    gemm_block<T, AKC, BKC, BM, BN, WM, WN, DIRECT, false>(a, epi, blockIdx.x, gridDim.x);
+    int b;
+    const int nb = a.tiles_m * a.tiles_n * a.splits;
+    if (block_number(nb, b)) gemm_block<T, AKC, BKC, BM, BN, WM, WN, DIRECT, false>(a, epi, b, nb);
 }
 
 // Joins split products, in the order of k, and runs the epilogue. A thread takes
@@ -418,8 +420,9 @@ inline int64_t join_blocks(const GemmArgs &a) {
 }
 
 template <typename EPI>
-__global__ __launch_bounds__(256) void k_gemm_join(GemmArgs a, EPI epi) {
-    join_block(a, epi, blockIdx.x);
+__global__ __launch_bounds__(256) void k_gemm_join(GemmArgs a, EPI epi, int nb) {
+    int b;
+    if (block_number(nb, b)) join_block(a, epi, b);
 }
 
 // A product's tiles of BM x BN and its split; returns its blocks.

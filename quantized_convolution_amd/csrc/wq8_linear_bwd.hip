@@ -44,8 +44,10 @@ template <typename XT, typename YT, int V>
 __global__ __launch_bounds__(256) void k_dz(LinearGeo g, LinearPtrs a, int ncol, int want_sum) {
     __shared__ float red[3][64 * V];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int chunk = blockIdx.x / ncol;
-    const int c = ((blockIdx.x - chunk * ncol) * 64 + lane) * V, n = min(c, g.N - V), lo = min(c - n, V);
+    int b;
+    if (!block_number(ncol * g.dz_nchunk, b)) return;
+    const int chunk = b / ncol;
+    const int c = ((b - chunk * ncol) * 64 + lane) * V, n = min(c, g.N - V), lo = min(c - n, V);
     const int r0 = chunk * g.dz_chunk, r1 = min(r0 + g.dz_chunk, g.M);
     const YT *dy = (const YT *)a.dy, *z = (const YT *)a.zin;
     XT *dz = (XT *)a.dz;
@@ -137,17 +139,20 @@ struct EpiStore {
 // Blocks [0, nw): dw; [nw, nw + nx): dx; the rest: dbias.
 template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(WM *WN * 64) void k_linear_bwd(GemmArgs dw, EpiStore<T> ew, int nw, GemmArgs dx, EpiStore<T> ex,
-                                                            int nx, LinearGeo g, LinearPtrs p) {
+                                                            int nx, int nb, LinearGeo g, LinearPtrs p) {
     constexpr bool TWO = sizeof(T) == 2;
-    const int b = blockIdx.x;
+    int b;
+    if (!block_number(nb, b)) return;
     if (b < nw) gemm_block<T, false, false, BM, BN, WM, WN, DIRECT, TWO>(dw, ew, b, nw);
     else if (b < nw + nx) gemm_block<T, true, false, BM, BN, WM, WN, DIRECT, TWO>(dx, ex, b - nw, nx);
     else dbias_block(g, p, b - nw - nx);
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void k_linear_bwd_join(GemmArgs dw, EpiStore<T> ew, int nw, GemmArgs dx, EpiStore<T> ex) {
-    const int b = blockIdx.x;
+__global__ __launch_bounds__(256) void k_linear_bwd_join(GemmArgs dw, EpiStore<T> ew, int nw, GemmArgs dx, EpiStore<T> ex,
+                                                         int nb) {
+    int b;
+    if (!block_number(nb, b)) return;
     if (b < nw) join_block(dw, ew, b);
     else join_block(dx, ex, b - nw);
 }
@@ -194,11 +199,12 @@ struct RunBackward {
         const int64_t blocks = nw + nx + (p.dbias ? (g.N + 15) / 16 : 0);
         if (blocks > 0) {
             const auto kernel = k_linear_bwd<T, BM, BN, WM, WN, DIRECT>;
-            hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(WM * WN * 64), (tile_lds<BM, BN>(kernel)), st, dw, ew,
-                               (int)nw, dx, ex, (int)nx, g, p);
+            hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(WM * WN * 64), (tile_lds<BM, BN>(kernel)), st, dw, ew, (int)nw, dx,
+                               ex, (int)nx, (int)blocks, g, p);
         }
         if (jw + jx > 0)
-            hipLaunchKernelGGL((k_linear_bwd_join<T>), dim3((unsigned)(jw + jx)), dim3(256), 0, st, dw, ew, (int)jw, dx, ex);
+            hipLaunchKernelGGL((k_linear_bwd_join<T>), grid_of(jw + jx), dim3(256), 0, st, dw, ew, (int)jw, dx, ex,
+                               (int)(jw + jx));
     }
 };
 
@@ -208,8 +214,7 @@ void backward(const LinearGeo &g, const LinearPtrs &p, hipStream_t st) {
     if (g.M > 0 && (p.dbias || (g.dz_own && (p.dx || p.dw)))) {
         const auto go = [&](auto kernel, int v) {
             const int ncol = (g.N + 64 * v - 1) / (64 * v);
-            hipLaunchKernelGGL(kernel, dim3((unsigned)((int64_t)ncol * g.dz_nchunk)), dim3(256), 0, st, g, p, ncol,
-                               p.dbias != nullptr);
+            hipLaunchKernelGGL(kernel, grid_of((int64_t)ncol * g.dz_nchunk), dim3(256), 0, st, g, p, ncol, p.dbias != nullptr);
         };
         if (g.N >= V) go(k_dz<XT, YT, V>, V);
         else go(k_dz<XT, YT, 1>, 1);

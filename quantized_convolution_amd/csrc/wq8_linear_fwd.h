@@ -106,9 +106,9 @@ struct RunForward {
         a.K = g.K;
         const int64_t blocks = set_tiles<BM, BN>(a, g.f, p.partial);
         const auto kernel = k_gemm<XT, true, true, BM, BN, WM, WN, DIRECT, EPI>;
-        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(WM * WN * 64), (tile_lds<BM, BN>(kernel)), st, a, epi);
+        hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(WM * WN * 64), (tile_lds<BM, BN>(kernel)), st, a, epi);
         if (a.splits > 1)
-            hipLaunchKernelGGL((k_gemm_join<EPI>), dim3((unsigned)join_blocks(a)), dim3(256), 0, st, a, epi);
+            hipLaunchKernelGGL((k_gemm_join<EPI>), grid_of(join_blocks(a)), dim3(256), 0, st, a, epi, (int)join_blocks(a));
     }
 };
 

@@ -161,8 +161,10 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_fused(NormGeo g, NormPtrs a) 
     constexpr int NC = thread_channels<V, KIND>(), NG = group_values<V, KIND>();
     extern __shared__ __align__(16) char smem[];
     const NormShape &s = g.b;
+    int b;
+    if (!block_number(norm_blocks(g, s), b)) return;
     float *const red = (float *)smem, *const gm = red + norm_sum_floats(s, CL);
-    const Where w = locate<V, KIND>(g, s);
+    const Where w = locate<V, KIND>(g, s, b);
     Vec<XT, V> fx[E];
     Vec<YT, V> fd[E];
     load_steps<XT, V, KIND, E>(fx, (const XT *)a.x, g, s, g.xs, w, 0);
@@ -191,8 +193,10 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_bwd_sums(NormGeo g, 
     constexpr int NC = thread_channels<V, KIND>();
     extern __shared__ __align__(16) char smem[];
     const NormShape &s = g.b;
+    int b;
+    if (!block_number(norm_blocks(g, s), b)) return;
     float *const red = (float *)smem, *const gm = red + norm_sum_floats(s, CL);
-    const Where w = locate<V, KIND>(g, s);
+    const Where w = locate<V, KIND>(g, s, b);
     Vec<XT, V> fx[E];
     Vec<YT, V> fd[E];
     load_steps<XT, V, KIND, E>(fx, (const XT *)a.x, g, s, g.xs, w, 0);
@@ -220,8 +224,10 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_bwd_apply(NormGeo g,
     constexpr int NG = group_values<V, KIND>();
     extern __shared__ __align__(16) char smem[];
     const NormShape &s = g.b;
+    int b;
+    if (!block_number(norm_blocks(g, s), b)) return;
     float *const tot = (float *)smem;
-    const Where w = locate<V, KIND>(g, s);
+    const Where w = locate<V, KIND>(g, s, b);
     Vec<XT, V> fx[E];
     load_steps<XT, V, KIND, E>(fx, (const XT *)a.x, g, s, g.xs, w, 0);
     Channels<V, KIND> c;
@@ -276,13 +282,15 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_bwd_apply(NormGeo g,
 
 // dgamma, dbeta: sums of `part` over images and chunks; dshift of image n from
 // its own: rstd (gamma S1 - P m1 - m2 S3). 16 channels a block, 16 lanes along
-// the rows of `part`; block row y < N is an image's dshift, the last one the
-// parameters' gradients.
-__global__ __launch_bounds__(256) void k_norm_params(NormGeo g, NormPtrs a, int ncol, int only_params) {
+// the rows of `part`; of the rows of blocks, one for each image does its dshift,
+// where that is wanted, and the last one, where they are, the parameters' gradients.
+__global__ __launch_bounds__(256) void k_norm_params(NormGeo g, NormPtrs a, int ncol, int nblocks) {
     __shared__ float red[2][16][17];
+    int b;
+    if (!block_number(nblocks, b)) return;
     const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4;
-    const int n = blockIdx.x / ncol, c = (blockIdx.x - n * ncol) * 16 + tc;
-    const bool shift = !only_params && n < g.N;
+    const int n = b / ncol, c = (b - n * ncol) * 16 + tc;
+    const bool shift = a.dshift && n < g.N;
     const int64_t row = 3 * (int64_t)g.C;
     const int64_t first = shift ? (int64_t)n * g.b.nchunk : 0;
     const int64_t last = shift ? first + g.b.nchunk : (int64_t)g.N * g.b.nchunk;
@@ -322,7 +330,7 @@ struct RunBackward {
     template <typename XT, typename YT, int V, int KIND, bool CROSS, bool SPLIT, int E>
     void operator()() const {
         const NormShape &s = g.b;
-        const dim3 grid((unsigned)((int64_t)g.N * s.nslab * s.nchunk)), blk(s.threads);
+        const dim3 grid = grid_of(norm_blocks(g, s)), blk(s.threads);
         const size_t red = (size_t)(2 * s.K + 2 * s.slabC + norm_sum_floats(s, KIND != kPlanar)) * 4;
         const size_t tile = CROSS ? tile_lds<YT>(s, KIND != kPlanar) : 0;
         const size_t most = red > tile ? red : tile, means = (size_t)2 * s.K * 4;
@@ -343,8 +351,8 @@ wq8_status norm_backward(const NormGeo &g, wq8_dtype ydt, const NormPtrs &p, voi
         else pick_vector<true, XT, bf16_t>(g, RunBackward{g, p, st});
     }
     if (p.dgamma || p.dbeta || (p.dshift && g.N > 0)) {
-        const int ncol = (g.C + 15) / 16, rows = p.dshift ? g.N + 1 : 1;
-        hipLaunchKernelGGL(k_norm_params, dim3((unsigned)((int64_t)ncol * rows)), dim3(256), 0, st, g, p, ncol, !p.dshift);
+        const int ncol = (g.C + 15) / 16, nblocks = ncol * ((p.dshift ? g.N : 0) + (p.dgamma || p.dbeta ? 1 : 0));
+        hipLaunchKernelGGL(k_norm_params, grid_of(nblocks), dim3(256), 0, st, g, p, ncol, nblocks);
     }
     return check_launch("group norm backward");
 }

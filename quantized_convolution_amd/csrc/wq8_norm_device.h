@@ -43,10 +43,12 @@ struct Where {
     int lo;                      // its channels that others own
 };
 
+__host__ __device__ inline int norm_blocks(const NormGeo &g, const NormShape &s) { return g.N * s.nslab * s.nchunk; }
+
 template <int V, int KIND>
-__device__ __forceinline__ Where locate(const NormGeo &g, const NormShape &s) {
+__device__ __forceinline__ Where locate(const NormGeo &g, const NormShape &s, int block) {
     Where w;
-    const int b = xcd_block(blockIdx.x, gridDim.x), tid = threadIdx.x;
+    const int b = xcd_block(block, norm_blocks(g, s)), tid = threadIdx.x;
     w.chunk = b % s.nchunk;
     const int r = b / s.nchunk, slab = r % s.nslab;
     w.n = r / s.nslab;

@@ -158,8 +158,10 @@ __global__ __launch_bounds__(1024) void k_norm_fused(NormGeo g, NormPtrs a) {
     constexpr int NC = thread_channels<V, KIND>(), NG = group_values<V, KIND>();
     extern __shared__ __align__(16) char smem[];
     const NormShape &s = g.f;
+    int b;
+    if (!block_number(norm_blocks(g, s), b)) return;
     float *const red = (float *)smem, *const gstat = red + norm_sum_floats(s, KIND != kPlanar);  // means, then M2, then rstd
-    const Where w = locate<V, KIND>(g, s);
+    const Where w = locate<V, KIND>(g, s, b);
 
     Vec<XT, V> f[E];
     load_steps<XT, V, KIND, E>(f, (const XT *)a.x, g, s, g.xs, w, 0);
@@ -212,8 +214,10 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_stats(NormGeo g, Nor
     constexpr int NC = thread_channels<V, KIND>(), NG = group_values<V, KIND>();
     extern __shared__ __align__(16) char smem[];
     const NormShape &s = g.f;
+    int b;
+    if (!block_number(norm_blocks(g, s), b)) return;
     float *const red = (float *)smem, *const gstat = red + norm_sum_floats(s, KIND != kPlanar);
-    const Where w = locate<V, KIND>(g, s);
+    const Where w = locate<V, KIND>(g, s, b);
     float off[NC];
     per_channel<V, KIND>(off, a.shift, (int64_t)w.n * g.C + w.c, kZeros);
 
@@ -283,8 +287,10 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_apply(NormGeo g, Nor
     constexpr int NC = thread_channels<V, KIND>();
     extern __shared__ __align__(16) char smem[];
     const NormShape &s = g.f;
+    int b;
+    if (!block_number(norm_blocks(g, s), b)) return;
     float *const gstat = (float *)smem;
-    const Where w = locate<V, KIND>(g, s);
+    const Where w = locate<V, KIND>(g, s, b);
     const int64_t group0 = (int64_t)w.n * g.G + w.g0;
     Vec<XT, V> f[E];
     load_steps<XT, V, KIND, E>(f, (const XT *)a.x, g, s, g.xs, w, 0);
@@ -315,7 +321,7 @@ struct RunForward {
     template <typename XT, typename YT, int V, int KIND, bool CROSS, bool SPLIT, int E>
     void operator()() const {
         const NormShape &s = g.f;
-        const dim3 grid((unsigned)((int64_t)g.N * s.nslab * s.nchunk)), blk(s.threads);
+        const dim3 grid = grid_of(norm_blocks(g, s)), blk(s.threads);
         const size_t red = (size_t)(2 * s.K + norm_sum_floats(s, KIND != kPlanar)) * 4, stats = (size_t)2 * s.K * 4;
         const size_t tile = CROSS ? tile_lds<YT>(s, KIND != kPlanar) : 0;
         if constexpr (!SPLIT) {

@@ -29,6 +29,18 @@ __device__ __forceinline__ bf16_t from_f32<bf16_t>(float v) {
     return __builtin_bit_cast(bf16_t, (__bf16)v);
 }
 
+// Grids: a launch takes fewer than 2^32 threads in a dimension (more are cut
+// off without an error), so blocks of up to 1024 threads stand in rows of 2^21.
+constexpr unsigned kGridRow = 1u << 21;
+inline dim3 grid_of(int64_t blocks) {
+    return blocks <= kGridRow ? dim3((unsigned)blocks) : dim3(kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
+}
+// This block's number; false for those that fill the last row up.
+__device__ __forceinline__ bool block_number(int blocks, int &b) {
+    b = (int)(blockIdx.y * kGridRow + blockIdx.x);
+    return (unsigned)b < (unsigned)blocks;
+}
+
 // V adjacent elements. Loads and stores copy bytes, so the address need only
 // be aligned to the element: the target takes unaligned 4- to 16-byte global
 // accesses in one instruction.

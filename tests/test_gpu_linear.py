@@ -326,3 +326,26 @@ def test_rounded_dz(act, yt, size):
         R.check(t, *want[k], k)
     assert torch.equal(got[2], exact[2]) and not torch.equal(got[0], exact[0])
     assert plans[1].backward_workspace_bytes < plans[0].backward_workspace_bytes
+
+
+def test_more_threads_than_one_grid_row_takes():
+    """2^30 rows: more than 2^32 threads in each kernel. The last rows are right in both directions, and
+    the sums over all of them: powers of two and few values that are not zero, exact in any order."""
+    rows, Cin, Cout = (1 << 30) + 65, 4, 4
+    x, dy = (torch.zeros((rows, Cin), dtype=BF, device="cuda") for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(4)
+    some = torch.cat([torch.arange(3), torch.arange(rows // 2, rows // 2 + 3), torch.arange(rows - 70, rows)]).cuda()
+    draw = lambda *s: torch.randint(-3, 4, s, generator=g, device="cuda").to(BF)  # noqa: E731
+    x[some], dy[some], w = draw(len(some), Cin), draw(len(some), Cout), draw(Cout, Cin)
+    plan = q.LinearPlan(rows, Cin, Cout, act="relu", x_dtype=BF)
+    y, z = q.wq8_linear_forward(plan, x, w, want_z=True)
+    want = x[some].double() @ w.double().T
+    assert torch.equal(z[some].double(), want) and torch.equal(y[some].double(), want.clamp(min=0))
+    assert torch.count_nonzero(y) == torch.count_nonzero(want > 0)
+    del y
+    dx, dw, db = q.wq8_linear_backward(plan, dy, x, w, z=z, want_dbias=True)
+    dz = dy[some].double() * (want > 0)
+    off = dx[some].double() - dz @ w.double()
+    assert off.abs().max().item() <= 1e-35 and torch.count_nonzero(dx.view(torch.int16)[8:rows // 2 - 8] & 0x7f80) == 0
+    assert (dw.double() - dz.T @ x[some].double()).abs().max().item() <= 1e-35
+    assert torch.equal(db.double(), dz.sum(0))

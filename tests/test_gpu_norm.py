@@ -219,3 +219,24 @@ def test_offsets_past_32_bits():
     assert (y[:-1] == 0).all()
     off = (y[-1].double().reshape(H * W, 32, 32) - want).abs()
     assert (off <= R.BF16 * want.abs() + 2e-5).all()
+
+
+def test_more_threads_than_one_grid_row_takes():
+    """2^26 images of 4 values: more than 2^32 threads in each kernel. The last images are right."""
+    N, C = (1 << 26) + 5, 4
+    plan = q.NormPlan(N, C, 1, 1, groups=1, act="silu")
+    x = torch.zeros(plan.x_shape, device="cuda")
+    g = torch.Generator().manual_seed(6)
+    last = torch.randn((9, 1, 1, C), generator=g)
+    x[-9:] = last.cuda()
+    y, mean, rstd = q.wq8_norm_forward(plan, x, want_stats=True)
+    ref = R.Norm(last, 1, 1e-5, "silu")
+    R.check(y[-9:], ref.y, ref.forward_errors(F32)[2], "y")
+    assert torch.count_nonzero(y[:-9]) == 0 and torch.count_nonzero(mean[:-9]) == 0
+    dy, shift = torch.ones_like(x), torch.zeros((N, C), device="cuda")
+    dx, _, _, ds = q.wq8_norm_backward(plan, dy, x, mean, rstd, shift=shift)
+    want = ref.backward(torch.ones(9, 1, 1, C), F32)
+    R.check(dx[-9:], want["dx"][0], 2 * want["dx"][1], "dx")
+    R.check(ds[-9:], want["dshift"][0], 2 * want["dshift"][1], "dshift")
+    # x is 0 in the others: z = h = 0, dz the slope 1/2 of silu at 0, and dx what that leaves of its mean
+    assert torch.count_nonzero(dx[:-9]) == 0 and torch.count_nonzero(ds[:-9]) == 0
