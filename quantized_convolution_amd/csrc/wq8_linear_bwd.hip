@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256) void k_dz(LinearGeo g, LinearPtrs a, int ncol,
 #pragma unroll
                     for (int k = 0; k < V; ++k) {
                         float v = to_f32(d[i].v[k]);
-                        if constexpr (A != WQ8_ACT_NONE) v *= act_slope<A>(to_f32(zz[i].v[k]));
+                        if constexpr (A != WQ8_ACT_NONE) v *= act_slope<A, exact_acts<XT, YT>()>(to_f32(zz[i].v[k]));
                         sum[k] += v;
                         if constexpr (sizeof(XT) == 2) split_dz(v, o.v[k], rest.v[k]);
                         if (sizeof(XT) == 4 || g.dz_planes == 1) o.v[k] = from_f32<XT>(v);

@@ -75,7 +75,7 @@ struct EpiForward {
             store_vec_n<YT, 8>(z + (int64_t)m * N + n, r, cnt);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v.v[e] = act_fwd<ACT>(v.v[e]);
+        for (int e = 0; e < 8; ++e) v.v[e] = act_fwd<ACT, exact_acts<YT, YT>()>(v.v[e]);
         if (residual)
 #pragma unroll
             for (int e = 0; e < 8; ++e) v.v[e] += to_f32(item.residual.v[e]);

@@ -5,7 +5,7 @@
 // forward: two tensors share the registers), else twice. Measured: 8 x 640 x 32 x 32
 // bf16 fused 18.7 us (31 MB; the activation's slope, two quarter-rate
 // instructions a value, is evaluated for the sums and again for dx: half of the
-// kernel's 17 us is arithmetic), 2 x 320 x 64 x 64 f32 with dy in NCHW split 27.8 us in
+// kernel's 17 us is arithmetic), 2 x 320 x 64 x 64 f32 with dy in NCHW split 28.9 us in
 // kernels of 13, 10 and 5 us (52 MB).
 #pragma once
 
@@ -75,7 +75,7 @@ __device__ __forceinline__ void add_sums(float *s1, float *s2, float *s3, const 
         for_values<V, KIND, E, BATCH>(g.b, w, first, [&](int e, int k, auto ok) {
             const int kc = c.NC == 1 ? 0 : k;
             const float hv = (to_f32(fx[e].v[k]) + c.off[kc]) * c.rstd[c.NG == 1 ? 0 : k], h = ok ? hv : 0.0f;
-            const float dv = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value>(fmaf(h, c.ga[kc], c.be[kc]));
+            const float dv = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value, exact_acts<XT, YT>()>(fmaf(h, c.ga[kc], c.be[kc]));
             const float dz = ok ? dv : 0.0f;
             s1[kc] += dz;
             s2[kc] = fmaf(dz, h, s2[kc]);
@@ -131,7 +131,7 @@ __device__ __forceinline__ void write_dx(const Vec<XT, V> (&fx)[E], const Vec<YT
                 for (int k = 0; k < V; ++k) {
                     const int kc = CL ? k : 0, kk = c.NG == 1 ? 0 : k;
                     const float h = (to_f32(fx[e].v[k]) + c.off[kc]) * c.rstd[kk];
-                    const float dz = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value>(fmaf(h, c.ga[kc], c.be[kc]));
+                    const float dz = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value, exact_acts<XT, YT>()>(fmaf(h, c.ga[kc], c.be[kc]));
                     r.v[k] = from_f32<XT>(c.rstd[kk] * (fmaf(dz, c.ga[kc], -m1[kk]) - h * m2[kk]));
                 }
                 XT *const to = addr<XT, V, KIND>(dx, g, g.xs, w, at.p);

@@ -24,7 +24,7 @@
 // Measured: 8 x 640 x 128 x 128 bf16 135 us: statistics 58 us (168 MB, 2.9 TB/s;
 // 4 vector operations a value for sum and square sum, and each block's joins),
 // output 77 us (336 MB, 4.4 TB/s, a large copy's rate is 4.7). 8 x 1280 x 16 x 16 f32
-// NCHW 7.2 us fused (21 MB), 32 x 512 x 7 x 7 bf16 6.9 us, 2 x 320 x 64 x 64 bf16 to
+// NCHW 7.8 us fused (21 MB), 32 x 512 x 7 x 7 bf16 6.9 us, 2 x 320 x 64 x 64 bf16 to
 // NCHW 18.4 us split (64 groups would leave three quarters of the card idle;
 // fused they took 35 us): launch and load latency bound these three.
 #pragma once
@@ -115,7 +115,7 @@ __device__ __forceinline__ void write_out(const Vec<XT, V> (&f)[E], const float 
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
                     const int kc = CL ? k : 0;
-                    r.v[k] = from_f32<YT>(act_fwd<decltype(act)::value>(fmaf(to_f32(f[e].v[k]) + off[kc], sc[kc], be[kc])));
+                    r.v[k] = from_f32<YT>(act_fwd<decltype(act)::value, exact_acts<YT, YT>()>(fmaf(to_f32(f[e].v[k]) + off[kc], sc[kc], be[kc])));
                 }
                 if constexpr (!CROSS) {
                     if (at.lo < V) store_vec<YT, V>(addr<YT, V, KIND>(y, g, g.ys, w, at.p), r);

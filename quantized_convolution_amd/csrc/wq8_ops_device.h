@@ -98,28 +98,76 @@ __device__ __forceinline__ void store_vec_n(T *p, const Vec<T, V> &r, int n) {
 }
 
 // ------------------------------------------------------------- activations
-// exp(x) on the hardware's 2^x: the argument's rounding gives a relative
-// error of |x| 2^-24, below 1e-6 where the result matters to an activation.
-__device__ __forceinline__ float fast_exp(float x) {
-    return __builtin_amdgcn_exp2f(x * 1.4426950408889634f);
+// EXACT: to some roundings of fp32, for results in fp32. Else, for bf16 ones,
+// whose own rounding is 2^-9, in fewer instructions: relative errors of |z|
+// 2^-24 in the exponentials, 1.5e-7 absolute in gelu's distribution function.
+// For bf16 the exact forms cost 815 -> 865 us at a product of 16384 x 2560 x 10240
+// with gelu and 18.7 -> 21.3 us at a norm's backward of 8 x 640 x 32 x 32 with silu;
+// the short ones would save fp32 0.7 of 7.8 us at a norm of 8 x 1280 x 16 x 16 and
+// 1.0 of 28.9 at a backward of 2 x 320 x 64 x 64.
+template <typename X, typename Y>
+constexpr bool exact_acts() { return sizeof(X) == 4 || sizeof(Y) == 4; }
+
+// exp(x + lo), on the hardware's 2^x (1 ulp). EXACT, for x <= 0: 2^n 2^f, |f| <=
+// 1/2, with n and f of the unrounded x log2(e), denormal results among them.
+template <bool EXACT>
+__device__ __forceinline__ float exp_of(float x, float lo = 0.0f) {
+    constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = 1.925963033e-8f;
+    if constexpr (!EXACT) return __builtin_amdgcn_exp2f(x * kLog2e);
+    x = fmaxf(x, -150.0f);  // 0 from there on
+    const float n = __builtin_rintf(x * kLog2e), f = fmaf(lo, kLog2e, fmaf(x, kLog2eRest, fmaf(x, kLog2e, -n)));
+    return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
 }
-__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }  // 1 ulp
+__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }  // 1 ulp, no denormals
 
-__device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.0f + fast_exp(-z)); }
+// 1 / (1 + exp(-z)) and what it leaves of 1. EXACT: both small ends without
+// cancellation; not the function's value for a NaN: the activations multiply
+// it by z.
+template <bool EXACT>
+__device__ __forceinline__ float sigmoid(float z, float *rest) {
+    if constexpr (EXACT) {
+        const float e = exp_of<true>(-fabsf(z)), r = fast_rcp(1.0f + e), er = e * r;
+        *rest = z >= 0.0f ? er : r;
+        return z >= 0.0f ? r : er;
+    } else {
+        const float s = fast_rcp(1.0f + exp_of<false>(-z));
+        *rest = 1.0f - s;
+        return s;
+    }
+}
 
-// Phi(z), the normal distribution function, and e = exp(-z^2 / 2).
-// Phi(-|z|) = poly(t) e / 2 with t = 1 / (1 + p |z| / sqrt 2): Abramowitz and
-// Stegun, Handbook of Mathematical Functions, 7.1.26 (|error of erf| <=
-// 1.5e-7, fp32's own at these sizes), a third of the library erf's
-// instructions.
+// Phi(z), the normal distribution function, and e = exp(-z^2 / 2), from
+// Phi(-|z|) = e r P(r) with r a reciprocal linear in |z|.
+// EXACT: P of degree 8 in (x - 2) / (x + 2), x = |z| / sqrt 2, of 0.5 (x + 2)
+// erfc(x) exp(x^2), fitted for the least relative error over |z| <= 13.5
+// (4.3e-8; the mapping of the half line is Shepherd and Laframboise's, Math.
+// Comp. 36, 1981): within 7 2^-24 of Phi(-|z|), relative, evaluated in fp32.
+// Else: Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26.
+template <bool EXACT>
 __device__ __forceinline__ float normal_cdf(float z, float *e_out) {
-    const float e = fast_exp(-0.5f * z * z);
-    const float t = fast_rcp(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.0f));
-    float s = fmaf(1.061405429f, t, -1.453152027f);
-    s = fmaf(s, t, 1.421413741f);
-    s = fmaf(s, t, -0.284496736f);
-    s = fmaf(s, t, 0.254829592f);
-    const float q = 0.5f * s * t * e;
+    float e, q;
+    if constexpr (EXACT) {
+        const float a = fminf(fabsf(z), 30.0f), h = a * a;  // 30: e is 0 from there on
+        e = exp_of<true>(-0.5f * h, -0.5f * fmaf(a, a, -h));
+        const float r = fast_rcp(a + 2.82842712475f), t = fmaf(-5.65685424949f, r, 1.0f);
+        float s = fmaf(-0.000325433502f, t, -0.000532054051f);
+        s = fmaf(s, t, 0.0021066654f);
+        s = fmaf(s, t, 0.00455091987f);
+        s = fmaf(s, t, -0.0151914684f);
+        s = fmaf(s, t, -0.0257634148f);
+        s = fmaf(s, t, 0.197614923f);
+        s = fmaf(s, t, -0.4858962f);
+        s = fmaf(s, t, 0.722368062f);
+        q = r * s * e;
+    } else {
+        e = exp_of<false>(-0.5f * z * z);
+        const float t = fast_rcp(fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.0f));
+        float s = fmaf(1.061405429f, t, -1.453152027f);
+        s = fmaf(s, t, 1.421413741f);
+        s = fmaf(s, t, -0.284496736f);
+        s = fmaf(s, t, 0.254829592f);
+        q = 0.5f * s * t * e;
+    }
     *e_out = e;
     return z >= 0.0f ? 1.0f - q : (z < 0.0f ? q : z);  // NaN stays NaN
 }
@@ -129,34 +177,32 @@ constexpr float kGeluCubic = 0.044715f;
 
 // z * gate, where a gate of 0 comes from z running to -infinity: the limit of
 // every activation there is 0, and -infinity itself gives NaN (-inf * 0).
-template <int ACT>
+template <int ACT, bool EXACT>
 __device__ __forceinline__ float act_fwd(float z) {
     if constexpr (ACT == WQ8_ACT_RELU) return z < 0.0f ? 0.0f : z;  // NaN stays NaN
-    if constexpr (ACT == WQ8_ACT_SILU) return z * sigmoid(z);
-    if constexpr (ACT == WQ8_ACT_GELU) {
-        float e;
-        return z * normal_cdf(z, &e);
-    }
+    float rest;
+    if constexpr (ACT == WQ8_ACT_SILU) return z * sigmoid<EXACT>(z, &rest);
+    if constexpr (ACT == WQ8_ACT_GELU) return z * normal_cdf<EXACT>(z, &rest);
     if constexpr (ACT == WQ8_ACT_GELU_TANH)  // (1 + tanh u) / 2 = sigmoid(2 u)
-        return z * sigmoid(kGeluTanh2 * fmaf(kGeluCubic * z * z, z, z));
+        return z * sigmoid<EXACT>(kGeluTanh2 * fmaf(kGeluCubic * z * z, z, z), &rest);
     return z;
 }
 
-template <int ACT>
+template <int ACT, bool EXACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == WQ8_ACT_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    float rest;
     if constexpr (ACT == WQ8_ACT_SILU) {
-        const float s = sigmoid(z);
-        return s * fmaf(z, 1.0f - s, 1.0f);
+        const float s = sigmoid<EXACT>(z, &rest);
+        return s * fmaf(z, rest, 1.0f);
     }
     if constexpr (ACT == WQ8_ACT_GELU) {
-        float e;
-        const float c = normal_cdf(z, &e);
-        return fmaf(z * 0.3989422804014327f, e, c);
+        const float c = normal_cdf<EXACT>(z, &rest);
+        return fmaf(z * 0.3989422804014327f, rest, c);
     }
     if constexpr (ACT == WQ8_ACT_GELU_TANH) {
-        const float s = sigmoid(kGeluTanh2 * fmaf(kGeluCubic * z * z, z, z));
-        return fmaf(z * s * (1.0f - s), kGeluTanh2 * fmaf(3.0f * kGeluCubic * z, z, 1.0f), s);
+        const float s = sigmoid<EXACT>(kGeluTanh2 * fmaf(kGeluCubic * z * z, z, z), &rest);
+        return fmaf(z * s * rest, kGeluTanh2 * fmaf(3.0f * kGeluCubic * z, z, 1.0f), s);
     }
     return 1.0f;
 }

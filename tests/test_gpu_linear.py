@@ -349,3 +349,51 @@ def test_more_threads_than_one_grid_row_takes():
     assert off.abs().max().item() <= 1e-35 and torch.count_nonzero(dx.view(torch.int16)[8:rows // 2 - 8] & 0x7f80) == 0
     assert (dw.double() - dz.T @ x[some].double()).abs().max().item() <= 1e-35
     assert torch.equal(db.double(), dz.sum(0))
+
+
+def exact_acts(z, name):
+    """(act, its slope, bounds of both) of fp32 values in 64 bits, for arithmetic
+    in fp32 throughout: a few roundings relative to the terms that are summed.
+    s, the gate: exp and reciprocal to one unit in the last place each (2 U), its
+    argument rounded as the formula has it; the sum, the products: U each."""
+    z = z.double()
+    if name == "silu":
+        s, rel = 1 / (1 + torch.exp(-z)), 8.0
+        return z * s, R.slope(z, name), rel * R.U * (z * s).abs(), 12 * R.U * s * (1 + z.abs())
+    if name == "gelu":
+        # the fit and its sum 12 U, the normal density 3, products
+        cdf = 0.5 * torch.erfc(-z / 2 ** 0.5)
+        pdf = torch.exp(-z * z / 2) / (2 * torch.pi) ** 0.5
+        return z * cdf, cdf + z * pdf, 20 * R.U * (z * cdf).abs(), 20 * R.U * (cdf + z.abs() * pdf)
+    k, c = 2 * (2 / torch.pi) ** 0.5, 0.044715
+    u = k * (z + c * z ** 3)
+    s, w, rel = 1 / (1 + torch.exp(-u)), k * (1 + 3 * c * z * z), 8 + 6 * u.abs()
+    p = z.abs() * s / (1 + torch.exp(u)) * w
+    return (z * s, s + z * s / (1 + torch.exp(u)) * w, rel * R.U * (z * s).abs(),
+            R.U * (rel * (s + p) + 4 * z.abs() * w * s))
+
+
+def act_points():
+    z = torch.cat([torch.linspace(-13, 13, 5000), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1e-3, -1e-3, 40.0, -40.0, 100.0, -100.0, 1e4, -1e4])])
+    return z.float()
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+def test_fp32_activations(name):
+    """fp32 results have fp32 activations, whatever the inputs' type: one column, so that z is x itself."""
+    z = act_points()
+    y, slope, ey, es = exact_acts(z, name)
+    plan = q.LinearPlan(len(z), 1, 1, act=name)
+    one = torch.ones(1, 1, device="cuda")
+    R.check(q.wq8_linear_forward(plan, z[:, None].cuda(), one)[:, 0], y, ey + 1e-37, "y")
+    row = q.LinearPlan(1, 1, len(z), act=name)
+    ones = torch.ones(1, len(z), device="cuda")
+    db = q.wq8_linear_backward(row, ones, one, ones.T.contiguous(), z=z[None].cuda(), want_dbias=True)[2]
+    R.check(db, slope, es + 1e-37, "slope")
+    zb = z.to(BF)
+    y, slope, ey, es = exact_acts(zb, name)
+    plan = q.LinearPlan(len(z), 1, 1, act=name, x_dtype=BF, y_dtype=F32)
+    R.check(q.wq8_linear_forward(plan, zb[:, None].cuda(), one.to(BF))[:, 0], y, ey + 1e-37, "y of bf16")
+    row = q.LinearPlan(1, 1, len(z), act=name, x_dtype=F32, y_dtype=BF)
+    db = q.wq8_linear_backward(row, ones.to(BF), one, ones.T.contiguous(), z=zb[None].cuda(), want_dbias=True)[2]
+    R.check(db, slope, es + 1e-37, "slope of bf16")

@@ -240,3 +240,27 @@ def test_more_threads_than_one_grid_row_takes():
     R.check(ds[-9:], want["dshift"][0], 2 * want["dshift"][1], "dshift")
     # x is 0 in the others: z = h = 0, dz the slope 1/2 of silu at 0, and dx what that leaves of its mean
     assert torch.count_nonzero(dx[:-9]) == 0 and torch.count_nonzero(ds[:-9]) == 0
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("xt", [F32, BF])
+def test_fp32_activations(name, xt):
+    """fp32 results have fp32 activations (bounds as for the product's)."""
+    from test_gpu_linear import act_points, exact_acts
+
+    z = act_points()[:5004].to(xt)
+    n = len(z)
+    # the backward takes mean and rstd: with 0 and 1, z is x itself and dbeta of one pixel the slope
+    plan = q.NormPlan(1, n, 1, 1, groups=1, act=name, x_dtype=xt, y_dtype=F32)
+    x, ones = z.reshape(plan.x_shape).cuda(), torch.ones(plan.y_shape, device="cuda")
+    zero, one = torch.zeros(1, 1, device="cuda"), torch.ones(1, 1, device="cuda")
+    _, slope, _, es = exact_acts(z, name)
+    db = q.wq8_norm_backward(plan, ones, x, zero, one, dbeta=torch.empty(n, device="cuda"))[2]
+    R.check(db, slope, es + 1e-37, "slope")
+    # forward: z as the mean and rstd that it returns give it, to 6 U
+    gamma, beta = torch.full((n,), 4.0, device="cuda"), torch.full((n,), -1.0, device="cuda")
+    y, mean, rstd = q.wq8_norm_forward(plan, x, gamma, beta, want_stats=True)
+    h = (z.double() - mean.cpu().double()) * rstd.cpu().double() * 4
+    ez = 6 * R.U * (h.abs() + (mean.cpu().double() * rstd.cpu().double() * 4).abs() + 1)
+    y64, slope, ey, _ = exact_acts((h - 1)[0], name)
+    R.check(y.reshape(-1), y64, ey + 1.2 * ez[0] * slope.abs() + ez[0] ** 2 + 1e-37, "y")
