@@ -241,7 +241,7 @@ __global__ __launch_bounds__(kNormSplitThreads) void k_norm_stats(NormGeo g, Nor
             });
             const float inv = 1.0f / fmaxf(more, 1.0f);
 #pragma unroll
-            for (int k = 0; k < NG; ++k) pivot[k] = t[k] * inv;
+            for (int k = 0; k < NG; ++k) pivot[k] = fabsf(t[k]) < INFINITY ? t[k] * inv : 0.0f;  // d of an infinity is that infinity
 #pragma unroll
             for (int k = 0; k < NC; ++k) off[k] -= pivot[NG == 1 ? 0 : k];
         }

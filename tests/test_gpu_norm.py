@@ -264,3 +264,29 @@ def test_fp32_activations(name, xt):
     ez = 6 * R.U * (h.abs() + (mean.cpu().double() * rstd.cpu().double() * 4).abs() + 1)
     y64, slope, ey, _ = exact_acts((h - 1)[0], name)
     R.check(y.reshape(-1), y64, ey + 1.2 * ez[0] * slope.abs() + ez[0] ** 2 + 1e-37, "y")
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("xl,yl", LAYOUTS)
+@pytest.mark.parametrize("C", [16, 24])
+@pytest.mark.parametrize("H", [6, 150])
+def test_statistics_of_what_is_not_finite(bad, xl, yl, C, H):
+    """mean = sum v / m as the formula gives it, in one kernel and split over two: an infinity
+    among finite values is the mean, two of opposite sign or a NaN make a NaN; rstd is a NaN."""
+    _, dev = make(2, C, H, 60, F32, xl, 1)
+    x = R.nhwc(dev["x"], xl)
+    w = C // 4
+    x[1, 2, 3, w + 1] = bad                                                  # group 1 of image 1
+    x[0, H - 1, 59, C - 1], x[0, 0, 0, C - 2] = bad, -bad                    # group 3 of image 0
+    x[0, 0, 0, 0] = bad                                                      # the first value of a block
+    plan = q.NormPlan(2, C, H, 60, groups=4, act="silu", x_layout=xl, y_layout=yl)
+    _, mean, rstd = q.wq8_norm_forward(plan, dev["x"], dev["gamma"], dev["beta"], want_stats=True)
+    torch.cuda.synchronize()
+    want = torch.tensor(bad)
+    for n, g in ((1, 1), (0, 0)):
+        assert torch.equal(mean[n, g].cpu(), want) or (torch.isnan(want) and torch.isnan(mean[n, g])), (n, g, mean)
+    assert torch.isnan(mean[0, 3])
+    sick = torch.zeros(2, 4, dtype=torch.bool)
+    sick[1, 1] = sick[0, 0] = sick[0, 3] = True
+    assert torch.isnan(rstd.cpu()[sick]).all()
+    assert torch.isfinite(mean.cpu()[~sick]).all() and torch.isfinite(rstd.cpu()[~sick]).all()
