@@ -5,7 +5,7 @@
 // forward: two tensors share the registers), else twice. Measured: 8 x 640 x 32 x 32
 // bf16 fused 18.7 us (31 MB; the activation's slope, two quarter-rate
 // instructions a value, is evaluated for the sums and again for dx: half of the
-// kernel's 17 us is arithmetic), 2 x 320 x 64 x 64 f32 with dy in NCHW split 28.9 us in
+// kernel's 17 us is arithmetic), 2 x 320 x 64 x 64 f32 with dy in NCHW split 29.3 us in
 // kernels of 13, 10 and 5 us (52 MB).
 #pragma once
 
@@ -24,8 +24,11 @@ namespace {
 template <int V, int KIND>
 struct Channels {
     static constexpr int NC = thread_channels<V, KIND>(), NG = group_values<V, KIND>();
-    float off[NC], ga[NC], be[NC], rstd[NG];  // off = shift - mean
+    float off[NC], ga[NC], sc[NC], be[NC], rstd[NG];  // off = shift - mean, sc = gamma rstd
     int kg[NC];
+
+    // z of v = x + off, in the forward's operations: relu's mask is the forward's
+    __device__ __forceinline__ float z(float v, int k) const { return fmaf(v, sc[k], be[k]); }
 
     __device__ __forceinline__ void load(const NormGeo &g, const NormPtrs &a, const Where &w) {
         const int64_t group0 = (int64_t)w.n * g.G + w.g0;
@@ -37,6 +40,8 @@ struct Channels {
         for (int k = 0; k < NC; ++k) off[k] -= a.mean_in[group0 + kg[k]];
 #pragma unroll
         for (int k = 0; k < NG; ++k) rstd[k] = a.rstd_in[group0 + kg[k]];
+#pragma unroll
+        for (int k = 0; k < NC; ++k) sc[k] = ga[k] * rstd[NG == 1 ? 0 : k];
     }
 };
 
@@ -74,8 +79,8 @@ __device__ __forceinline__ void add_sums(float *s1, float *s2, float *s3, const 
     with_act(g.act, [&](auto act) {
         for_values<V, KIND, E, BATCH>(g.b, w, first, [&](int e, int k, auto ok) {
             const int kc = c.NC == 1 ? 0 : k;
-            const float hv = (to_f32(fx[e].v[k]) + c.off[kc]) * c.rstd[c.NG == 1 ? 0 : k], h = ok ? hv : 0.0f;
-            const float dv = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value, exact_acts<XT, YT>()>(fmaf(h, c.ga[kc], c.be[kc]));
+            const float v = to_f32(fx[e].v[k]) + c.off[kc], hv = v * c.rstd[c.NG == 1 ? 0 : k], h = ok ? hv : 0.0f;
+            const float dv = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value, exact_acts<XT, YT>()>(c.z(v, kc));
             const float dz = ok ? dv : 0.0f;
             s1[kc] += dz;
             s2[kc] = fmaf(dz, h, s2[kc]);
@@ -130,8 +135,8 @@ __device__ __forceinline__ void write_dx(const Vec<XT, V> (&fx)[E], const Vec<YT
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
                     const int kc = CL ? k : 0, kk = c.NG == 1 ? 0 : k;
-                    const float h = (to_f32(fx[e].v[k]) + c.off[kc]) * c.rstd[kk];
-                    const float dz = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value, exact_acts<XT, YT>()>(fmaf(h, c.ga[kc], c.be[kc]));
+                    const float v = to_f32(fx[e].v[k]) + c.off[kc], h = v * c.rstd[kk];
+                    const float dz = to_f32(fd[e].v[k]) * act_slope<decltype(act)::value, exact_acts<XT, YT>()>(c.z(v, kc));
                     r.v[k] = from_f32<XT>(c.rstd[kk] * (fmaf(dz, c.ga[kc], -m1[kk]) - h * m2[kk]));
                 }
                 XT *const to = addr<XT, V, KIND>(dx, g, g.xs, w, at.p);

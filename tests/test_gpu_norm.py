@@ -290,3 +290,27 @@ def test_statistics_of_what_is_not_finite(bad, xl, yl, C, H):
     sick[1, 1] = sick[0, 0] = sick[0, 3] = True
     assert torch.isnan(rstd.cpu()[sick]).all()
     assert torch.isfinite(mean.cpu()[~sick]).all() and torch.isfinite(rstd.cpu()[~sick]).all()
+
+
+@pytest.mark.parametrize("xl,yl", LAYOUTS)
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("H,C,groups", [(5, 512, 32), (5, 480, 32), (140, 480, 4)])
+def test_relu_has_one_mask(xl, yl, xt, yt, H, C, groups):
+    """The backward's relu passes exactly where the forward's did. beta puts z of one pixel within rounding of 0
+    in every channel; dy is 1 there and 0 elsewhere, so that dbeta is the mask of the backward."""
+    W = 31
+    _, dev = make(1, C, H, W, xt, xl, 21)
+    plan = q.NormPlan(1, C, H, W, groups=groups, act="relu", x_dtype=xt, y_dtype=yt, x_layout=xl, y_layout=yl)
+    gamma = dev["gamma"]
+    _, mean, rstd = q.wq8_norm_forward(plan, dev["x"], want_stats=True)
+    x = R.nhwc(dev["x"], xl)[0, 2, 7].double()
+    spread = lambda s: s[0].double().repeat_interleave(C // groups)  # noqa: E731
+    beta = -((x - spread(mean)) * spread(rstd) * gamma.double()).float()
+    y, m2, r2 = q.wq8_norm_forward(plan, dev["x"], gamma, beta, want_stats=True)
+    assert torch.equal(m2, mean) and torch.equal(r2, rstd)
+    dy = torch.zeros(plan.y_shape, dtype=yt, device="cuda")
+    R.nhwc(dy, yl)[0, 2, 7] = 1
+    db = q.wq8_norm_backward(plan, dy, dev["x"], mean, rstd, gamma, beta)[2]
+    mask = (R.nhwc(y, yl)[0, 2, 7] > 0).float()
+    assert 0 < mask.sum() < C
+    assert torch.equal(db, mask)
