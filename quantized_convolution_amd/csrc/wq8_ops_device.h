@@ -202,7 +202,9 @@ __device__ __forceinline__ float act_slope(float z) {
     }
     if constexpr (ACT == WQ8_ACT_GELU_TANH) {
         const float s = sigmoid<EXACT>(kGeluTanh2 * fmaf(kGeluCubic * z * z, z, z), &rest);
-        return fmaf(z * s * rest, kGeluTanh2 * fmaf(3.0f * kGeluCubic * z, z, 1.0f), s);
+        // s rest is 0 long before z^2 overflows: 0 times infinity would be a NaN
+        const float b = __builtin_amdgcn_fmed3f(z, -1e9f, 1e9f);
+        return fmaf(z * s * rest, kGeluTanh2 * fmaf(3.0f * kGeluCubic * b, b, 1.0f), s);
     }
     return 1.0f;
 }

@@ -397,3 +397,22 @@ def test_fp32_activations(name):
     row = q.LinearPlan(1, 1, len(z), act=name, x_dtype=F32, y_dtype=BF)
     db = q.wq8_linear_backward(row, ones.to(BF), one, ones.T.contiguous(), z=zb[None].cuda(), want_dbias=True)[2]
     R.check(db, slope, es + 1e-37, "slope of bf16")
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh"])
+def test_activations_of_large_values(name, xt, yt):
+    """Finite values whose powers are not: act(z) is z or 0, its slope 1 or 0, to the ends of the type."""
+    z = torch.cat([s * 10.0 ** torch.arange(3, 38) for s in (1.0, -1.0)]).to(yt)
+    n = len(z)
+    one = torch.ones(1, 1, device="cuda")
+    x = z.to(xt)
+    y = q.wq8_linear_forward(q.LinearPlan(n, 1, 1, act=name, x_dtype=xt, y_dtype=yt), x[:, None].cuda(), one.to(xt))
+    assert torch.equal(y[:, 0].cpu(), x.to(yt).clamp(min=0))
+    row = q.LinearPlan(1, 1, n, act=name, x_dtype=xt, y_dtype=yt)
+    dy = torch.full((1, n), 3.0, device="cuda", dtype=yt)
+    dx, dw, db = q.wq8_linear_backward(row, dy, one.to(xt), torch.ones(n, 1, device="cuda", dtype=xt), z=z[None].cuda(),
+                                       want_dbias=True)
+    want = 3.0 * (z > 0)
+    assert torch.equal(db.cpu(), want.float()) and torch.equal(dw[:, 0].cpu().float(), want.float())
+    assert dx.item() == want.sum().item()
