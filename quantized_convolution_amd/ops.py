@@ -8,7 +8,9 @@ the library's own refusals raise Wq8Error.
 
 A call runs on `stream`, or on the current one; outputs and workspaces that it
 makes are allocated as that stream's. Buffers that a caller gives are ordered
-and kept by the caller, as with any work on another stream than their own.
+and kept by the caller, as with any work on another stream than their own. No
+autograd graph is recorded: the backwards are functions of their own, and a
+tensor that requires a gradient is refused unless under torch.no_grad().
 """
 from __future__ import annotations
 
@@ -199,6 +201,9 @@ class _Args:
                     raise ValueError(f"{name} must be contiguous")
             elif any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
                 raise ValueError(f"{name} must have strides {tuple(strides)}, got {tuple(t.stride())}")
+            if t.requires_grad and torch.is_grad_enabled():
+                raise ValueError(f"{name} requires a gradient, and no graph is recorded here: call this under "
+                                 "torch.no_grad() and form gradients with the operator's backward")
             d = t.get_device()
             if d != self.device:
                 if self.device is not None:

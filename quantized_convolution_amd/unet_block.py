@@ -72,7 +72,8 @@ class ResBlock:
 class FeedForward:
     """x [N][H][W][C] -> x + linear(gelu(linear(norm(x)))), with its backward.
 
-    weights: norm (gamma, beta), w1 [D][C], w2 [C][D] (dtype), b1, b2 (f32)."""
+    weights: norm (gamma, beta), w1 [D][C], w2 [C][D] (dtype), b1, b2 (f32);
+    they may be parameters, `backward` returns their gradients."""
 
     def __init__(self, weights, N, C, H, W, groups=32, dtype=torch.bfloat16, device="cuda"):
         self.w = weights
@@ -89,6 +90,12 @@ class FeedForward:
         self.da, self.du, self.dx = (torch.empty_like(t) for t in (self.a, self.u, self.a))
 
     def __call__(self, x):
+        if x.requires_grad and torch.is_grad_enabled():
+            raise ValueError("x requires a gradient, and no graph is recorded here: `backward` returns it")
+        with torch.no_grad():
+            return self._forward(x)
+
+    def _forward(self, x):
         w, ws, rows = self.w, self.ws, self.up.x_shape
         self.x = x
         wq8_norm_forward(self.norm, x, *w["norm"], y=self.a, mean=self.mean, rstd=self.rstd, workspace=ws)
@@ -96,6 +103,7 @@ class FeedForward:
         wq8_linear_forward(self.down, self.u, w["w2"], w["b2"], x.view(rows), y=self.out, workspace=ws)
         return self.out.view(x.shape)
 
+    @torch.no_grad()
     def backward(self, dout):
         """{name: gradient} of x and of every weight, for the last call."""
         w, ws, rows = self.w, self.ws, self.up.x_shape

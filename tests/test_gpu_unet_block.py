@@ -182,3 +182,17 @@ def test_other_stream_while_this_one_allocates():
     s.synchronize()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(inputs) == 6
+
+
+def test_feed_forward_with_parameters():
+    """Weights may be parameters: their gradients come from `backward`. An input that asks for a graph is refused."""
+    w, x, dy = ff_weights(F32)
+    move = lambda v, f: tuple(f(i.cuda()) for i in v) if isinstance(v, tuple) else f(v.cuda())  # noqa: E731
+    ffs = [FeedForward({k: move(v, f) for k, v in w.items()}, N, x.shape[3], H, W, dtype=F32) for f in (lambda t: t, torch.nn.Parameter)]
+    outs = [f(x.cuda()) for f in ffs]
+    grads = [f.backward(dy.cuda()) for f in ffs]
+    torch.cuda.synchronize()
+    assert torch.equal(*outs) and all(torch.equal(grads[0][k], grads[1][k]) for k in grads[0])
+    assert not any(t.requires_grad for t in grads[1].values())
+    with pytest.raises(ValueError, match="x requires a gradient"):
+        ffs[0](x.cuda().requires_grad_())

@@ -255,3 +255,24 @@ def test_positions_fit_32_bits(N, C, H, W, groups, status, x_layout, y_layout):
     for t in (0, 1):
         d = O.wq8_norm_desc(N, C, H, W, groups, 1e-5, 2, t, t, x_layout, y_layout, 0, 0)
         assert create("norm", d) == status
+
+
+def test_gradients_are_not_dropped():
+    """The operators record no graph: a tensor that asks for one is refused, and taken where none is recorded."""
+    n, p = O.NormPlan(2, 16, 4, 5, groups=4), O.LinearPlan(6, 8, 16)
+    x, g, s = torch.zeros(n.x_shape), torch.zeros(16), torch.zeros(2, 4)
+    t, w, y = torch.zeros(6, 8), torch.zeros(16, 8), torch.zeros(6, 16)
+    ask = lambda v: v.clone().requires_grad_()  # noqa: E731
+    calls = [(lambda: O.wq8_norm_forward(n, ask(x), y=x), "x"), (lambda: O.wq8_norm_forward(n, x, ask(g), y=x), "gamma"),
+             (lambda: O.wq8_norm_forward(n, x, g, ask(g), y=x), "beta"),
+             (lambda: O.wq8_norm_forward(n, x, shift=ask(torch.zeros(2, 16)), y=x), "shift"),
+             (lambda: O.wq8_norm_backward(n, ask(x), x, s, s, dx=x), "dy"),
+             (lambda: O.wq8_linear_forward(p, ask(t), w, y=y), "x"), (lambda: O.wq8_linear_forward(p, t, ask(w), y=y), "w"),
+             (lambda: O.wq8_linear_forward(p, t, w, ask(g), y=y), "bias"),
+             (lambda: O.wq8_linear_forward(p, t, w, None, ask(y), y=y), "residual"),
+             (lambda: O.wq8_linear_backward(p, y, t, ask(w), dx=t, dw=w), "w")]
+    for fn, name in calls:
+        with pytest.raises(ValueError, match=f"^{name} requires a gradient"):
+            fn()
+        with torch.no_grad(), pytest.raises(ValueError, match="must be on a GPU"):
+            fn()
