@@ -42,6 +42,15 @@ def _choice(table, key, name):
     return table[key]
 
 
+def _desc(cls, *values):
+    """The descriptor; ctypes cuts whole numbers to their fields without a word."""
+    d = cls(*values)
+    for (name, _), v in zip(cls._fields_, values):
+        if isinstance(v, int) and getattr(d, name) != v and name != "eps":
+            raise ValueError(f"{name} = {v} does not fit its field")
+    return d
+
+
 class _Plan:
     """Owns a plan handle, its workspace sizes and the buffers' forms."""
 
@@ -104,9 +113,9 @@ class NormPlan(_Plan):
         self.N, self.C, self.H, self.W, self.groups, self.eps, self.act = N, C, H, W, groups, eps, act
         self.x_dtype, self.y_dtype, self.x_layout, self.y_layout = x_dtype, y_dtype, x_layout, y_layout
         self.x_stride, self.y_stride = int(x_stride), int(y_stride)
-        d = wq8_norm_desc(N, C, H, W, groups, eps, _choice(ACTS, act, "act"), _choice(_DT, x_dtype, "x_dtype"),
-                          _choice(_DT, y_dtype, "y_dtype"), _choice(LAYOUTS, x_layout, "x_layout"),
-                          _choice(LAYOUTS, y_layout, "y_layout"), self.x_stride, self.y_stride)
+        d = _desc(wq8_norm_desc, N, C, H, W, groups, eps, _choice(ACTS, act, "act"), _choice(_DT, x_dtype, "x_dtype"),
+                  _choice(_DT, y_dtype, "y_dtype"), _choice(LAYOUTS, x_layout, "x_layout"),
+                  _choice(LAYOUTS, y_layout, "y_layout"), self.x_stride, self.y_stride)
         self._make(d)
         self.x_shape = (N, H, W, C) if x_layout == "nhwc" else (N, C, H, W)
         self.y_shape = (N, H, W, C) if y_layout == "nhwc" else (N, C, H, W)
@@ -143,9 +152,9 @@ class LinearPlan(_Plan):
         self.x_dtype, self.y_dtype, self.r_layout, self.pixels = x_dtype, y_dtype, r_layout, pixels
         self.x_stride, self.y_stride, self.r_stride = int(x_stride), int(y_stride), int(r_stride)
         self.round_dz = bool(round_dz)
-        d = wq8_linear_desc(rows, Cin, Cout, _choice(ACTS, act, "act"), _choice(_DT, x_dtype, "x_dtype"),
-                            _choice(_DT, y_dtype, "y_dtype"), _choice(LAYOUTS, r_layout, "r_layout"), pixels,
-                            self.x_stride, self.y_stride, self.r_stride, self.round_dz)
+        d = _desc(wq8_linear_desc, rows, Cin, Cout, _choice(ACTS, act, "act"), _choice(_DT, x_dtype, "x_dtype"),
+                  _choice(_DT, y_dtype, "y_dtype"), _choice(LAYOUTS, r_layout, "r_layout"), pixels,
+                  self.x_stride, self.y_stride, self.r_stride, self.round_dz)
         self._make(d)
         self.x_shape, self.y_shape, self.w_shape = (rows, Cin), (rows, Cout), (Cout, Cin)
         self.r_shape = (rows // pixels, Cout, pixels) if r_layout == "nchw" else self.y_shape

@@ -276,3 +276,16 @@ def test_gradients_are_not_dropped():
             fn()
         with torch.no_grad(), pytest.raises(ValueError, match="must be on a GPU"):
             fn()
+
+
+def test_sizes_are_not_cut_to_32_bits():
+    """A size that the descriptor's field does not hold is refused: cut off, the kernels would work on other sizes than the buffers have."""
+    for kw in (dict(N=(1 << 32) + 2), dict(C=(1 << 32) + 64), dict(H=1 << 32), dict(groups=(1 << 32) + 4), dict(x_stride=1 << 32),
+               dict(y_stride=(1 << 32) + 80)):
+        name, = kw
+        with pytest.raises(ValueError, match=f"^{name} = "):
+            O.NormPlan(**{**dict(N=2, C=64, H=4, W=5, groups=4), **kw})
+    for kw in (dict(rows=1 << 64), dict(Cin=(1 << 32) + 8), dict(Cout=-(1 << 32) + 16), dict(pixels=(1 << 32) + 3), dict(r_stride=1 << 32)):
+        name, = kw
+        with pytest.raises(ValueError, match=f"^{name} = "):
+            O.LinearPlan(**{**dict(rows=6, Cin=8, Cout=16), **kw})
