@@ -54,10 +54,11 @@ __device__ __forceinline__ void load_dy(Vec<YT, V> (&f)[E], const YT *dy, const 
     if constexpr (!CROSS) {
         load_steps<YT, V, KIND, E>(f, dy, g, s, g.ys, w, first);
     } else {
+        int te = 0;  // steps read from the tile
 #pragma unroll
-        for (int e = 0; e < E; ++e)
+        for (int e = 0; e < E; ++e) {
+            f[e] = {};
             if (first + e < s.steps) {  // uniform: the tile's barriers
-                const int te = e % s.tsteps;
                 if (te == 0) {
                     if (e > 0) __syncthreads();
                     global_to_tile<YT, CL>(tile, dy, g, s, w, g.ys, w.p0 + (first + e) * s.window);
@@ -67,7 +68,9 @@ __device__ __forceinline__ void load_dy(Vec<YT, V> (&f)[E], const YT *dy, const 
                 const int p0 = w.p0 + (first + e - te) * s.window;
 #pragma unroll
                 for (int k = 0; k < V; ++k) f[e].v[k] = k >= at.lo ? tile[tile_at<V, KIND>(s, w, p0, at.p, k)] : YT(0);
+                if (++te == s.tsteps) te = 0;
             }
+        }
         __syncthreads();
     }
 }

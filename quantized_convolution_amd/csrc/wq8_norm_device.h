@@ -429,15 +429,14 @@ size_t tile_lds(const NormShape &s, bool cl) {
 template <bool BWD, typename XT, typename YT, int V, int KIND, typename R>
 void pick_steps(const NormGeo &g, const R &run) {
     const NormShape &s = BWD ? g.b : g.f;
-    const auto go = [&](auto split, auto e) {
-        constexpr bool S = decltype(split)::value;
-        constexpr int E = decltype(e)::value;
-        if (g.x_nhwc != g.y_nhwc) run.template operator()<XT, YT, V, KIND, true, S, E>();
-        else run.template operator()<XT, YT, V, KIND, false, S, E>();
+    const auto go = [&](auto cross) {
+        constexpr bool X = decltype(cross)::value;
+        if (s.split) run.template operator()<XT, YT, V, KIND, X, true, kNormE>();
+        else if (s.steps <= kNormE) run.template operator()<XT, YT, V, KIND, X, false, kNormE>();
+        else run.template operator()<XT, YT, V, KIND, X, false, norm_max_steps(BWD, KIND == kStraddle, X)>();
     };
-    if (s.split) go(std::true_type{}, std::integral_constant<int, kNormE>{});
-    else if (s.steps <= kNormE) go(std::false_type{}, std::integral_constant<int, kNormE>{});
-    else go(std::false_type{}, std::integral_constant<int, norm_max_steps(BWD, KIND == kStraddle)>{});
+    if (g.x_nhwc != g.y_nhwc) go(std::true_type{});
+    else go(std::false_type{});
 }
 
 template <bool BWD, typename XT, typename YT, typename R>

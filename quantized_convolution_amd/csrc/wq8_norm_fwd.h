@@ -100,38 +100,56 @@ __device__ __forceinline__ void join_stats(const NormGeo &g, const NormPtrs &a, 
 
 // What remains of the fused and of the output kernel: z = (v - mean) rstd gamma
 // + beta as one fma, the activation, and the vectors' way out. first: the step
-// that f[0] holds.
+// that f[0] holds. With the other layout on y's side all values come first:
+// the tile's way out stands in the code once a step, not once a step and
+// activation.
 template <typename XT, typename YT, int V, int KIND, bool CROSS, int E>
 __device__ __forceinline__ void write_out(const Vec<XT, V> (&f)[E], const float *off, const float *sc, const float *be,
                                           const NormGeo &g, const Where &w, YT *y, int first, YT *tile) {
     constexpr bool CL = KIND != kPlanar;
     const NormShape &s = g.f;
-    with_act(g.act, [&](auto act) {
+    const auto value = [&](auto act, int e, int k) {
+        const int kc = CL ? k : 0;
+        return from_f32<YT>(act_fwd<decltype(act)::value, exact_acts<YT, YT>()>(fmaf(to_f32(f[e].v[k]) + off[kc], sc[kc], be[kc])));
+    };
+    if constexpr (!CROSS) {
+        with_act(g.act, [&](auto act) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (first + e < s.steps) {
+                    const Step at = step_of<V, KIND>(s, w, first + e);
+                    Vec<YT, V> r;
+#pragma unroll
+                    for (int k = 0; k < V; ++k) r.v[k] = value(act, e, k);
+                    if (at.lo < V) store_vec<YT, V>(addr<YT, V, KIND>(y, g, g.ys, w, at.p), r);
+                }
+        });
+    } else {
+        Vec<YT, V> r[E] = {};
+        with_act(g.act, [&](auto act) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (first + e < s.steps)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) r[e].v[k] = value(act, e, k);
+        });
+        int te = 0;  // steps in the tile
 #pragma unroll
         for (int e = 0; e < E; ++e)
             if (first + e < s.steps) {
                 const Step at = step_of<V, KIND>(s, w, first + e);
-                Vec<YT, V> r;
+                const int p0 = w.p0 + (first + e - te) * s.window;
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const int kc = CL ? k : 0;
-                    r.v[k] = from_f32<YT>(act_fwd<decltype(act)::value, exact_acts<YT, YT>()>(fmaf(to_f32(f[e].v[k]) + off[kc], sc[kc], be[kc])));
-                }
-                if constexpr (!CROSS) {
-                    if (at.lo < V) store_vec<YT, V>(addr<YT, V, KIND>(y, g, g.ys, w, at.p), r);
-                } else {
-                    const int te = e % s.tsteps, p0 = w.p0 + (first + e - te) * s.window;
-#pragma unroll
-                    for (int k = 0; k < V; ++k)
-                        if (k >= at.lo) tile[tile_at<V, KIND>(s, w, p0, at.p, k)] = r.v[k];
-                    if (te == s.tsteps - 1 || e == E - 1 || first + e == s.steps - 1) {
-                        __syncthreads();
-                        tile_to_global<YT, CL>(tile, y, g, s, w, g.ys, p0);
-                        __syncthreads();
-                    }
+                for (int k = 0; k < V; ++k)
+                    if (k >= at.lo) tile[tile_at<V, KIND>(s, w, p0, at.p, k)] = r[e].v[k];
+                if (++te == s.tsteps || e == E - 1 || first + e == s.steps - 1) {
+                    __syncthreads();
+                    tile_to_global<YT, CL>(tile, y, g, s, w, g.ys, p0);
+                    __syncthreads();
+                    te = 0;
                 }
             }
-    });
+    }
 }
 
 // off = shift - mean, sc = rstd gamma, be = beta of the thread's channels;

@@ -23,8 +23,11 @@ constexpr int norm_max_vec(size_t xs, size_t ys, bool backward) { return xs == 2
 
 // Steps whose values a thread of a 1024-thread block can hold: 128 registers,
 // 64 of them for the values of x (forward) or of x and dy (backward), fewer
-// where it keeps a group per channel as well.
-constexpr int norm_max_steps(bool backward, bool straddle) { return !backward ? 16 : straddle ? 4 : 8; }
+// where it keeps a group per channel as well, or where windows of y change
+// layout (16 steps of them need some 300 registers more than there are).
+constexpr int norm_max_steps(bool backward, bool straddle, bool cross) {
+    return backward ? (straddle ? 4 : 8) : cross ? 8 : 16;
+}
 
 // One pass of the group norm. A block handles a slab of `slabC` channels (K
 // whole groups, or 1/J of one) over `chunk` pixels of one image. With

@@ -142,7 +142,7 @@ NormShape split_shape(const NormGeo &g, int V, int batch, int xsz) {
 // batch of steps and its spare threads reach past the image's pixels, and its
 // slab past the channels, before they are clamped.
 bool positions_fit(const NormGeo &g, const NormShape &s) {
-    constexpr int64_t lim = (int64_t)1 << 31, batch = norm_max_steps(false, false);
+    constexpr int64_t lim = (int64_t)1 << 31, batch = norm_max_steps(false, false, false);
     const int64_t last = (int64_t)(s.nchunk - 1) * s.chunk, most = s.steps + batch;
     return last + s.chunk < lim && last + most * s.window + 1024 * norm_max_vec(2, 2, false) < lim &&
            (int64_t)g.G / s.K * s.J * s.slabC + 2 * kNormMaxSlab < lim;
@@ -176,7 +176,7 @@ NormShape choose_norm(const NormGeo &g, int xsz, int ysz, bool backward) {
     while (g.x_nhwc && V > 4 && g.cpg % V != 0) V /= 2;
     if (g.x_nhwc && g.cpg % V != 0) V = vmax;
     if (single) V = 1;
-    const int most = norm_max_steps(backward, g.x_nhwc && g.cpg % V != 0);
+    const int most = norm_max_steps(backward, g.x_nhwc && g.cpg % V != 0, g.x_nhwc != g.y_nhwc);
     NormShape s;
     s.steps = 1 << 30;
     for (int k = 1; k <= g.G; ++k) {
