@@ -29,15 +29,19 @@ namespace {
 constexpr int kDzRows = 4;
 
 // v as the sum of two bf16 values: its first 8 bits, cut off, and what that
-// leaves, rounded: within 2^-16 of v. Both have v's sign, and unless v is zero
-// the second is no smaller than the smallest normal number (1.2e-38, nothing
-// beside any product): an infinity that they are multiplied by gives the same
-// infinity twice, where a zero or another sign would make it a NaN.
+// leaves, rounded: within 2^-16 of v. Where nothing is left the first is the
+// next number towards zero and the second the difference, exactly. So both
+// have v's sign and neither is zero unless v is: an infinity that they are
+// multiplied by gives the same infinity twice, where a zero or another sign
+// would make it a NaN. (A smallest number in place of the zero is not the same:
+// the matrix cores drop a unit in the last place of a sum that it is taken from.)
 __device__ __forceinline__ void split_dz(float v, bf16_t &top, bf16_t &rest) {
     const uint32_t u = __float_as_uint(v);
-    top = v == v ? (bf16_t)(u >> 16) : from_f32<bf16_t>(v);
-    rest = from_f32<bf16_t>(v - to_f32(top));  // NaN if v is infinite
-    if (!(fabsf(to_f32(rest)) >= 0x1p-126f)) rest = (bf16_t)((u >> 16 & 0x8000u) | (v != 0.0f ? 0x0080u : 0u));
+    bf16_t t = (bf16_t)(u >> 16);
+    if (fabsf(v - to_f32(t)) < 0x1p-126f && (t & 0x7fff)) --t;
+    top = t;
+    rest = from_f32<bf16_t>(v - to_f32(t));
+    if (!(fabsf(v) < INFINITY)) top = rest = from_f32<bf16_t>(v);
 }
 
 template <typename XT, typename YT, int V>

@@ -416,3 +416,21 @@ def test_activations_of_large_values(name, xt, yt):
     want = 3.0 * (z > 0)
     assert torch.equal(db.cpu(), want.float()) and torch.equal(dw[:, 0].cpu().float(), want.float())
     assert dx.item() == want.sum().item()
+
+
+@pytest.mark.parametrize("round_dz", [False, True])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_backward_of_gradients_that_are_not_finite(bad, round_dz):
+    """An infinity in dy is one in its row of dx and its row of dw with the sign of what it meets, and nowhere else."""
+    d = make(40, 48, 56, BF, F32, 17)
+    d["dy"][3, 5] = bad
+    plan = q.LinearPlan(40, 48, 56, x_dtype=BF, y_dtype=F32, round_dz=round_dz)
+    dx, dw, db = q.wq8_linear_backward(plan, d["dy"].cuda(), d["x"].cuda(), d["w"].cuda(), want_dbias=True)
+    torch.cuda.synchronize()
+    for got, row, other in ((dx, 3, d["w"][5]), (dw, 5, d["x"][3])):
+        got = got.cpu().float()
+        want = torch.sign(other.float()) * bad
+        assert torch.equal(got[row].nan_to_num(7), want.nan_to_num(7))
+        got[row] = 0
+        assert torch.isfinite(got).all()
+    assert torch.equal(db.cpu()[5].nan_to_num(7), torch.tensor(bad).nan_to_num(7)) and torch.isfinite(db).sum() == 55

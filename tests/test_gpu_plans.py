@@ -1,5 +1,7 @@
 """Every kernel instance that the plans choose (plan_cases.py), on the GPU: the
-group norm against its definition in 64 bits."""
+product on whole numbers, where every sum is exact and a term that is lost, met
+twice or out of place is a wrong number; the group norm against its definition
+in 64 bits."""
 import pytest
 import torch
 
@@ -10,6 +12,50 @@ import quantized_convolution_amd as q
 pytestmark = pytest.mark.gpu
 TYPES = (torch.float32, torch.bfloat16)
 LAYOUTS = ("nhwc", "nchw")
+
+
+def whole(g, *shape, most=2):
+    return torch.randint(-most, most + 1, shape, generator=g, device="cuda", dtype=torch.int8)
+
+
+def same(got, want, what):
+    """Equal to the exact value, rounded to the result's type once."""
+    want = want.to(got.dtype)
+    off = got != want
+    assert not off.any(), f"{what}: {int(off.sum())} of {off.numel()} values differ, first at {off.nonzero()[0].tolist()}"
+
+
+@pytest.mark.parametrize("case", P.LINEAR, ids=lambda c: "x".join(map(str, c)))
+def test_linear(case):
+    rows, Cin, Cout, act, xt, yt, round_dz = case
+    print(f"[linear plan] {case}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    name, xt, yt = ("none", "relu")[act], TYPES[xt], TYPES[yt]
+    x, w, dy, res, z = whole(g, rows, Cin), whole(g, Cout, Cin), whole(g, rows, Cout), whole(g, rows, Cout, most=9), whole(g, rows, Cout)
+    bias = whole(g, Cout, most=9).float()
+    assert 4 * max(Cin, Cout, rows) + 18 < 2 ** 24  # any partial sum is exact in fp32
+    xd, wd = x.to(xt), w.to(xt)
+    z64 = x.double() @ w.double().T + bias.double()
+    y64 = z64.clamp(min=0) if act else z64
+    pixels = next(p for p in [*range(2, 400), rows] if rows % p == 0)
+    for planar in (False, True):
+        for t in TYPES:
+            plan = q.LinearPlan(rows, Cin, Cout, act=name, x_dtype=xt, y_dtype=t, r_layout=LAYOUTS[planar], pixels=pixels if planar else 0)
+            r = res.reshape(-1, pixels, Cout).permute(0, 2, 1).contiguous() if planar else res
+            y, zo = q.wq8_linear_forward(plan, xd, wd, bias, r.to(t), want_z=True)
+            same(y, y64 + res, f"y {t} {LAYOUTS[planar]}")
+            same(zo, z64, f"z {t}")
+            del y, zo, r
+    y = q.wq8_linear_forward(q.LinearPlan(rows, Cin, Cout, act=name, x_dtype=xt, y_dtype=yt), xd, wd)
+    y64 = z64 - bias
+    same(y, y64.clamp(min=0) if act else y64, "y alone")
+    del y, y64, z64, res
+    dz = dy.double() * (z > 0) if act else dy.double()
+    plan = q.LinearPlan(rows, Cin, Cout, act=name, x_dtype=xt, y_dtype=yt, round_dz=bool(round_dz))
+    got = q.wq8_linear_backward(plan, dy.to(yt), xd, wd, z=z.to(yt), want_dbias=True)
+    same(got[0], dz @ w.double(), "dx")
+    same(got[1], dz.T @ x.double(), "dw")
+    same(got[2], dz.sum(0), "dbias")
 
 
 def within(got, want, bound, what):

@@ -37,3 +37,12 @@ def test_norm_cases_reach_every_instance(shapes):
             more = "one" if batches == "batches=1" else "more"
             got.add(f"{TYPES[c[5]]}->{TYPES[c[6]]} {name} {more}{'' if parts == 'J=1' else ' J'}")
     assert not wanted(P.NORM_INSTANCES) - got
+
+
+def test_linear_cases_reach_every_instance(shapes):
+    got = set()
+    lines = [f"linear {m} {k} {n} {act} {xt} {yt} 0 0 {r}" for m, k, n, act, xt, yt, r in P.LINEAR]
+    for c, line in zip(P.LINEAR, shapes(lines)):
+        f, dw, dx, planes = line.split()
+        got |= {f"{TYPES[c[4]]} {f}", f"{TYPES[c[4]]} {dw} {planes}", f"{TYPES[c[4]]} {dx} {planes}"}
+    assert not wanted(P.LINEAR_INSTANCES) - got
