@@ -446,9 +446,9 @@ size_t tile_lds(K kernel) {
 }
 
 // Calls run<BM, BN, WM, WN, DIRECT>() for tile s.tile, in the order of
-// kGemmTiles. Not DIRECT, the largest tile has no registers for a step: the
-// plan does not choose it then.
-template <typename R>
+// kGemmTiles. Not DIRECT, the largest tile has no registers for a step; the
+// plan does not choose it then, nor 128 x 128 for SMALL.
+template <bool SMALL, typename R>
 void pick_tile(const GemmShape &s, const R &run) {
     const auto go = [&](auto direct) {
         constexpr bool D = decltype(direct)::value;
@@ -456,7 +456,9 @@ void pick_tile(const GemmShape &s, const R &run) {
             case 0:
                 if constexpr (D) run.template operator()<256, 256, 2, 4, D>();
                 return;
-            case 1: return run.template operator()<128, 128, 2, 2, D>();
+            case 1:
+                if constexpr (!SMALL) run.template operator()<128, 128, 2, 2, D>();
+                return;
             case 2: return run.template operator()<128, 64, 2, 2, D>();
             case 3: return run.template operator()<64, 64, 2, 2, D>();
             default: return run.template operator()<16, 128, 1, 2, D>();

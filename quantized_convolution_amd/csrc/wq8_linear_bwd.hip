@@ -223,7 +223,7 @@ void backward(const LinearGeo &g, const LinearPtrs &p, hipStream_t st) {
         if (g.N >= V) go(k_dz<XT, YT, V>, V);
         else go(k_dz<XT, YT, 1>, 1);
     }
-    pick_tile(g.dw, RunBackward<XT>{g, p, st});
+    pick_tile<sizeof(XT) == 4>(g.dw, RunBackward<XT>{g, p, st});
 }
 
 }  // namespace

@@ -115,8 +115,8 @@ struct RunForward {
 template <typename XT>
 wq8_status linear_forward(const LinearGeo &g, wq8_dtype ydt, const LinearPtrs &p, void *stream) {
     const hipStream_t st = (hipStream_t)stream;
-    if (ydt == WQ8_F32) pick_tile(g.f, RunForward<XT, float>{g, p, st});
-    else pick_tile(g.f, RunForward<XT, bf16_t>{g, p, st});
+    if (ydt == WQ8_F32) pick_tile<false>(g.f, RunForward<XT, float>{g, p, st});
+    else pick_tile<false>(g.f, RunForward<XT, bf16_t>{g, p, st});
     return check_launch("matrix product");
 }
 

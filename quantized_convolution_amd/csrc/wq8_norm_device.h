@@ -431,9 +431,11 @@ void pick_steps(const NormGeo &g, const R &run) {
     const NormShape &s = BWD ? g.b : g.f;
     const auto go = [&](auto cross) {
         constexpr bool X = decltype(cross)::value;
+        // single pixels are taken one by one of images that hold no vector: few steps
+        constexpr bool FEW = KIND == kPlanar && V == 1 && norm_max_vec(sizeof(XT), sizeof(YT), BWD) <= kNormE;
         if (s.split) run.template operator()<XT, YT, V, KIND, X, true, kNormE>();
-        else if (s.steps <= kNormE) run.template operator()<XT, YT, V, KIND, X, false, kNormE>();
-        else run.template operator()<XT, YT, V, KIND, X, false, norm_max_steps(BWD, KIND == kStraddle, X)>();
+        else if (FEW || s.steps <= kNormE) run.template operator()<XT, YT, V, KIND, X, false, kNormE>();
+        else run.template operator()<XT, YT, V, KIND, X, false, FEW ? kNormE : norm_max_steps(BWD, KIND == kStraddle, X)>();
     };
     if (g.x_nhwc != g.y_nhwc) go(std::true_type{});
     else go(std::false_type{});

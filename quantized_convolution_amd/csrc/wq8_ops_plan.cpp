@@ -273,6 +273,7 @@ void choose_gemm(const Product *q, int count, wq8_dtype t, int planes, bool dire
     double least = 1e30;
     for (int i = 0; i < count; ++i) memset(out[i], 0, sizeof *out[i]);
     for (int i = direct ? 0 : 1; i < kGemmTileCount; ++i) {
+        if (i == 1 && count == 2 && t == WQ8_F32) continue;  // 128 x 64 has the rate in fp32, and finer blocks
         const GemmTile &g = kGemmTiles[i];
         const double rate = t == WQ8_F32 ? 0.56 * g.f32 : 5.2 * g.bf16;  // Mflop per us and compute unit
         const double step = 2e-6 * g.bm * g.bn * kstep * planes / rate;
