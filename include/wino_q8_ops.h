@@ -53,7 +53,9 @@ typedef struct wq8_norm_plan wq8_norm_plan; /* opaque */
 
 typedef struct {
     int N, C, H, W;          /* N may be 0: an empty batch, nothing is launched but
-                                the zeros of dgamma and dbeta */
+                                the zeros of dgamma and dbeta. Images of 2^31 values
+                                are refused, and those whose last block's pixels or
+                                channels would be counted past 2^31 */
     int groups;              /* C % groups == 0 */
     float eps;               /* >= 0, finite */
     wq8_act act;

@@ -13,10 +13,12 @@
 // Rounded to bf16 once, as a caller may ask for, it adds as much error to dx
 // and dw as their own final rounding, sqrt 2 times the error of one rounding,
 // over few values and over many.
-// Measured: 8192 x 640 x 2560 bf16 with gelu 189 us, and 117 us with dz rounded
-// once: dz then takes 26 us (126 MB, 4.8 TB/s, bound by memory), the products
-// 84 us (640 TFLOP/s) and the join 7 us; 1001 x 333 x 515 fp32, rows at odd addresses, 23 us in kernels of
-// 4, 17 and 4 us, bound by launches and load latency. One kernel for both
+// Measured: 8192 x 640 x 2560 bf16 with gelu 187 to 192 us: dz 34 us (168 MB, 4.9
+// TB/s, bound by memory), the products 151 us (both halves of dz: 107 GFLOP, 710
+// TFLOP/s) and the join 7 us. With dz rounded once 117 to 121 us: 26, 84 and 7.
+// 16384 x 2560 x 10240 with gelu 3.58 ms, rounded 1.82 ms (946 TFLOP/s, in 256 x
+// 256 tiles, though these spill 31 registers); 1001 x 333 x 515 fp32, rows at odd addresses, 23 us in kernels of
+// 4, 16 and 4 us, bound by launches and load latency. One kernel for both
 // products instead of two, a join each and one for dbias: 127 and 36 us before.
 #include "wq8_gemm_device.h"
 

@@ -4,11 +4,12 @@
 // the fp32 sums (8 adjacent columns of a row per thread: 16-byte stores of
 // bf16). z, where the backward will want it, is rounded to y's type, as y is.
 // An NCHW residual is read 16 adjacent pixels at a time. Measured: 16384 x 2560 x
-// 10240 bf16 with gelu 806 to 830 us (1.05 PFLOP/s; the matrix cores bound it,
+// 10240 bf16 with gelu 807 to 833 us (1.05 PFLOP/s; the matrix cores bound it,
 // the product alone takes a library 686 us), 8192 x 640 x 640 bf16 with a residual
-// 15.0 us (32 MB; each block's start and end weigh as much as its 10 k steps),
-// 2048 x 2560 x 1280 fp32 114 us (118 TFLOP/s), 8 x 320 x 1280 bf16 6.1 us
-// (latency: the kernel takes 5, most of it launch, first loads and stores).
+// 15.2 us (32 MB; each block's start and end weigh as much as its 10 k steps),
+// 2048 x 2560 x 1280 fp32 115 us (117 TFLOP/s; 105 and a join of 10), 8 x 320 x
+// 1280 bf16 6.2 us (latency: the kernel takes 5, most of it launch, first loads
+// and stores), 1 x 10240 x 10240 bf16 42 us (5.0 TB/s of weights).
 #pragma once
 
 #include "wq8_gemm_device.h"

@@ -3,10 +3,10 @@
 //
 // x and dy are read once where a block holds a group (half as many values as
 // forward: two tensors share the registers), else twice. Measured: 8 x 640 x 32 x 32
-// bf16 fused 18.7 us (31 MB; the activation's slope, two quarter-rate
+// bf16 fused 18.5 us (31 MB; the activation's slope, two quarter-rate
 // instructions a value, is evaluated for the sums and again for dx: half of the
-// kernel's 17 us is arithmetic), 2 x 320 x 64 x 64 f32 with dy in NCHW split 29.3 us in
-// kernels of 13, 10 and 5 us (52 MB).
+// kernel's 17 us is arithmetic), 2 x 320 x 64 x 64 f32 with dy in NCHW split 28.5 us in
+// kernels of 14, 10 and 5.5 us (52 MB), 8 x 640 x 128 x 128 bf16 225 us (503 MB).
 #pragma once
 
 #include "wq8_norm_device.h"

@@ -21,10 +21,10 @@
 // layout windows of pixels x channels pass through LDS, so both sides access
 // global memory along their contiguous dimension.
 //
-// Measured: 8 x 640 x 128 x 128 bf16 135 us: statistics 58 us (168 MB, 2.9 TB/s;
-// 4 vector operations a value for sum and square sum, and each block's joins),
-// output 77 us (336 MB, 4.4 TB/s, a large copy's rate is 4.7). 8 x 1280 x 16 x 16 f32
-// NCHW 7.8 us fused (21 MB), 32 x 512 x 7 x 7 bf16 6.9 us, 2 x 320 x 64 x 64 bf16 to
+// Measured: 8 x 640 x 128 x 128 bf16 136 us: statistics 58 us (168 MB, 2.9 TB/s:
+// 98 registers leave four blocks on a compute unit, and each ends in joins),
+// output 77.5 us (336 MB, 4.3 TB/s, a large copy's rate is 4.7). 8 x 1280 x 16 x 16
+// f32 NCHW 7.8 us fused (21 MB), 32 x 512 x 7 x 7 bf16 7 us, 2 x 320 x 64 x 64 bf16 to
 // NCHW 18.4 us split (64 groups would leave three quarters of the card idle;
 // fused they took 35 us): launch and load latency bound these three.
 #pragma once

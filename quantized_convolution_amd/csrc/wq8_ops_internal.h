@@ -114,8 +114,9 @@ struct LinearPtrs {
     float *partial, *partial_dx, *partial_dw;  // workspace: split products
 };
 
-// The built tiles: rows, columns, blocks that a compute unit holds, and the
-// share of the largest tile's rate that a full card reaches in bf16 and in fp32
+// The built tiles: rows, columns, blocks that a compute unit holds (of the
+// kernels that load directly; by registers the backward's 128 x 128 holds one,
+// 128 x 64 and 16 x 128 two), and the share of the largest tile's rate that a full card reaches in bf16 and in fp32
 // (8192^3: 1337, 1150, 917 and 648 TFLOP/s in bf16; 8192 x 4096 x 4096: 146 to
 // 140 in fp32). The last one is for a few rows.
 struct GemmTile {

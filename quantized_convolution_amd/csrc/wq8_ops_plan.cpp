@@ -125,7 +125,8 @@ NormShape split_shape(const NormGeo &g, int V, int batch, int xsz) {
     }
     s.nslab = g.G / s.K * s.J;
     // one batch of steps to a block, or as many as still leave 8 blocks a
-    // compute unit, the most that run at once
+    // compute unit (by their registers 4 to 8 of the statistics' blocks run at
+    // once, and 5 or 6 of the output's)
     const int64_t rows = (int64_t)g.N * s.nslab;
     const int all = ceil_div(g.P, s.window);
     int steps = batch;
