@@ -24,7 +24,9 @@ constexpr int norm_max_vec(size_t xs, size_t ys, bool backward) { return xs == 2
 // Steps whose values a thread of a 1024-thread block can hold: 128 registers,
 // 64 of them for the values of x (forward) or of x and dy (backward), fewer
 // where it keeps a group per channel as well, or where windows of y change
-// layout (16 steps of them need some 300 registers more than there are).
+// layout. (16 steps of these spill, and a register that the compiler reloads
+// in the block between a tile's loop and its barrier, where no lane is active
+// yet, keeps what it held: an instance left windows unwritten so.)
 constexpr int norm_max_steps(bool backward, bool straddle, bool cross) {
     return backward ? (straddle ? 4 : 8) : cross ? 8 : 16;
 }
