@@ -52,7 +52,12 @@ EXPORTS = ("wq8_plan_create", "wq8_plan_destroy", "wq8_plan_query", "wq8_plan_ma
            # group norm and matrix product, wrapped in ops.py
            "wq8_norm_plan_create", "wq8_norm_plan_destroy", "wq8_norm_plan_query", "wq8_norm_forward",
            "wq8_norm_backward", "wq8_linear_plan_create", "wq8_linear_plan_destroy",
-           "wq8_linear_plan_query", "wq8_linear_forward", "wq8_linear_backward")
+           "wq8_linear_plan_query", "wq8_linear_forward", "wq8_linear_backward",
+           # the operators on 8-bit codes, wrapped in token_ops.py
+           "wq8_quant_plan_create", "wq8_quant_plan_destroy", "wq8_quant_pack", "wq8_quant_unpack",
+           "wq8_rms_plan_create", "wq8_rms_plan_destroy", "wq8_rms_plan_query", "wq8_rms_forward",
+           "wq8_rms_backward", "wq8_q8linear_plan_create", "wq8_q8linear_plan_destroy",
+           "wq8_q8linear_plan_query", "wq8_q8linear_forward", "wq8_q8linear_backward")
 
 # bytes of the device array wq8_conv_forward_noalloc uses as its workspace
 NOALLOC_MAX_WORKSPACE = 64 << 20
@@ -90,15 +95,21 @@ def load(path: str = LIB_PATH):
     lib.wq8_direct_conv.argtypes = [P, P, P, P, P, P, P]
     lib.wq8_direct_forward.argtypes = [P, P, P, P, P, P, S, P]
     lib.wq8_conv_forward_noalloc.argtypes = [P, P, P, P, P, P]
-    for kind in ("norm", "linear"):
+    for kind in ("norm", "linear", "quant", "rms", "q8linear"):
         getattr(lib, f"wq8_{kind}_plan_create").argtypes = [P, C.POINTER(P)]
         getattr(lib, f"wq8_{kind}_plan_destroy").argtypes = [P]
         getattr(lib, f"wq8_{kind}_plan_destroy").restype = None
-        getattr(lib, f"wq8_{kind}_plan_query").argtypes = [P, C.POINTER(S), C.POINTER(S)]
+        if kind != "quant":
+            getattr(lib, f"wq8_{kind}_plan_query").argtypes = [P, C.POINTER(S), C.POINTER(S)]
     lib.wq8_norm_forward.argtypes = [P] * 9 + [S, P]
     lib.wq8_norm_backward.argtypes = [P] * 13 + [S, P]
     lib.wq8_linear_forward.argtypes = [P] * 8 + [S, P]
     lib.wq8_linear_backward.argtypes = [P] * 9 + [S, P]
+    lib.wq8_quant_pack.argtypes = lib.wq8_quant_unpack.argtypes = [P] * 5
+    lib.wq8_rms_forward.argtypes = [P] * 10 + [S, P]
+    lib.wq8_rms_backward.argtypes = [P] * 9 + [S, P]
+    lib.wq8_q8linear_forward.argtypes = [P] * 12 + [S, P]
+    lib.wq8_q8linear_backward.argtypes = [P] * 13 + [S, P]
     lib.wq8_status_string.argtypes = [i]
     lib.wq8_status_string.restype = C.c_char_p
     lib.wq8_last_error.argtypes = []

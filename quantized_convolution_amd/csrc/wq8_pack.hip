@@ -1,0 +1,97 @@
+// Packing of rows to codes with one scale a row or one for 32, 64 or 128
+// columns, and back. Memory bounds all three.
+#include "wq8_rms_fwd.h"
+
+namespace wq8 {
+namespace {
+
+// Groups: a thread has 8 columns, the 4, 8 or 16 threads of a group are
+// neighbours in a wave. Rows of codes are whole lines, so groups start at
+// multiples of their threads, and what stands behind the last column is written
+// by threads of its own.
+template <typename XT, int G>
+__global__ __launch_bounds__(256) void k_pack_groups(RowsGeo g, const XT *x, int8_t *codes, float *scales, int blocks) {
+    int b;
+    if (!block_number(blocks, b)) return;
+    const int across = g.stride / kV;
+    const int64_t i = (int64_t)b * 256 + threadIdx.x;
+    const int64_t row = i / across;
+    const int c = (int)(i - row * across) * kV;
+    const bool in = row < g.rows;  // whole groups are in or out
+    const Vec<XT, kV> v = load_any<XT>(x + (in ? row : 0) * g.xs, c, g.C);
+    float t[kV];
+    uint32_t most = 0;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+        t[k] = to_f32(v.v[k]);
+        most = max(most, magnitude(t[k]));
+    }
+    const auto step = [&](int other) { most = max(most, (uint32_t)other); };
+    step(__builtin_amdgcn_update_dpp(0, (int)most, kDppXor1, 0xf, 0xf, true));
+    step(__builtin_amdgcn_update_dpp(0, (int)most, kDppXor2, 0xf, 0xf, true));
+    if constexpr (G >= 64) step(__builtin_amdgcn_update_dpp(0, (int)most, kDppXor7, 0xf, 0xf, true));
+    if constexpr (G >= 128) step(__builtin_amdgcn_update_dpp(0, (int)most, kDppXor8, 0xf, 0xf, true));
+    if (!in) return;
+    const Coder code(most);
+    store_codes(codes + row * g.stride + c, code.pack(t));
+    if (c % G == 0 && c < g.C) scales[row * ((g.C + G - 1) / G) + c / G] = code.scale;
+}
+
+template <typename XT>
+__global__ __launch_bounds__(256) void k_unpack(RowsGeo g, const int8_t *codes, const float *scales, XT *x, int blocks) {
+    int b;
+    if (!block_number(blocks, b)) return;
+    const int across = (g.C + kV - 1) / kV;
+    const int64_t i = (int64_t)b * 256 + threadIdx.x;
+    const int64_t row = i / across;
+    if (row >= g.rows) return;
+    const int c = (int)(i - row * across) * kV;
+    const uint64_t q = *(const uint64_t *)(codes + row * g.stride + c);
+    const float scale = g.group ? scales[row * ((g.C + g.group - 1) / g.group) + c / g.group] : scales[row];
+    Vec<XT, kV> v;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) v.v[k] = from_f32<XT>((float)(int8_t)(q >> (8 * k)) * scale);
+    store_cols<XT>(x + row * g.xs, c, g.C, v);
+}
+
+template <typename XT>
+void pack_groups(const RowsGeo &g, const XT *x, int8_t *codes, float *scales, hipStream_t st) {
+    const int64_t blocks = ((int64_t)g.rows * (g.stride / kV) + 255) / 256;
+    const auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(256), 0, st, g, x, codes, scales, (int)blocks);
+    };
+    if (g.group == 32) go(k_pack_groups<XT, 32>);
+    else if (g.group == 64) go(k_pack_groups<XT, 64>);
+    else go(k_pack_groups<XT, 128>);
+}
+
+}  // namespace
+
+wq8_status launch_pack_rows(const RowsGeo &g, wq8_dtype xdt, const void *x, int8_t *codes, float *scales, void *stream) {
+    RmsPtrs p = {};
+    p.x = x;
+    p.codes = codes;
+    p.scales = scales;
+    if (xdt == WQ8_F32) run_rows<float, float, false>(g, p, (hipStream_t)stream);
+    else run_rows<bf16_t, bf16_t, false>(g, p, (hipStream_t)stream);
+    return check_launch("packing of rows");
+}
+
+wq8_status launch_pack_groups(const RowsGeo &g, wq8_dtype xdt, const void *x, int8_t *codes, float *scales, void *stream) {
+    if (xdt == WQ8_F32) pack_groups<float>(g, (const float *)x, codes, scales, (hipStream_t)stream);
+    else pack_groups<bf16_t>(g, (const bf16_t *)x, codes, scales, (hipStream_t)stream);
+    return check_launch("packing of groups");
+}
+
+wq8_status launch_unpack(const RowsGeo &g, wq8_dtype xdt, const int8_t *codes, const float *scales, void *x, void *stream) {
+    const int64_t blocks = ((int64_t)g.rows * ((g.C + kV - 1) / kV) + 255) / 256;
+    if (xdt == WQ8_F32)
+        hipLaunchKernelGGL(k_unpack<float>, grid_of(blocks), dim3(256), 0, (hipStream_t)stream, g, codes, scales, (float *)x,
+                           (int)blocks);
+    else
+        hipLaunchKernelGGL(k_unpack<bf16_t>, grid_of(blocks), dim3(256), 0, (hipStream_t)stream, g, codes, scales, (bf16_t *)x,
+                           (int)blocks);
+    return check_launch("unpacking");
+}
+
+}  // namespace wq8

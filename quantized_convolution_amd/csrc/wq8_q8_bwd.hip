@@ -1,0 +1,453 @@
+// Backward of the product of codes.
+//   dz = dy act'(z);  dx = (dz sw) wq;  dw = (dz sx)^T xq;  dbias = sum over the rows of dz
+// Both products run on the int8 matrix cores: their left operands become whole
+// numbers in fixed point of the largest magnitude of their row (column), in 8-bit
+// digits, the right ones are the codes that the forward kept. The scales sw and
+// sx, which belong to the summed index, are taken into dz before that.
+//
+// One kernel finds the largest magnitudes and the column sums, and transposes
+// the codes, so that every operand has its summed index contiguous. A second
+// writes the digits, of dz sx transposed. A third runs both products and the
+// column sums' join side by side; a last one joins products that are split along
+// k. dz is formed twice rather than kept: 3 bytes a value are read again where 4
+// would be written and read.
+#include "wq8_q8_gemm.h"
+#include "wq8_rows.h"
+
+namespace wq8 {
+namespace {
+
+// Digits of the products whose results are of type T.
+template <typename T>
+constexpr int planes_of() { return sizeof(T) == 2 ? 2 : 4; }
+
+enum { kZNone, kZValues, kZCodes };  // what the forward kept of z
+
+// dz of 8 columns of a row, zeros past the last column.
+template <typename YT, int ZF, int ACT, bool EXACT>
+__device__ __forceinline__ void dz_of(const Q8Geo &g, const Q8Ptrs &a, int64_t row, int c, float (&dz)[kV]) {
+    const Vec<YT, kV> dy = load_any<YT>((const YT *)a.dy + row * g.ys, c, g.N);
+    float z[kV];
+    if constexpr (ZF == kZValues) {
+        const Vec<YT, kV> v = load_any<YT>((const YT *)a.z_in + row * g.N, c, g.N);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) z[k] = to_f32(v.v[k]);
+    } else if constexpr (ZF == kZCodes) {
+        const int at = min(c, g.Np - kV);
+        const uint64_t q = *(const uint64_t *)(a.zq_in + row * g.Np + at);
+        const float s = a.sz_in[row * ((g.N + 31) / 32) + min(c, g.N - 1) / 32];
+#pragma unroll
+        for (int k = 0; k < kV; ++k) z[k] = (float)(int8_t)(q >> (8 * k)) * s;
+    }
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+        dz[k] = to_f32(dy.v[k]);
+        if constexpr (ACT != WQ8_ACT_NONE) {
+            // past the end z may be anything: a slope of NaN times the zero there
+            const float v = dz[k] * act_slope<ACT, EXACT>(z[k]);
+            dz[k] = c + k < g.N ? v : 0.0f;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ first pass
+// 64 lanes x 8 columns of `chunk` rows, a wave each: the largest |dz sw| of every
+// row, the largest |dz sx| and the sum of dz of every column.
+constexpr int kMaxCols = 64 * kV;
+constexpr int kMaxRows = 2;  // rows of a wave whose loads are in flight together
+
+template <typename XT, typename YT, int ZF>
+__device__ __forceinline__ void max_block(const Q8Geo &g, const Q8Ptrs &a, int b) {
+    __shared__ float red[3][2][kMaxCols];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int chunk = b / g.ncol, col = b - chunk * g.ncol;
+    const int c = col * kMaxCols + lane * kV;
+    const int r0 = chunk * g.chunk, r1 = min(r0 + g.chunk, g.M);
+    const Vec<float, kV> sw = load_any<float>(a.sw, c, g.N);
+    float sum[kV] = {};
+    uint32_t most[kV] = {};
+    with_act(g.act, [&](auto act) {
+        constexpr int A = decltype(act)::value;
+        if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
+            for (int r = r0 + wave; r < r1; r += 4 * kMaxRows) {
+                float dz[kMaxRows][kV], sx[kMaxRows];
+#pragma unroll
+                for (int i = 0; i < kMaxRows; ++i) {
+                    const int row = min(r + 4 * i, r1 - 1);
+                    dz_of<YT, ZF, A, exact_acts<XT, YT>()>(g, a, row, c, dz[i]);
+                    sx[i] = a.sx[row];
+                }
+#pragma unroll
+                for (int i = 0; i < kMaxRows; ++i)
+                    if (r + 4 * i < r1) {
+                        uint32_t m = 0;
+#pragma unroll
+                        for (int k = 0; k < kV; ++k) {
+                            m = max(m, magnitude(dz[i][k] * sw.v[k]));
+                            most[k] = max(most[k], magnitude(dz[i][k] * sx[i]));
+                            sum[k] += dz[i][k];
+                        }
+                        m = wave_max(m);
+                        if (lane == 0) a.rowmax[(int64_t)(r + 4 * i) * g.ncol + col] = __uint_as_float(m);
+                    }
+            }
+    });
+    if (wave > 0)
+#pragma unroll
+        for (int k = 0; k < kV; ++k) {
+            red[wave - 1][0][k * 64 + lane] = __uint_as_float(most[k]);
+            red[wave - 1][1][k * 64 + lane] = sum[k];
+        }
+    __syncthreads();
+    if (wave > 0) return;
+    Vec<float, kV> m, s;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+#pragma unroll
+        for (int w = 0; w < 3; ++w) most[k] = max(most[k], __float_as_uint(red[w][0][k * 64 + lane]));
+        m.v[k] = __uint_as_float(most[k]);
+        s.v[k] = (sum[k] + red[0][1][k * 64 + lane]) + (red[1][1][k * 64 + lane] + red[2][1][k * 64 + lane]);
+    }
+    if (c < g.N) {
+        store_cols<float>(a.colmax + (int64_t)chunk * g.N, c, g.N, m);
+        store_cols<float>(a.colsum + (int64_t)chunk * g.N, c, g.N, s);
+    }
+}
+
+// A matrix of codes [rows][ld] transposed to [cols][tld], zeros behind its last
+// row: 128 x 128 codes a block. A thread has 4 rows of 16 columns.
+__device__ __forceinline__ void transpose_block(const int8_t *x, int64_t rows, int cols, int64_t ld, int8_t *t, int64_t tld, int b) {
+    constexpr int LD = 128 + 4;  // bytes between columns in LDS
+    __shared__ __align__(16) int8_t tile[128 * LD];
+    const int across = (int)(ld / 128);
+    const int64_t r0 = (int64_t)(b / across) * 128;
+    const int c0 = (b - b / across * across) * 128;
+    const int rg = threadIdx.x >> 3, cg = threadIdx.x & 7;
+    uint32_t v[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = r0 + rg * 4 + i;
+        const v4i q = *(const v4i *)(x + min(r, rows - 1) * ld + c0 + cg * 16);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) v[i][d] = r < rows ? (uint32_t)q[d] : 0u;
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint32_t o = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o |= (v[i][d] >> (8 * e) & 255u) << (8 * i);
+            *(uint32_t *)(tile + (cg * 16 + d * 4 + e) * LD + rg * 4) = o;
+        }
+    __syncthreads();
+    // a wave writes 8 columns' lines of 128 bytes at a time, 16 bytes a lane
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int col = i * 32 + (threadIdx.x >> 3), part = (threadIdx.x & 7) * 16;
+        v4i o;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) o[d] = *(const int *)(tile + col * LD + part + d * 4);
+        if (c0 + col < cols) *(v4i *)(t + (int64_t)(c0 + col) * tld + r0 + part) = o;
+    }
+}
+
+// Blocks [0, nm): largest magnitudes; then nx of xq's transposition and the rest of wq's.
+template <typename XT, typename YT, int ZF>
+__global__ __launch_bounds__(256) void k_q8_max(Q8Geo g, Q8Ptrs a, int nm, int nx, int nb) {
+    int b;
+    if (!block_number(nb, b)) return;
+    if (b < nm) max_block<XT, YT, ZF>(g, a, b);
+    else if (b < nm + nx) transpose_block(a.xq, g.M, g.K, g.Kp, a.xt, g.Mp, b - nm);
+    else transpose_block(a.wq, g.N, g.K, g.Kp, a.wt, g.Np, b - nm - nx);
+}
+
+// ----------------------------------------------------------------- second pass
+// Fixed point of a largest magnitude m (its bits): whole numbers of `planes` digits, the
+// highest in [-127, 127], the others in [-128, 127]. An infinity or a NaN: zeros, and a
+// scale of NaN.
+template <int PLANES>
+struct Digits {
+    static constexpr float kMost = PLANES == 2 ? 32512.0f : 2130706432.0f;  // 127 256^(planes - 1)
+    float up, f;
+
+    __device__ __forceinline__ explicit Digits(uint32_t bits) {
+        const float m = __uint_as_float(bits);
+        up = m < 0x1p-60f ? 0x1p64f : 1.0f;  // kMost / m overflows below 2^-96
+        f = bits == 0 || bits >= kInfBits ? 0.0f : kMost / (m * up);
+    }
+    // What a sum of products has to be multiplied by, in units of the highest digit.
+    __device__ __forceinline__ static float scale(uint32_t bits) {
+        return bits >= kInfBits ? __uint_as_float(0x7fc00000u) : __uint_as_float(bits) / 127.0f;
+    }
+    // Digit p of the number in the p-th byte from the top.
+    __device__ __forceinline__ uint32_t operator()(float v) const {
+        const float t = v * up * f;
+        int q = f == 0.0f ? 0 : (int)__builtin_rintf(t);
+        if constexpr (PLANES == 2) {
+            const uint32_t u = (uint32_t)(q + 128);  // hi = u >> 8, lo = (u & 255) - 128
+            return (u & 0xff00u) | ((u ^ 0x80u) & 0xffu);
+        } else {
+            // 2130706432 (1 + 2^-23) + 0x808080 is still below 2^31
+            const uint32_t u = (uint32_t)q + 0x00808080u;
+            return u ^ 0x00808080u;
+        }
+    }
+};
+
+// 128 rows x 64 columns: a thread has 4 rows of 8 columns.
+template <typename XT, typename YT, int ZF, int PLANES>
+__global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_dx, int want_dw, int across, int nb) {
+    constexpr int LD = 128 + 8;  // bytes between columns in LDS
+    __shared__ __align__(16) int8_t tile[PLANES * 64 * LD];
+    __shared__ uint32_t cpart[4][64], rpart[128];
+    int b;
+    if (!block_number(nb, b)) return;
+    const int br = b / across;
+    const int r0 = br * 128, c0 = (b - br * across) * 64;
+    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;
+    if (want_dw) {  // four threads a column along the chunks of the first pass
+        const int c = c0 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+        uint32_t m = 0;
+        if (c < g.N)
+            for (int i = q; i < g.nchunk; i += 4) m = max(m, __float_as_uint(a.colmax[(int64_t)i * g.N + c]));
+        cpart[q][threadIdx.x & 63] = m;
+    }
+    if (want_dx && threadIdx.x < 128) {
+        const int r = r0 + threadIdx.x;
+        uint32_t m = 0;
+        if (r < g.M)
+            for (int i = 0; i < g.ncol; ++i) m = max(m, __float_as_uint(a.rowmax[(int64_t)r * g.ncol + i]));
+        rpart[threadIdx.x] = m;
+        if (c0 == 0 && r < g.M) a.rscale[r] = Digits<PLANES>::scale(m);
+    }
+    __syncthreads();
+    const int c = c0 + cg * kV;
+    const auto colmax = [&](int i) {
+        return max(max(cpart[0][i], cpart[1][i]), max(cpart[2][i], cpart[3][i]));
+    };
+    if (want_dw && r0 == 0 && threadIdx.x < 64 && c0 + threadIdx.x < g.N)
+        a.cscale[c0 + threadIdx.x] = Digits<PLANES>::scale(colmax(threadIdx.x));
+    const Vec<float, kV> sw = load_any<float>(a.sw, c, g.N);
+    float dz[4][kV];
+    with_act(g.act, [&](auto act) {
+        constexpr int A = decltype(act)::value;
+        if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                dz_of<YT, ZF, A, exact_acts<XT, YT>()>(g, a, min(r0 + rg * 4 + i, g.M - 1), c, dz[i]);
+    });
+    if (want_dx)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + rg * 4 + i;
+            const Digits<PLANES> d(rpart[rg * 4 + i]);
+            uint32_t q[kV];
+#pragma unroll
+            for (int k = 0; k < kV; ++k) q[k] = d(dz[i][k] * sw.v[k]);
+            if (r < g.M)
+#pragma unroll
+                for (int p = 0; p < PLANES; ++p) {
+                    constexpr int kTop = (PLANES - 1) * 8;
+                    uint64_t o = 0;
+#pragma unroll
+                    for (int k = 0; k < kV; ++k) o |= (uint64_t)(q[k] >> (kTop - 8 * p) & 255u) << (8 * k);
+                    *(uint64_t *)(a.ur + ((int64_t)p * g.M + r) * g.Np + c) = o;
+                }
+        }
+    if (!want_dw) return;
+    float sx[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sx[i] = r0 + rg * 4 + i < g.M ? a.sx[r0 + rg * 4 + i] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+        const Digits<PLANES> d(colmax(cg * kV + k));
+        uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            q[i] = d(dz[i][k] * sx[i]);
+            if (r0 + rg * 4 + i >= g.M) q[i] = 0;  // dz there is another row's
+        }
+#pragma unroll
+        for (int p = 0; p < PLANES; ++p) {
+            constexpr int kTop = (PLANES - 1) * 8;
+            uint32_t o = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o |= (q[i] >> (kTop - 8 * p) & 255u) << (8 * i);
+            *(uint32_t *)(tile + (p * 64 + cg * kV + k) * LD + rg * 4) = o;
+        }
+    }
+    __syncthreads();
+    // 8 bytes a lane, 16 lanes a line
+#pragma unroll
+    for (int i = 0; i < PLANES * 4; ++i) {
+        const int line = i * 16 + (threadIdx.x >> 4), p = line / 64, col = line % 64, part = (threadIdx.x & 15) * 8;
+        if (c0 + col < g.N)
+            *(uint64_t *)(a.uc + ((int64_t)p * g.N + c0 + col) * g.Mp + r0 + part) = *(const uint64_t *)(tile + line * LD + part);
+    }
+}
+
+// ---------------------------------------------------------------- the products
+template <typename T>
+struct EpiScale {
+    T *out;
+    int64_t ld;
+    int M, N;
+    const float *scale;  // of the rows
+
+    struct Column {};
+    struct Item {
+        float scale;
+    };
+    __device__ __forceinline__ Column column(int) const { return {}; }
+    __device__ __forceinline__ Item item(int m, int) const { return {scale[min(m, M - 1)]}; }
+    template <typename F>
+    __device__ __forceinline__ void with(F f) const {
+        f(std::integral_constant<int, WQ8_ACT_NONE>{});
+    }
+
+    template <int ACT>
+    __device__ __forceinline__ void store(int m, int n, const Vec<float, 8> &v, int, Column, const Item &item) const {
+        if (m >= M || n >= N) return;
+        Vec<T, 8> r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.v[e] = from_f32<T>(v.v[e] * (sizeof(T) == 2 ? 0x1p-8f : 0x1p-16f) * item.scale);
+        store_vec_n<T, 8>(out + (int64_t)m * ld + n, r, N - n);
+    }
+};
+
+// dbias: the chunks' column sums, 16 columns a block, its other threads along the chunks.
+__device__ __forceinline__ void dbias_block(const Q8Geo &g, const Q8Ptrs &a, int b) {
+    extern __shared__ __align__(128) char smem[];
+    float *red = (float *)smem;
+    const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4, rows = blockDim.x >> 4, c = b * 16 + tc;
+    float t = 0.0f;
+    if (c < g.N)
+        for (int r = tr; r < g.nchunk; r += rows) t += a.colsum[(int64_t)r * g.N + c];
+    red[tr * 17 + tc] = t;
+    __syncthreads();
+    if (tr == 0 && c < g.N) {
+        float s = 0.0f;
+        for (int i = 0; i < rows; ++i) s += red[i * 17 + tc];
+        a.dbias[c] = s;
+    }
+}
+
+// Blocks [0, nw): dw; [nw, nw + nx): dx; the rest: dbias.
+template <typename T, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM *WN * 64) void k_q8_bwd(Q8Args dw, EpiScale<T> ew, int nw, Q8Args dx, EpiScale<T> ex, int nx,
+                                                        int nb, Q8Geo g, Q8Ptrs p) {
+    int b;
+    if (!block_number(nb, b)) return;
+    if (b < nw + nx) {  // one copy of the product: which one is the same for a whole block
+        const bool first = b < nw;
+        const Q8Args q = first ? dw : dx;
+        const EpiScale<T> e = first ? ew : ex;
+        q8_block<BM, BN, WM, WN, planes_of<T>()>(q, e, first ? b : b - nw, first ? nw : nx);
+    } else {
+        dbias_block(g, p, b - nw - nx);
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_q8_bwd_join(Q8Args dw, EpiScale<T> ew, int nw, Q8Args dx, EpiScale<T> ex, int nb) {
+    int b;
+    if (!block_number(nb, b)) return;
+    if (b < nw) q8_join_block<planes_of<T>()>(dw, ew, b);
+    else q8_join_block<planes_of<T>()>(dx, ex, b - nw);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_q8_zero(T *dw, int64_t values, float *dbias, int N) {
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; dw && i < values; i += step) dw[i] = T(0);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; dbias && i < N; i += step) dbias[i] = 0.0f;
+}
+
+template <typename T>
+struct RunQ8Backward {
+    const Q8Geo &g;
+    const Q8Ptrs &p;
+    hipStream_t st;
+
+    template <int BM, int BN, int WM, int WN>
+    void operator()() const {
+        Q8Args dw = {}, dx = {};
+        int64_t nw = 0, nx = 0, jw = 0, jx = 0;
+        if (p.dw) {
+            dw.A = p.uc;
+            dw.B = p.xt;
+            dw.lda = dw.ldb = g.Mp;
+            dw.M = g.N;
+            dw.N = g.K;
+            dw.steps = g.Mp / 128;
+            dw.plane = (int64_t)g.N * g.Mp;
+            nw = q8_tiles<BM, BN>(dw, g.dw, p.partial_dw);
+            jw = q8_join_blocks(dw);
+        }
+        if (p.dx) {
+            dx.A = p.ur;
+            dx.B = p.wt;
+            dx.lda = dx.ldb = g.Np;
+            dx.M = g.M;
+            dx.N = g.K;
+            dx.steps = g.Np / 128;
+            dx.plane = (int64_t)g.M * g.Np;
+            nx = q8_tiles<BM, BN>(dx, g.dx, p.partial_dx);
+            jx = q8_join_blocks(dx);
+        }
+        const EpiScale<T> ew = {(T *)p.dw, g.K, g.N, g.K, p.cscale}, ex = {(T *)p.dx, g.xs, g.M, g.K, p.rscale};
+        const int64_t blocks = nw + nx + (p.dbias ? (g.N + 15) / 16 : 0);
+        if (blocks > 0) {
+            const auto kernel = k_q8_bwd<T, BM, BN, WM, WN>;
+            hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(WM * WN * 64), (tile_lds<BM, BN>(kernel)), st, dw, ew, (int)nw, dx, ex,
+                               (int)nx, (int)blocks, g, p);
+        }
+        if (jw + jx > 0)
+            hipLaunchKernelGGL((k_q8_bwd_join<T>), grid_of(jw + jx), dim3(256), 0, st, dw, ew, (int)jw, dx, ex, (int)(jw + jx));
+    }
+};
+
+template <typename XT, typename YT, int ZF>
+void prepare(const Q8Geo &g, const Q8Ptrs &p, hipStream_t st) {
+    constexpr int PLANES = planes_of<XT>();
+    const auto tiles = [](int64_t rows, int64_t bytes) { return (rows + 127) / 128 * (bytes / 128); };
+    const int64_t nm = (int64_t)g.nchunk * g.ncol, nx = p.dw ? tiles(g.M, g.Kp) : 0, nw = p.dx ? tiles(g.N, g.Kp) : 0;
+    hipLaunchKernelGGL((k_q8_max<XT, YT, ZF>), grid_of(nm + nx + nw), dim3(256), 0, st, g, p, (int)nm, (int)nx,
+                       (int)(nm + nx + nw));
+    if (!p.dx && !p.dw) return;
+    const int across = g.Np / 64;
+    const int64_t nd = (int64_t)(g.Mp / 128) * across;
+    hipLaunchKernelGGL((k_q8_digits<XT, YT, ZF, PLANES>), grid_of(nd), dim3(256), 0, st, g, p, p.dx != nullptr, p.dw != nullptr,
+                       across, (int)nd);
+}
+
+template <typename XT, typename YT>
+void backward(const Q8Geo &g, const Q8Ptrs &p, hipStream_t st) {
+    if (g.M == 0) {
+        if (p.dw || p.dbias)
+            hipLaunchKernelGGL(k_q8_zero<XT>, dim3(256), dim3(256), 0, st, (XT *)p.dw, (int64_t)g.N * g.K, p.dbias, g.N);
+        return;
+    }
+    if (!p.dx && !p.dw && !p.dbias) return;
+    if (g.act == WQ8_ACT_NONE) prepare<XT, YT, kZNone>(g, p, st);
+    else if (p.z_in) prepare<XT, YT, kZValues>(g, p, st);
+    else prepare<XT, YT, kZCodes>(g, p, st);
+    pick_q8_tile<true>(g.dw.tile, RunQ8Backward<XT>{g, p, st});
+}
+
+}  // namespace
+
+wq8_status launch_q8_backward(const Q8Geo &g, wq8_dtype xdt, wq8_dtype ydt, const Q8Ptrs &p, void *stream) {
+    const hipStream_t st = (hipStream_t)stream;
+    if (xdt == WQ8_F32) {
+        if (ydt == WQ8_F32) backward<float, float>(g, p, st);
+        else backward<float, bf16_t>(g, p, st);
+    } else {
+        if (ydt == WQ8_F32) backward<bf16_t, float>(g, p, st);
+        else backward<bf16_t, bf16_t>(g, p, st);
+    }
+    return check_launch("backward of the product of codes");
+}
+
+}  // namespace wq8

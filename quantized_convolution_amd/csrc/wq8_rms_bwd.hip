@@ -1,0 +1,224 @@
+// Backward of the root-mean-square norm.
+//   n = h rstd;  t = gamma dy;  dx = rstd (t - n mean(t n)) + dh;  dgamma = sum_r dy n
+// A block goes through its rows a wave (or a block) each, held in registers:
+// one read of dy, h and dh, one write of dx. A thread has the same columns of
+// every row, so dgamma is summed in its registers, then over the block's waves
+// in LDS and over the blocks by a second kernel, in a fixed order.
+#include "wq8_rows.h"
+
+namespace wq8 {
+namespace {
+
+// ANY: rows of fewer columns than a vector too.
+template <typename XT, typename YT, bool ANY>
+struct RowGrad {
+    const RowsGeo &g;
+    const RmsPtrs &a;
+    int64_t row;
+
+    template <typename T>
+    __device__ __forceinline__ Vec<T, kV> load(const T *p, int c) const {
+        if constexpr (ANY) return load_any<T>(p, c, g.C);
+        else return load_cols<T>(p, c, g.C);
+    }
+    __device__ __forceinline__ Vec<XT, kV> h(int c) const { return load<XT>((const XT *)a.x + row * g.xs, c); }
+    __device__ __forceinline__ Vec<XT, kV> dh(int c) const { return load<XT>((const XT *)a.dh + row * g.xs, c); }
+    __device__ __forceinline__ Vec<YT, kV> dy(int c) const { return load<YT>((const YT *)a.dy + row * g.ys, c); }
+    __device__ __forceinline__ Vec<float, kV> gamma(int c) const {
+        Vec<float, kV> r;
+        if (a.gamma) return load<float>(a.gamma, c);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) r.v[k] = 1.0f;
+        return r;
+    }
+    __device__ __forceinline__ static float dot(const Vec<XT, kV> &h, const Vec<YT, kV> &dy, const Vec<float, kV> &gm,
+                                                float rstd) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) sum = fmaf(gm.v[k] * to_f32(dy.v[k]), to_f32(h.v[k]) * rstd, sum);
+        return sum;
+    }
+    __device__ __forceinline__ void dx(int c, const Vec<XT, kV> &h, const Vec<YT, kV> &dy, const Vec<float, kV> &gm,
+                                       const Vec<XT, kV> &dh, float rstd, float mean) const {
+        if (c >= g.C) return;
+        Vec<XT, kV> o;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) {
+            float v = rstd * fmaf(-(to_f32(h.v[k]) * rstd), mean, gm.v[k] * to_f32(dy.v[k]));
+            if (a.dh) v += to_f32(dh.v[k]);
+            o.v[k] = from_f32<XT>(v);
+        }
+        store_cols<XT>((XT *)a.dx + row * g.xs, c, g.C, o);
+    }
+};
+
+template <typename XT, typename YT, int L, int U>
+__global__ __launch_bounds__(L < 256 ? 256 : L) void k_rms_bwd(RowsGeo g, RmsPtrs a, int want_dgamma) {
+    constexpr int PER = L < 256 ? 256 / L : 1;
+    __shared__ float red[L > 64 ? 4 * L / 64 : 1];
+    __shared__ float join[PER > 1 ? (PER - 1) * U * L * kV : 1];
+    const int t = threadIdx.x % L, w = threadIdx.x / L;
+    Vec<float, kV> gm[U];
+    float dg[U][kV] = {};
+    {
+        const RowGrad<XT, YT, false> r = {g, a, 0};
+#pragma unroll
+        for (int s = 0; s < U; ++s) gm[s] = r.gamma((s * L + t) * kV);
+    }
+    const int r0 = blockIdx.x * g.chunk, r1 = min(r0 + g.chunk, g.rows);
+    int turn = 0;
+    for (int i = r0 + (L < 256 ? w : 0); i < r1; i += PER) {
+        const RowGrad<XT, YT, false> r = {g, a, i};
+        Vec<XT, kV> h[U], dh[U];
+        Vec<YT, kV> dy[U];
+#pragma unroll
+        for (int s = 0; s < U; ++s) {
+            h[s] = r.h((s * L + t) * kV);
+            dy[s] = r.dy((s * L + t) * kV);
+        }
+        if (a.dh)
+#pragma unroll
+            for (int s = 0; s < U; ++s) dh[s] = r.dh((s * L + t) * kV);
+        const float rstd = a.rstd_in[i];
+        float sum = 0.0f;
+        uint32_t none = 0;
+#pragma unroll
+        for (int s = 0; s < U; ++s) sum += RowGrad<XT, YT, false>::dot(h[s], dy[s], gm[s], rstd);
+        reduce_row<L>(sum, none, red, turn++);
+        const float mean = sum / (float)g.C;
+#pragma unroll
+        for (int s = 0; s < U; ++s) {
+            r.dx((s * L + t) * kV, h[s], dy[s], gm[s], dh[s], rstd, mean);
+#pragma unroll
+            for (int k = 0; k < kV; ++k) dg[s][k] = fmaf(to_f32(dy[s].v[k]), to_f32(h[s].v[k]) * rstd, dg[s][k]);
+        }
+    }
+    if (!want_dgamma) return;
+    if constexpr (PER > 1) {
+        if (w > 0)
+#pragma unroll
+            for (int s = 0; s < U; ++s)
+#pragma unroll
+                for (int k = 0; k < kV; ++k) join[(((w - 1) * U + s) * kV + k) * L + t] = dg[s][k];
+        __syncthreads();
+        if (w > 0) return;
+#pragma unroll
+        for (int s = 0; s < U; ++s)
+#pragma unroll
+            for (int k = 0; k < kV; ++k)
+#pragma unroll
+                for (int v = 0; v < PER - 1; ++v) dg[s][k] += join[((v * U + s) * kV + k) * L + t];
+    }
+#pragma unroll
+    for (int s = 0; s < U; ++s) {
+        const int c = (s * L + t) * kV;
+        Vec<float, kV> o;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) o.v[k] = dg[s][k];
+        if (c < g.C) store_cols<float>(a.part + (int64_t)blockIdx.x * g.C, c, g.C, o);
+    }
+}
+
+// Rows that no block holds, and those of fewer columns than a vector: dx in two
+// passes over each, and dgamma's parts in a
+// third, a block for 2048 columns of its rows.
+template <typename XT, typename YT>
+__global__ __launch_bounds__(1024) void k_rms_bwd_long(RowsGeo g, RmsPtrs a, int blocks) {
+    constexpr int L = 1024;
+    __shared__ float red[2 * L / 64];
+    int b;
+    if (!block_number(blocks, b)) return;
+    const RowGrad<XT, YT, true> r = {g, a, b};
+    const float rstd = a.rstd_in[b];
+    float sum = 0.0f;
+    uint32_t none = 0;
+    for (int c = threadIdx.x * kV; c < g.C; c += L * kV) sum += RowGrad<XT, YT, true>::dot(r.h(c), r.dy(c), r.gamma(c), rstd);
+    reduce_row<L>(sum, none, red, 0);
+    const float mean = sum / (float)g.C;
+    for (int c = threadIdx.x * kV; c < g.C; c += L * kV) {
+        Vec<XT, kV> dh = {};
+        if (a.dh) dh = r.dh(c);
+        r.dx(c, r.h(c), r.dy(c), r.gamma(c), dh, rstd, mean);
+    }
+}
+
+template <typename XT, typename YT>
+__global__ __launch_bounds__(256) void k_rms_dgamma_long(RowsGeo g, RmsPtrs a) {
+    const int c = (blockIdx.y * 256 + threadIdx.x) * kV;
+    if (c >= g.C) return;
+    const int r0 = blockIdx.x * g.chunk, r1 = min(r0 + g.chunk, g.rows);
+    Vec<float, kV> o = {};
+    for (int i = r0; i < r1; ++i) {
+        const RowGrad<XT, YT, true> r = {g, a, i};
+        const Vec<XT, kV> h = r.h(c);
+        const Vec<YT, kV> dy = r.dy(c);
+        const float rstd = a.rstd_in[i];
+#pragma unroll
+        for (int k = 0; k < kV; ++k) o.v[k] = fmaf(to_f32(dy.v[k]), to_f32(h.v[k]) * rstd, o.v[k]);
+    }
+    store_cols<float>(a.part + (int64_t)blockIdx.x * g.C, c, g.C, o);
+}
+
+// dgamma from the blocks' parts: 16 columns a block, 64 threads along the parts.
+__global__ __launch_bounds__(1024) void k_rms_dgamma(RowsGeo g, RmsPtrs a) {
+    __shared__ float red[64][17];
+    const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4, c = blockIdx.x * 16 + tc;
+    float t = 0.0f;
+    if (c < g.C)
+        for (int i = tr; i < g.nchunk; i += 64) t += a.part[(int64_t)i * g.C + c];
+    red[tr][tc] = t;
+    __syncthreads();
+    if (tr < 8) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += red[tr * 8 + i][tc];
+        red[tr * 8][tc] = s;
+    }
+    __syncthreads();
+    if (tr == 0 && c < g.C) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += red[i * 8][tc];
+        a.dgamma[c] = s;
+    }
+}
+
+template <typename XT, typename YT>
+void backward(const RowsGeo &g, const RmsPtrs &p, hipStream_t st) {
+    if (g.rows > 0) {
+        const auto go = [&](auto kernel, int threads) {
+            hipLaunchKernelGGL(kernel, dim3(g.nchunk), dim3(threads), 0, st, g, p, p.dgamma != nullptr);
+        };
+        if (g.s.lanes == 64) {
+            if (g.s.unroll == 1) go(k_rms_bwd<XT, YT, 64, 1>, 256);
+            else go(k_rms_bwd<XT, YT, 64, 2>, 256);
+        } else if (g.s.lanes == 256) {
+            if (g.s.unroll == 1) go(k_rms_bwd<XT, YT, 256, 1>, 256);
+            else go(k_rms_bwd<XT, YT, 256, 2>, 256);
+        } else if (g.s.lanes == 512) {
+            go(k_rms_bwd<XT, YT, 512, 2>, 512);
+        } else {
+            hipLaunchKernelGGL((k_rms_bwd_long<XT, YT>), grid_of(g.rows), dim3(1024), 0, st, g, p, g.rows);
+            if (p.dgamma)
+                hipLaunchKernelGGL((k_rms_dgamma_long<XT, YT>), dim3(g.nchunk, (g.C + 256 * kV - 1) / (256 * kV)), dim3(256), 0,
+                                   st, g, p);
+        }
+    }
+    if (p.dgamma) hipLaunchKernelGGL(k_rms_dgamma, dim3((g.C + 15) / 16), dim3(1024), 0, st, g, p);
+}
+
+}  // namespace
+
+wq8_status launch_rms_backward(const RowsGeo &g, wq8_dtype xdt, wq8_dtype ydt, const RmsPtrs &p, void *stream) {
+    const hipStream_t st = (hipStream_t)stream;
+    if (xdt == WQ8_F32) {
+        if (ydt == WQ8_F32) backward<float, float>(g, p, st);
+        else backward<float, bf16_t>(g, p, st);
+    } else {
+        if (ydt == WQ8_F32) backward<bf16_t, float>(g, p, st);
+        else backward<bf16_t, bf16_t>(g, p, st);
+    }
+    return check_launch("root-mean-square norm backward");
+}
+
+}  // namespace wq8
