@@ -5,6 +5,15 @@
 namespace wq8 {
 namespace {
 
+// The row and the vector in it of the `i`-th of a block's vectors, `across` of
+// which are a row: one division of the block's first by scalars, then 32 bits.
+__device__ __forceinline__ void place(int b, int per, int across, int i, int64_t &row, int &vec) {
+    const int64_t first = (int64_t)b * per, r0 = first / across;
+    const int at = (int)(first - r0 * across) + i, down = at / across;
+    row = r0 + down;
+    vec = at - down * across;
+}
+
 // Groups: a thread has 8 columns, the 4, 8 or 16 threads of a group are
 // neighbours in a wave. Rows of codes are whole lines, so groups start at
 // multiples of their threads, and what stands behind the last column is written
@@ -13,19 +22,16 @@ template <typename XT, int G>
 __global__ __launch_bounds__(256) void k_pack_groups(RowsGeo g, const XT *x, int8_t *codes, float *scales, int blocks) {
     int b;
     if (!block_number(blocks, b)) return;
-    const int across = g.stride / kV;
-    const int64_t i = (int64_t)b * 256 + threadIdx.x;
-    const int64_t row = i / across;
-    const int c = (int)(i - row * across) * kV;
+    int64_t row;
+    int vec;
+    place(b, 256, g.stride / kV, threadIdx.x, row, vec);
+    const int c = vec * kV;
     const bool in = row < g.rows;  // whole groups are in or out
     const Vec<XT, kV> v = load_any<XT>(x + (in ? row : 0) * g.xs, c, g.C);
     float t[kV];
-    uint32_t most = 0;
 #pragma unroll
-    for (int k = 0; k < kV; ++k) {
-        t[k] = to_f32(v.v[k]);
-        most = max(most, magnitude(t[k]));
-    }
+    for (int k = 0; k < kV; ++k) t[k] = to_f32(v.v[k]);
+    uint32_t most = bits_of(largest(t));
     const auto step = [&](int other) { most = max(most, (uint32_t)other); };
     step(__builtin_amdgcn_update_dpp(0, (int)most, kDppXor1, 0xf, 0xf, true));
     step(__builtin_amdgcn_update_dpp(0, (int)most, kDppXor2, 0xf, 0xf, true));
@@ -41,11 +47,11 @@ template <typename XT>
 __global__ __launch_bounds__(256) void k_unpack(RowsGeo g, const int8_t *codes, const float *scales, XT *x, int blocks) {
     int b;
     if (!block_number(blocks, b)) return;
-    const int across = (g.C + kV - 1) / kV;
-    const int64_t i = (int64_t)b * 256 + threadIdx.x;
-    const int64_t row = i / across;
+    int64_t row;
+    int vec;
+    place(b, 256, (g.C + kV - 1) / kV, threadIdx.x, row, vec);
     if (row >= g.rows) return;
-    const int c = (int)(i - row * across) * kV;
+    const int c = vec * kV;
     const uint64_t q = *(const uint64_t *)(codes + row * g.stride + c);
     const float scale = g.group ? scales[row * ((g.C + g.group - 1) / g.group) + c / g.group] : scales[row];
     Vec<XT, kV> v;

@@ -34,10 +34,11 @@ __device__ __forceinline__ void dz_of(const Q8Geo &g, const Q8Ptrs &a, int64_t r
         for (int k = 0; k < kV; ++k) z[k] = to_f32(v.v[k]);
     } else if constexpr (ZF == kZCodes) {
         const int at = min(c, g.Np - kV);
-        const uint64_t q = *(const uint64_t *)(a.zq_in + row * g.Np + at);
-        const float s = a.sz_in[row * ((g.N + 31) / 32) + min(c, g.N - 1) / 32];
+        const uint64_t q = *(const uint64_t *)(a.zq_in + row * g.Np + at) ^ 0x8080808080808080ull;
+        const float s = a.sz_in[row * ((g.N + 31) / 32) + min(c, g.N - 1) / 32], off = -128.0f * s;
+        // code s, rounded once, from code + 128: unsigned bytes convert in one step
 #pragma unroll
-        for (int k = 0; k < kV; ++k) z[k] = (float)(int8_t)(q >> (8 * k)) * s;
+        for (int k = 0; k < kV; ++k) z[k] = fmaf((float)(uint8_t)(q >> (8 * k)), s, off);
     }
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
@@ -64,8 +65,7 @@ __device__ __forceinline__ void max_block(const Q8Geo &g, const Q8Ptrs &a, int b
     const int c = col * kMaxCols + lane * kV;
     const int r0 = chunk * g.chunk, r1 = min(r0 + g.chunk, g.M);
     const Vec<float, kV> sw = load_any<float>(a.sw, c, g.N);
-    float sum[kV] = {};
-    uint32_t most[kV] = {};
+    float sum[kV] = {}, most[kV] = {};
     with_act(g.act, [&](auto act) {
         constexpr int A = decltype(act)::value;
         if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
@@ -80,37 +80,47 @@ __device__ __forceinline__ void max_block(const Q8Geo &g, const Q8Ptrs &a, int b
 #pragma unroll
                 for (int i = 0; i < kMaxRows; ++i)
                     if (r + 4 * i < r1) {
-                        uint32_t m = 0;
+                        float m = 0.0f;
 #pragma unroll
                         for (int k = 0; k < kV; ++k) {
-                            m = max(m, magnitude(dz[i][k] * sw.v[k]));
-                            most[k] = max(most[k], magnitude(dz[i][k] * sx[i]));
+                            m = larger(m, dz[i][k] * sw.v[k]);
+                            most[k] = larger(most[k], dz[i][k] * sx[i]);
                             sum[k] += dz[i][k];
                         }
-                        m = wave_max(m);
-                        if (lane == 0) a.rowmax[(int64_t)(r + 4 * i) * g.ncol + col] = __uint_as_float(m);
+                        const uint32_t top = wave_max(bits_of(m));
+                        if (lane == 0) a.rowmax[(int64_t)col * g.M + r + 4 * i] = __uint_as_float(top);
                     }
             }
     });
     if (wave > 0)
 #pragma unroll
         for (int k = 0; k < kV; ++k) {
-            red[wave - 1][0][k * 64 + lane] = __uint_as_float(most[k]);
+            red[wave - 1][0][k * 64 + lane] = most[k];
             red[wave - 1][1][k * 64 + lane] = sum[k];
         }
     __syncthreads();
-    if (wave > 0) return;
+    if (wave > 0 || c >= g.Np) return;
     Vec<float, kV> m, s;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-#pragma unroll
-        for (int w = 0; w < 3; ++w) most[k] = max(most[k], __float_as_uint(red[w][0][k * 64 + lane]));
-        m.v[k] = __uint_as_float(most[k]);
+        m.v[k] = larger(larger(larger(most[k], red[0][0][k * 64 + lane]), red[1][0][k * 64 + lane]), red[2][0][k * 64 + lane]);
         s.v[k] = (sum[k] + red[0][1][k * 64 + lane]) + (red[1][1][k * 64 + lane] + red[2][1][k * 64 + lane]);
     }
-    if (c < g.N) {
-        store_cols<float>(a.colmax + (int64_t)chunk * g.N, c, g.N, m);
-        store_cols<float>(a.colsum + (int64_t)chunk * g.N, c, g.N, s);
+    store_vec<float, kV>(a.colmax + (int64_t)chunk * g.Np + c, m);
+    store_vec<float, kV>(a.colsum + (int64_t)chunk * g.Np + c, s);
+}
+
+// The p-th bytes, from the top of N bytes, of four numbers: out[p].
+template <int N>
+__device__ __forceinline__ void bytes_of(const uint32_t (&q)[4], uint32_t (&out)[N]) {
+    const auto pick = [](uint32_t hi, uint32_t lo, uint32_t sel) { return __builtin_amdgcn_perm(hi, lo, sel); };
+    const uint32_t a = pick(q[1], q[0], 0x05010400u), b = pick(q[3], q[2], 0x05010400u);  // bytes 0, then 1, of both
+    out[N - 1] = pick(b, a, 0x05040100u);
+    out[N - 2] = pick(b, a, 0x07060302u);
+    if constexpr (N == 4) {
+        const uint32_t c = pick(q[1], q[0], 0x07030602u), d = pick(q[3], q[2], 0x07030602u);
+        out[1] = pick(d, c, 0x05040100u);
+        out[0] = pick(d, c, 0x07060302u);
     }
 }
 
@@ -132,14 +142,13 @@ __device__ __forceinline__ void transpose_block(const int8_t *x, int64_t rows, i
         for (int d = 0; d < 4; ++d) v[i][d] = r < rows ? (uint32_t)q[d] : 0u;
     }
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
+    for (int d = 0; d < 4; ++d) {
+        const uint32_t rows4[4] = {v[0][d], v[1][d], v[2][d], v[3][d]};
+        uint32_t o[4];
+        bytes_of<4>(rows4, o);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            uint32_t o = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o |= (v[i][d] >> (8 * e) & 255u) << (8 * i);
-            *(uint32_t *)(tile + (cg * 16 + d * 4 + e) * LD + rg * 4) = o;
-        }
+        for (int e = 0; e < 4; ++e) *(uint32_t *)(tile + (cg * 16 + d * 4 + e) * LD + rg * 4) = o[3 - e];
+    }
     __syncthreads();
     // a wave writes 8 columns' lines of 128 bytes at a time, 16 bytes a lane
 #pragma unroll
@@ -164,8 +173,8 @@ __global__ __launch_bounds__(256) void k_q8_max(Q8Geo g, Q8Ptrs a, int nm, int n
 
 // ----------------------------------------------------------------- second pass
 // Fixed point of a largest magnitude m (its bits): whole numbers of `planes` digits, the
-// highest in [-127, 127], the others in [-128, 127]. An infinity or a NaN: zeros, and a
-// scale of NaN.
+// highest in [-127, 127], the others in [-128, 127]. An infinity or a NaN: a scale of
+// NaN, and any digits.
 template <int PLANES>
 struct Digits {
     static constexpr float kMost = PLANES == 2 ? 32512.0f : 2130706432.0f;  // 127 256^(planes - 1)
@@ -180,110 +189,122 @@ struct Digits {
     __device__ __forceinline__ static float scale(uint32_t bits) {
         return bits >= kInfBits ? __uint_as_float(0x7fc00000u) : __uint_as_float(bits) / 127.0f;
     }
-    // Digit p of the number in the p-th byte from the top.
+    // The number plus 128 in each digit but the highest: its bytes, with 128 taken
+    // off again in each by lower(), are the digits.
     __device__ __forceinline__ uint32_t operator()(float v) const {
-        const float t = v * up * f;
-        int q = f == 0.0f ? 0 : (int)__builtin_rintf(t);
-        if constexpr (PLANES == 2) {
-            const uint32_t u = (uint32_t)(q + 128);  // hi = u >> 8, lo = (u & 255) - 128
-            return (u & 0xff00u) | ((u ^ 0x80u) & 0xffu);
-        } else {
-            // 2130706432 (1 + 2^-23) + 0x808080 is still below 2^31
-            const uint32_t u = (uint32_t)q + 0x00808080u;
-            return u ^ 0x00808080u;
-        }
+        if constexpr (PLANES == 2) return __float_as_uint(v * f + (kRoundMagic + 128.0f));  // the low half
+        // 2130706432 (1 + 2^-23) + 0x808080 is still below 2^31
+        return (uint32_t)(int)__builtin_rintf(v * f) + 0x00808080u;
+    }
+    __device__ __forceinline__ static void lower(uint32_t (&planes)[PLANES]) {
+#pragma unroll
+        for (int p = 1; p < PLANES; ++p) planes[p] ^= 0x80808080u;
     }
 };
 
-// 128 rows x 64 columns: a thread has 4 rows of 8 columns.
+// 64 columns of a strip of tiles of 128 rows: a thread has 4 rows of 8 columns. The
+// columns' largest magnitudes, of all the first pass's chunks, are found once a strip.
 template <typename XT, typename YT, int ZF, int PLANES>
-__global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_dx, int want_dw, int across, int nb) {
+__global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_dx, int want_dw, int nb) {
     constexpr int LD = 128 + 8;  // bytes between columns in LDS
     __shared__ __align__(16) int8_t tile[PLANES * 64 * LD];
-    __shared__ uint32_t cpart[4][64], rpart[128];
+    __shared__ float cpart[16][64];
+    __shared__ uint32_t cmax[64], rmax[128];
     int b;
     if (!block_number(nb, b)) return;
-    const int br = b / across;
-    const int r0 = br * 128, c0 = (b - br * across) * 64;
+    const int across = g.Np / 64, strip = b / across, c0 = (b - strip * across) * 64;
     const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;
-    if (want_dw) {  // four threads a column along the chunks of the first pass
-        const int c = c0 + (threadIdx.x & 63), q = threadIdx.x >> 6;
-        uint32_t m = 0;
-        if (c < g.N)
-            for (int i = q; i < g.nchunk; i += 4) m = max(m, __float_as_uint(a.colmax[(int64_t)i * g.N + c]));
-        cpart[q][threadIdx.x & 63] = m;
+    if (want_dw) {  // 4 columns a thread, 16 threads along the chunks
+        const int c = (threadIdx.x & 15) * 4, q = threadIdx.x >> 4;
+        Vec<float, 4> m = {};
+#pragma unroll 8
+        for (int i = q; i < g.nchunk; i += 16) {
+            const Vec<float, 4> v = load_vec<float, 4>(a.colmax + (int64_t)i * g.Np + c0 + c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m.v[k] = larger(m.v[k], v.v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cpart[q][c + k] = m.v[k];
+        __syncthreads();
+        if (threadIdx.x < 64) {
+            float t = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) t = larger(t, cpart[i][threadIdx.x]);
+            cmax[threadIdx.x] = bits_of(t);
+            if (strip == 0 && c0 + (int)threadIdx.x < g.N) a.cscale[c0 + threadIdx.x] = Digits<PLANES>::scale(bits_of(t));
+        }
     }
-    if (want_dx && threadIdx.x < 128) {
-        const int r = r0 + threadIdx.x;
-        uint32_t m = 0;
-        if (r < g.M)
-            for (int i = 0; i < g.ncol; ++i) m = max(m, __float_as_uint(a.rowmax[(int64_t)r * g.ncol + i]));
-        rpart[threadIdx.x] = m;
-        if (c0 == 0 && r < g.M) a.rscale[r] = Digits<PLANES>::scale(m);
-    }
-    __syncthreads();
-    const int c = c0 + cg * kV;
-    const auto colmax = [&](int i) {
-        return max(max(cpart[0][i], cpart[1][i]), max(cpart[2][i], cpart[3][i]));
-    };
-    if (want_dw && r0 == 0 && threadIdx.x < 64 && c0 + threadIdx.x < g.N)
-        a.cscale[c0 + threadIdx.x] = Digits<PLANES>::scale(colmax(threadIdx.x));
+    const int c = c0 + cg * kV, t1 = min((strip + 1) * g.strip, g.Mp / 128);
     const Vec<float, kV> sw = load_any<float>(a.sw, c, g.N);
-    float dz[4][kV];
-    with_act(g.act, [&](auto act) {
-        constexpr int A = decltype(act)::value;
-        if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
+    for (int t = strip * g.strip; t < t1; ++t) {
+        const int r0 = t * 128;
+        float dz[4][kV];
+        with_act(g.act, [&](auto act) {
+            constexpr int A = decltype(act)::value;
+            if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                dz_of<YT, ZF, A, exact_acts<XT, YT>()>(g, a, min(r0 + rg * 4 + i, g.M - 1), c, dz[i]);
-    });
-    if (want_dx)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = r0 + rg * 4 + i;
-            const Digits<PLANES> d(rpart[rg * 4 + i]);
-            uint32_t q[kV];
-#pragma unroll
-            for (int k = 0; k < kV; ++k) q[k] = d(dz[i][k] * sw.v[k]);
-            if (r < g.M)
-#pragma unroll
-                for (int p = 0; p < PLANES; ++p) {
-                    constexpr int kTop = (PLANES - 1) * 8;
-                    uint64_t o = 0;
-#pragma unroll
-                    for (int k = 0; k < kV; ++k) o |= (uint64_t)(q[k] >> (kTop - 8 * p) & 255u) << (8 * k);
-                    *(uint64_t *)(a.ur + ((int64_t)p * g.M + r) * g.Np + c) = o;
-                }
+                for (int i = 0; i < 4; ++i)
+                    dz_of<YT, ZF, A, exact_acts<XT, YT>()>(g, a, min(r0 + rg * 4 + i, g.M - 1), c, dz[i]);
+        });
+        if (want_dx && threadIdx.x < 128) {
+            const int r = min(r0 + (int)threadIdx.x, g.M - 1);
+            float m = 0.0f;
+            for (int i = 0; i < g.ncol; ++i) m = larger(m, a.rowmax[(int64_t)i * g.M + r]);
+            rmax[threadIdx.x] = bits_of(m);
+            if (c0 == 0 && r0 + (int)threadIdx.x < g.M) a.rscale[r] = Digits<PLANES>::scale(bits_of(m));
         }
-    if (!want_dw) return;
-    float sx[4];
+        __syncthreads();
+        if (want_dx)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sx[i] = r0 + rg * 4 + i < g.M ? a.sx[r0 + rg * 4 + i] : 0.0f;
+            for (int i = 0; i < 4; ++i) {
+                const int r = r0 + rg * 4 + i;
+                const Digits<PLANES> d(rmax[rg * 4 + i]);
+                float u[kV];
 #pragma unroll
-    for (int k = 0; k < kV; ++k) {
-        const Digits<PLANES> d(colmax(cg * kV + k));
-        uint32_t q[4];
+                for (int k = 0; k < kV; ++k) u[k] = dz[i][k] * sw.v[k];
+                if (__builtin_expect(__any(d.up != 1.0f), 0))
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            q[i] = d(dz[i][k] * sx[i]);
-            if (r0 + rg * 4 + i >= g.M) q[i] = 0;  // dz there is another row's
+                    for (int k = 0; k < kV; ++k) u[k] *= d.up;
+                uint32_t lo[PLANES], hi[PLANES];
+                bytes_of<PLANES>({d(u[0]), d(u[1]), d(u[2]), d(u[3])}, lo);
+                bytes_of<PLANES>({d(u[4]), d(u[5]), d(u[6]), d(u[7])}, hi);
+                Digits<PLANES>::lower(lo);
+                Digits<PLANES>::lower(hi);
+                if (r < g.M)
+#pragma unroll
+                    for (int p = 0; p < PLANES; ++p)
+                        *(uint64_t *)(a.ur + ((int64_t)p * g.M + r) * g.Np + c) = (uint64_t)hi[p] << 32 | lo[p];
+            }
+        if (want_dw) {
+            float sx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sx[i] = a.sx[min(r0 + rg * 4 + i, g.M - 1)];
+#pragma unroll
+            for (int k = 0; k < kV; ++k) {
+                const Digits<PLANES> d(cmax[cg * kV + k]);
+                float u[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[i] = r0 + rg * 4 + i < g.M ? dz[i][k] * sx[i] : 0.0f;
+                if (__builtin_expect(__any(d.up != 1.0f), 0))
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[i] *= d.up;
+                uint32_t o[PLANES];
+                bytes_of<PLANES>({d(u[0]), d(u[1]), d(u[2]), d(u[3])}, o);
+                Digits<PLANES>::lower(o);
+#pragma unroll
+                for (int p = 0; p < PLANES; ++p) *(uint32_t *)(tile + (p * 64 + cg * kV + k) * LD + rg * 4) = o[p];
+            }
+            __syncthreads();
+            // 8 bytes a lane, 16 lanes a line
+#pragma unroll
+            for (int i = 0; i < PLANES * 4; ++i) {
+                const int line = i * 16 + (threadIdx.x >> 4), p = line / 64, col = line % 64, part = (threadIdx.x & 15) * 8;
+                if (c0 + col < g.N)
+                    *(uint64_t *)(a.uc + ((int64_t)p * g.N + c0 + col) * g.Mp + r0 + part) =
+                        *(const uint64_t *)(tile + line * LD + part);
+            }
         }
-#pragma unroll
-        for (int p = 0; p < PLANES; ++p) {
-            constexpr int kTop = (PLANES - 1) * 8;
-            uint32_t o = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o |= (q[i] >> (kTop - 8 * p) & 255u) << (8 * i);
-            *(uint32_t *)(tile + (p * 64 + cg * kV + k) * LD + rg * 4) = o;
-        }
-    }
-    __syncthreads();
-    // 8 bytes a lane, 16 lanes a line
-#pragma unroll
-    for (int i = 0; i < PLANES * 4; ++i) {
-        const int line = i * 16 + (threadIdx.x >> 4), p = line / 64, col = line % 64, part = (threadIdx.x & 15) * 8;
-        if (c0 + col < g.N)
-            *(uint64_t *)(a.uc + ((int64_t)p * g.N + c0 + col) * g.Mp + r0 + part) = *(const uint64_t *)(tile + line * LD + part);
+        if (t + 1 < t1) __syncthreads();  // the tile and the rows' magnitudes are read
     }
 }
 
@@ -323,7 +344,7 @@ __device__ __forceinline__ void dbias_block(const Q8Geo &g, const Q8Ptrs &a, int
     const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4, rows = blockDim.x >> 4, c = b * 16 + tc;
     float t = 0.0f;
     if (c < g.N)
-        for (int r = tr; r < g.nchunk; r += rows) t += a.colsum[(int64_t)r * g.N + c];
+        for (int r = tr; r < g.nchunk; r += rows) t += a.colsum[(int64_t)r * g.Np + c];
     red[tr * 17 + tc] = t;
     __syncthreads();
     if (tr == 0 && c < g.N) {
@@ -416,10 +437,9 @@ void prepare(const Q8Geo &g, const Q8Ptrs &p, hipStream_t st) {
     hipLaunchKernelGGL((k_q8_max<XT, YT, ZF>), grid_of(nm + nx + nw), dim3(256), 0, st, g, p, (int)nm, (int)nx,
                        (int)(nm + nx + nw));
     if (!p.dx && !p.dw) return;
-    const int across = g.Np / 64;
-    const int64_t nd = (int64_t)(g.Mp / 128) * across;
+    const int64_t nd = (int64_t)((g.Mp / 128 + g.strip - 1) / g.strip) * (g.Np / 64);
     hipLaunchKernelGGL((k_q8_digits<XT, YT, ZF, PLANES>), grid_of(nd), dim3(256), 0, st, g, p, p.dx != nullptr, p.dw != nullptr,
-                       across, (int)nd);
+                       (int)nd);
 }
 
 template <typename XT, typename YT>

@@ -4,9 +4,7 @@
 // residual and what is kept of z (as it is, or in codes of 32 columns, which
 // four lanes of a wave have) are in the epilogue.
 //
-// A few rows (one token, a short batch) have a kernel of their own: it only has
-// to stream the weights, so its waves read their fragments from memory past LDS,
-// 16 or 32 columns a block, the waves of a block along k.
+// Up to four rows (single tokens) have a kernel of their own.
 #include "wq8_q8_gemm.h"
 #include "wq8_rows.h"
 
@@ -78,12 +76,9 @@ struct EpiQ8 {
             for (int e = 0; e < 8; ++e) v.v[e] += col.bias.v[e];
         if (zq) {  // all lanes: a group's four meet
             float t[8];
-            uint32_t most = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                t[e] = n + e < N ? v.v[e] : 0.0f;
-                most = max(most, magnitude(t[e]));
-            }
+            for (int e = 0; e < 8; ++e) t[e] = n + e < N ? v.v[e] : 0.0f;
+            uint32_t most = bits_of(largest(t));
             const auto r16 = __builtin_amdgcn_permlane16_swap(most, most, false, false);
             most = max(r16[0], r16[1]);
             const auto r32 = __builtin_amdgcn_permlane32_swap(most, most, false, false);
@@ -114,76 +109,66 @@ struct EpiQ8 {
     }
 };
 
-// MT tiles of 16 rows, 32 columns a block, W waves along k. A wave's fragment
-// is 16 rows of 64 adjacent bytes; two of them make its lines whole, so a wave
-// takes steps of 128 bytes, every W-th. Rows and columns past the end repeat the
-// last one.
-template <int MT, int W, typename EPI>
-__global__ __launch_bounds__(W * 64) void k_q8_few(Q8Args a, EPI epi, int blocks) {
-    constexpr int DEPTH = MT == 1 ? 4 : 2;  // steps whose loads are in flight together
-    __shared__ i32x4 red[W > 1 ? W : 1][MT][2][64];
+// Up to 4 rows: each weight is used so few times that it needs no matrix core,
+// and reads best along its row. A wave takes 4096 bytes of a weight row at a
+// time, 16 a lane, four products an instruction, OUT columns in turn, two of them
+// with their loads in flight; the rows' codes stay in registers meanwhile. Sums
+// over the lanes are whole numbers, in any order the same.
+constexpr int kDotWaves = 4;
+
+template <int ROWS, int OUT, typename EPI>
+__global__ __launch_bounds__(kDotWaves * 64) void k_q8_dot(Q8Args a, EPI epi, int blocks) {
+    constexpr int CHUNK = 4, COLS = kDotWaves * OUT, PAIR = 2;
+    __shared__ int sums[ROWS][COLS];
     int b;
     if (!block_number(blocks, b)) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int n0 = b * 32;
-    const int8_t *pa[MT], *pb[2];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n0 = b * COLS;
+    const int bytes = a.steps * 128;
+#pragma unroll 1
+    for (int o = 0; o < OUT; o += PAIR) {
+        const int8_t *w[PAIR];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) pa[i] = a.A + (int64_t)min(i * 16 + (lane & 15), a.M - 1) * a.lda + (lane >> 4) * 16;
+        for (int j = 0; j < PAIR; ++j) w[j] = a.B + (int64_t)min(n0 + wave * OUT + o + j, a.N - 1) * a.ldb;
+        int acc[PAIR][ROWS] = {};
+        for (int k0 = 0; k0 < bytes; k0 += CHUNK * 1024) {
+            i32x4 v[PAIR][CHUNK], x[ROWS][CHUNK];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) pb[j] = a.B + (int64_t)min(n0 + row_of<true>(lane & 15, j), a.N - 1) * a.ldb + (lane >> 4) * 16;
-    i32x4 acc[MT][2] = {};
-    for (int s = wave; s < a.steps; s += W * DEPTH) {
-        i32x4 fa[DEPTH][MT][2], fb[DEPTH][2][2];
+            for (int c = 0; c < CHUNK; ++c) {
+                const int k = k0 + c * 1024 + lane * 16, at = min(k, bytes - 16);
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            const int64_t k = (int64_t)min(s + d * W, a.steps - 1) * 128;
+                for (int j = 0; j < PAIR; ++j) v[j][c] = *(const i32x4 *)(w[j] + at);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+                for (int r = 0; r < ROWS; ++r) x[r][c] = *(const i32x4 *)(a.A + (int64_t)min(r, a.M - 1) * a.lda + at);
+                if (k != at)  // past the end: counted by the lane that has it
 #pragma unroll
-                for (int j = 0; j < 2; ++j) fb[d][j][h] = *(const i32x4 *)(pb[j] + k + h * 64);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) fa[d][i][h] = *(const i32x4 *)(pa[i] + k + h * 64);
+                    for (int r = 0; r < ROWS; ++r) x[r][c] = i32x4{};
             }
+#pragma unroll
+            for (int c = 0; c < CHUNK; ++c)
+#pragma unroll
+                for (int j = 0; j < PAIR; ++j)
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j][r] = __builtin_amdgcn_sdot4(v[j][c][e], x[r][c][e], acc[j][r], false);
         }
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            if (s + d * W < a.steps)
+        for (int j = 0; j < PAIR; ++j)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[d][j][h], fa[d][i][h], acc[i][j], 0, 0, 0);
-    }
-    if constexpr (W > 1) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) red[wave][i][j][lane] = acc[i][j];
-        __syncthreads();
-    }
-    const int n = n0 + (lane >> 4) * 8;
-    epi.with([&](auto act) {
-        for (int i = wave; i < MT; i += W) {  // a wave joins a tile of rows
-            i32x4 t[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if constexpr (W > 1) {
-                    t[j] = red[0][i][j][lane];
-#pragma unroll
-                    for (int w = 1; w < W; ++w) t[j] += red[w][i][j][lane];
-                } else {
-                    t[j] = acc[i][j];
-                }
+            for (int r = 0; r < ROWS; ++r) {
+                const int t = wave_add(acc[j][r]);
+                if (lane == 0) sums[r][wave * OUT + o + j] = t;
             }
-            const int m = i * 16 + (lane & 15);
-            Vec<float, 8> v;
+    }
+    __syncthreads();
+    if (wave > 0) return;
+    const int g = lane >> 4, n = n0 + g * 8;
+    const int m = g * 8 < COLS && (lane & 15) < ROWS ? (lane & 15) : a.M;
+    Vec<float, 8> v = {};
+    if (m < a.M)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v.v[e] = (float)t[0][e], v.v[4 + e] = (float)t[1][e];
-            epi.template store<decltype(act)::value>(m, n, v, blocks * 32, epi.column(n), epi.item(m, n));
-        }
-    });
+        for (int e = 0; e < 8; ++e) v.v[e] = (float)sums[m][g * 8 + e];
+    epi.with([&](auto act) { epi.template store<decltype(act)::value>(m, n, v, blocks * COLS, epi.column(n), epi.item(m, n)); });
 }
 
 template <typename YT>
@@ -218,20 +203,22 @@ struct RunQ8 {
                                (int)q8_join_blocks(a));
     }
 
-    template <int MT>
+    template <int ROWS>
     void few() const {
-        const int blocks = (g.N + 31) / 32;
-        const auto go = [&](auto kernel, int w) {
-            hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(w * 64), 0, st, args(), epi(), blocks);
+        const auto go = [&](auto kernel, int cols) {
+            const int blocks = (g.N + cols - 1) / cols;
+            hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(kDotWaves * 64), 0, st, args(), epi(), blocks);
         };
-        if (g.few_waves == 4) go(k_q8_few<MT, 4, EpiQ8<YT>>, 4);
-        else go(k_q8_few<MT, 8, EpiQ8<YT>>, 8);
+        // codes of z need their 32 columns in one block; else 8 spread evenly
+        // over the compute units
+        if (p.zq) go(k_q8_dot<ROWS, 8, EpiQ8<YT>>, 32);
+        else go(k_q8_dot<ROWS, 2, EpiQ8<YT>>, 8);
     }
 
     void run() const {
         if (g.f.tile >= 0) return pick_q8_tile<false>(g.f.tile, *this);
-        if (g.few_rows == 1) few<1>();
-        else if (g.few_rows == 2) few<2>();
+        if (g.M == 1) few<1>();
+        else if (g.M == 2) few<2>();
         else few<4>();
     }
 };

@@ -262,7 +262,9 @@ void pick_q8_tile(int tile, const R &run) {
             return;
         case 1: return run.template operator()<128, 128, 2, 2>();
         case 2: return run.template operator()<128, 64, 2, 2>();
-        default: return run.template operator()<64, 64, 2, 2>();
+        case 3: return run.template operator()<64, 64, 2, 2>();
+        default:
+            if constexpr (!MULTI) run.template operator()<16, 128, 1, 2>();
     }
 }
 

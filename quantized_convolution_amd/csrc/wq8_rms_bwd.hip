@@ -9,48 +9,37 @@
 namespace wq8 {
 namespace {
 
-// ANY: rows of fewer columns than a vector too.
-template <typename XT, typename YT, bool ANY>
-struct RowGrad {
-    const RowsGeo &g;
-    const RmsPtrs &a;
-    int64_t row;
+// The same values, of which the compiler knows nothing.
+template <typename T>
+__device__ __forceinline__ void forget(Vec<T, kV> &v) {
+    uint32_t w[sizeof v / 4];
+    __builtin_memcpy(w, &v, sizeof v);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof v / 4); ++i) asm("" : "+v"(w[i]));
+    __builtin_memcpy(&v, w, sizeof v);
+}
 
-    template <typename T>
-    __device__ __forceinline__ Vec<T, kV> load(const T *p, int c) const {
-        if constexpr (ANY) return load_any<T>(p, c, g.C);
-        else return load_cols<T>(p, c, g.C);
-    }
-    __device__ __forceinline__ Vec<XT, kV> h(int c) const { return load<XT>((const XT *)a.x + row * g.xs, c); }
-    __device__ __forceinline__ Vec<XT, kV> dh(int c) const { return load<XT>((const XT *)a.dh + row * g.xs, c); }
-    __device__ __forceinline__ Vec<YT, kV> dy(int c) const { return load<YT>((const YT *)a.dy + row * g.ys, c); }
-    __device__ __forceinline__ Vec<float, kV> gamma(int c) const {
-        Vec<float, kV> r;
-        if (a.gamma) return load<float>(a.gamma, c);
+// What a thread adds to sum t n: 8 columns.
+template <typename XT, typename YT>
+__device__ __forceinline__ float dot(const Vec<XT, kV> &h, const Vec<YT, kV> &dy, const Vec<float, kV> &gm, float rstd) {
+    float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kV; ++k) r.v[k] = 1.0f;
-        return r;
-    }
-    __device__ __forceinline__ static float dot(const Vec<XT, kV> &h, const Vec<YT, kV> &dy, const Vec<float, kV> &gm,
-                                                float rstd) {
-        float sum = 0.0f;
+    for (int k = 0; k < kV; ++k) sum = fmaf(gm.v[k] * to_f32(dy.v[k]), to_f32(h.v[k]) * rstd, sum);
+    return sum;
+}
+
+template <typename XT, typename YT>
+__device__ __forceinline__ Vec<XT, kV> grad(const Vec<XT, kV> &h, const Vec<YT, kV> &dy, const Vec<float, kV> &gm,
+                                            const Vec<XT, kV> &dh, bool more, float rstd, float mean) {
+    Vec<XT, kV> o;
 #pragma unroll
-        for (int k = 0; k < kV; ++k) sum = fmaf(gm.v[k] * to_f32(dy.v[k]), to_f32(h.v[k]) * rstd, sum);
-        return sum;
+    for (int k = 0; k < kV; ++k) {
+        float v = rstd * fmaf(-(to_f32(h.v[k]) * rstd), mean, gm.v[k] * to_f32(dy.v[k]));
+        if (more) v += to_f32(dh.v[k]);
+        o.v[k] = from_f32<XT>(v);
     }
-    __device__ __forceinline__ void dx(int c, const Vec<XT, kV> &h, const Vec<YT, kV> &dy, const Vec<float, kV> &gm,
-                                       const Vec<XT, kV> &dh, float rstd, float mean) const {
-        if (c >= g.C) return;
-        Vec<XT, kV> o;
-#pragma unroll
-        for (int k = 0; k < kV; ++k) {
-            float v = rstd * fmaf(-(to_f32(h.v[k]) * rstd), mean, gm.v[k] * to_f32(dy.v[k]));
-            if (a.dh) v += to_f32(dh.v[k]);
-            o.v[k] = from_f32<XT>(v);
-        }
-        store_cols<XT>((XT *)a.dx + row * g.xs, c, g.C, o);
-    }
-};
+    return o;
+}
 
 template <typename XT, typename YT, int L, int U>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void k_rms_bwd(RowsGeo g, RmsPtrs a, int want_dgamma) {
@@ -60,35 +49,32 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void k_rms_bwd(RowsGeo g, RmsPtr
     const int t = threadIdx.x % L, w = threadIdx.x / L;
     Vec<float, kV> gm[U];
     float dg[U][kV] = {};
-    {
-        const RowGrad<XT, YT, false> r = {g, a, 0};
-#pragma unroll
-        for (int s = 0; s < U; ++s) gm[s] = r.gamma((s * L + t) * kV);
-    }
+    load_gamma<L, U>(gm, a.gamma, t, g.C);
     const int r0 = blockIdx.x * g.chunk, r1 = min(r0 + g.chunk, g.rows);
     int turn = 0;
     for (int i = r0 + (L < 256 ? w : 0); i < r1; i += PER) {
-        const RowGrad<XT, YT, false> r = {g, a, i};
         Vec<XT, kV> h[U], dh[U];
         Vec<YT, kV> dy[U];
-#pragma unroll
-        for (int s = 0; s < U; ++s) {
-            h[s] = r.h((s * L + t) * kV);
-            dy[s] = r.dy((s * L + t) * kV);
-        }
-        if (a.dh)
-#pragma unroll
-            for (int s = 0; s < U; ++s) dh[s] = r.dh((s * L + t) * kV);
+        load_row<XT, L, U>(h, (const XT *)a.x + i * g.xs, t, g.C);
+        load_row<YT, L, U>(dy, (const YT *)a.dy + i * g.ys, t, g.C);
+        if (a.dh) load_row<XT, L, U>(dh, (const XT *)a.dh + i * g.xs, t, g.C);
         const float rstd = a.rstd_in[i];
         float sum = 0.0f;
         uint32_t none = 0;
 #pragma unroll
-        for (int s = 0; s < U; ++s) sum += RowGrad<XT, YT, false>::dot(h[s], dy[s], gm[s], rstd);
+        for (int s = 0; s < U; ++s) sum += dot(h[s], dy[s], gm[s], rstd);
         reduce_row<L>(sum, none, red, turn++);
         const float mean = sum / (float)g.C;
+        // what comes next is formed from the values again: held over the sum it
+        // would take the registers of another wave
 #pragma unroll
         for (int s = 0; s < U; ++s) {
-            r.dx((s * L + t) * kV, h[s], dy[s], gm[s], dh[s], rstd, mean);
+            forget(h[s]);
+            forget(dy[s]);
+        }
+#pragma unroll
+        for (int s = 0; s < U; ++s) {
+            store_step<XT, L, U>((XT *)a.dx + i * g.xs, s, t, g.C, grad(h[s], dy[s], gm[s], dh[s], a.dh != nullptr, rstd, mean));
 #pragma unroll
             for (int k = 0; k < kV; ++k) dg[s][k] = fmaf(to_f32(dy[s].v[k]), to_f32(h[s].v[k]) * rstd, dg[s][k]);
         }
@@ -128,17 +114,27 @@ __global__ __launch_bounds__(1024) void k_rms_bwd_long(RowsGeo g, RmsPtrs a, int
     __shared__ float red[2 * L / 64];
     int b;
     if (!block_number(blocks, b)) return;
-    const RowGrad<XT, YT, true> r = {g, a, b};
+    const XT *const h = (const XT *)a.x + (int64_t)b * g.xs, *const dh = (const XT *)a.dh + (int64_t)b * g.xs;
+    const YT *const dy = (const YT *)a.dy + (int64_t)b * g.ys;
+    const auto gamma = [&](int c) {
+        Vec<float, kV> r;
+        if (a.gamma) return load_any<float>(a.gamma, c, g.C);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) r.v[k] = 1.0f;
+        return r;
+    };
     const float rstd = a.rstd_in[b];
     float sum = 0.0f;
     uint32_t none = 0;
-    for (int c = threadIdx.x * kV; c < g.C; c += L * kV) sum += RowGrad<XT, YT, true>::dot(r.h(c), r.dy(c), r.gamma(c), rstd);
+    for (int c = threadIdx.x * kV; c < g.C; c += L * kV)
+        sum += dot(load_any<XT>(h, c, g.C), load_any<YT>(dy, c, g.C), gamma(c), rstd);
     reduce_row<L>(sum, none, red, 0);
     const float mean = sum / (float)g.C;
     for (int c = threadIdx.x * kV; c < g.C; c += L * kV) {
-        Vec<XT, kV> dh = {};
-        if (a.dh) dh = r.dh(c);
-        r.dx(c, r.h(c), r.dy(c), r.gamma(c), dh, rstd, mean);
+        Vec<XT, kV> more = {};
+        if (a.dh) more = load_any<XT>(dh, c, g.C);
+        store_cols<XT>((XT *)a.dx + (int64_t)b * g.xs, c, g.C,
+                       grad(load_any<XT>(h, c, g.C), load_any<YT>(dy, c, g.C), gamma(c), more, a.dh != nullptr, rstd, mean));
     }
 }
 
@@ -149,9 +145,8 @@ __global__ __launch_bounds__(256) void k_rms_dgamma_long(RowsGeo g, RmsPtrs a) {
     const int r0 = blockIdx.x * g.chunk, r1 = min(r0 + g.chunk, g.rows);
     Vec<float, kV> o = {};
     for (int i = r0; i < r1; ++i) {
-        const RowGrad<XT, YT, true> r = {g, a, i};
-        const Vec<XT, kV> h = r.h(c);
-        const Vec<YT, kV> dy = r.dy(c);
+        const Vec<XT, kV> h = load_any<XT>((const XT *)a.x + i * g.xs, c, g.C);
+        const Vec<YT, kV> dy = load_any<YT>((const YT *)a.dy + i * g.ys, c, g.C);
         const float rstd = a.rstd_in[i];
 #pragma unroll
         for (int k = 0; k < kV; ++k) o.v[k] = fmaf(to_f32(dy.v[k]), to_f32(h.v[k]) * rstd, o.v[k]);
@@ -191,10 +186,11 @@ void backward(const RowsGeo &g, const RmsPtrs &p, hipStream_t st) {
         };
         if (g.s.lanes == 64) {
             if (g.s.unroll == 1) go(k_rms_bwd<XT, YT, 64, 1>, 256);
-            else go(k_rms_bwd<XT, YT, 64, 2>, 256);
+            else if (g.s.unroll == 2) go(k_rms_bwd<XT, YT, 64, 2>, 256);
+            else if (g.s.unroll == 3) go(k_rms_bwd<XT, YT, 64, 3>, 256);
+            else go(k_rms_bwd<XT, YT, 64, 4>, 256);
         } else if (g.s.lanes == 256) {
-            if (g.s.unroll == 1) go(k_rms_bwd<XT, YT, 256, 1>, 256);
-            else go(k_rms_bwd<XT, YT, 256, 2>, 256);
+            go(k_rms_bwd<XT, YT, 256, 2>, 256);
         } else if (g.s.lanes == 512) {
             go(k_rms_bwd<XT, YT, 512, 2>, 512);
         } else {

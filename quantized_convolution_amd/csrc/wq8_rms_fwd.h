@@ -28,35 +28,33 @@ __device__ __forceinline__ Vec<XT, kV> add_rounded(const Vec<XT, kV> &x, const V
 
 // What a thread adds to its row's sum of squares and largest |h gamma|.
 template <typename XT, bool NORM>
-__device__ __forceinline__ void take(const Vec<XT, kV> &h, const Vec<float, kV> &gm, float &sum, uint32_t &most) {
+__device__ __forceinline__ void take(const Vec<XT, kV> &h, const Vec<float, kV> &gm, float &sum, float &most) {
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
         const float v = to_f32(h.v[k]);
         if constexpr (NORM) {
             sum = fmaf(v, v, sum);
-            most = max(most, magnitude(v * gm.v[k]));
+            most = larger(most, v * gm.v[k]);
         } else {
-            most = max(most, magnitude(v));
+            most = larger(most, v);
         }
     }
 }
 
-template <typename XT, typename YT, bool NORM>
-__device__ __forceinline__ void give(const RowsGeo &g, const RmsPtrs &a, int64_t row, int c, const Vec<XT, kV> &h,
-                                     const Vec<float, kV> &gm, float rstd, const Coder &code) {
-    if constexpr (NORM)
-        if (a.y && c < g.C) {
-            Vec<YT, kV> y;
+template <typename XT, typename YT>
+__device__ __forceinline__ Vec<YT, kV> normed(const Vec<XT, kV> &h, const Vec<float, kV> &gm, float rstd) {
+    Vec<YT, kV> y;
 #pragma unroll
-            for (int k = 0; k < kV; ++k) y.v[k] = from_f32<YT>(to_f32(h.v[k]) * rstd * gm.v[k]);
-            store_cols<YT>((YT *)a.y + row * g.ys, c, g.C, y);
-        }
-    if ((!NORM || a.codes) && c < g.stride) {
-        float t[kV];
+    for (int k = 0; k < kV; ++k) y.v[k] = from_f32<YT>(to_f32(h.v[k]) * rstd * gm.v[k]);
+    return y;
+}
+
+template <typename XT, bool NORM>
+__device__ __forceinline__ uint64_t coded(const Vec<XT, kV> &h, const Vec<float, kV> &gm, const Coder &code) {
+    float t[kV];
 #pragma unroll
-        for (int k = 0; k < kV; ++k) t[k] = NORM ? to_f32(h.v[k]) * gm.v[k] : to_f32(h.v[k]);
-        store_codes(a.codes + row * g.stride + c, code.pack(t));
-    }
+    for (int k = 0; k < kV; ++k) t[k] = NORM ? to_f32(h.v[k]) * gm.v[k] : to_f32(h.v[k]);
+    return code.pack(t);
 }
 
 template <bool NORM>
@@ -74,43 +72,45 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void k_row(RowsGeo g, RmsPtrs a,
     const int64_t row = (int64_t)b * PER + (L < 256 ? threadIdx.x / L : 0);
     if (row >= g.rows) return;  // a whole wave, which meets no barrier
     const int t = threadIdx.x % L;
-    const XT *const x = (const XT *)a.x + row * g.xs;
     Vec<XT, kV> h[U];
     Vec<float, kV> gm[U];
-#pragma unroll
-    for (int s = 0; s < U; ++s) h[s] = load_cols<XT>(x, (s * L + t) * kV, g.C);
+    load_row<XT, L, U>(h, (const XT *)a.x + row * g.xs, t, g.C);
     if constexpr (NORM) {
-        if (a.residual) {
-            const XT *const r = (const XT *)a.residual + row * g.xs;
+        load_gamma<L, U>(gm, a.gamma, t, g.C);
+        if (a.residual) {  // the last loads: all are on their way before one is waited for
             Vec<XT, kV> o[U];
-#pragma unroll
-            for (int s = 0; s < U; ++s) o[s] = load_cols<XT>(r, (s * L + t) * kV, g.C);
+            load_row<XT, L, U>(o, (const XT *)a.residual + row * g.xs, t, g.C);
 #pragma unroll
             for (int s = 0; s < U; ++s) h[s] = add_rounded(h[s], o[s]);
         }
-#pragma unroll
-        for (int s = 0; s < U; ++s) {
-            if (a.gamma) {
-                gm[s] = load_cols<float>(a.gamma, (s * L + t) * kV, g.C);
-            } else {
-#pragma unroll
-                for (int k = 0; k < kV; ++k) gm[s].v[k] = 1.0f;
-            }
-        }
         if (a.h)
 #pragma unroll
-            for (int s = 0; s < U; ++s)
-                if ((s * L + t) * kV < g.C) store_cols<XT>((XT *)a.h + row * g.xs, (s * L + t) * kV, g.C, h[s]);
+            for (int s = 0; s < U; ++s) store_step<XT, L, U>((XT *)a.h + row * g.xs, s, t, g.C, h[s]);
     }
-    float sum = 0.0f;
-    uint32_t most = 0;
+    float sum = 0.0f, top = 0.0f;
 #pragma unroll
-    for (int s = 0; s < U; ++s) take<XT, NORM>(h[s], gm[s], sum, most);
+    for (int s = 0; s < U; ++s) take<XT, NORM>(h[s], gm[s], sum, top);
+    uint32_t most = bits_of(top);
     reduce_row<L>(sum, most, red, 0);
     const float rstd = NORM ? rms_factor(sum, g) : 1.0f;
     const Coder code(most);
+    // gamma is read again, from the nearest cache, where holding it would cost
+    // a wave's place on the unit
+    if constexpr (NORM && U > 4) {
+        asm volatile("" ::: "memory");
+        load_gamma<L, U>(gm, a.gamma, t, g.C);
+    }
+    if constexpr (NORM)
+        if (a.y)
 #pragma unroll
-    for (int s = 0; s < U; ++s) give<XT, YT, NORM>(g, a, row, (s * L + t) * kV, h[s], gm[s], rstd, code);
+            for (int s = 0; s < U; ++s)
+                store_step<YT, L, U>((YT *)a.y + row * g.ys, s, t, g.C, normed<XT, YT>(h[s], gm[s], rstd));
+    if (!NORM || a.codes)
+#pragma unroll
+        for (int s = 0; s < U; ++s) {
+            const int c = (s * L + t) * kV;
+            if (s < full_steps<L, U>() || c < g.stride) store_codes(a.codes + row * g.stride + c, coded<XT, NORM>(h[s], gm[s], code));
+        }
     if (t == 0) give_row<NORM>(a, row, rstd, code);
 }
 
@@ -136,17 +136,17 @@ __global__ __launch_bounds__(1024) void k_long_row(RowsGeo g, RmsPtrs a, int blo
             }
         }
     };
-    float sum = 0.0f;
-    uint32_t most = 0;
+    float sum = 0.0f, top = 0.0f;
     for (int c = threadIdx.x * kV; c < g.stride; c += L * kV) {
         Vec<XT, kV> h;
         Vec<float, kV> gm;
         fetch(c, false, h, gm);
         if (NORM && a.h && c < g.C) store_cols<XT>((XT *)a.h + row * g.xs, c, g.C, h);
         float part = 0.0f;
-        take<XT, NORM>(h, gm, part, most);
+        take<XT, NORM>(h, gm, part, top);
         sum += part;
     }
+    uint32_t most = bits_of(top);
     reduce_row<L>(sum, most, red, 0);
     const float rstd = NORM ? rms_factor(sum, g) : 1.0f;
     const Coder code(most);
@@ -154,7 +154,9 @@ __global__ __launch_bounds__(1024) void k_long_row(RowsGeo g, RmsPtrs a, int blo
         Vec<XT, kV> h;
         Vec<float, kV> gm;
         fetch(c, true, h, gm);
-        give<XT, YT, NORM>(g, a, row, c, h, gm, rstd, code);
+        if constexpr (NORM)
+            if (a.y && c < g.C) store_cols<YT>((YT *)a.y + row * g.ys, c, g.C, normed<XT, YT>(h, gm, rstd));
+        if (!NORM || a.codes) store_codes(a.codes + row * g.stride + c, coded<XT, NORM>(h, gm, code));
     }
     if (threadIdx.x == 0) give_row<NORM>(a, row, rstd, code);
 }
@@ -169,11 +171,21 @@ void run_rows(const RowsGeo &g, const RmsPtrs &p, hipStream_t st) {
         switch (g.s.unroll) {
             case 1: return go(k_row<XT, YT, 64, 1, NORM>, 256);
             case 2: return go(k_row<XT, YT, 64, 2, NORM>, 256);
+            case 3: return go(k_row<XT, YT, 64, 3, NORM>, 256);
             case 4: return go(k_row<XT, YT, 64, 4, NORM>, 256);
+            case 5: return go(k_row<XT, YT, 64, 5, NORM>, 256);
+            case 6: return go(k_row<XT, YT, 64, 6, NORM>, 256);
             default: return go(k_row<XT, YT, 64, 8, NORM>, 256);
         }
     }
-    if (g.s.lanes == 256) return g.s.unroll == 4 ? go(k_row<XT, YT, 256, 4, NORM>, 256) : go(k_row<XT, YT, 256, 8, NORM>, 256);
+    if (g.s.lanes == 256) {
+        switch (g.s.unroll) {
+            case 3: return go(k_row<XT, YT, 256, 3, NORM>, 256);
+            case 4: return go(k_row<XT, YT, 256, 4, NORM>, 256);
+            case 5: return go(k_row<XT, YT, 256, 5, NORM>, 256);
+            default: return go(k_row<XT, YT, 256, 8, NORM>, 256);
+        }
+    }
     if (g.s.lanes == 1024) return go(k_row<XT, YT, 1024, 4, NORM>, 1024);
     go(k_long_row<XT, YT, NORM>, 1024);
 }

@@ -63,9 +63,28 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return max(r32[0], r32[1]);
 }
 
-// The bits of |v|: as whole numbers they order as the magnitudes do, infinities
-// above all finite ones and NaN above those.
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ int wave_add(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, kDppXor1, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, kDppXor2, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, kDppXor7, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, kDppXor8, 0xf, 0xf, true);
+    const auto r16 = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = (int)r16[0] + (int)r16[1];
+    const auto r32 = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (int)r32[0] + (int)r32[1];
+}
+
+// The larger magnitude of m >= 0 and v; a NaN stays.
+__device__ __forceinline__ float larger(float m, float v) { return __builtin_elementwise_maximum(m, __builtin_fabsf(v)); }
+__device__ __forceinline__ float largest(const float (&v)[kV]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) m = larger(m, v[k]);
+    return m;
+}
+// Its bits: as whole numbers they order as magnitudes do, infinities above all
+// finite ones and NaN above those.
+__device__ __forceinline__ uint32_t bits_of(float m) { return __float_as_uint(m) & 0x7fffffffu; }
 constexpr uint32_t kInfBits = 0x7f800000u;
 
 // How values of largest magnitude `a` (its bits) become codes: code = rint((x up) f).
@@ -81,10 +100,16 @@ struct Coder {
         scale = bad ? __uint_as_float(0x7fc00000u) : a / 127.0f;
     }
     // |(x up) f| <= 127 (1 + 2^-24)^2 < 127.5, so its nearest whole number is a code
-    __device__ __forceinline__ float raw(float x) const { return x * up * f + kRoundMagic; }
     __device__ __forceinline__ uint64_t pack(const float (&x)[kV]) const {
-        const uint32_t lo = pack4(raw(x[0]), raw(x[1]), raw(x[2]), raw(x[3]));
-        const uint32_t hi = pack4(raw(x[4]), raw(x[5]), raw(x[6]), raw(x[7]));
+        float t[kV];
+#pragma unroll
+        for (int k = 0; k < kV; ++k) t[k] = x[k];
+        if (__builtin_expect(__any(up != 1.0f), 0))  // times one is left out
+#pragma unroll
+            for (int k = 0; k < kV; ++k) t[k] *= up;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) t[k] = t[k] * f + kRoundMagic;
+        const uint32_t lo = pack4(t[0], t[1], t[2], t[3]), hi = pack4(t[4], t[5], t[6], t[7]);
         return bad ? 0 : (uint64_t)hi << 32 | lo;
     }
 };
@@ -116,11 +141,36 @@ __device__ __forceinline__ void reduce_row(float &sum, uint32_t &most, float *re
     }
 }
 
-// f(lanes, unroll) for the shape, both as constants.
+// Steps of a row held by L threads in U steps that lie in it whole, by the widths
+// that the plan gives that shape: the others alone look for the row's end.
 template <int L, int U>
-struct RowConst {
-    static constexpr int lanes = L, unroll = U;
-};
+constexpr int full_steps() {
+    return L == 1024 ? 2 : U == 8 ? (L == 64 ? 6 : 5) : U - 1;
+}
+
+template <typename T, int L, int U>
+__device__ __forceinline__ void load_row(Vec<T, kV> (&v)[U], const T *row, int t, int C) {
+#pragma unroll
+    for (int s = 0; s < U; ++s)
+        v[s] = s < full_steps<L, U>() ? load_vec<T, kV>(row + (s * L + t) * kV) : load_cols<T>(row, (s * L + t) * kV, C);
+}
+
+template <int L, int U>
+__device__ __forceinline__ void load_gamma(Vec<float, kV> (&v)[U], const float *gamma, int t, int C) {
+    if (gamma) return load_row<float, L, U>(v, gamma, t, C);
+#pragma unroll
+    for (int s = 0; s < U; ++s)
+#pragma unroll
+        for (int k = 0; k < kV; ++k) v[s].v[k] = 1.0f;
+}
+
+// Columns c of step s, which lies in the row whole or may pass its end.
+template <typename T, int L, int U>
+__device__ __forceinline__ void store_step(T *row, int s, int t, int C, const Vec<T, kV> &v) {
+    const int c = (s * L + t) * kV;
+    if (s < full_steps<L, U>()) store_vec<T, kV>(row + c, v);
+    else if (c < C) store_cols<T>(row, c, C, v);
+}
 
 }  // namespace
 }  // namespace wq8

@@ -10,10 +10,10 @@ namespace wq8 {
 constexpr int code_stride(int columns) { return (columns + 127) / 128 * 128; }
 
 // ------------------------------------------------------- rows held in registers
-// A row is held by `lanes` threads, V columns of each in `steps` steps; a block
+// A row is held by `lanes` threads, 8 columns of each in `unroll` steps; a block
 // has `per` rows. lanes = 0: longer rows, read twice by 1024 threads.
 struct RowShape {
-    int lanes, unroll, steps, per;
+    int lanes, unroll, per;
 };
 
 struct RowsGeo {
@@ -46,7 +46,7 @@ wq8_status launch_unpack(const RowsGeo &g, wq8_dtype xdt, const int8_t *codes, c
 constexpr int kQ8MaxSteps = 512;
 
 struct Q8Shape {
-    int tile;      // index into kQ8Tiles, -1: the kernel for a few rows
+    int tile;      // index into kQ8Tiles, -1: the kernel for up to 4 rows
     int splits, ksteps;
 };
 
@@ -58,9 +58,9 @@ struct Q8Geo {
     int r_planar, pixels;
     int planes;               // 8-bit digits of dz's products
     Q8Shape f, dx, dw;        // dx and dw share a tile: they run in one kernel
-    int few_rows, few_waves, few_cols;  // forward of a few rows: tiles of 16 rows, waves along k, columns of a block
     int chunk, nchunk;        // backward: rows per block of the first pass, blocks along the rows
     int ncol;                 // and along the columns
+    int strip;                // second pass: tiles of 128 rows that a block goes through
 };
 
 struct Q8Ptrs {
@@ -73,7 +73,7 @@ struct Q8Ptrs {
     void *partial, *partial_dx, *partial_dw;  // workspace: split products
     int8_t *xt, *wt;          // workspace: xq [K][Mp] and wq [K][Np] transposed
     int8_t *ur, *uc;          // workspace: digits of dz sw [planes][M][Np] and of dz sx [planes][N][Mp]
-    float *rowmax, *colmax, *colsum;  // workspace: [M][ncol], [nchunk][N], [nchunk][N]
+    float *rowmax, *colmax, *colsum;  // workspace: [ncol][M], [nchunk][Np], [nchunk][Np]
     float *rscale, *cscale;   // workspace: [M], [N]
 };
 
@@ -83,8 +83,9 @@ struct Q8Tile {
     int bm, bn, blocks;
     double rate;
 };
-constexpr Q8Tile kQ8Tiles[] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.8}, {128, 64, 3, 0.62}, {64, 64, 5, 0.45}};
-constexpr int kQ8TileCount = 4;
+constexpr Q8Tile kQ8Tiles[] = {
+    {256, 256, 1, 1.0}, {128, 128, 2, 0.8}, {128, 64, 3, 0.62}, {64, 64, 5, 0.45}, {16, 128, 4, 0.3}};
+constexpr int kQ8TileCount = 5;
 
 wq8_status launch_q8_forward(const Q8Geo &g, wq8_dtype ydt, const Q8Ptrs &p, void *stream);
 wq8_status launch_q8_backward(const Q8Geo &g, wq8_dtype xdt, wq8_dtype ydt, const Q8Ptrs &p, void *stream);

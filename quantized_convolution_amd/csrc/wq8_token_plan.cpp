@@ -65,26 +65,23 @@ wq8_status check_rows(int64_t rows, int C, int x_stride, int y_stride, int64_t m
 // How a row of C columns is held: by as few threads as hold it in registers.
 RowShape forward_shape(int C) {
     const int stride = code_stride(C);
-    if (C < 8) return {0, 0, 0, 1};
-    if (stride <= 512) return {64, 1, 0, 4};
-    if (stride <= 1024) return {64, 2, 0, 4};
-    if (stride <= 2048) return {64, 4, 0, 4};
-    if (stride <= 4096) return {64, 8, 0, 4};
-    if (stride <= 8192) return {256, 4, 0, 1};
-    if (stride <= 16384) return {256, 8, 0, 1};
-    if (stride <= 32768) return {1024, 4, 0, 1};
-    return {0, 0, 0, 1};
+    if (C < 8) return {0, 0, 1};
+    for (int steps : {1, 2, 3, 4, 5, 6, 8})
+        if (stride <= 512 * steps) return {64, steps, 4};
+    for (int steps : {3, 4, 5, 8})
+        if (stride <= 2048 * steps) return {256, steps, 1};
+    if (stride <= 32768) return {1024, 4, 1};
+    return {0, 0, 1};
 }
 
 RowShape backward_shape(int C) {
     const int stride = code_stride(C);
-    if (C < 8) return {0, 0, 0, 1};
-    if (stride <= 512) return {64, 1, 0, 4};
-    if (stride <= 1024) return {64, 2, 0, 4};
-    if (stride <= 2048) return {256, 1, 0, 1};
-    if (stride <= 4096) return {256, 2, 0, 1};
-    if (stride <= 8192) return {512, 2, 0, 1};
-    return {0, 0, 0, 1};
+    if (C < 8) return {0, 0, 1};
+    for (int steps : {1, 2, 3, 4})
+        if (stride <= 512 * steps) return {64, steps, 4};
+    if (stride <= 4096) return {256, 2, 1};
+    if (stride <= 8192) return {512, 2, 1};
+    return {0, 0, 1};
 }
 
 void set_rows(RowsGeo &g, int64_t rows, int C, int64_t xs, int64_t ys) {
@@ -140,7 +137,7 @@ struct Product {
 void choose_q8(const Product *q, int count, int planes, Q8Shape *const *out) {
     constexpr int kMost = 16;
     double least = 1e30;
-    for (int i = planes > 1 ? 1 : 0; i < kQ8TileCount; ++i) {
+    for (int i = planes > 1 ? 1 : 0; i < (planes > 1 ? 4 : kQ8TileCount); ++i) {
         const Q8Tile &g = kQ8Tiles[i];
         const double rate = 9.5 * g.rate;  // M operations per us and compute unit
         const double step = 2e-6 * g.bm * g.bn * 128 * planes / rate;
@@ -201,12 +198,9 @@ wq8_status build_q8linear(const wq8_q8linear_desc *d, wq8_q8linear_plan *p) {
     p->xdt = d->x_dtype;
     p->ydt = d->y_dtype;
     g.planes = p->xdt == WQ8_BF16 ? 2 : 4;
-    // Up to 64 rows the weights are streamed past LDS.
     const int64_t steps = g.Kp / 128;
-    if (g.M <= 64 && steps <= kQ8MaxSteps) {
+    if (g.M <= 4 && steps <= kQ8MaxSteps) {
         g.f = {-1, 1, (int)steps};
-        g.few_rows = g.M <= 16 ? 1 : g.M <= 32 ? 2 : 4;
-        g.few_waves = steps > 8 ? 8 : 4;
     } else {
         const Product f = {g.M, g.N, steps};
         Q8Shape *const fs[1] = {&g.f};
@@ -220,8 +214,11 @@ wq8_status build_q8linear(const wq8_q8linear_desc *d, wq8_q8linear_plan *p) {
     g.chunk = 128;
     while (g.chunk > 8 && ceil_div(g.M, g.chunk) * g.ncol < 4 * kCus) g.chunk /= 2;
     g.nchunk = (int)ceil_div(g.M, g.chunk);
+    // tiles per block of the second: about four blocks a compute unit
+    g.strip = (int)(((int64_t)(g.Mp / 128) * (g.Np / 64) + 4 * kCus - 1) / (4 * kCus));
+    if (g.strip < 1) g.strip = 1;
     const auto tiles = [](const Q8Shape &s, int64_t M, int64_t N) {
-        return s.tile < 0 ? ceil_div(N, 32) : ceil_div(M, kQ8Tiles[s.tile].bm) * ceil_div(N, kQ8Tiles[s.tile].bn) * s.splits;
+        return s.tile < 0 ? ceil_div(N, 8) : ceil_div(M, kQ8Tiles[s.tile].bm) * ceil_div(N, kQ8Tiles[s.tile].bn) * s.splits;
     };
     const int64_t lim = (int64_t)1 << 31;
     const int64_t lines = (int64_t)(g.Mp / 128) * (g.Kp / 128) + (int64_t)(g.Np / 128) * (g.Kp / 128);
@@ -245,8 +242,8 @@ wq8_status build_q8linear(const wq8_q8linear_desc *d, wq8_q8linear_plan *p) {
     p->off_ur = take((size_t)g.planes * M * g.Np);
     p->off_uc = take((size_t)g.planes * N * g.Mp);
     p->off_rowmax = take(M * g.ncol * 4);
-    p->off_colmax = take((size_t)g.nchunk * N * 4);
-    p->off_colsum = take((size_t)g.nchunk * N * 4);
+    p->off_colmax = take((size_t)g.nchunk * g.Np * 4);
+    p->off_colsum = take((size_t)g.nchunk * g.Np * 4);
     p->off_rscale = take(M * 4);
     p->off_cscale = take(N * 4);
     p->b_bytes = g.M ? at : 0;
