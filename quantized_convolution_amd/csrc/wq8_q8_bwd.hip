@@ -23,7 +23,8 @@ constexpr int planes_of() { return sizeof(T) == 2 ? 2 : 4; }
 
 enum { kZNone, kZValues, kZCodes };  // what the forward kept of z
 
-// dz of 8 columns of a row, zeros past the last column.
+// dz of 8 columns of a row, zeros past the last column (a group of z's codes that
+// stands for NaN has columns before it as well, and makes the row's products NaN).
 template <typename YT, int ZF, int ACT, bool EXACT>
 __device__ __forceinline__ void dz_of(const Q8Geo &g, const Q8Ptrs &a, int64_t row, int c, float (&dz)[kV]) {
     const Vec<YT, kV> dy = load_any<YT>((const YT *)a.dy + row * g.ys, c, g.N);
@@ -43,23 +44,21 @@ __device__ __forceinline__ void dz_of(const Q8Geo &g, const Q8Ptrs &a, int64_t r
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
         dz[k] = to_f32(dy.v[k]);
-        if constexpr (ACT != WQ8_ACT_NONE) {
-            // past the end z may be anything: a slope of NaN times the zero there
-            const float v = dz[k] * act_slope<ACT, EXACT>(z[k]);
-            dz[k] = c + k < g.N ? v : 0.0f;
-        }
+        if constexpr (ACT != WQ8_ACT_NONE) dz[k] *= act_slope<ACT, EXACT>(z[k]);
     }
 }
 
 // ------------------------------------------------------------------ first pass
 // 64 lanes x 8 columns of `chunk` rows, a wave each: the largest |dz sw| of every
 // row, the largest |dz sx| and the sum of dz of every column.
+// Eight waves a block: the second pass reads what each block has found.
 constexpr int kMaxCols = 64 * kV;
 constexpr int kMaxRows = 2;  // rows of a wave whose loads are in flight together
+constexpr int kMaxWaves = 8;
 
 template <typename XT, typename YT, int ZF>
 __device__ __forceinline__ void max_block(const Q8Geo &g, const Q8Ptrs &a, int b) {
-    __shared__ float red[3][2][kMaxCols];
+    __shared__ float red[kMaxWaves - 1][2][kMaxCols];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int chunk = b / g.ncol, col = b - chunk * g.ncol;
     const int c = col * kMaxCols + lane * kV;
@@ -69,17 +68,17 @@ __device__ __forceinline__ void max_block(const Q8Geo &g, const Q8Ptrs &a, int b
     with_act(g.act, [&](auto act) {
         constexpr int A = decltype(act)::value;
         if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
-            for (int r = r0 + wave; r < r1; r += 4 * kMaxRows) {
+            for (int r = r0 + wave; r < r1; r += kMaxWaves * kMaxRows) {
                 float dz[kMaxRows][kV], sx[kMaxRows];
 #pragma unroll
                 for (int i = 0; i < kMaxRows; ++i) {
-                    const int row = min(r + 4 * i, r1 - 1);
+                    const int row = min(r + kMaxWaves * i, r1 - 1);
                     dz_of<YT, ZF, A, exact_acts<XT, YT>()>(g, a, row, c, dz[i]);
                     sx[i] = a.sx[row];
                 }
 #pragma unroll
                 for (int i = 0; i < kMaxRows; ++i)
-                    if (r + 4 * i < r1) {
+                    if (r + kMaxWaves * i < r1) {
                         float m = 0.0f;
 #pragma unroll
                         for (int k = 0; k < kV; ++k) {
@@ -88,7 +87,7 @@ __device__ __forceinline__ void max_block(const Q8Geo &g, const Q8Ptrs &a, int b
                             sum[k] += dz[i][k];
                         }
                         const uint32_t top = wave_max(bits_of(m));
-                        if (lane == 0) a.rowmax[(int64_t)col * g.M + r + 4 * i] = __uint_as_float(top);
+                        if (lane == 0) a.rowmax[(int64_t)col * g.M + r + kMaxWaves * i] = __uint_as_float(top);
                     }
             }
     });
@@ -103,8 +102,13 @@ __device__ __forceinline__ void max_block(const Q8Geo &g, const Q8Ptrs &a, int b
     Vec<float, kV> m, s;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-        m.v[k] = larger(larger(larger(most[k], red[0][0][k * 64 + lane]), red[1][0][k * 64 + lane]), red[2][0][k * 64 + lane]);
-        s.v[k] = (sum[k] + red[0][1][k * 64 + lane]) + (red[1][1][k * 64 + lane] + red[2][1][k * 64 + lane]);
+        m.v[k] = most[k];
+        s.v[k] = sum[k];
+#pragma unroll
+        for (int w = 0; w < kMaxWaves - 1; ++w) {
+            m.v[k] = larger(m.v[k], red[w][0][k * 64 + lane]);
+            s.v[k] += red[w][1][k * 64 + lane];
+        }
     }
     store_vec<float, kV>(a.colmax + (int64_t)chunk * g.Np + c, m);
     store_vec<float, kV>(a.colsum + (int64_t)chunk * g.Np + c, s);
@@ -125,35 +129,35 @@ __device__ __forceinline__ void bytes_of(const uint32_t (&q)[4], uint32_t (&out)
 }
 
 // A matrix of codes [rows][ld] transposed to [cols][tld], zeros behind its last
-// row: 128 x 128 codes a block. A thread has 4 rows of 16 columns.
+// row: 128 x 128 codes a block. A thread has 4 rows of 8 columns.
 __device__ __forceinline__ void transpose_block(const int8_t *x, int64_t rows, int cols, int64_t ld, int8_t *t, int64_t tld, int b) {
     constexpr int LD = 128 + 4;  // bytes between columns in LDS
     __shared__ __align__(16) int8_t tile[128 * LD];
     const int across = (int)(ld / 128);
     const int64_t r0 = (int64_t)(b / across) * 128;
     const int c0 = (b - b / across * across) * 128;
-    const int rg = threadIdx.x >> 3, cg = threadIdx.x & 7;
-    uint32_t v[4][4];
+    const int rg = threadIdx.x >> 4, cg = threadIdx.x & 15;
+    uint32_t v[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t r = r0 + rg * 4 + i;
-        const v4i q = *(const v4i *)(x + min(r, rows - 1) * ld + c0 + cg * 16);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) v[i][d] = r < rows ? (uint32_t)q[d] : 0u;
+        const uint64_t q = *(const uint64_t *)(x + min(r, rows - 1) * ld + c0 + cg * 8);
+        v[i][0] = r < rows ? (uint32_t)q : 0u;
+        v[i][1] = r < rows ? (uint32_t)(q >> 32) : 0u;
     }
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
+    for (int d = 0; d < 2; ++d) {
         const uint32_t rows4[4] = {v[0][d], v[1][d], v[2][d], v[3][d]};
         uint32_t o[4];
         bytes_of<4>(rows4, o);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) *(uint32_t *)(tile + (cg * 16 + d * 4 + e) * LD + rg * 4) = o[3 - e];
+        for (int e = 0; e < 4; ++e) *(uint32_t *)(tile + (cg * 8 + d * 4 + e) * LD + rg * 4) = o[3 - e];
     }
     __syncthreads();
     // a wave writes 8 columns' lines of 128 bytes at a time, 16 bytes a lane
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int col = i * 32 + (threadIdx.x >> 3), part = (threadIdx.x & 7) * 16;
+    for (int i = 0; i < 2; ++i) {
+        const int col = i * 64 + (threadIdx.x >> 3), part = (threadIdx.x & 7) * 16;
         v4i o;
 #pragma unroll
         for (int d = 0; d < 4; ++d) o[d] = *(const int *)(tile + col * LD + part + d * 4);
@@ -163,7 +167,7 @@ __device__ __forceinline__ void transpose_block(const int8_t *x, int64_t rows, i
 
 // Blocks [0, nm): largest magnitudes; then nx of xq's transposition and the rest of wq's.
 template <typename XT, typename YT, int ZF>
-__global__ __launch_bounds__(256) void k_q8_max(Q8Geo g, Q8Ptrs a, int nm, int nx, int nb) {
+__global__ __launch_bounds__(kMaxWaves * 64) void k_q8_max(Q8Geo g, Q8Ptrs a, int nm, int nx, int nb) {
     int b;
     if (!block_number(nb, b)) return;
     if (b < nm) max_block<XT, YT, ZF>(g, a, b);
@@ -202,109 +206,103 @@ struct Digits {
     }
 };
 
-// 64 columns of a strip of tiles of 128 rows: a thread has 4 rows of 8 columns. The
-// columns' largest magnitudes, of all the first pass's chunks, are found once a strip.
+// 128 rows x 64 columns: a thread has 4 rows of 8 columns.
 template <typename XT, typename YT, int ZF, int PLANES>
 __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_dx, int want_dw, int nb) {
-    constexpr int LD = 128 + 8;  // bytes between columns in LDS
+    constexpr int LD = 128 + 4;  // bytes between columns in LDS: a wave's stores meet every bank twice
     __shared__ __align__(16) int8_t tile[PLANES * 64 * LD];
     __shared__ float cpart[16][64];
     __shared__ uint32_t cmax[64], rmax[128];
     int b;
     if (!block_number(nb, b)) return;
-    const int across = g.Np / 64, strip = b / across, c0 = (b - strip * across) * 64;
-    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;
-    if (want_dw) {  // 4 columns a thread, 16 threads along the chunks
-        const int c = (threadIdx.x & 15) * 4, q = threadIdx.x >> 4;
+    const int across = g.Np / 64, br = b / across, r0 = br * 128, c0 = (b - br * across) * 64;
+    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3, c = c0 + cg * kV;
+    float dz[4][kV];
+    with_act(g.act, [&](auto act) {
+        constexpr int A = decltype(act)::value;
+        if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                dz_of<YT, ZF, A, exact_acts<XT, YT>()>(g, a, min(r0 + rg * 4 + i, g.M - 1), c, dz[i]);
+    });
+    if (want_dw) {  // 4 columns a thread, 16 threads along the first pass's chunks
+        const int c4 = (threadIdx.x & 15) * 4, q = threadIdx.x >> 4;
         Vec<float, 4> m = {};
 #pragma unroll 8
         for (int i = q; i < g.nchunk; i += 16) {
-            const Vec<float, 4> v = load_vec<float, 4>(a.colmax + (int64_t)i * g.Np + c0 + c);
+            const Vec<float, 4> v = load_vec<float, 4>(a.colmax + (int64_t)i * g.Np + c0 + c4);
 #pragma unroll
             for (int k = 0; k < 4; ++k) m.v[k] = larger(m.v[k], v.v[k]);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) cpart[q][c + k] = m.v[k];
-        __syncthreads();
-        if (threadIdx.x < 64) {
-            float t = 0.0f;
+        for (int k = 0; k < 4; ++k) cpart[q][c4 + k] = m.v[k];
+    }
+    if (want_dx && threadIdx.x < 128) {
+        const int r = min(r0 + (int)threadIdx.x, g.M - 1);
+        float m = 0.0f;
+        for (int i = 0; i < g.ncol; ++i) m = larger(m, a.rowmax[(int64_t)i * g.M + r]);
+        rmax[threadIdx.x] = bits_of(m);
+        if (c0 == 0 && r0 + (int)threadIdx.x < g.M) a.rscale[r] = Digits<PLANES>::scale(bits_of(m));
+    }
+    __syncthreads();
+    if (want_dw && threadIdx.x < 64) {
+        float t = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) t = larger(t, cpart[i][threadIdx.x]);
-            cmax[threadIdx.x] = bits_of(t);
-            if (strip == 0 && c0 + (int)threadIdx.x < g.N) a.cscale[c0 + threadIdx.x] = Digits<PLANES>::scale(bits_of(t));
+        for (int i = 0; i < 16; ++i) t = larger(t, cpart[i][threadIdx.x]);
+        cmax[threadIdx.x] = bits_of(t);
+        if (br == 0 && c0 + (int)threadIdx.x < g.N) a.cscale[c0 + threadIdx.x] = Digits<PLANES>::scale(bits_of(t));
+    }
+    if (want_dx) {
+        const Vec<float, kV> sw = load_any<float>(a.sw, c, g.N);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + rg * 4 + i;
+            const Digits<PLANES> d(rmax[rg * 4 + i]);
+            float u[kV];
+#pragma unroll
+            for (int k = 0; k < kV; ++k) u[k] = dz[i][k] * sw.v[k];
+            if (__builtin_expect(__any(d.up != 1.0f), 0))
+#pragma unroll
+                for (int k = 0; k < kV; ++k) u[k] *= d.up;
+            uint32_t lo[PLANES], hi[PLANES];
+            bytes_of<PLANES>({d(u[0]), d(u[1]), d(u[2]), d(u[3])}, lo);
+            bytes_of<PLANES>({d(u[4]), d(u[5]), d(u[6]), d(u[7])}, hi);
+            Digits<PLANES>::lower(lo);
+            Digits<PLANES>::lower(hi);
+            if (r < g.M)
+#pragma unroll
+                for (int p = 0; p < PLANES; ++p)
+                    *(uint64_t *)(a.ur + ((int64_t)p * g.M + r) * g.Np + c) = (uint64_t)hi[p] << 32 | lo[p];
         }
     }
-    const int c = c0 + cg * kV, t1 = min((strip + 1) * g.strip, g.Mp / 128);
-    const Vec<float, kV> sw = load_any<float>(a.sw, c, g.N);
-    for (int t = strip * g.strip; t < t1; ++t) {
-        const int r0 = t * 128;
-        float dz[4][kV];
-        with_act(g.act, [&](auto act) {
-            constexpr int A = decltype(act)::value;
-            if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
+    if (!want_dw) return;
+    __syncthreads();
+    float sx[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    dz_of<YT, ZF, A, exact_acts<XT, YT>()>(g, a, min(r0 + rg * 4 + i, g.M - 1), c, dz[i]);
-        });
-        if (want_dx && threadIdx.x < 128) {
-            const int r = min(r0 + (int)threadIdx.x, g.M - 1);
-            float m = 0.0f;
-            for (int i = 0; i < g.ncol; ++i) m = larger(m, a.rowmax[(int64_t)i * g.M + r]);
-            rmax[threadIdx.x] = bits_of(m);
-            if (c0 == 0 && r0 + (int)threadIdx.x < g.M) a.rscale[r] = Digits<PLANES>::scale(bits_of(m));
-        }
-        __syncthreads();
-        if (want_dx)
+    for (int i = 0; i < 4; ++i) sx[i] = r0 + rg * 4 + i < g.M ? a.sx[r0 + rg * 4 + i] : 0.0f;  // past the end dz is the last row's
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = r0 + rg * 4 + i;
-                const Digits<PLANES> d(rmax[rg * 4 + i]);
-                float u[kV];
+    for (int k = 0; k < kV; ++k) {
+        const Digits<PLANES> d(cmax[cg * kV + k]);
+        float u[4];
 #pragma unroll
-                for (int k = 0; k < kV; ++k) u[k] = dz[i][k] * sw.v[k];
-                if (__builtin_expect(__any(d.up != 1.0f), 0))
+        for (int i = 0; i < 4; ++i) u[i] = dz[i][k] * sx[i];
+        if (__builtin_expect(__any(d.up != 1.0f), 0))
 #pragma unroll
-                    for (int k = 0; k < kV; ++k) u[k] *= d.up;
-                uint32_t lo[PLANES], hi[PLANES];
-                bytes_of<PLANES>({d(u[0]), d(u[1]), d(u[2]), d(u[3])}, lo);
-                bytes_of<PLANES>({d(u[4]), d(u[5]), d(u[6]), d(u[7])}, hi);
-                Digits<PLANES>::lower(lo);
-                Digits<PLANES>::lower(hi);
-                if (r < g.M)
+            for (int i = 0; i < 4; ++i) u[i] *= d.up;
+        uint32_t o[PLANES];
+        bytes_of<PLANES>({d(u[0]), d(u[1]), d(u[2]), d(u[3])}, o);
+        Digits<PLANES>::lower(o);
 #pragma unroll
-                    for (int p = 0; p < PLANES; ++p)
-                        *(uint64_t *)(a.ur + ((int64_t)p * g.M + r) * g.Np + c) = (uint64_t)hi[p] << 32 | lo[p];
-            }
-        if (want_dw) {
-            float sx[4];
+        for (int p = 0; p < PLANES; ++p) *(uint32_t *)(tile + (p * 64 + cg * kV + k) * LD + rg * 4) = o[p];
+    }
+    __syncthreads();
+    // 8 bytes a lane, 16 lanes a line
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sx[i] = a.sx[min(r0 + rg * 4 + i, g.M - 1)];
-#pragma unroll
-            for (int k = 0; k < kV; ++k) {
-                const Digits<PLANES> d(cmax[cg * kV + k]);
-                float u[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) u[i] = r0 + rg * 4 + i < g.M ? dz[i][k] * sx[i] : 0.0f;
-                if (__builtin_expect(__any(d.up != 1.0f), 0))
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) u[i] *= d.up;
-                uint32_t o[PLANES];
-                bytes_of<PLANES>({d(u[0]), d(u[1]), d(u[2]), d(u[3])}, o);
-                Digits<PLANES>::lower(o);
-#pragma unroll
-                for (int p = 0; p < PLANES; ++p) *(uint32_t *)(tile + (p * 64 + cg * kV + k) * LD + rg * 4) = o[p];
-            }
-            __syncthreads();
-            // 8 bytes a lane, 16 lanes a line
-#pragma unroll
-            for (int i = 0; i < PLANES * 4; ++i) {
-                const int line = i * 16 + (threadIdx.x >> 4), p = line / 64, col = line % 64, part = (threadIdx.x & 15) * 8;
-                if (c0 + col < g.N)
-                    *(uint64_t *)(a.uc + ((int64_t)p * g.N + c0 + col) * g.Mp + r0 + part) =
-                        *(const uint64_t *)(tile + line * LD + part);
-            }
-        }
-        if (t + 1 < t1) __syncthreads();  // the tile and the rows' magnitudes are read
+    for (int i = 0; i < PLANES * 4; ++i) {
+        const int line = i * 16 + (threadIdx.x >> 4), p = line / 64, col = line % 64, part = (threadIdx.x & 15) * 8;
+        const uint32_t *const from = (const uint32_t *)(tile + line * LD + part);
+        if (c0 + col < g.N)
+            *(uint64_t *)(a.uc + ((int64_t)p * g.N + c0 + col) * g.Mp + r0 + part) = (uint64_t)from[1] << 32 | from[0];
     }
 }
 
@@ -434,10 +432,10 @@ void prepare(const Q8Geo &g, const Q8Ptrs &p, hipStream_t st) {
     constexpr int PLANES = planes_of<XT>();
     const auto tiles = [](int64_t rows, int64_t bytes) { return (rows + 127) / 128 * (bytes / 128); };
     const int64_t nm = (int64_t)g.nchunk * g.ncol, nx = p.dw ? tiles(g.M, g.Kp) : 0, nw = p.dx ? tiles(g.N, g.Kp) : 0;
-    hipLaunchKernelGGL((k_q8_max<XT, YT, ZF>), grid_of(nm + nx + nw), dim3(256), 0, st, g, p, (int)nm, (int)nx,
+    hipLaunchKernelGGL((k_q8_max<XT, YT, ZF>), grid_of(nm + nx + nw), dim3(kMaxWaves * 64), 0, st, g, p, (int)nm, (int)nx,
                        (int)(nm + nx + nw));
     if (!p.dx && !p.dw) return;
-    const int64_t nd = (int64_t)((g.Mp / 128 + g.strip - 1) / g.strip) * (g.Np / 64);
+    const int64_t nd = (int64_t)(g.Mp / 128) * (g.Np / 64);
     hipLaunchKernelGGL((k_q8_digits<XT, YT, ZF, PLANES>), grid_of(nd), dim3(256), 0, st, g, p, p.dx != nullptr, p.dw != nullptr,
                        (int)nd);
 }

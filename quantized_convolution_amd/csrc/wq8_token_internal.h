@@ -60,7 +60,6 @@ struct Q8Geo {
     Q8Shape f, dx, dw;        // dx and dw share a tile: they run in one kernel
     int chunk, nchunk;        // backward: rows per block of the first pass, blocks along the rows
     int ncol;                 // and along the columns
-    int strip;                // second pass: tiles of 128 rows that a block goes through
 };
 
 struct Q8Ptrs {

@@ -209,14 +209,12 @@ wq8_status build_q8linear(const wq8_q8linear_desc *d, wq8_q8linear_plan *p) {
     const Product bwd[2] = {{g.N, g.K, g.Mp / 128}, {g.M, g.K, g.Np / 128}};
     Q8Shape *const bs[2] = {&g.dw, &g.dx};
     choose_q8(bwd, 2, g.planes, bs);
-    // rows per block of the first pass: 4 waves, more rows where blocks abound
+    // rows per block of the first pass: 8 waves of 2 rows in flight, blocks that all
+    // run at once, two a compute unit by their registers
     g.ncol = (int)ceil_div(g.N, 512);
-    g.chunk = 128;
-    while (g.chunk > 8 && ceil_div(g.M, g.chunk) * g.ncol < 4 * kCus) g.chunk /= 2;
+    g.chunk = (int)round_up(ceil_div(g.M, 2 * kCus > g.ncol ? 2 * kCus / g.ncol : 1), 16);
+    if (g.chunk < 16) g.chunk = 16;
     g.nchunk = (int)ceil_div(g.M, g.chunk);
-    // tiles per block of the second: about four blocks a compute unit
-    g.strip = (int)(((int64_t)(g.Mp / 128) * (g.Np / 64) + 4 * kCus - 1) / (4 * kCus));
-    if (g.strip < 1) g.strip = 1;
     const auto tiles = [](const Q8Shape &s, int64_t M, int64_t N) {
         return s.tile < 0 ? ceil_div(N, 8) : ceil_div(M, kQ8Tiles[s.tile].bm) * ceil_div(N, kQ8Tiles[s.tile].bn) * s.splits;
     };
