@@ -1,7 +1,8 @@
 """Build the HIP library libwino_q8_conv.so in-tree for gfx950.
 
 hipcc compiles the kernels, the host plan and the C ABI (one object per
-source, in parallel) and links them into a shared library next to this file. Numerics flags: no fp contraction (every fma
+source, in parallel) and links them into a shared library next to this file;
+g++ compiles the CPython module that checks a call's buffers. Numerics flags: no fp contraction (every fma
 is written out), IEEE fp32 division, fp32 denormals kept, no packed fp32
 instructions.
 """
@@ -19,6 +20,9 @@ SOURCES = ["wq8_kernels.hip", "wq8_hgemm.hip", "wq8_direct.hip", "wq8_noalloc.hi
            "wq8_norm_fwd_bf16_bf16.hip", "wq8_norm_bwd_f32.hip", "wq8_norm_bwd_bf16.hip", "wq8_linear_fwd_f32.hip",
            "wq8_linear_fwd_bf16.hip", "wq8_linear_bwd.hip", "wq8_ops_plan.cpp", "wq8_pack.hip", "wq8_rms_fwd.hip", "wq8_rms_bwd.hip",
            "wq8_q8_fwd.hip", "wq8_q8_bwd.hip", "wq8_token_plan.cpp"]
+# what checks the buffers of a call in front of the library: a CPython module
+BUFFERS = "wq8_buffers.cpp"
+BUFFERS_LIB = os.path.join(HERE, "_wq8_buffers.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -32,6 +36,20 @@ FLAGS = [
     "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-Wall", "-Wno-unused-function",
 ]
+
+
+def buffers_command(out: str) -> list:
+    """g++ on the CPython module, against the installed torch's headers and libraries (which importing torch has
+    loaded before it)."""
+    import sysconfig
+
+    from torch._C import _GLIBCXX_USE_CXX11_ABI as abi
+    from torch.utils import cpp_extension as c
+
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(abi)}",
+            *[a for p in c.include_paths() for a in ("-isystem", p)], f"-I{sysconfig.get_paths()['include']}",
+            os.path.join(CSRC, BUFFERS), *[f"-L{p}" for p in c.library_paths()], "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-o", out]
 
 
 def build(verbose: bool = False) -> str:
@@ -50,8 +68,19 @@ def build(verbose: bool = False) -> str:
             msgs = "\n".join(l for l in (r.stdout + r.stderr).splitlines() if noise not in l)
             return src, obj, r.returncode, msgs
 
+        def compile_buffers():
+            out = BUFFERS_LIB + ".tmp"
+            r = subprocess.run(buffers_command(out), capture_output=True, text=True)
+            if r.returncode == 0:
+                os.replace(out, BUFFERS_LIB)
+            return r.returncode, r.stdout + r.stderr
+
         with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+            module = ex.submit(compile_buffers)
             results = list(ex.map(compile_one, SOURCES))
+            rc, msgs = module.result()
+        if rc != 0:
+            raise RuntimeError(f"g++ failed on {BUFFERS} ({rc}):\n{msgs}")
         for src, _, rc, msgs in results:
             if rc != 0:
                 raise RuntimeError(f"hipcc failed on {src} ({rc}):\n{msgs}")

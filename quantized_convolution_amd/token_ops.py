@@ -17,7 +17,12 @@ import ctypes as C
 import torch
 
 from .binding import _DT, _check, load
-from .ops import ACTS, LAYOUTS, _Args, _choice, _desc, _empty, _Plan
+from .ops import ACTS, LAYOUTS, _Args, _choice, _desc, _empty, _Plan, _raw_stream
+
+try:  # built beside the library
+    from ._wq8_buffers import addresses as _addresses, form as _form
+except ImportError:  # not built yet: load() names that, when a plan is made
+    _addresses = _form = None
 
 Z_GROUP = 32  # columns that share a scale where a product's z is kept in codes
 
@@ -42,6 +47,30 @@ def code_stride(columns):
     return (columns + 127) // 128 * 128
 
 
+I8, F32 = torch.int8, torch.float32
+
+
+def _given(fn, handle, form, *buffers):
+    """Makes the call on the current stream if every buffer is given and as the
+    plan says, all on the current GPU. Else nothing is done: the checks that
+    follow name what is wrong, or make what is missing."""
+    if form is None:
+        return False
+    got = _addresses(form, *buffers)
+    if got is None or got[0] != torch._C._cuda_getDevice():
+        return False
+    st = fn(handle, *got[1:], _raw_stream(got[0]))
+    if st:
+        _check(st)
+    return True
+
+
+def _forms(*entries):
+    """The form of a call's buffers, for _given()."""
+    return _form(tuple(e if isinstance(e, int) else (e[0], tuple(e[1]), e[2], e[3]) for e in entries)) \
+        if _form and _raw_stream else None
+
+
 class QuantPlan(_Plan):
     """Rows of C values to 8-bit codes and back. group: columns that share a
     scale, 32, 64 or 128, or 0 for one scale a row (what products take).
@@ -56,6 +85,9 @@ class QuantPlan(_Plan):
         self.x_shape, self.x_strides = (rows, C), (self.x_stride, 1) if self.x_stride else None
         self.code_shape = (rows, code_stride(C))
         self.scale_shape = (rows, -(-C // group)) if group else (rows,)
+        x = (x_dtype, self.x_shape, self.x_strides, True)
+        codes = (I8, self.code_shape, None, True), (F32, self.scale_shape, None, True)
+        self._pack_form, self._unpack_form = _forms(x, *codes), _forms(*codes, x)
 
     def _make(self, desc):
         lib = load()
@@ -93,6 +125,11 @@ class RmsPlan(_Plan):
         self.x_strides = (self.x_stride, 1) if self.x_stride else None
         self.y_strides = (self.y_stride, 1) if self.y_stride else None
         self.code_shape, self.scale_shape = (rows, code_stride(C)), (rows,)
+        x, y = (lambda r: (x_dtype, self.x_shape, self.x_strides, r)), (lambda r: (y_dtype, self.y_shape, self.y_strides, r))
+        row, column = (lambda r: (F32, (rows,), None, r)), (F32, (C,), None, False)
+        self._forward_form = _forms(x(True), x(False), column, x(False), y(False), (I8, self.code_shape, None, False), row(False),
+                                    row(False), self.workspace_bytes)
+        self._backward_form = _forms(y(True), x(True), row(True), column, x(False), x(True), column, self.backward_workspace_bytes)
 
     def empty_input(self, device="cuda"):
         """A tensor of x's form (for h and dx)."""
@@ -137,6 +174,14 @@ class Q8LinearPlan(_Plan):
         self.r_strides = (self.r_stride, 1) if self.r_stride else None
         self.xq_shape, self.wq_shape = (rows, code_stride(Cin)), (Cout, code_stride(Cin))
         self.zq_shape, self.sz_shape = (rows, code_stride(Cout)), (rows, -(-Cout // Z_GROUP))
+        y = (y_dtype, self.y_shape, self.y_strides, True)
+        codes = ((I8, self.xq_shape, None, True), (F32, (rows,), None, True), (I8, self.wq_shape, None, True),
+                 (F32, (Cout,), None, True))
+        column, z = (F32, (Cout,), None, False), (y_dtype, self.y_shape, None, False)
+        zq = (I8, self.zq_shape, None, False), (F32, self.sz_shape, None, False)
+        self._forward_form = _forms(*codes, column, (y_dtype, self.r_shape, self.r_strides, False), y, z, *zq, self.workspace_bytes)
+        self._backward_form = _forms(y, *codes, z, *zq, (x_dtype, self.x_shape, self.x_strides, False),
+                                     (x_dtype, self.w_shape, None, False), column, self.backward_workspace_bytes)
 
     def empty_input(self, device="cuda"):
         """A tensor of dx's form."""
@@ -164,6 +209,8 @@ def _empty_codes(code_shape, scale_shape, device):
 
 def wq8_quant_pack(plan: QuantPlan, x, codes=None, scales=None, stream=None):
     """(codes, scales)."""
+    if stream is None and _given(plan._pack, plan._h, plan._pack_form, x, codes, scales):
+        return codes, scales
     a = _Args(stream)
     px = a.need(x, "x", plan.x_dtype, plan.x_shape, plan.x_strides)
     if codes is None:
@@ -178,6 +225,8 @@ def wq8_quant_pack(plan: QuantPlan, x, codes=None, scales=None, stream=None):
 
 def wq8_quant_unpack(plan: QuantPlan, codes, scales, x=None, stream=None):
     """x, the values that the codes stand for."""
+    if stream is None and _given(plan._unpack, plan._h, plan._unpack_form, codes, scales, x):
+        return x
     a = _Args(stream)
     pc = a.need(codes, "codes", torch.int8, plan.code_shape)
     ps = a.need(scales, "scales", torch.float32, plan.scale_shape)
@@ -193,6 +242,10 @@ def wq8_rms_forward(plan: RmsPlan, x, gamma=None, residual=None, y=None, h=None,
     """(y, h, codes, scales, rstd); what is neither given nor wanted is None. The
     stream h is made where a residual is given (it may be x or residual itself);
     without one it is x."""
+    if (stream is None and not (want_y and y is None) and not (want_codes and codes is None) and not (want_rstd and rstd is None) and
+            (h is None) == (residual is None) and
+            _given(plan._forward, plan._h, plan._forward_form, x, residual, gamma, h, y, codes, scales, rstd, workspace)):
+        return y, x if residual is None else h, codes, scales, rstd
     f32 = torch.float32
     a = _Args(stream)
     px = a.need(x, "x", plan.x_dtype, plan.x_shape, plan.x_strides)
@@ -221,6 +274,9 @@ def wq8_rms_forward(plan: RmsPlan, x, gamma=None, residual=None, y=None, h=None,
 def wq8_rms_backward(plan: RmsPlan, dy, h, rstd, gamma=None, dh=None, dx=None, dgamma=None, workspace=None, stream=None):
     """(dx, dgamma). dx, which may be dh itself, is the gradient of x and of the
     residual; dgamma is made where gamma is given."""
+    if stream is None and (dgamma is not None or gamma is None) and _given(
+            plan._backward, plan._h, plan._backward_form, dy, h, rstd, gamma, dh, dx, dgamma, workspace):
+        return dx, dgamma
     f32 = torch.float32
     a = _Args(stream)
     pdy = a.need(dy, "dy", plan.y_dtype, plan.y_shape, plan.y_strides)
@@ -242,6 +298,9 @@ def wq8_rms_backward(plan: RmsPlan, dy, h, rstd, gamma=None, dh=None, dx=None, d
 def wq8_q8linear_forward(plan: Q8LinearPlan, xq, sx, wq, sw, bias=None, residual=None, y=None, z=None, zq=None, sz=None,
                          want_z=False, want_zq=False, workspace=None, stream=None):
     """y, with want_z (y, z), with want_zq (y, zq, sz), with both (y, z, zq, sz)."""
+    if stream is None and not want_z and not want_zq and (zq is None) == (sz is None) and _given(
+            plan._forward, plan._h, plan._forward_form, xq, sx, wq, sw, bias, residual, y, z, zq, sz, workspace):
+        return y
     i8, f32 = torch.int8, torch.float32
     a = _Args(stream)
     px = a.need(xq, "xq", i8, plan.xq_shape)
@@ -272,6 +331,12 @@ def wq8_q8linear_backward(plan: Q8LinearPlan, dy, xq, sx, wq, sw, z=None, zq=Non
                           want_dx=True, want_dw=True, want_dbias=False, workspace=None, stream=None):
     """(dx, dw, dbias); what is neither given nor wanted is None. z, or (zq, sz):
     what the forward kept, unless act is "none"."""
+    none = plan.act == "none"
+    if (stream is None and (none or (z is None) != (zq is None)) and (zq is None) == (sz is None) and
+            not (want_dx and dx is None) and not (want_dw and dw is None) and not (want_dbias and dbias is None) and
+            _given(plan._backward, plan._h, plan._backward_form, dy, xq, sx, wq, sw, None if none else z, None if none else zq,
+                   None if none else sz, dx, dw, dbias, workspace)):
+        return dx, dw, dbias
     i8, f32 = torch.int8, torch.float32
     a = _Args(stream)
     pdy = a.need(dy, "dy", plan.y_dtype, plan.y_shape, plan.y_strides)
