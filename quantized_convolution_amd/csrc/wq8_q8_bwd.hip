@@ -23,30 +23,60 @@ constexpr int planes_of() { return sizeof(T) == 2 ? 2 : 4; }
 
 enum { kZNone, kZValues, kZCodes };  // what the forward kept of z
 
-// dz of 8 columns of a row, zeros past the last column (a group of z's codes that
-// stands for NaN has columns before it as well, and makes the row's products NaN).
-template <typename YT, int ZF, int ACT, bool EXACT>
-__device__ __forceinline__ void dz_of(const Q8Geo &g, const Q8Ptrs &a, int64_t row, int c, float (&dz)[kV]) {
-    const Vec<YT, kV> dy = load_any<YT>((const YT *)a.dy + row * g.ys, c, g.N);
-    float z[kV];
-    if constexpr (ZF == kZValues) {
-        const Vec<YT, kV> v = load_any<YT>((const YT *)a.z_in + row * g.N, c, g.N);
-#pragma unroll
-        for (int k = 0; k < kV; ++k) z[k] = to_f32(v.v[k]);
-    } else if constexpr (ZF == kZCodes) {
-        const int at = min(c, g.Np - kV);
-        const uint64_t q = *(const uint64_t *)(a.zq_in + row * g.Np + at) ^ 0x8080808080808080ull;
-        const float s = a.sz_in[row * ((g.N + 31) / 32) + min(c, g.N - 1) / 32], off = -128.0f * s;
-        // code s, rounded once, from code + 128: unsigned bytes convert in one step
-#pragma unroll
-        for (int k = 0; k < kV; ++k) z[k] = fmaf((float)(uint8_t)(q >> (8 * k)), s, off);
-    }
-#pragma unroll
-    for (int k = 0; k < kV; ++k) {
-        dz[k] = to_f32(dy.v[k]);
-        if constexpr (ACT != WQ8_ACT_NONE) dz[k] *= act_slope<ACT, EXACT>(z[k]);
-    }
+// gelu's slope for bf16 results, Phi(z) + z phi(z), by its symmetry about (0, 1/2):
+// what |z| has over 1/2 is 1/2 - Phi(-|z|) + |z| phi(z), with Phi(-|z|) as
+// normal_cdf<false>() has it (1.5e-7), its half taken into the coefficients. 17
+// operations for 25: the slope is formed in both passes, and they are bound by that.
+__device__ __forceinline__ float gelu_slope(float z) {
+    const float a = fabsf(z), e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);  // exp(-z^2 / 2)
+    const float t = fast_rcp(fmaf(0.3275911f * 0.70710678118654752f, a, 1.0f));
+    float s = fmaf(0.5307027145f, t, -0.7265760135f);
+    s = fmaf(s, t, 0.7107068705f);
+    s = fmaf(s, t, -0.142248368f);
+    s = fmaf(s, t, 0.127414796f);
+    const float over = fmaf(a * 0.3989422804014327f, e, fmaf(-s * t, e, 0.5f));
+    return 0.5f + __builtin_copysignf(over, z);
 }
+
+template <int ACT, bool EXACT>
+__device__ __forceinline__ float slope_of(float z) {
+    if constexpr (ACT == WQ8_ACT_GELU && !EXACT) return gelu_slope(z);
+    return act_slope<ACT, EXACT>(z);
+}
+
+// What dz of 8 columns of a row is made of, and dz: zeros past the last column (a
+// group of z's codes that stands for NaN has columns before it as well, and makes
+// the row's products NaN).
+template <typename YT, int ZF>
+struct DzParts {
+    Vec<YT, kV> dy, z;
+    uint64_t codes;
+    float scale;
+
+    __device__ __forceinline__ void load(const Q8Geo &g, const Q8Ptrs &a, int64_t row, int c) {
+        dy = load_any<YT>((const YT *)a.dy + row * g.ys, c, g.N);
+        if constexpr (ZF == kZValues) z = load_any<YT>((const YT *)a.z_in + row * g.N, c, g.N);
+        if constexpr (ZF == kZCodes) {
+            codes = *(const uint64_t *)(a.zq_in + row * g.Np + min(c, g.Np - kV));
+            scale = a.sz_in[row * ((g.N + 31) / 32) + min(c, g.N - 1) / 32];
+        }
+    }
+    template <int ACT, bool EXACT>
+    __device__ __forceinline__ void form(float (&dz)[kV]) const {
+#pragma unroll
+        for (int k = 0; k < kV; ++k) {
+            dz[k] = to_f32(dy.v[k]);
+            if constexpr (ACT != WQ8_ACT_NONE) {
+                float v;
+                // code scale, rounded once, from code + 128: unsigned bytes convert in one step
+                if constexpr (ZF == kZCodes)
+                    v = fmaf((float)(uint8_t)((codes ^ 0x8080808080808080ull) >> (8 * k)), scale, -128.0f * scale);
+                else v = to_f32(z.v[k]);
+                dz[k] *= slope_of<ACT, EXACT>(v);
+            }
+        }
+    }
+};
 
 // ------------------------------------------------------------------ first pass
 // 64 lanes x 8 columns of `chunk` rows, a wave each: the largest |dz sw| of every
@@ -68,14 +98,27 @@ __device__ __forceinline__ void max_block(const Q8Geo &g, const Q8Ptrs &a, int b
     with_act(g.act, [&](auto act) {
         constexpr int A = decltype(act)::value;
         if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
-            for (int r = r0 + wave; r < r1; r += kMaxWaves * kMaxRows) {
-                float dz[kMaxRows][kV], sx[kMaxRows];
+        {
+            // the next rows are on their way while these are worked on
+            DzParts<YT, ZF> next[kMaxRows];
+            float next_sx[kMaxRows];
+            const auto fetch = [&](int r) {
 #pragma unroll
                 for (int i = 0; i < kMaxRows; ++i) {
                     const int row = min(r + kMaxWaves * i, r1 - 1);
-                    dz_of<YT, ZF, A, exact_acts<XT, YT>()>(g, a, row, c, dz[i]);
-                    sx[i] = a.sx[row];
+                    next[i].load(g, a, row, c);
+                    next_sx[i] = a.sx[row];
                 }
+            };
+            fetch(r0 + wave);
+            for (int r = r0 + wave; r < r1; r += kMaxWaves * kMaxRows) {
+                DzParts<YT, ZF> now[kMaxRows];
+                float dz[kMaxRows][kV], sx[kMaxRows];
+#pragma unroll
+                for (int i = 0; i < kMaxRows; ++i) now[i] = next[i], sx[i] = next_sx[i];
+                fetch(r + kMaxWaves * kMaxRows);
+#pragma unroll
+                for (int i = 0; i < kMaxRows; ++i) now[i].template form<A, exact_acts<XT, YT>()>(dz[i]);
 #pragma unroll
                 for (int i = 0; i < kMaxRows; ++i)
                     if (r + kMaxWaves * i < r1) {
@@ -90,6 +133,7 @@ __device__ __forceinline__ void max_block(const Q8Geo &g, const Q8Ptrs &a, int b
                         if (lane == 0) a.rowmax[(int64_t)col * g.M + r + kMaxWaves * i] = __uint_as_float(top);
                     }
             }
+        }
     });
     if (wave > 0)
 #pragma unroll
@@ -182,9 +226,9 @@ __global__ __launch_bounds__(kMaxWaves * 64) void k_q8_max(Q8Geo g, Q8Ptrs a, in
 template <int PLANES>
 struct Digits {
     static constexpr float kMost = PLANES == 2 ? 32512.0f : 2130706432.0f;  // 127 256^(planes - 1)
-    float up, f;
+    float f, up;  // found once a row or column, and read from LDS
 
-    __device__ __forceinline__ explicit Digits(uint32_t bits) {
+    __device__ __forceinline__ void find(uint32_t bits) {
         const float m = __uint_as_float(bits);
         up = m < 0x1p-60f ? 0x1p64f : 1.0f;  // kMost / m overflows below 2^-96
         f = bits == 0 || bits >= kInfBits ? 0.0f : kMost / (m * up);
@@ -196,7 +240,7 @@ struct Digits {
     // The number plus 128 in each digit but the highest: its bytes, with 128 taken
     // off again in each by lower(), are the digits.
     __device__ __forceinline__ uint32_t operator()(float v) const {
-        if constexpr (PLANES == 2) return __float_as_uint(v * f + (kRoundMagic + 128.0f));  // the low half
+        if constexpr (PLANES == 2) return __float_as_uint(fmaf(v, f, kRoundMagic + 128.0f));  // the low half
         // 2130706432 (1 + 2^-23) + 0x808080 is still below 2^31
         return (uint32_t)(int)__builtin_rintf(v * f) + 0x00808080u;
     }
@@ -212,19 +256,15 @@ __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_d
     constexpr int LD = 128 + 4;  // bytes between columns in LDS: a wave's stores meet every bank twice
     __shared__ __align__(16) int8_t tile[PLANES * 64 * LD];
     __shared__ float cpart[16][64];
-    __shared__ uint32_t cmax[64], rmax[128];
+    __shared__ Digits<PLANES> cdig[64], rdig[128];
     int b;
     if (!block_number(nb, b)) return;
+    b = xcd_block(b, nb);  // blocks that share lines of z's codes and of the rows' digits behind one cache
     const int across = g.Np / 64, br = b / across, r0 = br * 128, c0 = (b - br * across) * 64;
     const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3, c = c0 + cg * kV;
-    float dz[4][kV];
-    with_act(g.act, [&](auto act) {
-        constexpr int A = decltype(act)::value;
-        if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
+    DzParts<YT, ZF> parts[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                dz_of<YT, ZF, A, exact_acts<XT, YT>()>(g, a, min(r0 + rg * 4 + i, g.M - 1), c, dz[i]);
-    });
+    for (int i = 0; i < 4; ++i) parts[i].load(g, a, min(r0 + rg * 4 + i, g.M - 1), c);
     if (want_dw) {  // 4 columns a thread, 16 threads along the first pass's chunks
         const int c4 = (threadIdx.x & 15) * 4, q = threadIdx.x >> 4;
         Vec<float, 4> m = {};
@@ -241,15 +281,22 @@ __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_d
         const int r = min(r0 + (int)threadIdx.x, g.M - 1);
         float m = 0.0f;
         for (int i = 0; i < g.ncol; ++i) m = larger(m, a.rowmax[(int64_t)i * g.M + r]);
-        rmax[threadIdx.x] = bits_of(m);
+        rdig[threadIdx.x].find(bits_of(m));
         if (c0 == 0 && r0 + (int)threadIdx.x < g.M) a.rscale[r] = Digits<PLANES>::scale(bits_of(m));
     }
+    float dz[4][kV];
+    with_act(g.act, [&](auto act) {
+        constexpr int A = decltype(act)::value;
+        if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
+#pragma unroll
+            for (int i = 0; i < 4; ++i) parts[i].template form<A, exact_acts<XT, YT>()>(dz[i]);
+    });
     __syncthreads();
     if (want_dw && threadIdx.x < 64) {
         float t = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) t = larger(t, cpart[i][threadIdx.x]);
-        cmax[threadIdx.x] = bits_of(t);
+        cdig[threadIdx.x].find(bits_of(t));
         if (br == 0 && c0 + (int)threadIdx.x < g.N) a.cscale[c0 + threadIdx.x] = Digits<PLANES>::scale(bits_of(t));
     }
     if (want_dx) {
@@ -257,7 +304,7 @@ __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_d
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = r0 + rg * 4 + i;
-            const Digits<PLANES> d(rmax[rg * 4 + i]);
+            const Digits<PLANES> d = rdig[rg * 4 + i];
             float u[kV];
 #pragma unroll
             for (int k = 0; k < kV; ++k) u[k] = dz[i][k] * sw.v[k];
@@ -282,7 +329,7 @@ __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_d
     for (int i = 0; i < 4; ++i) sx[i] = r0 + rg * 4 + i < g.M ? a.sx[r0 + rg * 4 + i] : 0.0f;  // past the end dz is the last row's
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-        const Digits<PLANES> d(cmax[cg * kV + k]);
+        const Digits<PLANES> d = cdig[cg * kV + k];
         float u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) u[i] = dz[i][k] * sx[i];
@@ -419,7 +466,7 @@ struct RunQ8Backward {
         const int64_t blocks = nw + nx + (p.dbias ? (g.N + 15) / 16 : 0);
         if (blocks > 0) {
             const auto kernel = k_q8_bwd<T, BM, BN, WM, WN>;
-            hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(WM * WN * 64), (tile_lds<BM, BN>(kernel)), st, dw, ew, (int)nw, dx, ex,
+            hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(WM * WN * 64), (q8_lds<BM, BN, planes_of<T>()>(kernel)), st, dw, ew, (int)nw, dx, ex,
                                (int)nx, (int)blocks, g, p);
         }
         if (jw + jx > 0)
@@ -451,7 +498,7 @@ void backward(const Q8Geo &g, const Q8Ptrs &p, hipStream_t st) {
     if (g.act == WQ8_ACT_NONE) prepare<XT, YT, kZNone>(g, p, st);
     else if (p.z_in) prepare<XT, YT, kZValues>(g, p, st);
     else prepare<XT, YT, kZCodes>(g, p, st);
-    pick_q8_tile<true>(g.dw.tile, RunQ8Backward<XT>{g, p, st});
+    pick_q8_pair_tile(g.dw.tile, RunQ8Backward<XT>{g, p, st});
 }
 
 }  // namespace

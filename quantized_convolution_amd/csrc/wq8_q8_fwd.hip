@@ -197,7 +197,7 @@ struct RunQ8 {
         Q8Args a = args();
         const int64_t blocks = q8_tiles<BM, BN>(a, g.f, p.partial);
         const auto kernel = k_q8<BM, BN, WM, WN, 1, EpiQ8<YT>>;
-        hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(WM * WN * 64), (tile_lds<BM, BN>(kernel)), st, a, epi());
+        hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(WM * WN * 64), (q8_lds<BM, BN, 1>(kernel)), st, a, epi());
         if (a.splits > 1)
             hipLaunchKernelGGL((k_q8_join<1, EpiQ8<YT>>), grid_of(q8_join_blocks(a)), dim3(256), 0, st, a, epi(),
                                (int)q8_join_blocks(a));
@@ -216,7 +216,7 @@ struct RunQ8 {
     }
 
     void run() const {
-        if (g.f.tile >= 0) return pick_q8_tile<false>(g.f.tile, *this);
+        if (g.f.tile >= 0) return pick_q8_tile(g.f.tile, *this);
         if (g.M == 1) few<1>();
         else if (g.M == 2) few<2>();
         else few<4>();

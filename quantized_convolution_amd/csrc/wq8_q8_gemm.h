@@ -3,15 +3,17 @@
 // C[m][n] = sum_p 256^-p sum_k A_p(m, k) B(n, k), A in 1, 2 or 4 planes of 8-bit
 // digits, both operands with k contiguous in whole lines of 128 bytes, zeros
 // behind the last one. A block computes a BM x BN tile in k steps of 128, which
-// go from memory to LDS past the registers into one of two buffers while the
-// other is multiplied: the layout, the swizzle and the loads are those of the
-// bf16 product, whose k steps have the same bytes.
+// go from memory to LDS past the registers into one of some buffers while another
+// is multiplied: the layout, the swizzle and the loads are those of the bf16
+// product, whose k steps have the same bytes. Small tiles, whose blocks are few
+// and wait for memory, have three or four buffers, all but one on their way.
 //
-// Several planes share the sums' registers. The lowest comes first; after each
-// but the highest a sum is shifted down by 8 bits and the next plane is added to
-// what is left. The bits that the shifts drop are kept in a byte each and put
-// back at the end, so the sums of 2 planes are exact; of 4 planes the lowest 8
-// bits, below 2^-16 of the highest plane's unit, are rounded off.
+// Two planes are multiplied together, each with sums of its own: what a k step
+// has of B serves both, a fragment of it twice the matrix instructions. Of four
+// planes the lower two come first; their sum, rounded to the third plane's unit,
+// is carried into the second plane's, but for its last byte, which is kept and
+// put back at the end. So the sums of 2 planes are exact, of 4 to 2^-17 of the
+// highest plane's unit.
 #pragma once
 
 #include "wq8_gemm_device.h"
@@ -34,6 +36,26 @@ struct Q8Args {
     void *partial;     // [splits][M][N] where k is split, int32 (one plane) or f32, else NULL
 };
 
+// Rows of LDS of a k step, and its buffers: what leaves room for two blocks on a
+// compute unit, two at least.
+constexpr int q8_rows(int bm, int bn, int planes) { return (planes > 1 ? 2 : 1) * bm + bn; }
+constexpr int q8_depth(int rows) { return rows <= 144 ? 4 : rows <= 192 || rows == 384 ? 3 : 2; }
+template <int BM, int BN, int PLANES, typename K>
+size_t q8_lds(K kernel) {
+    constexpr int rows = q8_rows(BM, BN, PLANES);
+    constexpr size_t bytes = (size_t)q8_depth(rows) * rows * 128;
+    static_assert(bytes <= 163840, "a compute unit's LDS");
+    if (bytes > 65536)
+        (void)hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    return bytes;
+}
+
+// Waits until all but the last n of this wave's loads have landed.
+template <int n>
+__device__ __forceinline__ void wait_all_but() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
+}
+
 // EPI, an epilogue: column(n) and item(m, n) read, for any m and n, what belongs
 // to 8 columns and to 8 columns of a row; with(f) calls f once with the
 // activation; store<ACT>(m, n, 8 sums, span, column, item) ends it, for any m
@@ -47,7 +69,7 @@ __device__ __forceinline__ void q8_block(const Q8Args &a, const EPI &epi, int b,
     static_assert(TN % 2 == 0, "column tiles come in pairs");
     extern __shared__ __align__(128) char smem[];
     int8_t *const lds = (int8_t *)smem;
-    constexpr int STAGE = (BM + BN) * BK, BS = BM * BK;
+    constexpr int NP = PLANES > 1 ? 2 : 1, ROWS = q8_rows(BM, BN, PLANES), STAGE = ROWS * BK, AS = BM * BK, BS = NP * AS;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int tiles = a.tiles_m * a.tiles_n;
     b = xcd_block(b, nb);
@@ -64,85 +86,93 @@ __device__ __forceinline__ void q8_block(const Q8Args &a, const EPI &epi, int b,
     sb.prepare();
     const int k0 = split * a.ksteps, k1 = min(k0 + a.ksteps, a.steps), n = k1 - k0;
 
-    i32x4 acc[TM][TN] = {};
-    constexpr int KEPT = PLANES / 2;  // bytes of a sum that shifts have dropped
-    uint32_t rest[KEPT ? KEPT : 1][TM][TN];  // the p-th of four sums
+    i32x4 acc[NP][TM][TN] = {};
+    uint32_t rest[PLANES == 4 ? TM : 1][TN];  // the kept bytes of four sums
     const auto multiply = [&](const int8_t *buf) {
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            i32x4 fa[TM], fb[TN];
+            i32x4 fa[NP][TM], fb[TN];
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const int row = wm + i * 16 + row_of<false>(lane & 15, 0);
-                fa[i] = *(const i32x4 *)(buf + lds_unit<int8_t, true, false, BM>(row, kk * 4 + (lane >> 4)));
-            }
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const int row = wm + i * 16 + row_of<false>(lane & 15, 0);
+                    fa[p][i] = *(const i32x4 *)(buf + p * AS + lds_unit<int8_t, true, false, BM>(row, kk * 4 + (lane >> 4)));
+                }
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int row = wn + (j / 2) * 32 + row_of<true>(lane & 15, j % 2);
                 fb[j] = *(const i32x4 *)(buf + BS + lds_unit<int8_t, true, true, BN>(row, kk * 4 + (lane >> 4)));
             }
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+            for (int p = 0; p < NP; ++p)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+                        acc[p][i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[p][i], acc[p][i][j], 0, 0, 0);
         }
     };
 
-    int s = 0;  // steps of all planes, counted through
-    sa.src = a.A + (PLANES - 1) * a.plane;
-    if (n > 0) {
-        sa.direct(lds, k0);
-        sb.direct(lds + BS, k0);
-    }
-    const auto add_plane = [&](bool last) {
-        for (int k = 0; k < n; ++k, ++s) {
-            int8_t *const cur = lds + (s & 1) * STAGE, *const nxt = lds + ((s + 1) & 1) * STAGE;
-            wait_direct();
-            __syncthreads();
-            if (k + 1 < n) {
-                sa.direct(nxt, k0 + k + 1);
-                sb.direct(nxt + BS, k0 + k + 1);
-            } else if (!last) {
-                sa.src -= a.plane;
-                sa.direct(nxt, k0);
-                sb.direct(nxt + BS, k0);
-            }
-            multiply(cur);
+    // Steps of both passes over the planes, counted through.
+    constexpr int D = q8_depth(ROWS), LOADS = NP * SA::COUNT + decltype(sb)::COUNT, PASSES = PLANES / NP;
+    const int8_t *plane = a.A + (PLANES - NP) * a.plane;
+    int sent = 0, sent_k = 0, to = 0, from = 0, left = n * PASSES;
+    const int total = left;
+    const auto send = [&] {
+        int8_t *const buf = lds + to * STAGE;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            sa.src = plane + p * a.plane;
+            sa.direct(buf + p * AS, k0 + sent_k);
+        }
+        sb.direct(buf + BS, k0 + sent_k);
+        to = to + 1 < D ? to + 1 : 0;
+        ++sent;
+        if (++sent_k == n) {
+            sent_k = 0;
+            plane -= NP * a.plane;
         }
     };
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d)
+        if (d < total) send();
+    const auto pass = [&] {
+        for (int k = 0; k < n; ++k, --left) {
+            if (D == 2 || left < D - 1) wait_all_but<0>();
+            else wait_all_but<LOADS *(D - 2)>();
+            __syncthreads();
+            if (sent < total) send();
+            multiply(lds + from * STAGE);
+            from = from + 1 < D ? from + 1 : 0;
+        }
+    };
+    pass();
     if constexpr (PLANES == 4) {
-        add_plane(false);
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = (acc[i][j] + 128) >> 8;
-    }
-#pragma unroll
-    for (int q = KEPT - 1; q >= 0; --q) {
-        add_plane(false);
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                const i32x4 v = acc[i][j];
-                rest[q][i][j] = (v[0] & 255) | (v[1] & 255) << 8 | (v[2] & 255) << 16 | (uint32_t)v[3] << 24;
-                acc[i][j] = v >> 8;
+                const i32x4 low = acc[0][i][j] + ((acc[1][i][j] + 128) >> 8);
+                rest[i][j] = (low[0] & 255) | (low[1] & 255) << 8 | (low[2] & 255) << 16 | (uint32_t)low[3] << 24;
+                acc[0][i][j] = i32x4{};
+                acc[1][i][j] = low >> 8;
             }
+        pass();
     }
-    add_plane(true);
 
-    // the 8 adjacent columns that a lane has in a pair of tiles
+    // the 8 adjacent columns that a lane has in a pair of tiles, in units of the
+    // lowest byte that is left
     const auto sums = [&](int i, int j) {
         Vec<float, 8> r;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const auto value = [&](int jj) {  // in units of the lowest byte kept
-                const float v = (float)acc[i][jj][e];
-                if constexpr (PLANES == 2) return fmaf(v, 256.0f, (float)(rest[0][i][jj] >> (8 * e) & 255));
-                if constexpr (PLANES == 4)
-                    return fmaf(v, 65536.0f,
-                                (float)((rest[0][i][jj] >> (8 * e) & 255) << 8 | (rest[KEPT - 1][i][jj] >> (8 * e) & 255)));
-                return v;
+            const auto value = [&](int jj) {
+                const float v = (float)acc[0][i][jj][e];
+                if constexpr (PLANES == 1) return v;
+                const float w = fmaf(v, 256.0f, (float)acc[NP - 1][i][jj][e]);
+                if constexpr (PLANES == 2) return w;
+                return fmaf(w, 256.0f, (float)(rest[PLANES == 4 ? i : 0][jj] >> (8 * e) & 255));
             };
             r.v[e] = value(j);
             r.v[4 + e] = value(j + 1);
@@ -163,7 +193,7 @@ __device__ __forceinline__ void q8_block(const Q8Args &a, const EPI &epi, int b,
                 } else {
                     Vec<int, 8> r;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) r.v[e] = acc[i][j][e], r.v[4 + e] = acc[i][j + 1][e];
+                    for (int e = 0; e < 4; ++e) r.v[e] = acc[0][i][j][e], r.v[4 + e] = acc[0][i][j + 1][e];
                     store_vec_n<int, 8>((int *)a.partial + at, r, a.N - c);
                 }
             }
@@ -253,18 +283,25 @@ int64_t q8_tiles(Q8Args &a, const Q8Shape &s, void *partial) {
     return (int64_t)a.tiles_m * a.tiles_n * s.splits;
 }
 
-// Calls run<BM, BN, WM, WN>() for the tile, in the order of kQ8Tiles.
-template <bool MULTI, typename R>
+// Calls run<BM, BN, WM, WN>() for the tile, in the order of kQ8Tiles, or of
+// kQ8PairTiles for more than one plane.
+template <typename R>
 void pick_q8_tile(int tile, const R &run) {
     switch (tile) {
-        case 0:
-            if constexpr (!MULTI) run.template operator()<256, 256, 2, 4>();
-            return;
+        case 0: return run.template operator()<256, 256, 2, 4>();
         case 1: return run.template operator()<128, 128, 2, 2>();
         case 2: return run.template operator()<128, 64, 2, 2>();
         case 3: return run.template operator()<64, 64, 2, 2>();
-        default:
-            if constexpr (!MULTI) run.template operator()<16, 128, 1, 2>();
+        default: return run.template operator()<16, 128, 1, 2>();
+    }
+}
+template <typename R>
+void pick_q8_pair_tile(int tile, const R &run) {
+    switch (tile) {
+        case 0: return run.template operator()<256, 128, 4, 2>();
+        case 1: return run.template operator()<128, 128, 4, 2>();
+        case 2: return run.template operator()<128, 64, 2, 2>();
+        default: return run.template operator()<64, 64, 2, 2>();
     }
 }
 

@@ -46,7 +46,7 @@ wq8_status launch_unpack(const RowsGeo &g, wq8_dtype xdt, const int8_t *codes, c
 constexpr int kQ8MaxSteps = 512;
 
 struct Q8Shape {
-    int tile;      // index into kQ8Tiles, -1: the kernel for up to 4 rows
+    int tile;      // index into kQ8Tiles (backward: kQ8PairTiles), -1: the kernel for up to 4 rows
     int splits, ksteps;
 };
 
@@ -77,14 +77,13 @@ struct Q8Ptrs {
 };
 
 // Tiles: rows, columns, blocks that a compute unit holds, share of the largest
-// tile's rate.
+// tile's rate. The second table is for products of two planes at once.
 struct Q8Tile {
     int bm, bn, blocks;
     double rate;
 };
-constexpr Q8Tile kQ8Tiles[] = {
-    {256, 256, 1, 1.0}, {128, 128, 2, 0.8}, {128, 64, 3, 0.62}, {64, 64, 5, 0.45}, {16, 128, 4, 0.3}};
-constexpr int kQ8TileCount = 5;
+constexpr Q8Tile kQ8Tiles[] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.8}, {128, 64, 2, 0.62}, {64, 64, 2, 0.45}, {16, 128, 2, 0.3}};
+constexpr Q8Tile kQ8PairTiles[] = {{256, 128, 1, 1.0}, {128, 128, 1, 0.92}, {128, 64, 2, 0.72}, {64, 64, 2, 0.6}};
 
 wq8_status launch_q8_forward(const Q8Geo &g, wq8_dtype ydt, const Q8Ptrs &p, void *stream);
 wq8_status launch_q8_backward(const Q8Geo &g, wq8_dtype xdt, wq8_dtype ydt, const Q8Ptrs &p, void *stream);

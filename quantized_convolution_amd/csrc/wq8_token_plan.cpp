@@ -137,10 +137,12 @@ struct Product {
 void choose_q8(const Product *q, int count, int planes, Q8Shape *const *out) {
     constexpr int kMost = 16;
     double least = 1e30;
-    for (int i = planes > 1 ? 1 : 0; i < (planes > 1 ? 4 : kQ8TileCount); ++i) {
-        const Q8Tile &g = kQ8Tiles[i];
+    const bool pair = planes > 1;
+    for (int i = 0; i < (pair ? 4 : 5); ++i) {
+        const Q8Tile &g = pair ? kQ8PairTiles[i] : kQ8Tiles[i];
         const double rate = 9.5 * g.rate;  // M operations per us and compute unit
-        const double step = 2e-6 * g.bm * g.bn * 128 * planes / rate;
+        // a step's loads, barrier and LDS reads take a quarter of a microsecond
+        const double step = fmax(2e-6 * g.bm * g.bn * 128 * planes / rate, 0.25 * (planes > 2 ? 2 : 1));
         for (int combo = 0; combo < (count == 1 ? kMost : kMost * kMost); ++combo) {
             const int64_t more[2] = {combo % kMost, combo / kMost};
             int64_t blocks = 0, work = 0, longest = 0, per[2] = {0, 0}, sp[2] = {1, 1};
@@ -215,12 +217,13 @@ wq8_status build_q8linear(const wq8_q8linear_desc *d, wq8_q8linear_plan *p) {
     g.chunk = (int)round_up(ceil_div(g.M, 2 * kCus > g.ncol ? 2 * kCus / g.ncol : 1), 16);
     if (g.chunk < 16) g.chunk = 16;
     g.nchunk = (int)ceil_div(g.M, g.chunk);
-    const auto tiles = [](const Q8Shape &s, int64_t M, int64_t N) {
-        return s.tile < 0 ? ceil_div(N, 8) : ceil_div(M, kQ8Tiles[s.tile].bm) * ceil_div(N, kQ8Tiles[s.tile].bn) * s.splits;
+    const auto tiles = [](const Q8Shape &s, const Q8Tile *t, int64_t M, int64_t N) {
+        return s.tile < 0 ? ceil_div(N, 8) : ceil_div(M, t[s.tile].bm) * ceil_div(N, t[s.tile].bn) * s.splits;
     };
     const int64_t lim = (int64_t)1 << 31;
     const int64_t lines = (int64_t)(g.Mp / 128) * (g.Kp / 128) + (int64_t)(g.Np / 128) * (g.Kp / 128);
-    if (tiles(g.f, g.M, g.N) >= lim || tiles(g.dx, g.M, g.K) + tiles(g.dw, g.N, g.K) + g.N >= lim ||
+    if (tiles(g.f, kQ8Tiles, g.M, g.N) >= lim ||
+        tiles(g.dx, kQ8PairTiles, g.M, g.K) + tiles(g.dw, kQ8PairTiles, g.N, g.K) + g.N >= lim ||
         (int64_t)g.nchunk * g.ncol + lines >= lim || (int64_t)(g.Mp / 128) * (g.Np / 64) >= lim ||
         ceil_div(g.M, 16) * ceil_div(g.N > g.K ? g.N : g.K, 128) >= lim)
         return fail(WQ8_ERR_UNSUPPORTED, "more than 2^31 blocks");
