@@ -5,26 +5,33 @@
 namespace wq8 {
 namespace {
 
-// The row and the vector in it of the `i`-th of a block's vectors, `across` of
-// which are a row: one division of the block's first by scalars, then 32 bits.
-__device__ __forceinline__ void place(int b, int per, int across, int i, int64_t &row, int &vec) {
-    const int64_t first = (int64_t)b * per, r0 = first / across;
-    const int at = (int)(first - r0 * across) + i, down = at / across;
-    row = r0 + down;
-    vec = at - down * across;
+// The row and the vector in it of a thread, `across` vectors being a row: 32-bit
+// division where all vectors are counted in 32 bits.
+template <bool WIDE>
+__device__ __forceinline__ void place(int b, int across, int64_t &row, int &vec) {
+    if constexpr (WIDE) {
+        const int64_t first = (int64_t)b * 256, r0 = first / across;
+        const int at = (int)(first - r0 * across) + threadIdx.x, down = at / across;
+        row = r0 + down;
+        vec = at - down * across;
+    } else {
+        const uint32_t i = (uint32_t)b * 256 + threadIdx.x, r = i / (uint32_t)across;
+        row = r;
+        vec = (int)(i - r * across);
+    }
 }
 
 // Groups: a thread has 8 columns, the 4, 8 or 16 threads of a group are
 // neighbours in a wave. Rows of codes are whole lines, so groups start at
 // multiples of their threads, and what stands behind the last column is written
 // by threads of its own.
-template <typename XT, int G>
+template <typename XT, int G, bool WIDE>
 __global__ __launch_bounds__(256) void k_pack_groups(RowsGeo g, const XT *x, int8_t *codes, float *scales, int blocks) {
     int b;
     if (!block_number(blocks, b)) return;
     int64_t row;
     int vec;
-    place(b, 256, g.stride / kV, threadIdx.x, row, vec);
+    place<WIDE>(b, g.stride / kV, row, vec);
     const int c = vec * kV;
     const bool in = row < g.rows;  // whole groups are in or out
     const Vec<XT, kV> v = load_any<XT>(x + (in ? row : 0) * g.xs, c, g.C);
@@ -43,13 +50,13 @@ __global__ __launch_bounds__(256) void k_pack_groups(RowsGeo g, const XT *x, int
     if (c % G == 0 && c < g.C) scales[row * ((g.C + G - 1) / G) + c / G] = code.scale;
 }
 
-template <typename XT>
+template <typename XT, bool WIDE>
 __global__ __launch_bounds__(256) void k_unpack(RowsGeo g, const int8_t *codes, const float *scales, XT *x, int blocks) {
     int b;
     if (!block_number(blocks, b)) return;
     int64_t row;
     int vec;
-    place(b, 256, (g.C + kV - 1) / kV, threadIdx.x, row, vec);
+    place<WIDE>(b, (g.C + kV - 1) / kV, row, vec);
     if (row >= g.rows) return;
     const int c = vec * kV;
     const uint64_t q = *(const uint64_t *)(codes + row * g.stride + c);
@@ -60,15 +67,28 @@ __global__ __launch_bounds__(256) void k_unpack(RowsGeo g, const int8_t *codes, 
     store_cols<XT>(x + row * g.xs, c, g.C, v);
 }
 
+constexpr int64_t kWide = 1 << 23;  // blocks whose threads pass 31 bits
+
+template <typename XT>
+void unpack(const RowsGeo &g, const int8_t *codes, const float *scales, XT *x, hipStream_t st) {
+    const int64_t blocks = ((int64_t)g.rows * ((g.C + kV - 1) / kV) + 255) / 256;
+    const auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(256), 0, st, g, codes, scales, x, (int)blocks);
+    };
+    if (blocks >= kWide) go(k_unpack<XT, true>);
+    else go(k_unpack<XT, false>);
+}
+
 template <typename XT>
 void pack_groups(const RowsGeo &g, const XT *x, int8_t *codes, float *scales, hipStream_t st) {
     const int64_t blocks = ((int64_t)g.rows * (g.stride / kV) + 255) / 256;
     const auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(256), 0, st, g, x, codes, scales, (int)blocks);
     };
-    if (g.group == 32) go(k_pack_groups<XT, 32>);
-    else if (g.group == 64) go(k_pack_groups<XT, 64>);
-    else go(k_pack_groups<XT, 128>);
+    const bool wide = blocks >= kWide;
+    if (g.group == 32) wide ? go(k_pack_groups<XT, 32, true>) : go(k_pack_groups<XT, 32, false>);
+    else if (g.group == 64) wide ? go(k_pack_groups<XT, 64, true>) : go(k_pack_groups<XT, 64, false>);
+    else wide ? go(k_pack_groups<XT, 128, true>) : go(k_pack_groups<XT, 128, false>);
 }
 
 }  // namespace
@@ -90,13 +110,8 @@ wq8_status launch_pack_groups(const RowsGeo &g, wq8_dtype xdt, const void *x, in
 }
 
 wq8_status launch_unpack(const RowsGeo &g, wq8_dtype xdt, const int8_t *codes, const float *scales, void *x, void *stream) {
-    const int64_t blocks = ((int64_t)g.rows * ((g.C + kV - 1) / kV) + 255) / 256;
-    if (xdt == WQ8_F32)
-        hipLaunchKernelGGL(k_unpack<float>, grid_of(blocks), dim3(256), 0, (hipStream_t)stream, g, codes, scales, (float *)x,
-                           (int)blocks);
-    else
-        hipLaunchKernelGGL(k_unpack<bf16_t>, grid_of(blocks), dim3(256), 0, (hipStream_t)stream, g, codes, scales, (bf16_t *)x,
-                           (int)blocks);
+    if (xdt == WQ8_F32) unpack<float>(g, codes, scales, (float *)x, (hipStream_t)stream);
+    else unpack<bf16_t>(g, codes, scales, (bf16_t *)x, (hipStream_t)stream);
     return check_launch("unpacking");
 }
 

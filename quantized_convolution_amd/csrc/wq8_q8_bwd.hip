@@ -53,9 +53,15 @@ struct DzParts {
     uint64_t codes;
     float scale;
 
+    // WHOLE: all 8 columns exist.
+    template <bool WHOLE>
     __device__ __forceinline__ void load(const Q8Geo &g, const Q8Ptrs &a, int64_t row, int c) {
-        dy = load_any<YT>((const YT *)a.dy + row * g.ys, c, g.N);
-        if constexpr (ZF == kZValues) z = load_any<YT>((const YT *)a.z_in + row * g.N, c, g.N);
+        if constexpr (WHOLE) dy = load_vec<YT, kV>((const YT *)a.dy + row * g.ys + c);
+        else dy = load_any<YT>((const YT *)a.dy + row * g.ys, c, g.N);
+        if constexpr (ZF == kZValues) {
+            if constexpr (WHOLE) z = load_vec<YT, kV>((const YT *)a.z_in + row * g.N + c);
+            else z = load_any<YT>((const YT *)a.z_in + row * g.N, c, g.N);
+        }
         if constexpr (ZF == kZCodes) {
             codes = *(const uint64_t *)(a.zq_in + row * g.Np + min(c, g.Np - kV));
             scale = a.sz_in[row * ((g.N + 31) / 32) + min(c, g.N - 1) / 32];
@@ -99,40 +105,35 @@ __device__ __forceinline__ void max_block(const Q8Geo &g, const Q8Ptrs &a, int b
         constexpr int A = decltype(act)::value;
         if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
         {
-            // the next rows are on their way while these are worked on
-            DzParts<YT, ZF> next[kMaxRows];
-            float next_sx[kMaxRows];
-            const auto fetch = [&](int r) {
+            const auto rows = [&](auto whole) {
+                for (int r = r0 + wave; r < r1; r += kMaxWaves * kMaxRows) {
+                    DzParts<YT, ZF> parts[kMaxRows];
+                    float dz[kMaxRows][kV], sx[kMaxRows];
 #pragma unroll
-                for (int i = 0; i < kMaxRows; ++i) {
-                    const int row = min(r + kMaxWaves * i, r1 - 1);
-                    next[i].load(g, a, row, c);
-                    next_sx[i] = a.sx[row];
+                    for (int i = 0; i < kMaxRows; ++i) {
+                        const int row = min(r + kMaxWaves * i, r1 - 1);
+                        parts[i].template load<decltype(whole)::value>(g, a, row, c);
+                        sx[i] = a.sx[row];
+                    }
+#pragma unroll
+                    for (int i = 0; i < kMaxRows; ++i) parts[i].template form<A, exact_acts<XT, YT>()>(dz[i]);
+#pragma unroll
+                    for (int i = 0; i < kMaxRows; ++i)
+                        if (r + kMaxWaves * i < r1) {
+                            float m = 0.0f;
+#pragma unroll
+                            for (int k = 0; k < kV; ++k) {
+                                m = larger(m, dz[i][k] * sw.v[k]);
+                                most[k] = larger(most[k], dz[i][k] * sx[i]);
+                                sum[k] += dz[i][k];
+                            }
+                            const uint32_t top = wave_max(bits_of(m));
+                            if (lane == 0) a.rowmax[(int64_t)col * g.M + r + kMaxWaves * i] = __uint_as_float(top);
+                        }
                 }
             };
-            fetch(r0 + wave);
-            for (int r = r0 + wave; r < r1; r += kMaxWaves * kMaxRows) {
-                DzParts<YT, ZF> now[kMaxRows];
-                float dz[kMaxRows][kV], sx[kMaxRows];
-#pragma unroll
-                for (int i = 0; i < kMaxRows; ++i) now[i] = next[i], sx[i] = next_sx[i];
-                fetch(r + kMaxWaves * kMaxRows);
-#pragma unroll
-                for (int i = 0; i < kMaxRows; ++i) now[i].template form<A, exact_acts<XT, YT>()>(dz[i]);
-#pragma unroll
-                for (int i = 0; i < kMaxRows; ++i)
-                    if (r + kMaxWaves * i < r1) {
-                        float m = 0.0f;
-#pragma unroll
-                        for (int k = 0; k < kV; ++k) {
-                            m = larger(m, dz[i][k] * sw.v[k]);
-                            most[k] = larger(most[k], dz[i][k] * sx[i]);
-                            sum[k] += dz[i][k];
-                        }
-                        const uint32_t top = wave_max(bits_of(m));
-                        if (lane == 0) a.rowmax[(int64_t)col * g.M + r + kMaxWaves * i] = __uint_as_float(top);
-                    }
-            }
+            if ((col + 1) * kMaxCols <= g.N) rows(std::true_type{});
+            else rows(std::false_type{});
         }
     });
     if (wave > 0)
@@ -264,7 +265,11 @@ __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_d
     const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3, c = c0 + cg * kV;
     DzParts<YT, ZF> parts[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) parts[i].load(g, a, min(r0 + rg * 4 + i, g.M - 1), c);
+    for (int i = 0; i < 4; ++i) {
+        const int r = min(r0 + rg * 4 + i, g.M - 1);
+        if (c0 + 64 <= g.N) parts[i].template load<true>(g, a, r, c);
+        else parts[i].template load<false>(g, a, r, c);
+    }
     if (want_dw) {  // 4 columns a thread, 16 threads along the first pass's chunks
         const int c4 = (threadIdx.x & 15) * 4, q = threadIdx.x >> 4;
         Vec<float, 4> m = {};

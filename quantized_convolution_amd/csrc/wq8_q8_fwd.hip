@@ -13,6 +13,25 @@ namespace {
 
 static __device__ const float kNothing[8] = {};
 
+// gelu for bf16 results, z Phi(z) = max(z, 0) - |z| Phi(-|z|), with Phi(-|z|) as
+// normal_cdf<false>() has it, its half taken into the coefficients: 12 operations
+// and two transcendental ones for 20. The bound on |z| keeps infinity times 0 out.
+__device__ __forceinline__ float gelu_of(float z) {
+    const float a = fminf(fabsf(z), 1e18f), e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);  // exp(-z^2 / 2)
+    const float t = fast_rcp(fmaf(0.3275911f * 0.70710678118654752f, a, 1.0f));
+    float s = fmaf(0.5307027145f, t, -0.7265760135f);
+    s = fmaf(s, t, 0.7107068705f);
+    s = fmaf(s, t, -0.142248368f);
+    s = fmaf(s, t, 0.127414796f);
+    return fmaf(-a, s * t * e, fmaxf(z, 0.0f));
+}
+
+template <int ACT, bool EXACT>
+__device__ __forceinline__ float act_of(float z) {
+    if constexpr (ACT == WQ8_ACT_GELU && !EXACT) return gelu_of(z);
+    return act_fwd<ACT, EXACT>(z);
+}
+
 template <typename YT>
 struct EpiQ8 {
     const float *bias, *sx, *sw;
@@ -77,7 +96,10 @@ struct EpiQ8 {
         if (zq) {  // all lanes: a group's four meet
             float t[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = n + e < N ? v.v[e] : 0.0f;
+            for (int e = 0; e < 8; ++e) t[e] = v.v[e];
+            if (N % 32 != 0)  // else a group's columns exist all or none
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] = n + e < N ? t[e] : 0.0f;
             uint32_t most = bits_of(largest(t));
             const auto r16 = __builtin_amdgcn_permlane16_swap(most, most, false, false);
             most = max(r16[0], r16[1]);
@@ -86,7 +108,7 @@ struct EpiQ8 {
             const Coder code(most);
             if (m < M) {
                 int8_t *const to = zq + (int64_t)m * Np;
-                if (n < Np) store_codes(to + n, code.pack(t));
+                if (n < Np) store_codes(to + n, n < N ? code.pack(t) : 0);
                 for (int c = n + span; c < Np; c += span) store_codes(to + c, 0);
                 if (n % 32 == 0 && n < N) sz[(int64_t)m * ((N + 31) / 32) + n / 32] = code.scale;
             }
@@ -99,7 +121,7 @@ struct EpiQ8 {
             store_vec_n<YT, 8>(z + (int64_t)m * N + n, r, N - n);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v.v[e] = act_fwd<ACT, exact_acts<YT, YT>()>(v.v[e]);
+        for (int e = 0; e < 8; ++e) v.v[e] = act_of<ACT, exact_acts<YT, YT>()>(v.v[e]);
         if (residual)
 #pragma unroll
             for (int e = 0; e < 8; ++e) v.v[e] += to_f32(item.residual.v[e]);

@@ -160,6 +160,7 @@ __global__ __launch_bounds__(1024) void k_rms_dgamma(RowsGeo g, RmsPtrs a) {
     const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4, c = blockIdx.x * 16 + tc;
     float t = 0.0f;
     if (c < g.C)
+#pragma unroll 8
         for (int i = tr; i < g.nchunk; i += 64) t += a.part[(int64_t)i * g.C + c];
     red[tr][tc] = t;
     __syncthreads();

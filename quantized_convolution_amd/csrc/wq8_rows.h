@@ -86,6 +86,7 @@ __device__ __forceinline__ float largest(const float (&v)[kV]) {
 // finite ones and NaN above those.
 __device__ __forceinline__ uint32_t bits_of(float m) { return __float_as_uint(m) & 0x7fffffffu; }
 constexpr uint32_t kInfBits = 0x7f800000u;
+constexpr float kInv127 = 1.0f / 127.0f;
 
 // How values of largest magnitude `a` (its bits) become codes: code = rint((x up) f).
 struct Coder {
@@ -94,6 +95,20 @@ struct Coder {
 
     __device__ __forceinline__ explicit Coder(uint32_t bits) {
         const float a = __uint_as_float(bits);
+        bad = false;
+        up = 1.0f;
+        if (__builtin_expect(!__any(!(a >= 0x1p-100f && a < 0x1p100f)), 1)) {
+            // Both quotients as division rounds them (all significands checked; the
+            // exponent does not matter here), in 9 operations for some 24: an
+            // approximation, and what it leaves times the reciprocal (Markstein, IBM
+            // J. Res. Dev. 34, 1990).
+            float y = fast_rcp(a);
+            y = fmaf(fmaf(-a, y, 1.0f), y, y);
+            const float q = 127.0f * y, s = a * kInv127;
+            f = fmaf(fmaf(-a, q, 127.0f), y, q);
+            scale = fmaf(fmaf(-127.0f, s, a), kInv127, s);
+            return;
+        }
         bad = bits >= kInfBits;
         up = a < 0x1p-100f ? 0x1p64f : 1.0f;  // 127 / a overflows below 2^-121
         f = bits == 0 ? 0.0f : 127.0f / (a * up);

@@ -162,11 +162,11 @@ void choose_q8(const Product *q, int count, int planes, Q8Shape *const *out) {
             }
             if (!fits) continue;
             const int64_t n = ceil_div(blocks, kCus);
-            double us = count == 1 ? (double)n * longest * step : (double)ceil_div(work, kCus) * step + 0.5 * longest * step;
+            double us = count == 1 ? (double)n * longest * step : (double)ceil_div(work, kCus) * step + 0.25 * longest * step;
             if (us < longest * step) us = longest * step;
             if (n == 1 && g.blocks > 1) us *= 1.3;
             us += (double)ceil_div(n, g.blocks) * (i == 0 ? 10.0 : i == 1 ? 4.0 : 2.5);
-            if (join > 0.0) us += 3.0 + join;
+            if (join > 0.0) us += (count == 1 ? 3.0 : 5.0) + join;
             if (us < least) {
                 least = us;
                 for (int j = 0; j < count; ++j) *out[j] = {i, (int)sp[j], (int)per[j]};
