@@ -1,0 +1,281 @@
+"""The operators on 8-bit codes together (token_block.py): every stage against 64
+bits from what the stage before it gave, in graphs, on other streams, from
+several threads, and with buffers that have to be refused."""
+import threading
+
+import pytest
+import token_reference as R
+import torch
+
+import quantized_convolution_amd as q
+from quantized_convolution_amd.token_block import Q8FeedForward
+
+pytestmark = pytest.mark.gpu
+F32, BF = torch.float32, torch.bfloat16
+ROWS, C, D = 77, 200, 520
+
+
+@pytest.fixture(scope="module", autouse=True)
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    q.load()
+
+
+def weights(dtype, seed=0, rows=ROWS):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    w = {"gamma": 1 + 0.1 * r(C), "w1": (r(D, C) / C ** 0.5).to(dtype), "w2": (r(C, D) / D ** 0.5).to(dtype), "b1": 0.1 * r(D),
+         "b2": 0.1 * r(C)}
+    return w, r(rows, C).to(dtype), r(rows, C).to(dtype), r(rows, C).to(dtype)
+
+
+def cuda(w):
+    return {k: v.cuda() for k, v in w.items()}
+
+
+def check(got, pair, what):
+    want, bound = pair
+    bad = ~((got.detach().cpu().double() - want).abs() <= bound)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()}"
+
+
+@pytest.mark.parametrize("rows", [1, 3, ROWS, 300])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_stages(rows, dtype, with_residual):
+    w, x, r, dout = weights(dtype, rows, rows)
+    ff = Q8FeedForward(cuda(w), rows, C, dtype)
+    out = ff(x.cuda(), r.cuda() if with_residual else None)
+    grads = {k: v.cpu() for k, v in ff.backward(dout.cuda()).items()}
+    cpu = lambda pair: tuple(t.cpu() for t in pair)  # noqa: E731
+    h = (x.float() + r.float()).to(dtype) if with_residual else x
+    assert torch.equal(ff.stream.cpu(), h)
+    w1, w2, a, uq, z = (cpu(t) for t in (ff.w1, ff.w2, ff.a, ff.uq, ff.z))
+    for got, want in ((w1, R.codes_of(w["w1"].float().numpy())), (w2, R.codes_of(w["w2"].float().numpy())),
+                      (uq, R.codes_of(ff.u.float().cpu().numpy()))):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    ref = R.Rms(h, 1e-6, w["gamma"])
+    t = R.codes_of(h.float().numpy() * w["gamma"].numpy())
+    assert torch.equal(a[0], t[0])
+    check(a[1], ref.scales(t[1]), "scales")
+    check(ff.rstd, ref.forward(dtype)["rstd"], "rstd")
+    zz = R.product(*a, *w1, C, w["b1"])
+    zc = R.codes_of(zz.numpy(), 32)
+    assert torch.equal(z[0], zc[0]) and torch.equal(z[1], zc[1])
+    check(ff.u, R.forward(zz, "gelu", None, dtype), "u")
+    check(out, R.forward(R.product(*uq, *w2, D, w["b2"]), "none", h, dtype), "out")
+    down = R.backward(dout, *uq, *w2, D, dtype)
+    check(ff.du, down["dx"], "du")
+    check(grads["w2"], down["dw"], "dw2")
+    check(grads["b2"], down["dbias"], "db2")
+    kept = z[0][:, :D].float() * z[1].repeat_interleave(32, 1)[:, :D]
+    up = R.backward(ff.du.cpu(), *a, *w1, C, dtype, "gelu", kept)
+    check(ff.da, up["dx"], "da")
+    check(grads["w1"], up["dw"], "dw1")
+    check(grads["b1"], up["dbias"], "db1")
+    last = ref.backward(ff.da.cpu(), ff.rstd.cpu(), dout, dtype)
+    check(grads["x"], last["dx"], "dx")
+    check(grads["gamma"], last["dgamma"], "dgamma")
+    serve = Q8FeedForward(cuda(w), rows, C, dtype, train=False)
+    assert torch.equal(serve(x.cuda(), r.cuda() if with_residual else None), out)
+    with pytest.raises(ValueError, match="train=False"):
+        serve.backward(dout.cuda())
+
+
+def test_near_the_unpacked_block():
+    """Against the block in 64 bits without codes: off by what 8 bits a value leave, some hundredths of the norm."""
+    w, x, r, dout = weights(F32)
+    ff = Q8FeedForward(cuda(w), ROWS, C, F32)
+    out, grads = ff(x.cuda(), r.cuda()), ff.backward(dout.cuda())
+    leaves = {k: v.double().requires_grad_() for k, v in {**w, "x": x}.items()}
+    h = leaves["x"] + r.double()
+    n = h / torch.sqrt(h.square().mean(1, keepdim=True) + 1e-6) * leaves["gamma"]
+    want = h + torch.nn.functional.gelu(n @ leaves["w1"].T + leaves["b1"]) @ leaves["w2"].T + leaves["b2"]
+    want.backward(dout.double())
+    # a code is off by half a step at most, a / 254: with a about 3 deviations, 0.7 % of the values' norm in each
+    # of two operands of two products, and more in what slopes make of it
+    rel = lambda a, b: float((a.cpu().double() - b).norm() / b.norm())  # noqa: E731
+    assert rel(out, want.detach()) < 0.05
+    for k in grads:
+        assert rel(grads[k], leaves[k].grad) < 0.05, k
+
+
+def test_graph_replays():
+    """Forward and backward in one graph, replayed with new inputs between eager passes of the same operators."""
+    w, x, r, dout = weights(BF)
+    ff, eager = Q8FeedForward(cuda(w), ROWS, C), Q8FeedForward(cuda(w), ROWS, C)
+    xs, rs, ds = x.cuda(), r.cuda(), dout.cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ff(xs, rs)
+        ff.backward(ds)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ff.pack()
+        out = ff(xs, rs)
+        grads = ff.backward(ds)
+    g = torch.Generator().manual_seed(3)
+    for rep in range(4):
+        for t in (xs, rs, ds, ff.w["w1"]):
+            t.copy_(torch.randn(t.shape, generator=g))
+        eager.w["w1"].copy_(ff.w["w1"])
+        ff.ws.fill_(0x5A)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager.pack()
+        want, wg = eager(xs, rs), eager.backward(ds)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), rep
+        assert all(torch.equal(grads[k], wg[k]) for k in wg), rep
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured products that use one workspace, replayed in turn on one stream."""
+    p = q.Q8LinearPlan(200, 9000, 64, act="silu", x_dtype=BF)
+    assert p.workspace_bytes > 0
+    ws = torch.empty(max(p.workspace_bytes, p.backward_workspace_bytes), dtype=torch.uint8, device="cuda")
+    pack = q.QuantPlan(200, 9000), q.QuantPlan(64, 9000)
+    sets, graphs = [], []
+    for seed in (1, 2):
+        g = torch.Generator().manual_seed(seed)
+        x, w = torch.randn(200, 9000, generator=g).cuda(), torch.randn(64, 9000, generator=g).cuda()
+        dy = torch.randn(200, 64, generator=g).to(BF).cuda()
+        a = q.wq8_quant_pack(pack[0], x) + q.wq8_quant_pack(pack[1], w)
+        y, z = p.empty_output(), p.empty_z()
+        dx, dw = p.empty_input(), p.empty_weight_gradient()
+
+        def run(a=a, y=y, z=z, dx=dx, dw=dw, dy=dy):
+            q.wq8_q8linear_forward(p, *a, y=y, z=z, workspace=ws)
+            q.wq8_q8linear_backward(p, dy, *a, z=z, dx=dx, dw=dw, workspace=ws)
+
+        run()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (y, z, dx, dw)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        sets.append(((y, z, dx, dw), want, run))  # what a graph reads lives as long as it
+        graphs.append(graph)
+    for rep in range(3):
+        for got, _, _ in sets:
+            for t in got:
+                t.fill_(float("nan"))
+        for graph in graphs:
+            graph.replay()
+        ws.fill_(0xA5)
+        torch.cuda.synchronize()
+        for got, want, _ in sets:
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), rep
+
+
+def calls():
+    """Calls that make what they return, and their workspaces; inputs differ by seed."""
+    pack, norm = q.QuantPlan(300, 1000), q.RmsPlan(300, 1000)
+    lin, wpack = q.Q8LinearPlan(300, 1000, 200, act="gelu"), q.QuantPlan(200, 1000)
+
+    def run(seed, stream=None):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+        x, res, gm, w, dy, dz = r(300, 1000), r(300, 1000), r(1000), r(200, 1000), r(300, 1000), r(300, 200)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        for _ in range(10):
+            wq = q.wq8_quant_pack(wpack, w, stream=stream)
+            y, h, c, s, rstd = q.wq8_rms_forward(norm, x, gm, res, want_codes=True, want_rstd=True, stream=stream)
+            out, zq, sz = q.wq8_q8linear_forward(lin, c, s, *wq, want_zq=True, stream=stream)
+            grads = q.wq8_q8linear_backward(lin, dz, c, s, *wq, zq=zq, sz=sz, want_dbias=True, stream=stream)
+            more = q.wq8_rms_backward(norm, dy, h, rstd, gm, stream=stream)
+            back = q.wq8_quant_unpack(pack, *q.wq8_quant_pack(pack, x, stream=stream), stream=stream)
+        return [*wq, y, h, c, s, rstd, out, zq, sz, *grads, *more, back], (x, res, gm, w, dy, dz)
+
+    return run
+
+
+def test_threads():
+    """Calls of several threads on one stream, and on a stream each, with shared plans."""
+    run = calls()
+    want = [run(s)[0] for s in range(4)]
+    torch.cuda.synchronize()
+    for own_stream in (False, True):
+        got, errors = [None] * 4, []
+
+        def work(s):
+            try:
+                stream = torch.cuda.Stream() if own_stream else None
+                got[s] = run(s, stream)
+                if stream is not None:
+                    stream.synchronize()
+            except Exception as e:  # reported by the main thread
+                errors.append(e)
+
+        threads = [threading.Thread(target=work, args=(s,)) for s in range(4)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        assert not errors, errors
+        for (a, _), b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_other_stream_while_this_one_allocates():
+    """What a call on another stream makes is not handed to this one while its kernels run."""
+    run = calls()
+    want = run(5)[0]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got, inputs = run(5, s)
+    for n in (1 << 12, 1 << 16, 1 << 20, 1 << 22):
+        for _ in range(8):
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(inputs) == 6
+
+
+def test_given_buffers_are_refused_too():
+    """Calls whose buffers are all given take a shorter way through the checks: it refuses what the longer one does."""
+    z = lambda *s, t=F32: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+    n, m = q.QuantPlan(6, 40), q.RmsPlan(6, 40, y_stride=48)
+    p = q.Q8LinearPlan(100, 8, 16, act="silu")
+    x, c, s, g, y = z(6, 40), z(6, 128, t=torch.int8), z(6), z(40), m.empty_output()
+    xq, wq, sx, sw, o = z(100, 128, t=torch.int8), z(16, 128, t=torch.int8), z(100), z(16), z(100, 16)
+    ws = p.empty_backward_workspace()
+    dx, dw = z(100, 8), z(16, 8)
+    back = lambda **kw: q.wq8_q8linear_backward(p, o, xq, sx, wq, sw, **{**dict(z=o, dx=dx, dw=dw, workspace=ws), **kw})  # noqa: E731
+    cases = [
+        (lambda: q.wq8_quant_pack(n, x, c[:5], s), "codes must have shape"), (lambda: q.wq8_quant_pack(n, x.double(), c, s), "x must be"),
+        (lambda: q.wq8_quant_pack(n, z(40, 6).T, c, s), "x must be contiguous"),
+        (lambda: q.wq8_quant_pack(n, x.cpu(), c, s), "codes is on cuda"), (lambda: q.wq8_quant_pack(n, x, c, s.cpu()), "scales is on cpu"),
+        (lambda: q.wq8_quant_pack(n, x.clone().requires_grad_(), c, s), "x requires a gradient"),
+        (lambda: q.wq8_quant_pack(n, x.cpu(), c.cpu(), s.cpu()), "must be on a GPU"), (lambda: q.wq8_quant_pack(n, "x", c, s), "must be a torch"),
+        (lambda: q.wq8_rms_forward(m, x, g, y=x), "y must have strides"), (lambda: q.wq8_rms_forward(m, x, g[:8], y=y), "gamma must have"),
+        (lambda: q.wq8_rms_forward(m, x, g, x[:, :8], y=y, h=x), "residual must have"),
+        (lambda: back(z=None), "z is required"), (lambda: back(zq=z(100, 128, t=torch.int8), sz=z(100, 1)), "one of the two"),
+        (lambda: back(dw=z(8, 16)), "dw must have"), (lambda: back(workspace=ws[:100]), "workspace holds"),
+        (lambda: back(workspace=ws.cpu()), "workspace is on cpu"), (lambda: back(workspace=5), "workspace must be a torch"),
+    ]
+    for fn, what in cases:
+        with pytest.raises(ValueError, match=what):
+            fn()
+    for fn, what in ((lambda: q.wq8_rms_forward(m, x, g, y=y, h=z(6, 40)), "h is x itself"),
+                     (lambda: q.wq8_rms_forward(m, x, g, want_y=False), "y or codes"),
+                     (lambda: q.wq8_rms_forward(q.RmsPlan(6, 40), x, g, y=x), "must not overlap")):
+        with pytest.raises(q.Wq8Error, match=what):
+            fn()
+
+
+def test_parameters():
+    w, x, r, dout = weights(F32)
+    a, b = Q8FeedForward(cuda(w), ROWS, C, F32), Q8FeedForward({k: torch.nn.Parameter(v) for k, v in cuda(w).items()}, ROWS, C, F32)
+    outs = a(x.cuda(), r.cuda()), b(x.cuda(), r.cuda())
+    ga, gb = a.backward(dout.cuda()), b.backward(dout.cuda())
+    assert torch.equal(*outs) and all(torch.equal(ga[k], gb[k]) for k in ga)
+    assert not any(t.requires_grad for t in gb.values())
+    with pytest.raises(ValueError, match="an input requires a gradient"):
+        a(x.cuda().requires_grad_())
