@@ -370,20 +370,24 @@ struct EpiScale {
     struct Item {
         float scale;
     };
+    __device__ __forceinline__ bool plain() const { return true; }
+    template <bool>
     __device__ __forceinline__ Column column(int) const { return {}; }
+    template <bool>
     __device__ __forceinline__ Item item(int m, int) const { return {scale[min(m, M - 1)]}; }
     template <typename F>
     __device__ __forceinline__ void with(F f) const {
         f(std::integral_constant<int, WQ8_ACT_NONE>{});
     }
 
-    template <int ACT>
+    template <int ACT, bool WHOLE>
     __device__ __forceinline__ void store(int m, int n, const Vec<float, 8> &v, int, Column, const Item &item) const {
-        if (m >= M || n >= N) return;
+        if (!WHOLE && (m >= M || n >= N)) return;
         Vec<T, 8> r;
 #pragma unroll
         for (int e = 0; e < 8; ++e) r.v[e] = from_f32<T>(v.v[e] * (sizeof(T) == 2 ? 0x1p-8f : 0x1p-16f) * item.scale);
-        store_vec_n<T, 8>(out + (int64_t)m * ld + n, r, N - n);
+        if constexpr (WHOLE) store_vec<T, 8>(out + (int64_t)m * ld + n, r);
+        else store_vec_n<T, 8>(out + (int64_t)m * ld + n, r, N - n);
     }
 };
 

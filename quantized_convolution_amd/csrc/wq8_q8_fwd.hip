@@ -50,11 +50,19 @@ struct EpiQ8 {
         float sx;
     };
 
+    // Whether whole tiles have nothing that is read across their rows. (With both
+    // kinds of residual in one body the compiler reads either by single values.)
+    __device__ __forceinline__ bool plain() const { return !(planar && residual); }
+
     // Rows and columns past the end read the last ones' values, and what is not
     // given reads zeros, so that loads stand under no condition but one for all.
+    template <bool WHOLE>
     __device__ __forceinline__ Column column(int n) const {
-        Column c;
-        if (N % 8 == 0) {
+        Column c = {};
+        if constexpr (WHOLE) {
+            if (bias) c.bias = load_vec<float, 8>(bias + n);
+            c.sw = load_vec<float, 8>(sw + n);
+        } else if (N % 8 == 0) {
             c.bias = load_vec<float, 8>(bias ? bias + min(n, N - 8) : kNothing);
             c.sw = load_vec<float, 8>(sw + min(n, N - 8));
         } else {
@@ -64,11 +72,14 @@ struct EpiQ8 {
         return c;
     }
 
+    template <bool WHOLE>
     __device__ __forceinline__ Item item(int m, int n) const {
-        Item r;
+        Item r = {};
         const int row = min(m, M - 1);
         r.sx = sx[row];
-        if (planar && residual) {
+        if constexpr (WHOLE) {
+            if (residual) r.residual = load_vec<YT, 8>(residual + row * rs + n);
+        } else if (planar && residual) {
             const int img = row / pixels, p = row - img * pixels;
             const YT *src = residual + (int64_t)img * N * pixels + p;
 #pragma unroll
@@ -86,7 +97,16 @@ struct EpiQ8 {
         with_act(act, f);
     }
 
-    template <int ACT>
+    template <bool WHOLE>
+    __device__ __forceinline__ void put(YT *p, int n, const Vec<float, 8> &v) const {
+        Vec<YT, 8> r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.v[e] = from_f32<YT>(v.v[e]);
+        if constexpr (WHOLE) store_vec<YT, 8>(p, r);
+        else store_vec_n<YT, 8>(p, r, N - n);
+    }
+
+    template <int ACT, bool WHOLE>
     __device__ __forceinline__ void store(int m, int n, Vec<float, 8> v, int span, const Column &col, const Item &item) const {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v.v[e] = v.v[e] * item.sx * col.sw.v[e];
@@ -97,7 +117,7 @@ struct EpiQ8 {
             float t[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] = v.v[e];
-            if (N % 32 != 0)  // else a group's columns exist all or none
+            if (!WHOLE && N % 32 != 0)  // else a group's columns exist all or none
 #pragma unroll
                 for (int e = 0; e < 8; ++e) t[e] = n + e < N ? t[e] : 0.0f;
             uint32_t most = bits_of(largest(t));
@@ -106,28 +126,21 @@ struct EpiQ8 {
             const auto r32 = __builtin_amdgcn_permlane32_swap(most, most, false, false);
             most = max(r32[0], r32[1]);
             const Coder code(most);
-            if (m < M) {
+            if (WHOLE || m < M) {
                 int8_t *const to = zq + (int64_t)m * Np;
-                if (n < Np) store_codes(to + n, n < N ? code.pack(t) : 0);
+                if (WHOLE || n < Np) store_codes(to + n, WHOLE || n < N ? code.pack(t) : 0);
                 for (int c = n + span; c < Np; c += span) store_codes(to + c, 0);
-                if (n % 32 == 0 && n < N) sz[(int64_t)m * ((N + 31) / 32) + n / 32] = code.scale;
+                if (n % 32 == 0 && (WHOLE || n < N)) sz[(int64_t)m * ((N + 31) / 32) + n / 32] = code.scale;
             }
         }
-        if (m >= M || n >= N) return;
-        Vec<YT, 8> r;
-        if (z) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) r.v[e] = from_f32<YT>(v.v[e]);
-            store_vec_n<YT, 8>(z + (int64_t)m * N + n, r, N - n);
-        }
+        if (!WHOLE && (m >= M || n >= N)) return;
+        if (z) put<WHOLE>(z + (int64_t)m * N + n, n, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v.v[e] = act_of<ACT, exact_acts<YT, YT>()>(v.v[e]);
         if (residual)
 #pragma unroll
             for (int e = 0; e < 8; ++e) v.v[e] += to_f32(item.residual.v[e]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r.v[e] = from_f32<YT>(v.v[e]);
-        store_vec_n<YT, 8>(y + (int64_t)m * ys + n, r, N - n);
+        put<WHOLE>(y + (int64_t)m * ys + n, n, v);
     }
 };
 
@@ -190,7 +203,10 @@ __global__ __launch_bounds__(kDotWaves * 64) void k_q8_dot(Q8Args a, EPI epi, in
     if (m < a.M)
 #pragma unroll
         for (int e = 0; e < 8; ++e) v.v[e] = (float)sums[m][g * 8 + e];
-    epi.with([&](auto act) { epi.template store<decltype(act)::value>(m, n, v, blocks * COLS, epi.column(n), epi.item(m, n)); });
+    epi.with([&](auto act) {
+        epi.template store<decltype(act)::value, false>(m, n, v, blocks * COLS, epi.template column<false>(n),
+                                                        epi.template item<false>(m, n));
+    });
 }
 
 template <typename YT>

@@ -56,12 +56,13 @@ __device__ __forceinline__ void wait_all_but() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
 }
 
-// EPI, an epilogue: column(n) and item(m, n) read, for any m and n, what belongs
-// to 8 columns and to 8 columns of a row; with(f) calls f once with the
-// activation; store<ACT>(m, n, 8 sums, span, column, item) ends it, for any m
-// and n: four neighbouring lanes (16 apart) have 32 columns of a row, and the
-// lanes of the last columns see to what stands behind them, `span` being the
-// distance to the columns that no lane has.
+// EPI, an epilogue: column(n) and item(m, n) read what belongs to 8 columns and to
+// 8 columns of a row; with(f) calls f once with the activation; store<ACT>(m, n, 8
+// sums, span, column, item) ends it: four neighbouring lanes (16 apart) have 32
+// columns of a row, and the lanes of the last columns see to what stands behind
+// them, `span` being the distance to the columns that no lane has. Each WHOLE:
+// all rows and columns of the tile exist (asked for only
+// where plain()), or for any m and n.
 template <int BM, int BN, int WM, int WN, int PLANES, typename EPI>
 __device__ __forceinline__ void q8_block(const Q8Args &a, const EPI &epi, int b, int nb) {
     constexpr int BK = 128, THREADS = WM * WN * 64;
@@ -200,28 +201,35 @@ __device__ __forceinline__ void q8_block(const Q8Args &a, const EPI &epi, int b,
         return;
     }
     // what the epilogue reads is on its way a row of tiles ahead
-    typename EPI::Column col[TN / 2];
-    typename EPI::Item next[TN / 2];
+    const auto finish = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        typename EPI::Column col[TN / 2];
+        typename EPI::Item next[TN / 2];
 #pragma unroll
-    for (int j = 0; j < TN / 2; ++j) {
-        col[j] = epi.column(nc + j * 32);
-        next[j] = epi.item(mr, nc + j * 32);
-    }
-    epi.with([&](auto act) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            typename EPI::Item item[TN / 2];
-#pragma unroll
-            for (int j = 0; j < TN / 2; ++j) {
-                item[j] = next[j];
-                if (i + 1 < TM) next[j] = epi.item(mr + (i + 1) * 16, nc + j * 32);
-            }
-#pragma unroll
-            for (int j = 0; j < TN / 2; ++j)
-                epi.template store<decltype(act)::value>(mr + i * 16, nc + j * 32, sums(i, 2 * j), a.tiles_n * BN, col[j],
-                                                         item[j]);
+        for (int j = 0; j < TN / 2; ++j) {
+            col[j] = epi.template column<WHOLE>(nc + j * 32);
+            next[j] = epi.template item<WHOLE>(mr, nc + j * 32);
         }
-    });
+        epi.with([&](auto act) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                typename EPI::Item item[TN / 2];
+#pragma unroll
+                for (int j = 0; j < TN / 2; ++j) {
+                    item[j] = next[j];
+                    if (i + 1 < TM) next[j] = epi.template item<WHOLE>(mr + (i + 1) * 16, nc + j * 32);
+                }
+                // the loads stay in front of the stores: behind them they would wait for these
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < TN / 2; ++j)
+                    epi.template store<decltype(act)::value, WHOLE>(mr + i * 16, nc + j * 32, sums(i, 2 * j), a.tiles_n * BN,
+                                                                    col[j], item[j]);
+            }
+        });
+    };
+    if (m0 + BM <= a.M && n0 + BN <= a.N && epi.plain()) finish(std::true_type{});
+    else finish(std::false_type{});
 }
 
 template <int BM, int BN, int WM, int WN, int PLANES, typename EPI>
@@ -258,9 +266,9 @@ __device__ __forceinline__ void q8_join_block(const Q8Args &a, const EPI &epi, i
 #pragma unroll
         for (int e = 0; e < 8; ++e) s.v[e] = (float)t[e];
     }
-    const auto column = epi.column(n);
-    const auto item = epi.item(m, n);
-    epi.with([&](auto act) { epi.template store<decltype(act)::value>(m, n, s, ncol * 128, column, item); });
+    const auto column = epi.template column<false>(n);
+    const auto item = epi.template item<false>(m, n);
+    epi.with([&](auto act) { epi.template store<decltype(act)::value, false>(m, n, s, ncol * 128, column, item); });
 }
 inline int64_t q8_join_blocks(const Q8Args &a) {
     return a.splits > 1 ? (int64_t)((a.M + 15) / 16) * ((a.N + 127) / 128) : 0;
