@@ -4,7 +4,7 @@
 // residual and what is kept of z (as it is, or in codes of 32 columns, which
 // four lanes of a wave have) are in the epilogue.
 //
-// Up to four rows (single tokens) have a kernel of their own.
+// One or two rows (single tokens) and short batches have kernels of their own.
 #include "wq8_q8_gemm.h"
 #include "wq8_rows.h"
 
@@ -144,7 +144,7 @@ struct EpiQ8 {
     }
 };
 
-// Up to 4 rows: each weight is used so few times that it needs no matrix core,
+// One or two rows: each weight is used so few times that it needs no matrix core,
 // and reads best along its row. A wave takes 4096 bytes of a weight row at a
 // time, 16 a lane, four products an instruction, OUT columns in turn, two of them
 // with their loads in flight; the rows' codes stay in registers meanwhile. Sums
@@ -209,6 +209,107 @@ __global__ __launch_bounds__(kDotWaves * 64) void k_q8_dot(Q8Args a, EPI epi, in
     });
 }
 
+// A short batch: blocks of 16 or 32 rows by 32 columns whose four waves take every
+// fourth k step each, so that few steps follow one another. A wave loads its own
+// lines of both operands into buffers of its own and waits for no other; the
+// sums of the four, whole numbers, meet at the end. 16 rows of 10240 x 10240 take
+// 18.8 us, 5.6 TB/s of weights, and 23.8 in a tile whose k steps are split over
+// blocks; 64 rows of 1280 x 1280 3.8 us, of which 2.2 are the launch, and 5.7 in
+// the smallest tile, whose ten steps follow one another.
+constexpr int kThinWaves = 4, kThinCols = 32;
+constexpr int thin_depth(int rt) { return rt == 1 ? 3 : 2; }  // two blocks fit a compute unit
+constexpr int thin_lds(int rt) { return kThinWaves * thin_depth(rt) * (rt * 16 + kThinCols) * 128; }
+
+template <int RT, typename EPI>
+__global__ __launch_bounds__(kThinWaves * 64) void k_q8_thin(Q8Args a, EPI epi, int blocks) {
+    constexpr int D = thin_depth(RT), AROWS = RT * 16, STAGE = (AROWS + kThinCols) * 128, AL = AROWS / 8, BL = kThinCols / 8;
+    extern __shared__ __align__(128) char smem[];
+    int b;
+    if (!block_number(blocks, b)) return;
+    b = xcd_block(b, blocks);  // blocks of the same columns behind one cache
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tm = (a.M + AROWS - 1) / AROWS, col = b / tm, m0 = (b - col * tm) * AROWS, n0 = col * kThinCols;
+    int8_t *const lds = (int8_t *)smem + wave * D * STAGE;
+    uint32_t off[AL + BL];
+#pragma unroll
+    for (int i = 0; i < AL + BL; ++i) {  // 8 rows of 128 bytes a load
+        const bool first = i < AL;
+        const int row = (first ? i : i - AL) * 8 + (lane >> 3);
+        const int unit = first ? swizzle<int8_t, true, false, 16>(row, lane & 7) : swizzle<int8_t, true, true, 16>(row, lane & 7);
+        off[i] = first ? (uint32_t)min(row, a.M - 1 - m0) * (uint32_t)a.lda + unit * 16
+                       : (uint32_t)min(row, a.N - 1 - n0) * (uint32_t)a.ldb + unit * 16;
+    }
+    const int n = (a.steps - wave + kThinWaves - 1) / kThinWaves;  // of this wave
+    const auto send = [&](int i) {
+        const int64_t k = (int64_t)(wave + i * kThinWaves) * 128;
+        const __amdgpu_buffer_rsrc_t ra =
+            __builtin_amdgcn_make_buffer_rsrc((void *)(a.A + (int64_t)m0 * a.lda + k), 0, -1, kBufferFlags);
+        const __amdgpu_buffer_rsrc_t rb =
+            __builtin_amdgcn_make_buffer_rsrc((void *)(a.B + (int64_t)n0 * a.ldb + k), 0, -1, kBufferFlags);
+        const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)(lds + i % D * STAGE);
+#pragma unroll
+        for (int j = 0; j < AL + BL; ++j) {
+            const uint32_t m0reg = __builtin_amdgcn_readfirstlane(at + j * 1024);
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                         :
+                         : "s"(m0reg), "v"(off[j]), "s"(j < AL ? ra : rb)
+                         : "memory");
+        }
+    };
+    i32x4 acc[RT][2] = {};
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d)
+        if (d < n) send(d);
+    for (int i = 0; i < n; ++i) {
+        if (D == 2 || n - i < D - 1) wait_all_but<0>();
+        else wait_all_but<(AL + BL) * (D - 2)>();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last step's reads: their buffer is filled anew
+        if (i + D - 1 < n) send(i + D - 1);
+        const int8_t *const buf = lds + i % D * STAGE;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            i32x4 fa[RT], fb[2];
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                fa[t] = *(const i32x4 *)(buf + lds_unit<int8_t, true, false, 16>(t * 16 + (lane & 15), kk * 4 + (lane >> 4)));
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                fb[j] = *(const i32x4 *)(buf + AROWS * 128 +
+                                         lds_unit<int8_t, true, true, 16>(row_of<true>(lane & 15, j), kk * 4 + (lane >> 4)));
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[t], acc[t][j], 0, 0, 0);
+        }
+    }
+    const int t = wave, m = m0 + t * 16 + (lane & 15), c = n0 + (lane >> 4) * 8;  // a wave ends a tile of rows
+    typename EPI::Column column;
+    typename EPI::Item item;
+    if (t < RT) {
+        column = epi.template column<false>(c);
+        item = epi.template item<false>(m, c);
+    }
+    __syncthreads();
+    i32x4 *const red = (i32x4 *)smem;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) red[((wave * RT + r) * 2 + j) * 64 + lane] = acc[r][j];
+    __syncthreads();
+    if (t >= RT) return;
+    Vec<float, 8> v;
+    i32x4 sum[2] = {};
+#pragma unroll
+    for (int w = 0; w < kThinWaves; ++w)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) sum[j] += red[((w * RT + t) * 2 + j) * 64 + lane];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v.v[e] = (float)sum[0][e], v.v[4 + e] = (float)sum[1][e];
+    epi.with([&](auto act) {
+        epi.template store<decltype(act)::value, false>(m, c, v, (a.N + kThinCols - 1) / kThinCols * kThinCols, column, item);
+    });
+}
+
 template <typename YT>
 struct RunQ8 {
     const Q8Geo &g;
@@ -253,11 +354,20 @@ struct RunQ8 {
         else go(k_q8_dot<ROWS, 2, EpiQ8<YT>>, 8);
     }
 
+    template <int RT>
+    void thin() const {
+        const int blocks = ((g.M + RT * 16 - 1) / (RT * 16)) * ((g.N + kThinCols - 1) / kThinCols);
+        const auto kernel = k_q8_thin<RT, EpiQ8<YT>>;
+        if constexpr (thin_lds(RT) > 65536)
+            (void)hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, thin_lds(RT));
+        hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(kThinWaves * 64), thin_lds(RT), st, args(), epi(), blocks);
+    }
+
     void run() const {
         if (g.f.tile >= 0) return pick_q8_tile(g.f.tile, *this);
+        if (g.f.tile == kQ8Thin) return g.M <= 16 ? thin<1>() : thin<2>();
         if (g.M == 1) few<1>();
-        else if (g.M == 2) few<2>();
-        else few<4>();
+        else few<2>();
     }
 };
 

@@ -39,7 +39,7 @@ struct Q8Args {
 // Rows of LDS of a k step, and its buffers: what leaves room for two blocks on a
 // compute unit, two at least.
 constexpr int q8_rows(int bm, int bn, int planes) { return (planes > 1 ? 2 : 1) * bm + bn; }
-constexpr int q8_depth(int rows) { return rows <= 144 ? 4 : rows <= 192 || rows == 384 ? 3 : 2; }
+constexpr int q8_depth(int rows) { return rows <= 128 ? 4 : rows <= 192 || rows == 384 ? 3 : 2; }
 template <int BM, int BN, int PLANES, typename K>
 size_t q8_lds(K kernel) {
     constexpr int rows = q8_rows(BM, BN, PLANES);
@@ -299,8 +299,7 @@ void pick_q8_tile(int tile, const R &run) {
         case 0: return run.template operator()<256, 256, 2, 4>();
         case 1: return run.template operator()<128, 128, 2, 2>();
         case 2: return run.template operator()<128, 64, 2, 2>();
-        case 3: return run.template operator()<64, 64, 2, 2>();
-        default: return run.template operator()<16, 128, 1, 2>();
+        default: return run.template operator()<64, 64, 2, 2>();
     }
 }
 template <typename R>

@@ -45,8 +45,11 @@ wq8_status launch_unpack(const RowsGeo &g, wq8_dtype xdt, const int8_t *codes, c
 // 128 x 128, and what a lower plane carries.
 constexpr int kQ8MaxSteps = 512;
 
+constexpr int kQ8Rows = -1;  // the kernel for up to 2 rows
+constexpr int kQ8Thin = -2;  // the kernel for a short batch
+
 struct Q8Shape {
-    int tile;      // index into kQ8Tiles (backward: kQ8PairTiles), -1: the kernel for up to 4 rows
+    int tile;      // index into kQ8Tiles (backward: kQ8PairTiles), or one of the below
     int splits, ksteps;
 };
 
@@ -82,7 +85,7 @@ struct Q8Tile {
     int bm, bn, blocks;
     double rate;
 };
-constexpr Q8Tile kQ8Tiles[] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.8}, {128, 64, 2, 0.62}, {64, 64, 2, 0.45}, {16, 128, 2, 0.3}};
+constexpr Q8Tile kQ8Tiles[] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.8}, {128, 64, 2, 0.62}, {64, 64, 2, 0.45}};
 constexpr Q8Tile kQ8PairTiles[] = {{256, 128, 1, 1.0}, {128, 128, 1, 0.92}, {128, 64, 2, 0.72}, {64, 64, 2, 0.6}};
 
 wq8_status launch_q8_forward(const Q8Geo &g, wq8_dtype ydt, const Q8Ptrs &p, void *stream);

@@ -134,11 +134,29 @@ struct Product {
     int64_t M, N, steps;
 };
 
+// The forward's kernel for short batches: microseconds of its blocks of 32 rows by
+// 32 columns, two a compute unit, whose waves take a quarter of the k steps each.
+// A round that leaves units with one block is half as long; a step takes 0.22 us
+// where no block has a neighbour, 0.5 where one round has it all, 0.7 in many. What
+// it reads through the caches comes at 17 TB/s at best, the weights at 5.5. 64 rows
+// of 5120 x 5120 take 7.8 us so and 11.9 in the best tile, 512 rows 38.8 and 26.0.
+double thin_us(const Product &q) {
+    const double blocks = (double)(ceil_div(q.M, q.M <= 16 ? 16 : 32) * ceil_div(q.N, 32)), steps = (double)ceil_div(q.steps, 4);
+    const double halves = ceil(blocks / kCus);
+    const double us = halves <= 1 ? 0.22 * steps : halves <= 2 ? 0.5 * steps : halves / 2 * (2.0 + 0.7 * steps) - 2.2;
+    const double read = fmax(blocks * 64 / 17.0, (double)q.N / 5.5) * (double)q.steps * 128e-6;
+    return 2.2 + fmax(us, read);
+}
+
 void choose_q8(const Product *q, int count, int planes, Q8Shape *const *out) {
     constexpr int kMost = 16;
     double least = 1e30;
     const bool pair = planes > 1;
-    for (int i = 0; i < (pair ? 4 : 5); ++i) {
+    if (!pair && q[0].steps <= kQ8MaxSteps) {
+        least = thin_us(q[0]);
+        *out[0] = {kQ8Thin, 1, (int)q[0].steps};
+    }
+    for (int i = 0; i < 4; ++i) {
         const Q8Tile &g = pair ? kQ8PairTiles[i] : kQ8Tiles[i];
         const double rate = 9.5 * g.rate;  // M operations per us and compute unit
         // a step's loads, barrier and LDS reads take a quarter of a microsecond
@@ -164,6 +182,7 @@ void choose_q8(const Product *q, int count, int planes, Q8Shape *const *out) {
             const int64_t n = ceil_div(blocks, kCus);
             double us = count == 1 ? (double)n * longest * step : (double)ceil_div(work, kCus) * step + 0.25 * longest * step;
             if (us < longest * step) us = longest * step;
+            if (!pair) us = fmax(us, (double)(q[0].M + q[0].N) * (double)q[0].steps * 128e-6 / 5.5);  // read from memory
             if (n == 1 && g.blocks > 1) us *= 1.3;
             us += (double)ceil_div(n, g.blocks) * (i == 0 ? 10.0 : i == 1 ? 4.0 : 2.5);
             if (join > 0.0) us += (count == 1 ? 3.0 : 5.0) + join;
@@ -201,8 +220,11 @@ wq8_status build_q8linear(const wq8_q8linear_desc *d, wq8_q8linear_plan *p) {
     p->ydt = d->y_dtype;
     g.planes = p->xdt == WQ8_BF16 ? 2 : 4;
     const int64_t steps = g.Kp / 128;
-    if (g.M <= 4 && steps <= kQ8MaxSteps) {
-        g.f = {-1, 1, (int)steps};
+    // two rows at most: 3.1 us for 1280 x 1280, 17.6 for 10240 x 10240, where the
+    // kernel for short batches takes 3.4 and 18.8; at three rows 3.8 and 18.2, and
+    // 7.6 for 5120 x 5120 where that takes 5.0
+    if (g.M <= 2 && steps <= kQ8MaxSteps) {
+        g.f = {kQ8Rows, 1, (int)steps};
     } else {
         const Product f = {g.M, g.N, steps};
         Q8Shape *const fs[1] = {&g.f};
@@ -218,7 +240,9 @@ wq8_status build_q8linear(const wq8_q8linear_desc *d, wq8_q8linear_plan *p) {
     if (g.chunk < 16) g.chunk = 16;
     g.nchunk = (int)ceil_div(g.M, g.chunk);
     const auto tiles = [](const Q8Shape &s, const Q8Tile *t, int64_t M, int64_t N) {
-        return s.tile < 0 ? ceil_div(N, 8) : ceil_div(M, t[s.tile].bm) * ceil_div(N, t[s.tile].bn) * s.splits;
+        if (s.tile == kQ8Rows) return ceil_div(N, 8);
+        if (s.tile == kQ8Thin) return ceil_div(M, 16) * ceil_div(N, 32);
+        return ceil_div(M, t[s.tile].bm) * ceil_div(N, t[s.tile].bn) * s.splits;
     };
     const int64_t lim = (int64_t)1 << 31;
     const int64_t lines = (int64_t)(g.Mp / 128) * (g.Kp / 128) + (int64_t)(g.Np / 128) * (g.Kp / 128);

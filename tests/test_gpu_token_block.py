@@ -135,14 +135,14 @@ def test_graph_replays():
 
 def test_two_graphs_share_a_workspace():
     """Two captured products that use one workspace, replayed in turn on one stream."""
-    p = q.Q8LinearPlan(200, 9000, 64, act="silu", x_dtype=BF)
+    p = q.Q8LinearPlan(200, 70000, 64, act="silu", x_dtype=BF)
     assert p.workspace_bytes > 0
     ws = torch.empty(max(p.workspace_bytes, p.backward_workspace_bytes), dtype=torch.uint8, device="cuda")
-    pack = q.QuantPlan(200, 9000), q.QuantPlan(64, 9000)
+    pack = q.QuantPlan(200, 70000), q.QuantPlan(64, 70000)
     sets, graphs = [], []
     for seed in (1, 2):
         g = torch.Generator().manual_seed(seed)
-        x, w = torch.randn(200, 9000, generator=g).cuda(), torch.randn(64, 9000, generator=g).cuda()
+        x, w = torch.randn(200, 70000, generator=g).cuda(), torch.randn(64, 70000, generator=g).cuda()
         dy = torch.randn(200, 64, generator=g).to(BF).cuda()
         a = q.wq8_quant_pack(pack[0], x) + q.wq8_quant_pack(pack[1], w)
         y, z = p.empty_output(), p.empty_z()

@@ -108,7 +108,7 @@ def test_pointers_are_refused_before_launch():
     refused(lib.wq8_rms_backward, m.handle, ok,
             [({0: None}, -1), ({1: None}, -1), ({2: None}, -1), ({3: odd}, -5), ({4: odd}, -5), ({5: None}, -1), ({5: p(0)}, -1),
              ({5: p(1)}, -1), ({6: p(5)}, -1), ({6: p(3)}, -1), ({6: odd}, -5), ({7: None}, -1), ({8: wb - 1}, -4), ({7: odd}, -5)])
-    q = T.Q8LinearPlan(200, 9000, 64, act="silu")
+    q = T.Q8LinearPlan(200, 70000, 64, act="silu")
     assert q.workspace_bytes > 0
     # xq sx wq sw bias residual y z zq sz workspace
     ok = [p(0), p(1), p(2), p(3), p(4), p(5), p(6), p(7), p(8), p(9), p(10), q.workspace_bytes, None]
@@ -270,9 +270,9 @@ class _Allocations:
 
 
 def op_calls():
-    n, m, p = T.QuantPlan(6, 8), T.RmsPlan(600, 8), T.Q8LinearPlan(200, 9000, 64, act="silu")
+    n, m, p = T.QuantPlan(6, 8), T.RmsPlan(600, 8), T.Q8LinearPlan(200, 70000, 64, act="silu")
     x, g = torch.zeros(600, 8), torch.zeros(8)
-    xq, wq = torch.zeros(200, 9088, dtype=I8), torch.zeros(64, 9088, dtype=I8)
+    xq, wq = torch.zeros(200, 70016, dtype=I8), torch.zeros(64, 70016, dtype=I8)
     sx, sw, y = torch.zeros(200), torch.zeros(64), torch.zeros(200, 64)
     c, s = torch.zeros(6, 128, dtype=I8), torch.zeros(6)
     return [

@@ -2,12 +2,14 @@
 instance that they can choose, with ends inside tiles and steps.
 
 FORWARD and BACKWARD: rows, Cin, Cout; ROWS: columns. The instances that they
-have to reach: tiles, + k split; "rows" the kernel of up to four rows; lanes x
+have to reach: tiles, + k split; "rows" the kernel of one or two rows,
+thin16 and thin32 those of short batches; lanes x
 steps of a row held in registers, 0x0 one that is read twice."""
 
 FORWARD = [(1, 145, 37), (2, 145, 37), (4, 1451, 97), (5, 175, 37), (5, 1551, 41), (5, 4091, 1109), (8512, 143, 71), (4134, 2811, 35),
-           (514, 139, 6649), (154, 6569, 5551), (8257, 519, 1555), (1864, 7473, 2179)]
-FORWARD_INSTANCES = {"rows", "64x64", "64x64+", "16x128+", "128x64", "128x64+", "128x128", "128x128+", "256x256", "256x256+"}
+           (514, 139, 6649), (154, 6569, 5551), (8257, 519, 1555), (1864, 7473, 2179),
+           (16, 4091, 333), (38, 139, 8209), (3, 12835, 41), (97, 9697, 2659), (144, 7326, 6005)]
+FORWARD_INSTANCES = {"rows", "thin16", "thin32", "64x64", "64x64+", "128x64", "128x64+", "128x128", "128x128+", "256x256", "256x256+"}
 
 BACKWARD = {
     "f32": [(33, 139, 43), (917, 177, 37), (35, 189, 925), (33, 3627, 491), (6172, 267, 35), (33, 367, 4943), (553, 323, 4925),

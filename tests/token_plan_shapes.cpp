@@ -28,8 +28,8 @@ int main() {
             const wq8_q8linear_desc d = {rows, a[0], a[1], WQ8_ACT_GELU, (wq8_dtype)a[2], (wq8_dtype)a[2], WQ8_NHWC, 0, 0, 0, 0};
             wq8_q8linear_plan *p;
             if (wq8_q8linear_plan_create(&d, &p) != WQ8_OK) return 1;
-            const auto print = [](const char *name, const Q8Tile *t, const Q8Shape &s) {
-                if (s.tile < 0) printf("%s=rows ", name);
+            const auto print = [&](const char *name, const Q8Tile *t, const Q8Shape &s) {
+                if (s.tile < 0) printf("%s=%s ", name, s.tile != kQ8Thin ? "rows" : rows <= 16 ? "thin16" : "thin32");
                 else printf("%s=%dx%d%s ", name, t[s.tile].bm, t[s.tile].bn, s.splits > 1 ? "+" : "");
             };
             print("f", kQ8Tiles, p->geo.f);
