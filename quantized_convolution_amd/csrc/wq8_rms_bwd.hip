@@ -4,6 +4,8 @@
 // one read of dy, h and dh, one write of dx. A thread has the same columns of
 // every row, so dgamma is summed in its registers, then over the block's waves
 // in LDS and over the blocks by a second kernel, in a fixed order.
+// Memory bounds it: 8192 x 1280 bf16 takes 18 to 23 us (84 MB, 3.7 to 4.7 TB/s)
+// and 4 more for the parts of dgamma, 1001 x 333 f32 4.4 and 3.
 #include "wq8_rows.h"
 
 namespace wq8 {
