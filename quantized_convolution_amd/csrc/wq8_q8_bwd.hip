@@ -11,9 +11,9 @@
 // column sums' join side by side; a last one joins products that are split along
 // k. dz is formed twice rather than kept: 3 bytes a value are read again where 4
 // would be written and read. 8192 x 640 x 2560 bf16 with gelu and z in codes takes
-// 28 + 47 + 75 us: the first two are bound by gelu's slope and by the loads' latency
-// (2.3 and 3.1 TB/s), the third by the matrix cores (1430 TOPS in tiles of 128 x 128).
-// In fp32, 4 digits, 1001 x 333 x 515 takes 6.7 + 11.6 + 11.7.
+// 28 + 45 + 75 us: the first two are bound by gelu's slope and by the loads' latency
+// (2.3 and 3.3 TB/s), the third by the matrix cores (1430 TOPS in tiles of 128 x 128).
+// In fp32, 4 digits, 1001 x 333 x 515 takes 6.6 + 7.8 + 11.4.
 #include "wq8_q8_gemm.h"
 #include "wq8_rows.h"
 
@@ -47,39 +47,44 @@ __device__ __forceinline__ float slope_of(float z) {
     return act_slope<ACT, EXACT>(z);
 }
 
-// What dz of 8 columns of a row is made of, and dz: zeros past the last column (a
+// What dz of V columns of a row is made of, and dz: zeros past the last column (a
 // group of z's codes that stands for NaN has columns before it as well, and makes
 // the row's products NaN).
-template <typename YT, int ZF>
+template <typename YT, int ZF, int V = kV>
 struct DzParts {
-    Vec<YT, kV> dy, z;
-    uint64_t codes;
+    using Codes = std::conditional_t<V == 8, uint64_t, uint32_t>;
+    Vec<YT, V> dy, z;
+    Codes codes;
     float scale;
 
-    // WHOLE: all 8 columns exist.
+    __device__ __forceinline__ static Vec<YT, V> some(const YT *row, int c, int C) {
+        if constexpr (V == kV) return load_any<YT>(row, c, C);
+        else return load_vec_n<YT, V>(row + c, C - c);
+    }
+    // WHOLE: all columns exist.
     template <bool WHOLE>
     __device__ __forceinline__ void load(const Q8Geo &g, const Q8Ptrs &a, int64_t row, int c) {
-        if constexpr (WHOLE) dy = load_vec<YT, kV>((const YT *)a.dy + row * g.ys + c);
-        else dy = load_any<YT>((const YT *)a.dy + row * g.ys, c, g.N);
+        if constexpr (WHOLE) dy = load_vec<YT, V>((const YT *)a.dy + row * g.ys + c);
+        else dy = some((const YT *)a.dy + row * g.ys, c, g.N);
         if constexpr (ZF == kZValues) {
-            if constexpr (WHOLE) z = load_vec<YT, kV>((const YT *)a.z_in + row * g.N + c);
-            else z = load_any<YT>((const YT *)a.z_in + row * g.N, c, g.N);
+            if constexpr (WHOLE) z = load_vec<YT, V>((const YT *)a.z_in + row * g.N + c);
+            else z = some((const YT *)a.z_in + row * g.N, c, g.N);
         }
         if constexpr (ZF == kZCodes) {
-            codes = *(const uint64_t *)(a.zq_in + row * g.Np + min(c, g.Np - kV));
+            codes = *(const Codes *)(a.zq_in + row * g.Np + min(c, g.Np - V));
             scale = a.sz_in[row * ((g.N + 31) / 32) + min(c, g.N - 1) / 32];
         }
     }
     template <int ACT, bool EXACT>
-    __device__ __forceinline__ void form(float (&dz)[kV]) const {
+    __device__ __forceinline__ void form(float (&dz)[V]) const {
 #pragma unroll
-        for (int k = 0; k < kV; ++k) {
+        for (int k = 0; k < V; ++k) {
             dz[k] = to_f32(dy.v[k]);
             if constexpr (ACT != WQ8_ACT_NONE) {
                 float v;
                 // code scale, rounded once, from code + 128: unsigned bytes convert in one step
                 if constexpr (ZF == kZCodes)
-                    v = fmaf((float)(uint8_t)((codes ^ 0x8080808080808080ull) >> (8 * k)), scale, -128.0f * scale);
+                    v = fmaf((float)(uint8_t)((codes ^ (Codes)0x8080808080808080ull) >> (8 * k)), scale, -128.0f * scale);
                 else v = to_f32(z.v[k]);
                 dz[k] *= slope_of<ACT, EXACT>(v);
             }
@@ -254,30 +259,33 @@ struct Digits {
     }
 };
 
-// 128 rows x 64 columns: a thread has 4 rows of 8 columns.
+// 128 rows x 32 columns: a thread has 4 rows of 4 columns. With 8 columns it has
+// fewer and longer waves: 1024 x 640 x 640 then takes 22.2 us for 20.0 in bf16 and
+// 33.1 for 29.3 in fp32, 8192 x 640 x 2560 130.3 for 128.5 and 238 for 248.
 template <typename XT, typename YT, int ZF, int PLANES>
 __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_dx, int want_dw, int nb) {
+    constexpr int V = 4, COLS = 8 * V, ACROSS = COLS / 4, ALONG = 256 / ACROSS;
     constexpr int LD = 128 + 4;  // bytes between columns in LDS: a wave's stores meet every bank twice
-    __shared__ __align__(16) int8_t tile[PLANES * 64 * LD];
-    __shared__ float cpart[16][64];
-    __shared__ Digits<PLANES> cdig[64], rdig[128];
+    __shared__ __align__(16) int8_t tile[PLANES * COLS * LD];
+    __shared__ float cpart[ALONG][COLS];
+    __shared__ Digits<PLANES> cdig[COLS], rdig[128];
     int b;
     if (!block_number(nb, b)) return;
     b = xcd_block(b, nb);  // blocks that share lines of z's codes and of the rows' digits behind one cache
-    const int across = g.Np / 64, br = b / across, r0 = br * 128, c0 = (b - br * across) * 64;
-    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3, c = c0 + cg * kV;
-    DzParts<YT, ZF> parts[4];
+    const int across = g.Np / COLS, br = b / across, r0 = br * 128, c0 = (b - br * across) * COLS;
+    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3, c = c0 + cg * V;
+    DzParts<YT, ZF, V> parts[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = min(r0 + rg * 4 + i, g.M - 1);
-        if (c0 + 64 <= g.N) parts[i].template load<true>(g, a, r, c);
+        if (c0 + COLS <= g.N) parts[i].template load<true>(g, a, r, c);
         else parts[i].template load<false>(g, a, r, c);
     }
-    if (want_dw) {  // 4 columns a thread, 16 threads along the first pass's chunks
-        const int c4 = (threadIdx.x & 15) * 4, q = threadIdx.x >> 4;
+    if (want_dw) {  // 4 columns a thread, the others along the first pass's chunks
+        const int c4 = (threadIdx.x % ACROSS) * 4, q = threadIdx.x / ACROSS;
         Vec<float, 4> m = {};
 #pragma unroll 8
-        for (int i = q; i < g.nchunk; i += 16) {
+        for (int i = q; i < g.nchunk; i += ALONG) {
             const Vec<float, 4> v = load_vec<float, 4>(a.colmax + (int64_t)i * g.Np + c0 + c4);
 #pragma unroll
             for (int k = 0; k < 4; ++k) m.v[k] = larger(m.v[k], v.v[k]);
@@ -292,7 +300,7 @@ __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_d
         rdig[threadIdx.x].find(bits_of(m));
         if (c0 == 0 && r0 + (int)threadIdx.x < g.M) a.rscale[r] = Digits<PLANES>::scale(bits_of(m));
     }
-    float dz[4][kV];
+    float dz[4][V];
     with_act(g.act, [&](auto act) {
         constexpr int A = decltype(act)::value;
         if constexpr ((A == WQ8_ACT_NONE) == (ZF == kZNone))
@@ -300,34 +308,31 @@ __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_d
             for (int i = 0; i < 4; ++i) parts[i].template form<A, exact_acts<XT, YT>()>(dz[i]);
     });
     __syncthreads();
-    if (want_dw && threadIdx.x < 64) {
+    if (want_dw && threadIdx.x < COLS) {
         float t = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) t = larger(t, cpart[i][threadIdx.x]);
+        for (int i = 0; i < ALONG; ++i) t = larger(t, cpart[i][threadIdx.x]);
         cdig[threadIdx.x].find(bits_of(t));
         if (br == 0 && c0 + (int)threadIdx.x < g.N) a.cscale[c0 + threadIdx.x] = Digits<PLANES>::scale(bits_of(t));
     }
     if (want_dx) {
-        const Vec<float, kV> sw = load_any<float>(a.sw, c, g.N);
+        const Vec<float, V> sw = load_vec_n<float, V>(a.sw + c, g.N - c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = r0 + rg * 4 + i;
             const Digits<PLANES> d = rdig[rg * 4 + i];
-            float u[kV];
+            float u[V];
 #pragma unroll
-            for (int k = 0; k < kV; ++k) u[k] = dz[i][k] * sw.v[k];
+            for (int k = 0; k < V; ++k) u[k] = dz[i][k] * sw.v[k];
             if (__builtin_expect(__any(d.up != 1.0f), 0))
 #pragma unroll
-                for (int k = 0; k < kV; ++k) u[k] *= d.up;
-            uint32_t lo[PLANES], hi[PLANES];
-            bytes_of<PLANES>({d(u[0]), d(u[1]), d(u[2]), d(u[3])}, lo);
-            bytes_of<PLANES>({d(u[4]), d(u[5]), d(u[6]), d(u[7])}, hi);
-            Digits<PLANES>::lower(lo);
-            Digits<PLANES>::lower(hi);
+                for (int k = 0; k < V; ++k) u[k] *= d.up;
+            uint32_t o[PLANES];
+            bytes_of<PLANES>({d(u[0]), d(u[1]), d(u[2]), d(u[3])}, o);
+            Digits<PLANES>::lower(o);
             if (r < g.M)
 #pragma unroll
-                for (int p = 0; p < PLANES; ++p)
-                    *(uint64_t *)(a.ur + ((int64_t)p * g.M + r) * g.Np + c) = (uint64_t)hi[p] << 32 | lo[p];
+                for (int p = 0; p < PLANES; ++p) *(uint32_t *)(a.ur + ((int64_t)p * g.M + r) * g.Np + c) = o[p];
         }
     }
     if (!want_dw) return;
@@ -336,8 +341,8 @@ __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_d
 #pragma unroll
     for (int i = 0; i < 4; ++i) sx[i] = r0 + rg * 4 + i < g.M ? a.sx[r0 + rg * 4 + i] : 0.0f;  // past the end dz is the last row's
 #pragma unroll
-    for (int k = 0; k < kV; ++k) {
-        const Digits<PLANES> d = cdig[cg * kV + k];
+    for (int k = 0; k < V; ++k) {
+        const Digits<PLANES> d = cdig[cg * V + k];
         float u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) u[i] = dz[i][k] * sx[i];
@@ -348,13 +353,13 @@ __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_d
         bytes_of<PLANES>({d(u[0]), d(u[1]), d(u[2]), d(u[3])}, o);
         Digits<PLANES>::lower(o);
 #pragma unroll
-        for (int p = 0; p < PLANES; ++p) *(uint32_t *)(tile + (p * 64 + cg * kV + k) * LD + rg * 4) = o[p];
+        for (int p = 0; p < PLANES; ++p) *(uint32_t *)(tile + (p * COLS + cg * V + k) * LD + rg * 4) = o[p];
     }
     __syncthreads();
     // 8 bytes a lane, 16 lanes a line
 #pragma unroll
-    for (int i = 0; i < PLANES * 4; ++i) {
-        const int line = i * 16 + (threadIdx.x >> 4), p = line / 64, col = line % 64, part = (threadIdx.x & 15) * 8;
+    for (int i = 0; i < PLANES * COLS / 16; ++i) {
+        const int line = i * 16 + (threadIdx.x >> 4), p = line / COLS, col = line % COLS, part = (threadIdx.x & 15) * 8;
         const uint32_t *const from = (const uint32_t *)(tile + line * LD + part);
         if (c0 + col < g.N)
             *(uint64_t *)(a.uc + ((int64_t)p * g.N + c0 + col) * g.Mp + r0 + part) = (uint64_t)from[1] << 32 | from[0];
@@ -494,7 +499,7 @@ void prepare(const Q8Geo &g, const Q8Ptrs &p, hipStream_t st) {
     hipLaunchKernelGGL((k_q8_max<XT, YT, ZF>), grid_of(nm + nx + nw), dim3(kMaxWaves * 64), 0, st, g, p, (int)nm, (int)nx,
                        (int)(nm + nx + nw));
     if (!p.dx && !p.dw) return;
-    const int64_t nd = (int64_t)(g.Mp / 128) * (g.Np / 64);
+    const int64_t nd = (int64_t)(g.Mp / 128) * (g.Np / 32);
     hipLaunchKernelGGL((k_q8_digits<XT, YT, ZF, PLANES>), grid_of(nd), dim3(256), 0, st, g, p, p.dx != nullptr, p.dw != nullptr,
                        (int)nd);
 }

@@ -248,7 +248,7 @@ wq8_status build_q8linear(const wq8_q8linear_desc *d, wq8_q8linear_plan *p) {
     const int64_t lines = (int64_t)(g.Mp / 128) * (g.Kp / 128) + (int64_t)(g.Np / 128) * (g.Kp / 128);
     if (tiles(g.f, kQ8Tiles, g.M, g.N) >= lim ||
         tiles(g.dx, kQ8PairTiles, g.M, g.K) + tiles(g.dw, kQ8PairTiles, g.N, g.K) + g.N >= lim ||
-        (int64_t)g.nchunk * g.ncol + lines >= lim || (int64_t)(g.Mp / 128) * (g.Np / 64) >= lim ||
+        (int64_t)g.nchunk * g.ncol + lines >= lim || (int64_t)(g.Mp / 128) * (g.Np / 32) >= lim ||
         ceil_div(g.M, 16) * ceil_div(g.N > g.K ? g.N : g.K, 128) >= lim)
         return fail(WQ8_ERR_UNSUPPORTED, "more than 2^31 blocks");
     const size_t M = g.M, N = g.N, K = g.K;

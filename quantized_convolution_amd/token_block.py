@@ -41,7 +41,7 @@ class Q8FeedForward:
         self.a, self.rstd = self.norm.empty_codes(device), self.norm.empty_rstd(device) if train else None
         self.h, self.u, self.uq = self.norm.empty_input(device), self.up.empty_output(device), self.inner.empty_codes(device)
         self.z = self.up.empty_z_codes(device) if train and act != "none" else (None, None)
-        self.out = self.down.empty_output(device)
+        self.out, self.stream = self.down.empty_output(device), None
         if train:
             self.du, self.da, self.dx = (torch.empty_like(t) for t in (self.u, self.h, self.h))
         self.pack()
@@ -74,6 +74,8 @@ class Q8FeedForward:
         """{name: gradient} for the last call; "x" is that of x and of the residual."""
         if not self.train:
             raise ValueError("made with train=False: nothing is kept for a backward")
+        if self.stream is None:
+            raise ValueError("nothing has been called yet that this could be the backward of")
         w, ws = self.w, self.ws
         _, dw2, db2 = wq8_q8linear_backward(self.down, dout, *self.uq, *self.w2, dx=self.du, want_dbias=True, workspace=ws)
         _, dw1, db1 = wq8_q8linear_backward(self.up, self.du, *self.a, *self.w1, zq=self.z[0], sz=self.z[1], dx=self.da,

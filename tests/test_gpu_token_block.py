@@ -279,3 +279,22 @@ def test_parameters():
     assert not any(t.requires_grad for t in gb.values())
     with pytest.raises(ValueError, match="an input requires a gradient"):
         a(x.cuda().requires_grad_())
+
+
+def test_backward_needs_a_call():
+    ff = Q8FeedForward(cuda(weights(F32)[0]), ROWS, C, F32)
+    with pytest.raises(ValueError, match="nothing has been called yet"):
+        ff.backward(torch.zeros(ROWS, C, device="cuda"))
+    with pytest.raises(ValueError, match="train=False"):
+        Q8FeedForward(cuda(weights(F32)[0]), ROWS, C, F32, train=False).backward(torch.zeros(ROWS, C, device="cuda"))
+
+
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_no_rows(with_residual):
+    """An empty batch: empty results, and gradients of the weights that are 0."""
+    ff = Q8FeedForward(cuda(weights(BF)[0]), 0, C, BF)
+    x = torch.zeros(0, C, dtype=BF, device="cuda")
+    assert ff(x, x.clone() if with_residual else None).shape == (0, C)
+    grads = ff.backward(x)
+    assert grads["x"].shape == (0, C)
+    assert all(not bool(grads[k].any()) and grads[k].shape == ff.w[k].shape for k in ff.w)

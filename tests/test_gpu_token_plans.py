@@ -55,6 +55,9 @@ def test_forward(rows, Cin, Cout, dtype):
         codes, scales = q.wq8_quant_pack(q.QuantPlan(rows, Cout, group=32), want)
         assert torch.equal(zq, codes) and torch.equal(sz, scales)
         check(y, R.forward(want, act, residual, DT[dtype]), "y")
+        over = residual.clone()
+        q.wq8_q8linear_forward(p, xq, sx, wq, sw, bias, over, y=over)
+        assert torch.equal(over, y)
 
 
 @pytest.mark.parametrize("kept", ["codes", "values"])
