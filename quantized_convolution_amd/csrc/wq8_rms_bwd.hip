@@ -4,8 +4,9 @@
 // one read of dy, h and dh, one write of dx. A thread has the same columns of
 // every row, so dgamma is summed in its registers, then over the block's waves
 // in LDS and over the blocks by a second kernel, in a fixed order.
-// Memory bounds it: 8192 x 1280 bf16 takes 18 to 23 us (84 MB, 3.7 to 4.7 TB/s)
-// and 4 more for the parts of dgamma, 1001 x 333 f32 4.4 and 3.
+// Memory bounds it: with the parts of dgamma 8192 x 1280 bf16 takes 21 us (84 MB,
+// 4.0 TB/s), 32768 x 1280 70 (4.8), 8192 x 16000 221 (4.8), 1001 x 333 f32 7.6, of
+// which two launches are 5.4. A row of 9000 read twice instead: 222 us for 145.
 #include "wq8_rows.h"
 
 namespace wq8 {
@@ -44,7 +45,7 @@ __device__ __forceinline__ Vec<XT, kV> grad(const Vec<XT, kV> &h, const Vec<YT, 
 }
 
 template <typename XT, typename YT, int L, int U>
-__global__ __launch_bounds__(L < 256 ? 256 : L) void k_rms_bwd(RowsGeo g, RmsPtrs a, int want_dgamma) {
+__global__ __launch_bounds__(L < 256 ? 256 : L, L == 64 && U == 3 ? 3 : 1) void k_rms_bwd(RowsGeo g, RmsPtrs a, int want_dgamma) {
     constexpr int PER = L < 256 ? 256 / L : 1;
     __shared__ float red[L > 64 ? 4 * L / 64 : 1];
     __shared__ float join[PER > 1 ? (PER - 1) * U * L * kV : 1];
@@ -196,6 +197,8 @@ void backward(const RowsGeo &g, const RmsPtrs &p, hipStream_t st) {
             go(k_rms_bwd<XT, YT, 256, 2>, 256);
         } else if (g.s.lanes == 512) {
             go(k_rms_bwd<XT, YT, 512, 2>, 512);
+        } else if (g.s.lanes == 1024) {
+            go(k_rms_bwd<XT, YT, 1024, 2>, 1024);
         } else {
             hipLaunchKernelGGL((k_rms_bwd_long<XT, YT>), grid_of(g.rows), dim3(1024), 0, st, g, p, g.rows);
             if (p.dgamma)

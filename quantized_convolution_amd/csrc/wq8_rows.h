@@ -160,7 +160,7 @@ __device__ __forceinline__ void reduce_row(float &sum, uint32_t &most, float *re
 // that the plan gives that shape: the others alone look for the row's end.
 template <int L, int U>
 constexpr int full_steps() {
-    return L == 1024 ? 2 : U == 8 ? (L == 64 ? 6 : 5) : U - 1;
+    return L == 1024 && U == 4 ? 2 : U == 8 ? (L == 64 ? 6 : 5) : U - 1;
 }
 
 template <typename T, int L, int U>

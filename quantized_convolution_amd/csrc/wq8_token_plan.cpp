@@ -81,6 +81,7 @@ RowShape backward_shape(int C) {
         if (stride <= 512 * steps) return {64, steps, 4};
     if (stride <= 4096) return {256, 2, 1};
     if (stride <= 8192) return {512, 2, 1};
+    if (stride <= 16384) return {1024, 2, 1};
     return {0, 0, 1};
 }
 
@@ -117,9 +118,14 @@ wq8_status build_rms(const wq8_rms_desc *d, wq8_rms_plan *p) {
     p->f.s = forward_shape(p->f.C);
     RowsGeo &g = p->b;
     g.s = backward_shape(g.C);
-    // as many blocks as run at once, three a compute unit by their registers
-    const int64_t blocks = (g.s.lanes == 512 || g.s.lanes == 0 ? 1 : 3) * kCus;
-    g.chunk = (int)round_up(ceil_div(g.rows, blocks), g.s.per);
+    // as many blocks as run at once by their registers (8192 x 5120 bf16, two a compute
+    // unit: 78 us, with three 97, with one 103), but no more than 256 of fewer than four
+    // rows: each has a part of dgamma to be joined (1001 x 2560 bf16 12.8 us, with one
+    // row a block 18.1)
+    const int L = g.s.lanes, U = g.s.unroll, units = L == 0 || L == 1024 ? 1 : L == 512 || U == 4 ? 2 : U == 3 ? 3 : 4;
+    g.chunk = (int)round_up(ceil_div(g.rows, units * kCus), g.s.per);
+    const int least = (int)ceil_div(g.rows, kCus);
+    if (g.chunk < 4) g.chunk = least < 4 ? (g.chunk < least ? least : g.chunk) : 4;
     g.nchunk = g.rows ? (int)ceil_div(g.rows, g.chunk) : 0;
     p->xdt = d->x_dtype;
     p->ydt = d->y_dtype;

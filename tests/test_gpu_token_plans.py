@@ -109,3 +109,20 @@ def test_rows(C, dtype):
         plain = q.wq8_quant_pack(q.QuantPlan(9, width, x_dtype=DT[dtype]), x.cuda())
         t = R.codes_of(x.float().numpy())
         assert torch.equal(plain[0].cpu(), t[0]) and torch.equal(plain[1].cpu(), t[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [333, 1290, 2100, 5000, 9000, 15001])
+def test_backward_rows_in_turn(C, dtype):
+    """Several rows a wave or block, one after the other, the last block with fewer."""
+    print("[case] rows in turn", C, dtype, flush=True)
+    rows = 4801 if C < 2048 else 601
+    g = torch.Generator().manual_seed(C)
+    h, dh, dy = (torch.randn(rows, C, generator=g).to(DT[dtype]) for _ in range(3))
+    gm = 1 + 0.2 * torch.randn(C, generator=g)
+    p = q.RmsPlan(rows, C, x_dtype=DT[dtype])
+    rstd = q.wq8_rms_forward(p, h.cuda(), gm.cuda(), want_rstd=True)[4]
+    dx, dg = q.wq8_rms_backward(p, dy.cuda(), h.cuda(), rstd, gm.cuda(), dh=dh.cuda())
+    want = R.Rms(h, 1e-6, gm).backward(dy, rstd.cpu(), dh, DT[dtype])
+    check(dx.cpu(), want["dx"], "dx")
+    check(dg.cpu(), want["dgamma"], "dgamma")

@@ -21,4 +21,4 @@ BACKWARD_INSTANCES = {f"{o}={t}" for o in ("dw", "dx") for t in ("64x64", "64x64
 
 ROWS = [7, 512, 600, 1200, 2000, 2100, 2600, 3100, 5000, 7000, 9000, 15000, 30000, 40000]
 ROWS_INSTANCES = {f"f={s}" for s in ("64x1", "64x2", "64x3", "64x4", "64x5", "64x6", "64x8", "256x3", "256x4", "256x5", "256x8", "1024x4",
-                                     "0x0")} | {f"b={s}" for s in ("64x1", "64x2", "64x3", "64x4", "256x2", "512x2", "0x0")}
+                                     "0x0")} | {f"b={s}" for s in ("64x1", "64x2", "64x3", "64x4", "256x2", "512x2", "1024x2", "0x0")}
