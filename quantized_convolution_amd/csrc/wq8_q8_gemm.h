@@ -241,6 +241,38 @@ __global__ __launch_bounds__(WM *WN * 64) void k_q8(Q8Args a, EPI epi) {
     if (block_number(nb, b)) q8_block<BM, BN, WM, WN, PLANES>(a, epi, b, nb);
 }
 
+// The sum over the splits of 8 columns from n on of row m, those past the end any
+// number. Loads stand under no condition, so that some are on their way together:
+// they start earlier at a row's end, and the sums are moved to their places.
+template <typename T, typename S>
+__device__ __forceinline__ void sum_splits(const Q8Args &a, int m, int n, S (&s)[8]) {
+    const int64_t size = (int64_t)a.M * a.N;
+    const T *const row = (const T *)a.partial + (int64_t)min(m, a.M - 1) * a.N;
+    S t[8] = {};
+    if (a.N < 8) {
+        for (int k = 0; k < a.splits; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += row[k * size + min(n + e, a.N - 1)];
+        return;
+    }
+    const int at = min(n, a.N - 8), shift = n - at;
+#pragma unroll 4
+    for (int k = 0; k < a.splits; ++k) {
+        const Vec<T, 8> v = load_vec<T, 8>(row + k * size + at);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] += v.v[e];
+    }
+#pragma unroll
+    for (int step = 4; step >= 1; step >>= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const S far = e + step < 8 ? t[e + step < 8 ? e + step : e] : S(0);
+            t[e] = (shift & step) ? far : t[e];
+        }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = t[e];
+}
+
 // Joins split products in the order of k and runs the epilogue: 32 columns of 16
 // rows a wave, 8 columns of a row a lane, as in the product. Whole numbers are
 // summed as such.
@@ -249,22 +281,12 @@ __device__ __forceinline__ void q8_join_block(const Q8Args &a, const EPI &epi, i
     const int lane = threadIdx.x & 63, ncol = (a.N + 127) / 128;
     const int row = b / ncol, col = b - row * ncol;
     const int m = row * 16 + (lane & 15), n = col * 128 + (threadIdx.x >> 6) * 32 + (lane >> 4) * 8;
-    const bool in = m < a.M && n < a.N;
     Vec<float, 8> s = {};
     if constexpr (PLANES > 1) {
-        for (int k = 0; k < a.splits; ++k) {
-            const Vec<float, 8> v =
-                load_vec_n<float, 8>((const float *)a.partial + ((int64_t)k * a.M + m) * a.N + n, in ? a.N - n : 0);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s.v[e] += v.v[e];
-        }
+        sum_splits<float>(a, m, n, s.v);
     } else {
         int64_t t[8] = {};
-        for (int k = 0; k < a.splits; ++k) {
-            const Vec<int, 8> v = load_vec_n<int, 8>((const int *)a.partial + ((int64_t)k * a.M + m) * a.N + n, in ? a.N - n : 0);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] += v.v[e];
-        }
+        sum_splits<int>(a, m, n, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s.v[e] = (float)t[e];
     }
