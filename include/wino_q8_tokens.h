@@ -103,10 +103,12 @@ wq8_status wq8_rms_backward(const wq8_rms_plan *plan, const void *dy, const void
  * and w^ = sw wq, what the codes stand for,
  *   dx = dz w^;  dw = dz^T x^;  dbias = sum_r dz
  * so no 16- or 32-bit activation or weight is read. dz sw (for dx) and dz sx (for
- * dw) are multiplied as whole numbers in fixed point: to 15 bits and a sign of
- * the largest magnitude of their row (column) where dx and dw are bf16, to 31
- * where they are f32. Each then is off by at most 2^-16 (2^-32) of that largest
- * one, or, in f32, its own rounding; the products and their sums are exact. dbias
+ * dw) are multiplied as whole numbers in fixed point, 31 bits and a sign of the
+ * largest magnitude of their row (column): each is off by at most 2^-32 of that
+ * largest one, or its own rounding. With round_dz, where dx and dw are bf16, they
+ * have 15 bits and a sign, and are off by at most 2^-16 of the largest one; where a
+ * row (column) holds one value some hundred times the others, that is more than
+ * bf16 results lose by themselves. The products and their sums are exact. dbias
  * sums fp32 values. A row of dz sw that holds an infinity or a NaN makes its row
  * of dx NaN, a column of dz sx its row of dw. */
 typedef struct wq8_q8linear_plan wq8_q8linear_plan; /* opaque */
@@ -123,6 +125,7 @@ typedef struct {
     int pixels;
     int x_stride, y_stride, r_stride; /* elements between rows of dx, of y and dy, and of an
                                          NHWC residual; 0 = contiguous */
+    int round_dz;            /* backward to bf16: dz in 16 bits, for half the matrix work */
 } wq8_q8linear_desc;
 
 wq8_status wq8_q8linear_plan_create(const wq8_q8linear_desc *desc, wq8_q8linear_plan **out);

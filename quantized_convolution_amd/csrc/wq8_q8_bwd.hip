@@ -10,19 +10,22 @@
 // writes the digits, of dz sx transposed. A third runs both products and the
 // column sums' join side by side; a last one joins products that are split along
 // k. dz is formed twice rather than kept: 3 bytes a value are read again where 4
-// would be written and read. 8192 x 640 x 2560 bf16 with gelu and z in codes takes
-// 28 + 45 + 75 us: the first two are bound by gelu's slope and by the loads' latency
-// (2.3 and 3.3 TB/s), the third by the matrix cores (1430 TOPS in tiles of 128 x 128).
-// In fp32, 4 digits, 1001 x 333 x 515 takes 6.6 + 7.8 + 11.4.
+// would be written and read.
+//
+// Four digits, whatever type the results have: a scale serves a whole row (for dw a
+// column over all tokens), and what one loud token leaves the others of 16 bits is
+// less than bf16 keeps. 2048 tokens, one with a gradient 10^4 times the others': dw is
+// off by 10 % in norm where that token's code is 0 with two digits, by bf16's own
+// 0.17 % with four. A plan may ask for two digits (round_dz). 8192 x 640 x 2560 bf16
+// with gelu and z in codes takes 232 us with four, 133 with two: 28 + 45 + 75, the
+// first two bound by gelu's slope and by the loads' latency (2.3 and 3.3 TB/s), the
+// third by the matrix cores (1430 TOPS in tiles of 128 x 128). In fp32
+// 1001 x 333 x 515 takes 6.6 + 7.8 + 11.4.
 #include "wq8_q8_gemm.h"
 #include "wq8_rows.h"
 
 namespace wq8 {
 namespace {
-
-// Digits of the products whose results are of type T.
-template <typename T>
-constexpr int planes_of() { return sizeof(T) == 2 ? 2 : 4; }
 
 enum { kZNone, kZValues, kZCodes };  // what the forward kept of z
 
@@ -367,7 +370,7 @@ __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_d
 }
 
 // ---------------------------------------------------------------- the products
-template <typename T>
+template <typename T, int PLANES>
 struct EpiScale {
     T *out;
     int64_t ld;
@@ -393,7 +396,7 @@ struct EpiScale {
         if (!WHOLE && (m >= M || n >= N)) return;
         Vec<T, 8> r;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r.v[e] = from_f32<T>(v.v[e] * (sizeof(T) == 2 ? 0x1p-8f : 0x1p-16f) * item.scale);
+        for (int e = 0; e < 8; ++e) r.v[e] = from_f32<T>(v.v[e] * (PLANES == 2 ? 0x1p-8f : 0x1p-16f) * item.scale);
         if constexpr (WHOLE) store_vec<T, 8>(out + (int64_t)m * ld + n, r);
         else store_vec_n<T, 8>(out + (int64_t)m * ld + n, r, N - n);
     }
@@ -417,27 +420,28 @@ __device__ __forceinline__ void dbias_block(const Q8Geo &g, const Q8Ptrs &a, int
 }
 
 // Blocks [0, nw): dw; [nw, nw + nx): dx; the rest: dbias.
-template <typename T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM *WN * 64) void k_q8_bwd(Q8Args dw, EpiScale<T> ew, int nw, Q8Args dx, EpiScale<T> ex, int nx,
-                                                        int nb, Q8Geo g, Q8Ptrs p) {
+template <typename T, int PLANES, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM *WN * 64) void k_q8_bwd(Q8Args dw, EpiScale<T, PLANES> ew, int nw, Q8Args dx, EpiScale<T, PLANES> ex,
+                                                        int nx, int nb, Q8Geo g, Q8Ptrs p) {
     int b;
     if (!block_number(nb, b)) return;
     if (b < nw + nx) {  // one copy of the product: which one is the same for a whole block
         const bool first = b < nw;
         const Q8Args q = first ? dw : dx;
-        const EpiScale<T> e = first ? ew : ex;
-        q8_block<BM, BN, WM, WN, planes_of<T>()>(q, e, first ? b : b - nw, first ? nw : nx);
+        const EpiScale<T, PLANES> e = first ? ew : ex;
+        q8_block<BM, BN, WM, WN, PLANES>(q, e, first ? b : b - nw, first ? nw : nx);
     } else {
         dbias_block(g, p, b - nw - nx);
     }
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void k_q8_bwd_join(Q8Args dw, EpiScale<T> ew, int nw, Q8Args dx, EpiScale<T> ex, int nb) {
+template <typename T, int PLANES>
+__global__ __launch_bounds__(256) void k_q8_bwd_join(Q8Args dw, EpiScale<T, PLANES> ew, int nw, Q8Args dx, EpiScale<T, PLANES> ex,
+                                                     int nb) {
     int b;
     if (!block_number(nb, b)) return;
-    if (b < nw) q8_join_block<planes_of<T>()>(dw, ew, b);
-    else q8_join_block<planes_of<T>()>(dx, ex, b - nw);
+    if (b < nw) q8_join_block<PLANES>(dw, ew, b);
+    else q8_join_block<PLANES>(dx, ex, b - nw);
 }
 
 template <typename T>
@@ -447,7 +451,7 @@ __global__ __launch_bounds__(256) void k_q8_zero(T *dw, int64_t values, float *d
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; dbias && i < N; i += step) dbias[i] = 0.0f;
 }
 
-template <typename T>
+template <typename T, int PLANES>
 struct RunQ8Backward {
     const Q8Geo &g;
     const Q8Ptrs &p;
@@ -479,21 +483,20 @@ struct RunQ8Backward {
             nx = q8_tiles<BM, BN>(dx, g.dx, p.partial_dx);
             jx = q8_join_blocks(dx);
         }
-        const EpiScale<T> ew = {(T *)p.dw, g.K, g.N, g.K, p.cscale}, ex = {(T *)p.dx, g.xs, g.M, g.K, p.rscale};
+        const EpiScale<T, PLANES> ew = {(T *)p.dw, g.K, g.N, g.K, p.cscale}, ex = {(T *)p.dx, g.xs, g.M, g.K, p.rscale};
         const int64_t blocks = nw + nx + (p.dbias ? (g.N + 15) / 16 : 0);
         if (blocks > 0) {
-            const auto kernel = k_q8_bwd<T, BM, BN, WM, WN>;
-            hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(WM * WN * 64), (q8_lds<BM, BN, planes_of<T>()>(kernel)), st, dw, ew, (int)nw, dx, ex,
+            const auto kernel = k_q8_bwd<T, PLANES, BM, BN, WM, WN>;
+            hipLaunchKernelGGL(kernel, grid_of(blocks), dim3(WM * WN * 64), (q8_lds<BM, BN, PLANES>(kernel)), st, dw, ew, (int)nw, dx, ex,
                                (int)nx, (int)blocks, g, p);
         }
         if (jw + jx > 0)
-            hipLaunchKernelGGL((k_q8_bwd_join<T>), grid_of(jw + jx), dim3(256), 0, st, dw, ew, (int)jw, dx, ex, (int)(jw + jx));
+            hipLaunchKernelGGL((k_q8_bwd_join<T, PLANES>), grid_of(jw + jx), dim3(256), 0, st, dw, ew, (int)jw, dx, ex, (int)(jw + jx));
     }
 };
 
-template <typename XT, typename YT, int ZF>
+template <typename XT, typename YT, int ZF, int PLANES>
 void prepare(const Q8Geo &g, const Q8Ptrs &p, hipStream_t st) {
-    constexpr int PLANES = planes_of<XT>();
     const auto tiles = [](int64_t rows, int64_t bytes) { return (rows + 127) / 128 * (bytes / 128); };
     const int64_t nm = (int64_t)g.nchunk * g.ncol, nx = p.dw ? tiles(g.M, g.Kp) : 0, nw = p.dx ? tiles(g.N, g.Kp) : 0;
     hipLaunchKernelGGL((k_q8_max<XT, YT, ZF>), grid_of(nm + nx + nw), dim3(kMaxWaves * 64), 0, st, g, p, (int)nm, (int)nx,
@@ -504,6 +507,14 @@ void prepare(const Q8Geo &g, const Q8Ptrs &p, hipStream_t st) {
                        (int)nd);
 }
 
+template <typename XT, typename YT, int PLANES>
+void products(const Q8Geo &g, const Q8Ptrs &p, hipStream_t st) {
+    if (g.act == WQ8_ACT_NONE) prepare<XT, YT, kZNone, PLANES>(g, p, st);
+    else if (p.z_in) prepare<XT, YT, kZValues, PLANES>(g, p, st);
+    else prepare<XT, YT, kZCodes, PLANES>(g, p, st);
+    pick_q8_pair_tile(g.dw.tile, RunQ8Backward<XT, PLANES>{g, p, st});
+}
+
 template <typename XT, typename YT>
 void backward(const Q8Geo &g, const Q8Ptrs &p, hipStream_t st) {
     if (g.M == 0) {
@@ -512,10 +523,9 @@ void backward(const Q8Geo &g, const Q8Ptrs &p, hipStream_t st) {
         return;
     }
     if (!p.dx && !p.dw && !p.dbias) return;
-    if (g.act == WQ8_ACT_NONE) prepare<XT, YT, kZNone>(g, p, st);
-    else if (p.z_in) prepare<XT, YT, kZValues>(g, p, st);
-    else prepare<XT, YT, kZCodes>(g, p, st);
-    pick_q8_pair_tile(g.dw.tile, RunQ8Backward<XT>{g, p, st});
+    if constexpr (sizeof(XT) == 2)
+        if (g.planes == 2) return products<XT, YT, 2>(g, p, st);
+    products<XT, YT, 4>(g, p, st);
 }
 
 }  // namespace

@@ -59,7 +59,7 @@ struct Q8Geo {
     int act;
     int64_t xs, ys, rs;
     int r_planar, pixels;
-    int planes;               // 8-bit digits of dz's products
+    int planes;               // 8-bit digits of dz's products: 4, or 2 where the caller asks for them
     Q8Shape f, dx, dw;        // dx and dw share a tile: they run in one kernel
     int chunk, nchunk;        // backward: rows per block of the first pass, blocks along the rows
     int ncol;                 // and along the columns

@@ -224,7 +224,7 @@ wq8_status build_q8linear(const wq8_q8linear_desc *d, wq8_q8linear_plan *p) {
     g.pixels = d->pixels;
     p->xdt = d->x_dtype;
     p->ydt = d->y_dtype;
-    g.planes = p->xdt == WQ8_BF16 ? 2 : 4;
+    g.planes = p->xdt == WQ8_BF16 && d->round_dz ? 2 : 4;
     const int64_t steps = g.Kp / 128;
     // two rows at most: 3.1 us for 1280 x 1280, 17.6 for 10240 x 10240, where the
     // kernel for short batches takes 3.4 and 18.8; at three rows 3.8 and 18.2, and

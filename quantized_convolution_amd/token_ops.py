@@ -39,7 +39,7 @@ class wq8_rms_desc(C.Structure):
 class wq8_q8linear_desc(C.Structure):
     _fields_ = [("rows", C.c_int64), ("Cin", C.c_int), ("Cout", C.c_int), ("act", C.c_int), ("x_dtype", C.c_int),
                 ("y_dtype", C.c_int), ("r_layout", C.c_int), ("pixels", C.c_int), ("x_stride", C.c_int), ("y_stride", C.c_int),
-                ("r_stride", C.c_int)]
+                ("r_stride", C.c_int), ("round_dz", C.c_int)]
 
 
 def code_stride(columns):
@@ -154,19 +154,24 @@ class Q8LinearPlan(_Plan):
     x_dtype: of the gradients dx and dw; y_dtype: of y, z, residual and dy.
     r_layout "nchw": the residual is [rows / pixels][Cout][pixels], as a
     convolution gives it. x_stride (dx), y_stride, r_stride: elements between the
-    rows of tensors that are slices of wider ones (0: contiguous)."""
+    rows of tensors that are slices of wider ones (0: contiguous). round_dz: a
+    backward to bf16 holds dz sw and dz sx in 16 bits of the largest of their row or
+    column, for half the matrix work. Where one token's gradient is some hundred times
+    the others', what these give to dw loses more than bf16's own rounding, and so
+    for a loud channel in dx (False: in 32 bits)."""
 
     _kind = "q8linear"
 
     def __init__(self, rows, Cin, Cout, act="none", x_dtype=torch.float32, y_dtype=None, r_layout="nhwc", pixels=0, x_stride=0,
-                 y_stride=0, r_stride=0):
+                 y_stride=0, r_stride=0, round_dz=False):
         y_dtype = x_dtype if y_dtype is None else y_dtype
         self.rows, self.Cin, self.Cout, self.act = rows, Cin, Cout, act
         self.x_dtype, self.y_dtype, self.r_layout, self.pixels = x_dtype, y_dtype, r_layout, pixels
         self.x_stride, self.y_stride, self.r_stride = int(x_stride), int(y_stride), int(r_stride)
+        self.round_dz = bool(round_dz)
         self._make(_desc(wq8_q8linear_desc, rows, Cin, Cout, _choice(ACTS, act, "act"), _choice(_DT, x_dtype, "x_dtype"),
                          _choice(_DT, y_dtype, "y_dtype"), _choice(LAYOUTS, r_layout, "r_layout"), pixels, self.x_stride,
-                         self.y_stride, self.r_stride))
+                         self.y_stride, self.r_stride, self.round_dz))
         self.x_shape, self.y_shape, self.w_shape = (rows, Cin), (rows, Cout), (Cout, Cin)
         self.r_shape = (rows // pixels, Cout, pixels) if r_layout == "nchw" else self.y_shape
         self.x_strides = (self.x_stride, 1) if self.x_stride else None
