@@ -53,7 +53,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L, L == 64 && U == 3 ? 3 : 1) void 
     Vec<float, kV> gm[U];
     float dg[U][kV] = {};
     load_gamma<L, U>(gm, a.gamma, t, g.C);
-    const int r0 = blockIdx.x * g.chunk, r1 = min(r0 + g.chunk, g.rows);
+    const int r0 = blockIdx.x * g.chunk, r1 = r0 + min(g.chunk, g.rows - r0);  // r0 + chunk may pass 2^31
     int turn = 0;
     for (int i = r0 + (L < 256 ? w : 0); i < r1; i += PER) {
         Vec<XT, kV> h[U], dh[U];
@@ -145,7 +145,7 @@ template <typename XT, typename YT>
 __global__ __launch_bounds__(256) void k_rms_dgamma_long(RowsGeo g, RmsPtrs a) {
     const int c = (blockIdx.y * 256 + threadIdx.x) * kV;
     if (c >= g.C) return;
-    const int r0 = blockIdx.x * g.chunk, r1 = min(r0 + g.chunk, g.rows);
+    const int r0 = blockIdx.x * g.chunk, r1 = r0 + min(g.chunk, g.rows - r0);
     Vec<float, kV> o = {};
     for (int i = r0; i < r1; ++i) {
         const Vec<XT, kV> h = load_any<XT>((const XT *)a.x + i * g.xs, c, g.C);
