@@ -17,6 +17,12 @@ from .token_ops import (Q8LinearPlan, QuantPlan, RmsPlan, wq8_q8linear_backward,
                         wq8_rms_backward, wq8_rms_forward)
 
 
+def _is(x, own):
+    """Whether x, a tensor of own's form, is the memory of own."""
+    return isinstance(x, torch.Tensor) and x.shape == own.shape and x.dtype == own.dtype and x.is_contiguous() and \
+        x.data_ptr() == own.data_ptr() and x.device == own.device
+
+
 class Q8FeedForward:
     """x [rows][C], a residual of its shape or None -> out [rows][C].
 
@@ -24,7 +30,12 @@ class Q8FeedForward:
     they may be parameters. They are packed when the block is made and by `pack`,
     after they change; `backward` returns their gradients, those of the packed
     weights as the weights' own. Plans, workspaces and outputs are made once; a
-    call only launches. train=False keeps nothing for a backward."""
+    call only launches, and the next one writes over what it returned. train=False
+    keeps nothing for a backward.
+
+    Without a residual x itself is the stream that `backward` reads: it stays as it
+    is until then. What the block has returned may be given to it again (it is
+    copied, since the call, or its backward, writes over it)."""
 
     def __init__(self, weights, rows, C, dtype=torch.bfloat16, eps=1e-6, act="gelu", train=True, device="cuda"):
         self.w, self.train = weights, train
@@ -62,6 +73,8 @@ class Q8FeedForward:
     def _forward(self, x, residual):
         w, ws = self.w, self.ws
         h = None if residual is None else self.h
+        if self.train and h is None and (_is(x, self.out) or _is(x, self.dx)):
+            x = self.h.copy_(x)
         wq8_rms_forward(self.norm, x, w["gamma"], residual, h=h, codes=self.a[0], scales=self.a[1], rstd=self.rstd, want_y=False,
                         workspace=ws)
         self.stream = x if residual is None else h
