@@ -248,7 +248,7 @@ def wq8_rms_forward(plan: RmsPlan, x, gamma=None, residual=None, y=None, h=None,
     stream h is made where a residual is given (it may be x or residual itself);
     without one it is x."""
     if (stream is None and not (want_y and y is None) and not (want_codes and codes is None) and not (want_rstd and rstd is None) and
-            (h is None) == (residual is None) and
+            (h is None) == (residual is None) and (codes is None) == (scales is None) and
             _given(plan._forward, plan._h, plan._forward_form, x, residual, gamma, h, y, codes, scales, rstd, workspace)):
         return y, x if residual is None else h, codes, scales, rstd
     f32 = torch.float32
