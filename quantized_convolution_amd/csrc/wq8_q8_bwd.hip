@@ -29,10 +29,12 @@ namespace {
 
 enum { kZNone, kZValues, kZCodes };  // what the forward kept of z
 
-// gelu's slope for bf16 results, Phi(z) + z phi(z), by its symmetry about (0, 1/2):
-// what |z| has over 1/2 is 1/2 - Phi(-|z|) + |z| phi(z), with Phi(-|z|) as
-// normal_cdf<false>() has it (1.5e-7), its half taken into the coefficients. 17
-// operations for 25: the slope is formed in both passes, and they are bound by that.
+// gelu's slope for bf16 results, Phi(z) + z phi(z), from that at -|z|, Phi(-|z|) - |z|
+// phi(z), of which it is what is left of 1 for z >= 0. Phi(-|z|) as normal_cdf<false>()
+// has it (1.5e-7), its half taken into the coefficients. 16 operations for 25: the
+// slope is formed in both passes, and they are bound by that. Neither term is near
+// 1/2, so the negative tail keeps three digits; as a difference from 1/2 it was off by
+// 6 % at -5.5.
 __device__ __forceinline__ float gelu_slope(float z) {
     const float a = fabsf(z), e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);  // exp(-z^2 / 2)
     const float t = fast_rcp(fmaf(0.3275911f * 0.70710678118654752f, a, 1.0f));
@@ -40,8 +42,8 @@ __device__ __forceinline__ float gelu_slope(float z) {
     s = fmaf(s, t, 0.7107068705f);
     s = fmaf(s, t, -0.142248368f);
     s = fmaf(s, t, 0.127414796f);
-    const float over = fmaf(a * 0.3989422804014327f, e, fmaf(-s * t, e, 0.5f));
-    return 0.5f + __builtin_copysignf(over, z);
+    const float low = fmaf(a * -0.3989422804014327f, e, s * t * e);
+    return z < 0.0f ? low : 1.0f - low;
 }
 
 template <int ACT, bool EXACT>
