@@ -17,9 +17,10 @@ static __device__ const float kNothing[8] = {};
 
 // gelu for bf16 results, z Phi(z) = max(z, 0) - |z| Phi(-|z|), with Phi(-|z|) as
 // normal_cdf<false>() has it, its half taken into the coefficients: 12 operations
-// and two transcendental ones for 20. The bound on |z| keeps infinity times 0 out.
+// and two transcendental ones for 20. The bound keeps infinity times 0 out where z is
+// +infinity; -infinity gives a NaN as act_fwd() does.
 __device__ __forceinline__ float gelu_of(float z) {
-    const float a = fminf(fabsf(z), 1e18f), e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);  // exp(-z^2 / 2)
+    const float a = fabsf(fminf(z, 1e18f)), e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);  // exp(-z^2 / 2)
     const float t = fast_rcp(fmaf(0.3275911f * 0.70710678118654752f, a, 1.0f));
     float s = fmaf(0.5307027145f, t, -0.7265760135f);
     s = fmaf(s, t, 0.7107068705f);
