@@ -71,7 +71,8 @@ bool fits(const at::Tensor &t, const Buffer &b) {
 
 // addresses(form, tensor or None, ...): (device, address, ...), a workspace as
 // its address and bytes; None where a tensor is not as its form says, asks for a
-// gradient while graphs are recorded, or is not on the same GPU as the others.
+// gradient while graphs are recorded, carries a tangent, or is not on the same GPU
+// as the others.
 PyObject *addresses(PyObject *, PyObject *const *args, Py_ssize_t n) {
     auto *v = n > 0 ? (std::vector<Buffer> *)PyCapsule_GetPointer(args[0], kName) : nullptr;
     if (!v || (size_t)n != v->size() + 1) {
@@ -94,7 +95,7 @@ PyObject *addresses(PyObject *, PyObject *const *args, Py_ssize_t n) {
             }
             if (!THPVariable_CheckExact(o)) Py_RETURN_NONE;
             const at::Tensor &t = THPVariable_Unpack(o);
-            if (!t.is_cuda() || (t.requires_grad() && c10::GradMode::is_enabled())) Py_RETURN_NONE;
+            if (!t.is_cuda() || (t.requires_grad() && c10::GradMode::is_enabled()) || t._fw_grad(0).defined()) Py_RETURN_NONE;
             if (device < 0) device = t.get_device();
             if (t.get_device() != device) Py_RETURN_NONE;
             if (b.workspace) {

@@ -10,13 +10,15 @@ A call runs on `stream`, or on the current one; outputs and workspaces that it
 makes are allocated as that stream's. Buffers that a caller gives are ordered
 and kept by the caller, as with any work on another stream than their own. No
 autograd graph is recorded: the backwards are functions of their own, and a
-tensor that requires a gradient is refused unless under torch.no_grad().
+tensor that requires a gradient is refused unless under torch.no_grad(). One that
+carries a tangent of forward-mode differentiation is refused: none would come out.
 """
 from __future__ import annotations
 
 import ctypes as C
 
 import torch
+from torch.autograd import forward_ad
 
 from .binding import _DT, _check, load
 
@@ -213,6 +215,8 @@ class _Args:
             if t.requires_grad and torch.is_grad_enabled():
                 raise ValueError(f"{name} requires a gradient, and no graph is recorded here: call this under "
                                  "torch.no_grad() and form gradients with the operator's backward")
+            if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError(f"{name} carries a tangent, and no tangents are formed here: give its primal")
             d = t.get_device()
             if d != self.device:
                 if self.device is not None:
