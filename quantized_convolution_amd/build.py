@@ -2,7 +2,8 @@
 
 hipcc compiles the kernels, the host plan and the C ABI (one object per
 source, in parallel) and links them into a shared library next to this file;
-g++ compiles the CPython module that checks a call's buffers. Numerics flags: no fp contraction (every fma
+g++ compiles the CPython module that checks a call's buffers, without which the
+checks are those in Python. Numerics flags: no fp contraction (every fma
 is written out), IEEE fp32 division, fp32 denormals kept, no packed fp32
 instructions.
 """
@@ -11,6 +12,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -70,17 +72,23 @@ def build(verbose: bool = False) -> str:
 
         def compile_buffers():
             out = BUFFERS_LIB + ".tmp"
-            r = subprocess.run(buffers_command(out), capture_output=True, text=True)
-            if r.returncode == 0:
+            try:
+                r = subprocess.run(buffers_command(out), capture_output=True, text=True)
+                rc, msgs = r.returncode, r.stdout + r.stderr
+            except (ImportError, OSError) as e:  # no g++, no headers
+                rc, msgs = 1, str(e)
+            if rc == 0:
                 os.replace(out, BUFFERS_LIB)
-            return r.returncode, r.stdout + r.stderr
+            elif os.path.exists(BUFFERS_LIB):  # of another source
+                os.remove(BUFFERS_LIB)
+            return rc, msgs
 
         with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
             module = ex.submit(compile_buffers)
             results = list(ex.map(compile_one, SOURCES))
             rc, msgs = module.result()
-        if rc != 0:
-            raise RuntimeError(f"g++ failed on {BUFFERS} ({rc}):\n{msgs}")
+        if rc != 0:  # the library does without
+            warnings.warn(f"g++ failed on {BUFFERS} ({rc}), calls take the longer way through their checks:\n{msgs}", RuntimeWarning)
         for src, _, rc, msgs in results:
             if rc != 0:
                 raise RuntimeError(f"hipcc failed on {src} ({rc}):\n{msgs}")

@@ -13,16 +13,12 @@ in whole lines of 128 bytes with zeros behind the last column, and f32 scales,
 from __future__ import annotations
 
 import ctypes as C
+import warnings
 
 import torch
 
 from .binding import _DT, _check, load
 from .ops import ACTS, LAYOUTS, _Args, _choice, _desc, _empty, _Plan, _raw_stream
-
-try:  # built beside the library
-    from ._wq8_buffers import addresses as _addresses, form as _form
-except ImportError:  # not built yet: load() names that, when a plan is made
-    _addresses = _form = None
 
 Z_GROUP = 32  # columns that share a scale where a product's z is kept in codes
 
@@ -65,8 +61,25 @@ def _given(fn, handle, form, *buffers):
     return True
 
 
+_addresses = _form = None  # the module's functions; False where it cannot be loaded
+
+
+def _load_buffers():
+    """The CPython module that is built beside the library. Without it every call
+    takes the longer way through the checks."""
+    global _addresses, _form
+    try:
+        from ._wq8_buffers import addresses as _addresses, form as _form
+    except ImportError as e:
+        _addresses = _form = False
+        warnings.warn(f"_wq8_buffers cannot be loaded ({e}): calls whose buffers are all given take some microseconds more. Build it "
+                      "again with `python -c 'import __graft_entry__ as g; g.build()'`", RuntimeWarning, stacklevel=4)
+
+
 def _forms(*entries):
     """The form of a call's buffers, for _given()."""
+    if _form is None:
+        _load_buffers()
     return _form(tuple(e if isinstance(e, int) else (e[0], tuple(e[1]), e[2], e[3]) for e in entries)) \
         if _form and _raw_stream else None
 
