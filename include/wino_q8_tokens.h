@@ -103,12 +103,14 @@ wq8_status wq8_rms_backward(const wq8_rms_plan *plan, const void *dy, const void
  * and w^ = sw wq, what the codes stand for,
  *   dx = dz w^;  dw = dz^T x^;  dbias = sum_r dz
  * so no 16- or 32-bit activation or weight is read. dz sw (for dx) and dz sx (for
- * dw) are multiplied as whole numbers in fixed point, 31 bits and a sign of the
- * largest magnitude of their row (column): each is off by at most 2^-32 of that
- * largest one, or its own rounding. With round_dz, where dx and dw are bf16, they
- * have 15 bits and a sign, and are off by at most 2^-16 of the largest one; where a
- * row (column) holds one value some hundred times the others, that is more than
- * bf16 results lose by themselves. The products and their sums are exact. dbias
+ * dw) are multiplied as whole numbers in fixed point of the largest magnitude m of
+ * their row (column), which is 127 256^3 units: each is off by at most half a unit,
+ * m / 4261412864, and by its own rounding to f32. With round_dz, where dx and dw are
+ * bf16, m is 127 256 units and half a unit m / 65024; where a row (column) holds one
+ * value some hundred times the others, that is more than bf16 results lose by
+ * themselves. Sums of products are whole numbers: those of round_dz exact, the others
+ * to 2^-17 m / 127 (in units of the codes). A sum that is split over several blocks
+ * is joined from parts in f32, each with its rounding, in a fixed order. dbias
  * sums fp32 values. A row of dz sw that holds an infinity or a NaN makes its row
  * of dx NaN, a column of dz sx its row of dw. */
 typedef struct wq8_q8linear_plan wq8_q8linear_plan; /* opaque */

@@ -14,8 +14,9 @@
 // has of B serves both, a fragment of it twice the matrix instructions. Of four
 // planes the lower two come first; their sum, rounded to the third plane's unit,
 // is carried into the second plane's, but for its last byte, which is kept and
-// put back at the end. So the sums of 2 planes are exact, of 4 to 2^-17 of the
-// highest plane's unit.
+// put back at the end. So a block's sums of 2 planes are exact, of 4 to 2^-17 of the
+// highest plane's unit. Where k is split the parts of more than one plane are
+// rounded to f32 and joined in f32; those of one plane are whole numbers.
 #pragma once
 
 #include "wq8_gemm_device.h"

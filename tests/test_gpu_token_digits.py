@@ -118,3 +118,25 @@ def test_rounded_dz_of_borders(y_dtype):
     want = R.backward(small, xq, sx, wq, sw, 70, BF)
     check(dx, want["dx"], "small dx")
     check(dw, want["dw"], "small dw")
+
+
+@pytest.mark.parametrize("round_dz", [False, True])
+def test_the_stated_bounds(round_dz):
+    """dz sw itself, as products with a single code of 1 give it: off by half a unit of the fixed point (which is more
+    than a half of 2^-15 or 2^-31 of the largest), and with four digits by what the sum leaves of the last one."""
+    n, dtype = 128, BF if round_dz else F32
+    unit = 1 / 32512 if round_dz else 1 / 2130706432
+    eye = torch.eye(n, dtype=torch.int8, device="cuda")
+    one = torch.ones(n, device="cuda")
+    g = torch.Generator().manual_seed(1)
+    k = torch.randint(0, 100 if round_dz else 1 << 20, (n, n), generator=g).double()
+    k[:, 1] = 0
+    dy = ((k + 0.4999) * unit).float()
+    dy[:, 0] = 1
+    p = q.Q8LinearPlan(n, n, n, x_dtype=dtype, y_dtype=F32, round_dz=round_dz)
+    dx = q.wq8_q8linear_backward(p, dy.cuda(), eye, one, eye, one)[0].cpu().double()
+    want = dy.double()
+    left = 0.0 if round_dz else 2.0 ** -17 / 127
+    bound = unit / 2 + left + 3 * R.U * want + R.rounding(dx, dtype)
+    assert bool(((dx - want).abs() <= bound).all())
+    assert bool(((dx - want)[:, 1].abs() > (2.0 ** -16 if round_dz else 2.0 ** -32)).all())
