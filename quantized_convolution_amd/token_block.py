@@ -6,8 +6,12 @@ are used together, for serving and for training:
 Both products run on 8-bit codes: the norm hands its own on, the inner
 activations are packed. What the backward needs is kept in 8 bits (codes of both
 products' inputs and of the first one's z), beside the stream h and one number a
-row: 1 + 4 (1 + 1.125) bytes a value of the stream for an inner width of 4 C,
-where bf16 activations would be 2 (1 + 4 + 4).
+row: 1 + 4 (1 + 1.125) = 9.5 bytes a value of the stream for an inner width of 4 C,
+where bf16 activations would be 2 (1 + 4 + 4) = 18. The block also owns the buffers
+that it works in for as long as it lives: in bf16 the inner activations and their
+gradient (8 + 8), the stream, the output and two gradients of it (2 each), 24 bytes a
+value more. One block serves layers one after the other only if their backwards
+follow their calls; a block for each layer holds them for each.
 """
 from __future__ import annotations
 
