@@ -192,13 +192,14 @@ class _Args:
     strides that the plan gives, all on one GPU. The kernels size their
     accesses from the plan, so anything else would be out of bounds."""
 
-    __slots__ = ("stream", "device", "where", "ws")
+    __slots__ = ("stream", "device", "where", "ws", "dual")
 
     def __init__(self, stream=None):
         self.stream = stream
         self.device = None  # index; -1: not a GPU
         self.where = None   # the first buffer and its name
         self.ws = None      # the workspace, kept until the call is enqueued
+        self.dual = forward_ad._current_level >= 0  # whether tensors may carry tangents
 
     def need(self, t, name, dtype, shape, strides=None):
         """The tensor's address."""
@@ -215,7 +216,7 @@ class _Args:
             if t.requires_grad and torch.is_grad_enabled():
                 raise ValueError(f"{name} requires a gradient, and no graph is recorded here: call this under "
                                  "torch.no_grad() and form gradients with the operator's backward")
-            if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+            if self.dual and forward_ad.unpack_dual(t).tangent is not None:
                 raise ValueError(f"{name} carries a tangent, and no tangents are formed here: give its primal")
             d = t.get_device()
             if d != self.device:
