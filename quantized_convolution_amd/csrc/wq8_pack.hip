@@ -1,6 +1,7 @@
 // Packing of rows to codes with one scale a row or one for 32, 64 or 128
 // columns, and back. Memory bounds all three: 8192 x 5120 bf16 unpacked take 21 us
-// (6.0 TB/s), 1001 x 2565 f32 in groups of 32 columns 4.6 packed and 5.3 unpacked
+// (6.0 TB/s), in groups of 32 columns 22.9 packed and 22.5 unpacked (5.5 TB/s), in
+// f32 31.5 and 32.9 (6.7 and 6.4); 1001 x 2565 f32 in groups of 32 columns 4.6 and 5.3
 // (2.8 and 2.4 TB/s, a third of it the launch).
 #include "wq8_rms_fwd.h"
 

@@ -17,10 +17,11 @@
 // less than bf16 keeps. 2048 tokens, one with a gradient 10^4 times the others': dw is
 // off by 10 % in norm where that token's code is 0 with two digits, by bf16's own
 // 0.17 % with four. A plan may ask for two digits (round_dz). 8192 x 640 x 2560 bf16
-// with gelu and z in codes takes 232 us with four, 133 with two: 28 + 45 + 75, the
-// first two bound by gelu's slope and by the loads' latency (2.3 and 3.3 TB/s), the
-// third by the matrix cores (1430 TOPS in tiles of 128 x 128). In fp32
-// 1001 x 333 x 515 takes 6.6 + 7.8 + 11.4.
+// with gelu and z in codes takes 229 us with four, 30 + 71 + 143 + 8 in the trace, and
+// 130 with two, 28 + 45 + 75: the first two kernels are bound by gelu's slope and by
+// the loads' latency (2.3 and 3.3 TB/s), the third by the matrix cores
+// (1500 TOPS in tiles of 128 x 128, 1430 with two digits). In fp32 1001 x 333 x 515
+// takes 6.6 + 7.9 + 10.9.
 #include "wq8_q8_gemm.h"
 #include "wq8_rows.h"
 
@@ -265,8 +266,8 @@ struct Digits {
 };
 
 // 128 rows x 32 columns: a thread has 4 rows of 4 columns. With 8 columns it has
-// fewer and longer waves: 1024 x 640 x 640 then takes 22.2 us for 20.0 in bf16 and
-// 33.1 for 29.3 in fp32, 8192 x 640 x 2560 130.3 for 128.5 and 238 for 248.
+// fewer and longer waves: 1024 x 640 x 640 then takes 22.2 us for 20.0 with two digits
+// and 33.1 for 29.3 with four, 8192 x 640 x 2560 130.3 for 128.5 and 238 for 248.
 template <typename XT, typename YT, int ZF, int PLANES>
 __global__ __launch_bounds__(256) void k_q8_digits(Q8Geo g, Q8Ptrs a, int want_dx, int want_dw, int nb) {
     constexpr int V = 4, COLS = 8 * V, ACROSS = COLS / 4, ALONG = 256 / ACROSS;

@@ -3,8 +3,8 @@
 // The sums are whole numbers on the int8 matrix cores; scales, bias, activation,
 // residual and what is kept of z (as it is, or in codes of 32 columns, which
 // four lanes of a wave have) are in the epilogue. With gelu, z in codes and y in bf16
-// 16384 x 2560 x 10240 takes 516 to 549 us, without either 424 to 460: the epilogue
-// of the largest tile runs alone on its compute unit.
+// 16384 x 2560 x 10240 takes 513 to 538 us, without either 410, in fp32 586 and 475:
+// the epilogue of the largest tile runs alone on its compute unit.
 //
 // One or two rows (single tokens) and short batches have kernels of their own.
 #include "wq8_q8_gemm.h"
@@ -152,7 +152,8 @@ struct EpiQ8 {
 // time, 16 a lane, four products an instruction, OUT columns in turn, two of them
 // with their loads in flight; the rows' codes stay in registers meanwhile. Sums
 // over the lanes are whole numbers, in any order the same. Memory bounds it: one row
-// by 10240 x 10240 takes 19.4 us in a chain of such calls (5.4 TB/s), 33.7 in a tile.
+// by 10240 x 10240 takes 17.8 to 19.4 us in a chain of such calls (5.4 to 5.9 TB/s),
+// 33.7 in a tile.
 constexpr int kDotWaves = 4;
 
 template <int ROWS, int OUT, typename EPI>
@@ -217,8 +218,8 @@ __global__ __launch_bounds__(kDotWaves * 64) void k_q8_dot(Q8Args a, EPI epi, in
 // fourth k step each, so that few steps follow one another. A wave loads its own
 // lines of both operands into buffers of its own and waits for no other; the
 // sums of the four, whole numbers, meet at the end. 16 rows of 10240 x 10240 take
-// 18.8 us, 5.6 TB/s of weights, and 23.8 in a tile whose k steps are split over
-// blocks; 64 rows of 1280 x 1280 3.8 us, of which 2.2 are the launch, and 5.7 in
+// 18.8 to 21.6 us, 4.9 to 5.6 TB/s of weights, and 23.8 in a tile whose k steps are
+// split over blocks; 64 rows of 1280 x 1280 3.8 us, of which 2.2 are the launch, and 5.7 in
 // the smallest tile, whose ten steps follow one another.
 constexpr int kThinWaves = 4, kThinCols = 32;
 constexpr int thin_depth(int rt) { return rt == 1 ? 3 : 2; }  // two blocks fit a compute unit

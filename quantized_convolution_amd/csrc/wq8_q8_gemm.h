@@ -7,8 +7,9 @@
 // is multiplied: the layout, the swizzle and the loads are those of the bf16
 // product, whose k steps have the same bytes. Small tiles, whose blocks are few
 // and wait for memory, have three or four buffers, all but one on their way.
-// The matrix cores bound it: 8192^3 runs at 2020 to 2090 TOPS, a library's at 1948,
-// 16384 x 2560 x 10240 in 424 to 460 us (1870 to 2030 TOPS) before its epilogue.
+// The matrix cores bound it: 8192^3 of random codes in a chain of such calls runs at
+// 2400 TOPS (458 us), a library's on the same card at 2270 (485), and
+// 16384 x 2560 x 10240 in 411 us (2090 TOPS) before its epilogue.
 //
 // Two planes are multiplied together, each with sums of its own: what a k step
 // has of B serves both, a fragment of it twice the matrix instructions. Of four
